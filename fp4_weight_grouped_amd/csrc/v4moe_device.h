@@ -112,6 +112,44 @@ __device__ __forceinline__ v4f mfma_e4m3_e2m1_sel(int sel, v8i a, uint4 b, int s
     }
 }
 
+// ---- direct-to-LDS copies ----
+
+// Wait until at most N of this wave's vector memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Direct-to-LDS copy: each lane moves 16 bytes from its own global address to
+// lds_base + lane*16 (lds_base wave-uniform, in M0); lanes outside EXEC do not
+// write.  As inline asm it is invisible to the compiler's wait insertion:
+// completion is awaited with an explicit wait_vm.
+__device__ __forceinline__ void dma16(const void* g, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(g), "s"(lds_base) : "memory", "m0");
+}
+
+// Direct-to-LDS copies: each lane moves 16 (or 4) bytes from its own global
+// address to lds_base + lane*16 (lane*4); lds_base is wave-uniform (M0).  As
+// inline asm they are invisible to the compiler's wait insertion, which would
+// otherwise drain the whole pipeline before every LDS read; completion is
+// awaited explicitly with wait_vm<N>() (at most N of this wave's vector memory
+// operations still outstanding).  The global address is a wave-uniform 64-bit
+// base (SGPRs) plus a 32-bit per-lane byte offset.
+__device__ __forceinline__ void dma16s(const void* base, uint32_t off, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4s(const void* base, uint32_t off, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_base) : "memory", "m0");
+}
+
 // splitmix64 output function (Steele, Lea & Flood, OOPSLA 2014).
 __device__ __forceinline__ uint64_t splitmix64(uint64_t v)
 {

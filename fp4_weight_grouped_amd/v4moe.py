@@ -28,6 +28,16 @@ ACT_SWIGLU = 0
 ACT_RELU2 = 1
 ACT_RELU = 2
 
+TYPE_F32 = 0
+TYPE_BF16 = 1
+
+SCORE_SIGMOID = 0
+SCORE_SOFTMAX = 1
+SCORE_SQRTSOFTPLUS = 2
+
+SCALE_BLOCK = 0
+SCALE_ROW = 1
+
 
 class V4MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
@@ -48,9 +58,32 @@ class ExpertsC(ctypes.Structure):
     _fields_ = [("gate", Mat), ("up", Mat), ("down", Mat)]
 
 
+class GateC(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class GemmC(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("b_scale", ctypes.c_int32),
+                ("c_type", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("lda", ctypes.c_int64),
+                ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64), ("bs_n", ctypes.c_int64), ("bs_k", ctypes.c_int64)]
+
+
+class FP8MatC(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("q", ctypes.c_void_p), ("qt", ctypes.c_void_p),
+                ("blk", ctypes.c_void_p)]
+
+
+class TensorC(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
+_f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 _DP = ctypes.POINTER(Dims)
 
@@ -85,12 +118,28 @@ def lib():
                                                 _vp, _vp, _vp, _vp, _vp]
         L.moe_noalloc_max_workspace_bytes.argtypes = []
         L.moe_noalloc_max_workspace_bytes.restype = _sz
+        GP, MP = ctypes.POINTER(GateC), ctypes.POINTER(FP8MatC)
+        L.moe_gate.argtypes = [GP, _vp, _i32, _i64, _vp, _vp, _vp, _vp]
+        L.moe_gate_backward.argtypes = [GP, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp]
+        L.moe_fp8_quantize.argtypes = [_i32, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp]
+        L.moe_fp8_quantize_weights.argtypes = [_i32, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp]
+        L.moe_fp8_gemm.argtypes = [ctypes.POINTER(GemmC), _vp, _vp, _vp, _vp, _vp, _vp]
+        L.moe_fp8_linear_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
+        L.moe_fp8_linear_workspace_bytes.restype = _sz
+        L.moe_fp8_linear.argtypes = [_i32, _vp, _i32, _i64, MP, _vp, _i32, _i64, _vp, _sz, _vp]
+        L.moe_fp8_linear_backward.argtypes = [_i32, _vp, _i32, _i64, _vp, _i32, _i64, MP, _vp, _i32, _i64, _vp, _i32,
+                                              _i64, _i32, _vp, _sz, _vp]
+        L.moe_clip_workspace_bytes.argtypes = [_i32]
+        L.moe_clip_workspace_bytes.restype = _sz
+        L.moe_clip_grads.argtypes = [_i32, ctypes.POINTER(TensorC), _f32, _vp, _vp, _sz, _vp]
         L.moe_time_next_ffn.argtypes = [_vp, _vp]
         L.moe_time_next_ffn.restype = None
         for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
                   "moe_layer_forward_noalloc",
                   "moe_prepack_weights", "moe_dequant_fp8", "moe_quantize_weights", "moe_transpose_weights",
-                  "moe_layer_backward"):
+                  "moe_layer_backward", "moe_gate", "moe_gate_backward", "moe_fp8_quantize",
+                  "moe_fp8_quantize_weights", "moe_fp8_gemm", "moe_fp8_linear", "moe_fp8_linear_backward",
+                  "moe_clip_grads"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -245,6 +294,198 @@ def moe_time_next_ffn(start_event, stop_event):
     a = None if start_event is None else ctypes.c_void_p(start_event.cuda_event)
     b = None if stop_event is None else ctypes.c_void_p(stop_event.cuda_event)
     lib().moe_time_next_ffn(a, b)
+
+
+# ---- operators next to the layer ---------------------------------------------------------------
+_TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
+
+
+def _type(t: torch.Tensor) -> int:
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"float32 or bfloat16 expected, got {t.dtype}") from None
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dtype=None):
+    """t's leading dimension, after checking that it is [rows][cols] with contiguous columns on a GPU."""
+    _require(t.is_cuda, f"{what} must be on a GPU")
+    _require(t.shape == (rows, cols), f"{what} must be [{rows}][{cols}], got {list(t.shape)}")
+    _require(dtype is None or t.dtype == dtype, f"{what} must be {dtype}, got {t.dtype}")
+    st = t.stride()
+    _require(cols <= 1 or st[1] == 1, f"{what} must have contiguous rows")
+    if rows <= 1:
+        return cols
+    _require(st[0] >= cols, f"{what} must not have overlapping rows")
+    return st[0]
+
+
+def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Optional[torch.Tensor] = None,
+         groups: int = 1, topk_groups: int = 1, renorm: bool = True, scale: float = 1.0):
+    """Routing from logits [T][E] (fp32 or bf16, rows may be strided); bias: fp32 [E], selection only.
+    Returns (topk_ids int32 [T][topk], topk_w fp32 [T][topk]).  See moe_gate in include/v4moe.h."""
+    T, E = logits.shape
+    ld = _matrix(logits, T, E, "logits")
+    if bias is not None:
+        _require(bias.is_cuda and bias.shape == (E,) and bias.dtype == torch.float32 and bias.is_contiguous(),
+                 f"bias must be contiguous float32 [{E}] on a GPU")
+    g = GateC(T, E, topk, score, groups, topk_groups, 1 if renorm else 0, scale)
+    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    w = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    _check(lib().moe_gate(ctypes.byref(g), _p(logits), _type(logits), ld, _p(bias), _p(ids), _p(w), _stream()))
+    return ids, w
+
+
+def gate_backward(logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, dw: torch.Tensor,
+                  score: int = SCORE_SIGMOID, renorm: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """dL/dlogits [T][E] (the logits' type) from dw = dL/dtopk_w and gate()'s outputs."""
+    T, E = logits.shape
+    ld = _matrix(logits, T, E, "logits")
+    k = topk_ids.shape[1]
+    for t, name, dt in ((topk_ids, "topk_ids", torch.int32), (topk_w, "topk_w", torch.float32), (dw, "dw", torch.float32)):
+        _matrix(t, T, k, name, dt)
+        _require(t.is_contiguous(), f"{name} must be contiguous")
+    g = GateC(T, E, k, score, 1, 1, 1 if renorm else 0, scale)
+    dl = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check(lib().moe_gate_backward(ctypes.byref(g), _p(logits), _type(logits), ld, _p(topk_ids), _p(topk_w), _p(dw),
+                                   _p(dl), E, _stream()))
+    return dl
+
+
+def _up16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def _chunks(n: int) -> int:
+    return (n + 127) // 128
+
+
+@dataclasses.dataclass
+class FP8Matrix:
+    """A dense weight [N][K] in E4M3 (v4moe_fp8mat)."""
+    N: int
+    K: int
+    q: torch.Tensor     # uint8 [N][K rounded up to 16]
+    qt: torch.Tensor    # uint8 [K][N rounded up to 16]
+    blk: torch.Tensor   # float32 [ceil(N/128)][ceil(K/128)]
+
+    def c(self) -> FP8MatC:
+        for t, shape, dt in ((self.q, (self.N, _up16(self.K)), torch.uint8), (self.qt, (self.K, _up16(self.N)), torch.uint8),
+                             (self.blk, (_chunks(self.N), _chunks(self.K)), torch.float32)):
+            _require(t.is_cuda and t.shape == shape and t.dtype == dt and t.is_contiguous(),
+                     f"an FP8Matrix part must be contiguous {dt} {list(shape)} on a GPU, got {t.dtype} {list(t.shape)}")
+        return FP8MatC(self.N, self.K, self.q.data_ptr(), self.qt.data_ptr(), self.blk.data_ptr())
+
+
+def fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False):
+    """E4M3 codes of x [M][K] and their scales: (q, s) by rows and / or (qt, st) by columns, None where not asked."""
+    M, K = x.shape
+    ld = _matrix(x, M, K, "x")
+    dev = x.device
+    q = torch.empty((M, _up16(K)), dtype=torch.uint8, device=dev) if rows else None
+    s = torch.empty((_chunks(K), M), dtype=torch.float32, device=dev) if rows else None
+    qt = torch.empty((K, _up16(M)), dtype=torch.uint8, device=dev) if cols else None
+    st = torch.empty((_chunks(M), K), dtype=torch.float32, device=dev) if cols else None
+    _check(lib().moe_fp8_quantize(M, K, _p(x), _type(x), ld, _p(q), _p(s), _p(qt), _p(st), _stream()))
+    return q, s, qt, st
+
+
+def fp8_weights(w: torch.Tensor) -> FP8Matrix:
+    """E4M3 codes of a weight [N][K] (fp32 or bf16) in both orders, a scale for each 128x128 block."""
+    N, K = w.shape
+    ld = _matrix(w, N, K, "w")
+    dev = w.device
+    m = FP8Matrix(N, K, torch.empty((N, _up16(K)), dtype=torch.uint8, device=dev),
+                  torch.empty((K, _up16(N)), dtype=torch.uint8, device=dev),
+                  torch.empty((_chunks(N), _chunks(K)), dtype=torch.float32, device=dev))
+    _check(lib().moe_fp8_quantize_weights(N, K, _p(w), _type(w), ld, _p(m.q), _p(m.qt), _p(m.blk), _stream()))
+    return m
+
+
+def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, rows: bool = False,
+             out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
+    """a [M][K] times b [N][K] transposed, E4M3 codes (K a multiple of 16) with scales a_scale [ceil(K/128)][M] and
+    b_scale: [ceil(N/128)][ceil(K/128)] (any strides), or with ``rows`` [ceil(K/128)][N].  out: [M][N], bf16 by default."""
+    (M, K), N = a.shape, b.shape[0]
+    lda, ldb = _matrix(a, M, K, "a", torch.uint8), _matrix(b, N, K, "b", torch.uint8)
+    n = _chunks(K)
+    _matrix(a_scale, n, M, "a_scale", torch.float32)
+    _require(a_scale.is_contiguous(), "a_scale must be contiguous")
+    if rows:
+        _matrix(b_scale, n, N, "b_scale", torch.float32)
+        _require(b_scale.is_contiguous(), "b_scale must be contiguous")
+    else:
+        _require(b_scale.is_cuda and b_scale.shape == (_chunks(N), n) and b_scale.dtype == torch.float32,
+                 f"b_scale must be float32 [{_chunks(N)}][{n}] on a GPU")
+    if out is None:
+        _require(not accumulate, "accumulate needs out")
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    ldc = _matrix(out, M, N, "out")
+    bs = (0, 0) if rows else b_scale.stride()
+    g = GemmC(M, N, K, SCALE_ROW if rows else SCALE_BLOCK, _type(out), 1 if accumulate else 0, lda, ldb, ldc, bs[0], bs[1])
+    _check(lib().moe_fp8_gemm(ctypes.byref(g), _p(a), _p(a_scale), _p(b), _p(b_scale), _p(out), _stream()))
+    return out
+
+
+def fp8_linear(x: torch.Tensor, w: FP8Matrix, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = x W^T: x [M][K] bf16 or fp32, quantised by rows; y [M][N] (bf16 unless ``out`` says otherwise)."""
+    M = x.shape[0]
+    ldx = _matrix(x, M, w.K, "x")
+    if out is None:
+        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
+    ldy = _matrix(out, M, w.N, "out")
+    c = w.c()
+    n = lib().moe_fp8_linear_workspace_bytes(M, w.N, w.K, 0)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_fp8_linear(M, _p(x), _type(x), ldx, ctypes.byref(c), _p(out), _type(out), ldy, _p(ws), n, _stream()))
+    return out
+
+
+def fp8_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: FP8Matrix, dx: Optional[torch.Tensor] = None,
+                        dw: Optional[torch.Tensor] = None, accumulate: bool = False):
+    """Gradients of fp8_linear: (dx [M][K], dw [N][K]), bf16 unless given; accumulate adds to the given dw."""
+    M = x.shape[0]
+    ldx, lddy = _matrix(x, M, w.K, "x"), _matrix(dy, M, w.N, "dy")
+    _require(dw is not None or not accumulate, "accumulate needs dw")
+    if dx is None:
+        dx = torch.empty((M, w.K), dtype=torch.bfloat16, device=x.device)
+    if dw is None:
+        dw = torch.empty((w.N, w.K), dtype=torch.bfloat16, device=x.device)
+    lddx, lddw = _matrix(dx, M, w.K, "dx"), _matrix(dw, w.N, w.K, "dw")
+    c = w.c()
+    n = lib().moe_fp8_linear_workspace_bytes(M, w.N, w.K, 1)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_fp8_linear_backward(M, _p(x), _type(x), ldx, _p(dy), _type(dy), lddy, ctypes.byref(c), _p(dx),
+                                         _type(dx), lddx, _p(dw), _type(dw), lddw, 1 if accumulate else 0, _p(ws), n,
+                                         _stream()))
+    return dx, dw
+
+
+def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Scales contiguous fp32 / bf16 gradients so that their joint norm is at most max_norm: in place, or into the
+    tensors of ``out`` (same shapes and types).  Returns the norm before (fp32, on the GPU, no synchronisation)."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    _require(len(outs) == len(grads), "out must match grads")
+    _require(len(grads) > 0, "no gradients")
+    dev = grads[0].device
+    table = (TensorC * len(grads))()
+    for e, g, o in zip(table, grads, outs):
+        _require(g.is_cuda and g.device == dev and g.is_contiguous(), "gradients must be contiguous on one GPU")
+        if o is not g:
+            _require(o.device == dev and o.is_contiguous() and o.shape == g.shape and o.dtype == g.dtype,
+                     "out must match grads")
+        e.g, e.out, e.n, e.type = g.data_ptr(), o.data_ptr(), g.numel(), _type(g)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    n = lib().moe_clip_workspace_bytes(len(grads))
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib().moe_clip_grads(len(grads), table, max_norm, _p(norm), _p(ws), n, _stream()))
+    return norm
 
 
 # ---- conveniences for callers holding host (numpy) weights ----------------------------------

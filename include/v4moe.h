@@ -302,6 +302,149 @@ int moe_layer_backward(const v4moe_dims* d, const uint16_t* x, const float* w_ro
                        const uint16_t* dout, float* dx, float* dw, float* dWg, float* dWu,
                        float* dWd, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Operators next to the layer: gating from given logits, dense FP8
+ * products, gradient clipping.  They follow the conventions above, except
+ * that pointers need only the alignment stated with each call (V4MOE_EALIGN
+ * otherwise) and that matrices may have a leading dimension (in elements)
+ * larger than their rows. ---- */
+
+/* Element types. */
+#define V4MOE_TYPE_F32  0
+#define V4MOE_TYPE_BF16 1
+
+/* Scores of moe_gate. */
+#define V4MOE_SCORE_SIGMOID      0   /* 1 / (1 + exp(-z))                  */
+#define V4MOE_SCORE_SOFTMAX      1   /* exp(z - max) / sum over the experts */
+#define V4MOE_SCORE_SQRTSOFTPLUS 2   /* sqrt(softplus(z))                  */
+
+/* Gate: 0 <= T <= 2^24; 1 <= E <= 1024; 1 <= topk <= 16; 1 <= groups <= 64
+ * dividing E; 1 <= topk_groups <= groups; topk <= topk_groups * E / groups. */
+typedef struct {
+    int32_t T;            /* tokens                                            */
+    int32_t E;            /* experts                                           */
+    int32_t topk;         /* experts per token                                 */
+    int32_t score;        /* V4MOE_SCORE_*                                     */
+    int32_t groups;       /* groups of E/groups consecutive experts (1: none)  */
+    int32_t topk_groups;  /* groups a token may pick from                      */
+    int32_t renorm;       /* non-zero: weights divided by their sum            */
+    float   scale;        /* factor of the weights                             */
+} v4moe_gate;
+
+/* Routing from given logits; its outputs are what moe_permute and moe_combine
+ * take.
+ *   logits fp32 or bf16 (type) [T][ld], E used; NaN and values <= -1e30 (so
+ *          -inf and the types' lowest values) mask an expert, values above
+ *          1e30 count as 1e30
+ *   bias   fp32 [E] or NULL, added to the scores for the selection only
+ *          (-inf switches an expert off)
+ *   topk_ids int32 [T][topk], topk_w fp32 [T][topk] (out)
+ * key = score + bias, each one fp32 operation; a group's value is the sum of
+ * its two largest keys (masked experts add nothing); of the topk_groups largest
+ * groups the topk largest keys are picked in order; ties go to the lower group
+ * and expert.  Weights are scale * score, divided by the sum of the picked
+ * scores with renorm (0 where that is 0).  A token with fewer than topk
+ * unmasked experts fills its slots with the lowest other ids, weight 0, so
+ * that ids are distinct and in range in every row.  Pointers: aligned to their
+ * element. */
+int moe_gate(const v4moe_gate* g, const void* logits, int32_t type, int64_t ld, const float* bias,
+             int32_t* topk_ids, float* topk_w, void* stream);
+
+/* Gradient of L with respect to the logits of moe_gate, given dw = dL/dtopk_w
+ * fp32 [T][topk] (moe_layer_backward's dw) and moe_gate's outputs; the selection
+ * is held fixed, and slots of weight 0 have no gradient.
+ *   dlogits [T][ldd] of the logits' type (out), its E columns written in full. */
+int moe_gate_backward(const v4moe_gate* g, const void* logits, int32_t type, int64_t ld,
+                      const int32_t* topk_ids, const float* topk_w, const float* dw, void* dlogits,
+                      int64_t ldd, void* stream);
+
+/* E4M3 codes of x [M][K] (fp32 or bf16) with an fp32 scale for each group of
+ * 128: s = fp32(amax / 448) (1 where that is 0), code = E4M3(fp32(x / s)),
+ * nearest even, saturating.  A group holding an infinity or NaN gets scale NaN and
+ * codes 0: every product it enters is NaN.  Either order, or both in one pass:
+ *   q  [M][K16], s  [ceil(K/128)][M]: groups of 128 along a row (K16 = K rounded up
+ *      to 16, the columns past K zero)
+ *   qt [K][M16], st [ceil(M/128)][K]: the transpose, groups of 128 along a column
+ * A pair may be NULL.  0 <= M, K <= 2^22.  q, qt: 16-byte aligned. */
+int moe_fp8_quantize(int32_t M, int32_t K, const void* x, int32_t type, int64_t ldx,
+                     uint8_t* q, float* s, uint8_t* qt, float* st, void* stream);
+
+/* E4M3 weights: one scale for each 128x128 block, the same codes in both orders.
+ *   w [N][K] fp32 or bf16; q [N][K16], qt [K][N16], blk fp32 [ceil(N/128)][ceil(K/128)] */
+int moe_fp8_quantize_weights(int32_t N, int32_t K, const void* w, int32_t type, int64_t ldw,
+                             uint8_t* q, uint8_t* qt, float* blk, void* stream);
+
+/* Scales of the second operand of moe_fp8_gemm. */
+#define V4MOE_SCALE_BLOCK 0   /* one per 128 rows and 128 of K: bs[(n/128)*bs_n + (k/128)*bs_k] */
+#define V4MOE_SCALE_ROW   1   /* one per row and 128 of K: bs [ceil(K/128)][N]                  */
+
+/* 0 <= M, N, K, lda, ldb <= 2^22; K, lda, ldb multiples of 16. */
+typedef struct {
+    int32_t M, N, K;
+    int32_t b_scale;      /* V4MOE_SCALE_*                          */
+    int32_t c_type;       /* V4MOE_TYPE_*                           */
+    int32_t accumulate;   /* non-zero: added to what c holds        */
+    int64_t lda, ldb, ldc;
+    int64_t bs_n, bs_k;   /* V4MOE_SCALE_BLOCK only                 */
+} v4moe_gemm;
+
+/* c[m][n] = sum over chunks i of 128 of as[i][m] * bs(n, i) * sum_{k in i} a[m][k] b[n][k].
+ *   a uint8 [M][lda], as fp32 [ceil(K/128)][M], b uint8 [N][ldb], c [M][ldc]
+ * Chunk sums come from the matrix cores, which align a chunk's products to the
+ * largest and drop what lies far below it: a chunk is off by up to 4e-4 of its
+ * largest product (measured; 1.3e-5 of the result in the 2-norm for codes of
+ * normal numbers).  Chunks are added in fp32, in order, in every variant, so a row
+ * does not depend on the other rows.  K = 0 writes zeros.  a, b: 16-byte
+ * aligned. */
+int moe_fp8_gemm(const v4moe_gemm* g, const uint8_t* a, const float* as, const uint8_t* b,
+                 const float* bs, void* c, void* stream);
+
+/* A dense weight [N][K] as moe_fp8_quantize_weights writes it.  q is read by the
+ * forward, qt by the data gradient. */
+typedef struct {
+    int32_t N, K;
+    const uint8_t* q;
+    const uint8_t* qt;
+    const float* blk;
+} v4moe_fp8mat;
+
+/* Workspace bytes of moe_fp8_linear (backward = 0) and moe_fp8_linear_backward
+ * (host-only, pure; 0 for invalid sizes).  16-byte aligned, no initialisation. */
+size_t moe_fp8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t backward);
+
+/* y = x W^T: x [M][K] quantised by rows, then the product. */
+int moe_fp8_linear(int32_t M, const void* x, int32_t x_type, int64_t ldx, const v4moe_fp8mat* w,
+                   void* y, int32_t y_type, int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_fp8_linear, quantisation straight-through (as in
+ * moe_layer_backward), with dy quantised by rows for dx and by columns for dW:
+ *   dx [M][K] = dy W, dW [N][K] (+)= dy^T x.  dx or dw may be NULL.  With M = 0, dw
+ * is set to zero (left alone with accumulate). */
+int moe_fp8_linear_backward(int32_t M, const void* x, int32_t x_type, int64_t ldx, const void* dy,
+                            int32_t dy_type, int64_t lddy, const v4moe_fp8mat* w, void* dx,
+                            int32_t dx_type, int64_t lddx, void* dw, int32_t dw_type, int64_t lddw,
+                            int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* A gradient of n elements (0 <= n <= 2^36), contiguous, aligned to its
+ * element; out NULL or equal to g: in place. */
+typedef struct {
+    const void* g;
+    void* out;
+    int64_t n;
+    int32_t type;         /* V4MOE_TYPE_* */
+} v4moe_tensor;
+
+/* Workspace bytes of moe_clip_grads for a list of `count` (<= 2^20) tensors. */
+size_t moe_clip_workspace_bytes(int32_t count);
+
+/* norm = sqrt(sum of the squares of all elements of all tensors) (squares and
+ * sums in fp64, a fixed order), coef = norm > max_norm ? max_norm / norm : 1, and
+ * out = g * coef in each tensor's type.  A norm that is not finite leaves the
+ * gradients unscaled.  Nothing is read back to the host.
+ *   tensors: HOST array; norm: device fp32 [1] (out); max_norm >= 0 (infinity: the
+ * norm only, and copies where out is not g). */
+int moe_clip_grads(int32_t count, const v4moe_tensor* tensors, float max_norm, float* norm,
+                   void* workspace, size_t ws_bytes, void* stream);
+
 /* Profiling hook (no effect on results).  start/stop are hipEvent_t handles
  * created by the caller (or NULL to clear).  The next moe_expert_ffn or
  * moe_layer_forward call made by this host thread records `start` on its
