@@ -184,7 +184,7 @@ struct GemmArgs {
     const uint8_t* b; int64_t ldb; const float* bs;     // B [N][ldb]
     int64_t bs_n, bs_k;                                  // block scales: bs[(n/128)*bs_n + c*bs_k]; ROWS: bs [c][N]
     void* c; int64_t ldc;
-    int c_bf16, accumulate, vec;                         // vec: C rows allow 4-column stores
+    int c_bf16, accumulate, vec;                         // vec: C rows allow 16-byte stores
 };
 
 // Both operands E4M3, no hardware scale (E8M0 127 = 2^0).  Weights (rows of B)
@@ -194,6 +194,57 @@ __device__ __forceinline__ v4f mfma_e4m3(v8i w, v8i x)
 {
     const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, z, 0, 0, 0, 127, 0, 127);
+}
+
+// A wave's MI x NI tiles to C, 16 rows at a time through LDS (two buffers of
+// 16 rows): a lane's four columns become 16-byte stores along the rows, whole
+// lines where a row's part is one (straight from the registers the stores cost
+// 22 us of 139 at 8192 x 4096).  16-byte segments XOR-swizzled by the row.
+template <int MI, int NI, typename T>
+__device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* stage, T* __restrict__ c, const GemmArgs& g,
+                                           int m0, int n0)
+{
+    constexpr int ES = sizeof(T), RB = NI * 16 * ES, LR = RB / 16, PER = 16 / ES;    // bytes, lanes per row; elements per lane
+    constexpr int RP = 64 / LR;                                                    // rows per pass
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < MI; i++) {
+        uint8_t* buf = stage + (i & 1) * (16 * NI * 16 * 4);
+#pragma unroll
+        for (int j = 0; j < NI; j++) {
+            const int at = (16 * j + 4 * kq) * ES;
+            uint8_t* d = buf + r16 * RB + (((at >> 4) ^ (r16 & (LR - 1))) << 4) + (at & 15);
+            if constexpr (ES == 2) *reinterpret_cast<uint2*>(d) = make_uint2(bf16x2(acc[i][j][0], acc[i][j][1]),
+                                                                             bf16x2(acc[i][j][2], acc[i][j][3]));
+            else *reinterpret_cast<float4*>(d) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 16; q += RP) {
+            const int r = q + lane / LR, sg = lane % LR;
+            if (r >= 16) continue;                                     // (RP > 16: half the lanes)
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + r * RB + ((sg ^ (r & (LR - 1))) << 4));
+            const int m = m0 + 16 * i + r, n = n0 + sg * PER;
+            if (m >= g.M || n >= g.N) continue;
+            T* o = c + (int64_t)m * g.ldc + n;
+            if (g.vec && n + PER <= g.N && !g.accumulate) {
+                *reinterpret_cast<uint4*>(o) = v;
+                continue;
+            }
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < PER; e++) {
+                if (n + e >= g.N) break;
+                if constexpr (ES == 2) {
+                    const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                    o[e] = g.accumulate ? (uint16_t)bf16x2(bf16_to_f32(o[e]) + bf16_to_f32(b), 0.0f) : (uint16_t)b;
+                } else {
+                    o[e] = g.accumulate ? o[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 template <int WM, int WN, int MI, int NI, int NS, bool ROWS>
@@ -206,9 +257,24 @@ struct GemmTile {
     static constexpr int A_OFF = 0, B_OFF = BM * 128, S_OFF = B_OFF + BN * 128;
     static constexpr int STAGE = S_OFF + (AS + BS) * 256;
     static constexpr int BYTES = NS * STAGE;
-    static_assert(OPS * (NS - 2) < 64 && NS >= 2, "vmcnt range");
+    static_assert(NW * 2 * 16 * NI * 16 * 4 <= BYTES, "staging of C fits the ring");
+    static_assert(NW > 1, "the barrier, not only the order of one wave, frees a slot");
+    static_assert(OPS * (NS - 1) < 64 && NS >= 2, "vmcnt range");
     static_assert(NI * 16 <= 128 && 128 % (NI * 16) == 0, "a wave's rows of B lie in one 128-row block");
 };
+
+// The tile of a block.  Blocks go to the eight XCDs in turn: XCD x takes the
+// x-th eighth of the tiles, in columns of eight tiles of m, so that the blocks
+// that run together on one XCD share operand rows in its L2.
+__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    const int n = tiles_m * tiles_n, x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const int each = n >> 3, rest = n & 7;
+    const int t = x * each + min(x, rest) + i;
+    const int col = t / (8 * tiles_n), rows = min(8, tiles_m - col * 8), in = t - col * 8 * tiles_n;
+    tm = col * 8 + in % rows;
+    tn = in / rows;
+}
 
 // A tile of C per block: WM x WN waves, each with MI x NI tiles of 16x16.
 // Operand rows are staged in LDS, a chunk of 128 per stage, by direct-to-LDS
@@ -220,7 +286,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
     using L = GemmTile<WM, WN, MI, NI, NS, ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int tm = (int)blockIdx.x % tiles_m, tn = (int)blockIdx.x / tiles_m;
+    int tm, tn;
+    tile_of(tiles_m, tiles_n, tm, tn);
     const int m0 = tm * L::BM, n0 = tn * L::BN;
     const int nch = (g.K + 127) / 128;
     const uint8_t* abase = g.a + (int64_t)m0 * g.lda;
@@ -229,7 +296,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
 
     // byte offsets of this lane's 16-byte segments from the tile's first row
     uint32_t aoff[L::AJ], boff[L::BJ];
-    int seg[L::AJ > L::BJ ? L::AJ : L::BJ];
 #pragma unroll
     for (int j = 0; j < L::AJ; j++) {
         const int p = min(wave + j * L::NW, L::BM / 8 - 1), r = p * 8 + (lane >> 3);
@@ -240,117 +306,362 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
         const int p = min(wave + j * L::NW, L::BN / 8 - 1), r = p * 8 + (lane >> 3);
         boff[j] = (uint32_t)(min(r, g.N - 1 - n0) * (int)g.ldb + (((lane & 7) ^ ((r >> 1) & 7)) * 16));
     }
-    (void)seg;
-    auto issue = [&](int c) {
-        const uint32_t slot = lds0 + (uint32_t)(c % NS) * L::STAGE;
+    // this wave's copies of chunk c into the slot of chunk `at`; tail: the last, shorter chunk, zeros past its end
+    auto issue = [&](int at, int c, auto tail) {
+        const uint32_t slot = lds0 + (uint32_t)(at % NS) * L::STAGE;
         const uint8_t *ac = abase + (int64_t)c * 128, *bc = bbase + (int64_t)c * 128;
-        const int left = g.K - c * 128;              // bytes of a row inside the contraction
+        auto copy = [&](const uint8_t* base, uint32_t off, int p, uint32_t to) {
+            const uint32_t dst = __builtin_amdgcn_readfirstlane(to);
+            if constexpr (decltype(tail)::value) {
+                const int r = p * 8 + (lane >> 3), sg = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+                dma16(sg < (g.K & 127) ? (const void*)(base + off) : (const void*)&g_zeros[lane], dst);
+            } else {
+                dma16s(base, off, dst);
+            }
+        };
 #pragma unroll
         for (int j = 0; j < L::AJ; j++) {
-            const int p = min(wave + j * L::NW, L::BM / 8 - 1), r = p * 8 + (lane >> 3);
-            const int sg = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-            if (left >= 128) dma16s(ac, aoff[j], slot + L::A_OFF + p * 1024);
-            else dma16(sg < left ? (const void*)(ac + aoff[j]) : (const void*)&g_zeros[lane], slot + L::A_OFF + p * 1024);
+            const int p = min(wave + j * L::NW, L::BM / 8 - 1);
+            copy(ac, aoff[j], p, slot + L::A_OFF + p * 1024);
         }
 #pragma unroll
         for (int j = 0; j < L::BJ; j++) {
-            const int p = min(wave + j * L::NW, L::BN / 8 - 1), r = p * 8 + (lane >> 3);
-            const int sg = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-            if (left >= 128) dma16s(bc, boff[j], slot + L::B_OFF + p * 1024);
-            else dma16(sg < left ? (const void*)(bc + boff[j]) : (const void*)&g_zeros[lane], slot + L::B_OFF + p * 1024);
+            const int p = min(wave + j * L::NW, L::BN / 8 - 1);
+            copy(bc, boff[j], p, slot + L::B_OFF + p * 1024);
         }
 #pragma unroll
         for (int j = 0; j < L::SJ; j++) {
             const int p = min(wave + j * L::NW, L::AS + L::BS - 1);
-            if (p < L::AS)
-                dma4s(g.as + (int64_t)c * g.M, (uint32_t)min(m0 + p * 64 + lane, g.M - 1) * 4u, slot + L::S_OFF + p * 256);
-            else
-                dma4s(g.bs + (int64_t)c * g.N, (uint32_t)min(n0 + (p - L::AS) * 64 + lane, g.N - 1) * 4u,
-                      slot + L::S_OFF + p * 256);
+            const bool is_a = p < L::AS;
+            const float* base = is_a ? g.as + (int64_t)c * g.M : g.bs + (int64_t)c * g.N;
+            const int row = is_a ? m0 + p * 64 : n0 + (p - L::AS) * 64;
+            dma4s(base, (uint32_t)min(row + lane, (is_a ? g.M : g.N) - 1) * 4u,
+                  __builtin_amdgcn_readfirstlane(slot + L::S_OFF + p * 256));
         }
     };
 
     const int wm = wave / WN, wn = wave % WN;
     const int arow = wm * MI * 16 + (lane & 15), brow = wn * NI * 16 + (lane & 15), kq = lane >> 4;
-    const int nblk = min((n0 + wn * NI * 16), g.N - 1) >> 7;
+    // the wave's block scales, a scalar load a chunk ahead: a vector load would
+    // wait for the copies issued before it
+    typedef const __attribute__((address_space(4))) float* cfloat;
+    const cfloat bsp = (cfloat)(uintptr_t)(g.bs + (ROWS ? 0 : (min(n0 + wn * NI * 16, g.N - 1) >> 7) * g.bs_n));
+    float bs_next = ROWS || nch == 0 ? 1.0f : bsp[0];
     v4f acc[MI][NI];
 #pragma unroll
     for (int i = 0; i < MI; i++)
 #pragma unroll
         for (int j = 0; j < NI; j++) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-#pragma unroll
-    for (int c = 0; c < NS - 1; c++)
-        if (c < nch) issue(c);
-    for (int c = 0; c < nch; c++) {
-        // stage c has landed once at most the copies of the later stages are out
-        if (c + NS - 2 < nch) wait_vm<L::OPS * (NS - 2)>();
-        else wait_vm<0>();
-        __syncthreads();
-        if (c + NS - 1 < nch) issue(c + NS - 1);     // into the slot every wave left before the barrier
+    // this lane's operand segments: rows 16 apart share the swizzle
+    const int sw = (lane >> 1) & 7;
+    const int alo = L::A_OFF + arow * 128 + ((kq ^ sw) * 16), ahi = L::A_OFF + arow * 128 + (((4 + kq) ^ sw) * 16);
+    const int blo = L::B_OFF + brow * 128 + ((kq ^ sw) * 16), bhi = L::B_OFF + brow * 128 + (((4 + kq) ^ sw) * 16);
+    auto frag = [&](const uint8_t* st, int lo, int hi, int tile) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + lo + tile * 2048);
+        const uint4 y = *reinterpret_cast<const uint4*>(st + hi + tile * 2048);
+        return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+    };
+    v8i af[2], bf[NI];
+    float sa[MI], bs = 1.0f;
+    float4 br[ROWS ? NI : 1];
+    v4f p[NI];
+    // operands that every step of chunk c needs, and its first row tile
+    auto open = [&](int c) {
         const uint8_t* st = smem + (c % NS) * L::STAGE;
-        auto frag = [&](const uint8_t* base, int row) {
-            const int sw = (row >> 1) & 7;
-            const uint4 lo = *reinterpret_cast<const uint4*>(base + row * 128 + ((kq ^ sw) * 16));
-            const uint4 hi = *reinterpret_cast<const uint4*>(base + row * 128 + (((4 + kq) ^ sw) * 16));
-            return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-        };
-        v8i bf[NI];
+        af[0] = frag(st, alo, ahi, 0);
 #pragma unroll
-        for (int j = 0; j < NI; j++) bf[j] = frag(st + L::B_OFF, brow + 16 * j);
-        float bs = 1.0f;
-        float4 br[ROWS ? NI : 1];
+        for (int j = 0; j < NI; j++) bf[j] = frag(st, blo, bhi, j);
+#pragma unroll
+        for (int i = 0; i < MI; i++) sa[i] = *reinterpret_cast<const float*>(st + L::S_OFF + (arow + 16 * i) * 4);
         if constexpr (ROWS) {
 #pragma unroll
             for (int j = 0; j < NI; j++)
                 br[j] = *reinterpret_cast<const float4*>(st + L::S_OFF + L::AS * 256 + (wn * NI * 16 + 16 * j + 4 * kq) * 4);
         } else {
-            bs = g.bs[nblk * g.bs_n + c * g.bs_k];
+            bs = bs_next;
+            bs_next = bsp[min(c + 1, nch - 1) * g.bs_k];
         }
+    };
+    auto add = [&](int i, int j, float s, float4 r) {
+        if constexpr (ROWS) {
+            acc[i][j][0] = fmaf(s * r.x, p[j][0], acc[i][j][0]);
+            acc[i][j][1] = fmaf(s * r.y, p[j][1], acc[i][j][1]);
+            acc[i][j][2] = fmaf(s * r.z, p[j][2], acc[i][j][2]);
+            acc[i][j][3] = fmaf(s * r.w, p[j][3], acc[i][j][3]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < MI; i++) {
-            const v8i af = frag(st + L::A_OFF, arow + 16 * i);
-            const float sa = *reinterpret_cast<const float*>(st + L::S_OFF + (arow + 16 * i) * 4) * bs;
+            for (int e = 0; e < 4; e++) acc[i][j][e] = fmaf(s, p[j][e], acc[i][j][e]);
+        }
+    };
+    // Products of chunk c, whose operands open() has begun: row tile i's go out
+    // while the previous tile's are added; mid() runs once every operand is in
+    // registers, next() once the last products are out.
+    auto chunk = [&](int c, auto mid, auto next) {
+        const uint8_t* st = smem + (c % NS) * L::STAGE;
+#pragma unroll
+        for (int i = 0; i < MI - 1; i++) {
+            af[(i + 1) & 1] = frag(st, alo, ahi, i + 1);
 #pragma unroll
             for (int j = 0; j < NI; j++) {
-                const v4f p = mfma_e4m3(bf[j], af);
-                if constexpr (ROWS) {
-                    acc[i][j][0] = fmaf(sa * br[j].x, p[0], acc[i][j][0]);
-                    acc[i][j][1] = fmaf(sa * br[j].y, p[1], acc[i][j][1]);
-                    acc[i][j][2] = fmaf(sa * br[j].z, p[2], acc[i][j][2]);
-                    acc[i][j][3] = fmaf(sa * br[j].w, p[3], acc[i][j][3]);
+                if (i > 0) add(i - 1, j, sa[i - 1] * bs, br[ROWS ? j : 0]);
+                p[j] = mfma_e4m3(bf[j], af[i & 1]);
+            }
+        }
+        mid();
+#pragma unroll
+        for (int j = 0; j < NI; j++) {
+            if (MI > 1) add(MI - 2, j, sa[MI > 1 ? MI - 2 : 0] * bs, br[ROWS ? j : 0]);
+            p[j] = mfma_e4m3(bf[j], af[(MI - 1) & 1]);
+        }
+        // (with row scales the last tile is added first: both chunks' would not fit the registers)
+        const float last = sa[MI - 1] * bs;
+        if (!ROWS) next();
+#pragma unroll
+        for (int j = 0; j < NI; j++) add(MI - 1, j, last, br[ROWS ? j : 0]);
+        if (ROWS) next();
+    };
+    const std::false_type whole;
+    const std::true_type tail;
+    const int full = g.K >> 7;
+    if (full > 0) {
+#pragma unroll
+        for (int c = 0; c < NS; c++) issue(c, min(c, full - 1), whole);
+        wait_vm<L::OPS * (NS - 1)>();
+        __syncthreads();
+        open(0);
+    }
+    // The barrier in a chunk frees its slot and makes the next stage whole: only
+    // copies of later stages are then out.  Copies past the last stage fetch it
+    // again, into slots that are not read any more.
+    for (int c = 0; c < full - 1; c++)
+        chunk(c, [&]() { wait_vm<L::OPS * (NS - 2)>(); __syncthreads(); },
+              [&]() { issue(c, min(c + NS, full - 1), whole); open(c + 1); });
+    for (int c = full > 0 ? full - 1 : 0; c < nch; c++) {
+        if (c == full) {
+            wait_vm<0>();
+            __syncthreads();
+            issue(c, c, tail);
+            wait_vm<0>();
+            __syncthreads();
+            open(c);
+        }
+        chunk(c, []() {}, []() {});
+    }
+    wait_vm<0>();
+    __syncthreads();   // every wave is done with the ring: it becomes staging space
+    uint8_t* stage = smem + wave * (2 * 16 * NI * 16 * 4);
+    const int mw = m0 + wm * MI * 16, nw = n0 + wn * NI * 16;
+    if (g.c_bf16) store_tile<MI, NI>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
+    else store_tile<MI, NI>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
+}
+
+// x / s rounded once to fp32: y = 1/s rounded, then two corrections by the
+// exact residual.  Needs s and the quotient well inside the normal range.
+__device__ __forceinline__ float quotient(float x, float s, float y)
+{
+    float q = x * y;
+    q = fmaf(fmaf(-q, s, x), y, q);
+    return fmaf(fmaf(-q, s, x), y, q);
+}
+
+// Few rows: the chunks of a tile of (16 MT) x (16 NT) are spread over the NW
+// waves of a block, each loading its operands straight into registers, so that
+// a block's whole stretch of weights is in flight at once and nothing waits
+// for a barrier per chunk.  The chunk sums meet in LDS, where one thread per
+// four columns adds them in increasing chunk order: the same operations, and
+// so the same bits, as k_fp8_gemm.  X (MT = 1): A is x itself (bf16), each
+// chunk quantised by the wave that needs it, in every block: 16 rows cost less
+// than a launch of their own.
+// Bound by latency, then by the weights' bytes.
+template <int MT, int NT, int NW, bool ROWS, bool X>
+struct SplitLds {
+    static constexpr int P = 16 * MT * (16 * NT + 4);          // floats of a chunk's products (rows padded)
+    static constexpr int S = 16 * MT + (ROWS ? 16 * NT : 0);   // its scales
+    static constexpr int BYTES = 2 * NW * (P + S) * 4;         // two rounds
+    static_assert(MT * NT * 64 <= NW * 64 && (!X || (MT == 1 && !ROWS)), "a thread per four columns");
+    static_assert(NW % 8 == 0, "chunks are added eight at a time");
+};
+template <int MT, int NT, int NW, bool ROWS, bool X>
+__global__ __launch_bounds__(64 * NW) void k_fp8_split(GemmArgs g, const uint16_t* __restrict__ x, int64_t ldx, int kx)
+{
+    using L = SplitLds<MT, NT, NW, ROWS, X>;
+    extern __shared__ __align__(16) float lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, kq = lane >> 4;
+    const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
+    const int nch = (g.K + 127) / 128;
+
+    const uint8_t* brow[NT];
+    const uint8_t* arow[MT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) brow[j] = g.b + (int64_t)min(n0 + 16 * j + r16, g.N - 1) * g.ldb + 16 * kq;
+    if constexpr (!X) {
+#pragma unroll
+        for (int i = 0; i < MT; i++) arow[i] = g.a + (int64_t)min(m0 + 16 * i + r16, g.M - 1) * g.lda + 16 * kq;
+    }
+    const uint16_t* xrow = X ? x + (int64_t)min(m0 + r16, g.M - 1) * ldx + 16 * kq : nullptr;
+
+    struct Operands {
+        uint4 b[NT][2], a[MT][2], xv[X ? 4 : 1];
+        float sa[MT], sb[ROWS ? NT : 1];
+    };
+    // this lane's segments kq and 4 + kq of chunk c, zeros past the end (by their address: no branch between loads)
+    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+    typedef const __attribute__((address_space(1))) v4u* gptr;
+    const gptr zeros = (gptr)&g_zeros[lane];
+    auto fetch = [&](bool in, const void* p) {
+        const gptr q = in ? (gptr)p : zeros;
+        const v4u v = *q;
+        return make_uint4(v.x, v.y, v.z, v.w);
+    };
+    // a zero the compiler does not know, so that the block scale is a vector load like the rest and
+    // is waited for with them
+    int opaque;
+    asm("v_mov_b32 %0, 0" : "=v"(opaque));
+    auto load = [&](int c, Operands& o) {
+        const int left = g.K - c * 128;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const bool in = 64 * h + 16 * kq < left;
+#pragma unroll
+            for (int j = 0; j < NT; j++) o.b[j][h] = fetch(in, brow[j] + c * 128 + 64 * h);
+            if constexpr (X) {
+                const int xl = kx - c * 128 - 64 * h - 16 * kq;       // elements of x left (kx a multiple of 8)
+#pragma unroll
+                for (int u = 0; u < 2; u++)
+                    o.xv[2 * h + u] = fetch(8 * u < xl, xrow + c * 128 + 64 * h + 8 * u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < MT; i++) o.a[i][h] = fetch(in, arow[i] + c * 128 + 64 * h);
+            }
+        }
+        if constexpr (!X) {
+#pragma unroll
+            for (int i = 0; i < MT; i++) o.sa[i] = g.as[(int64_t)c * g.M + min(m0 + 16 * i + r16, g.M - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < (ROWS ? NT : 1); j++)
+            o.sb[j] = ROWS ? g.bs[(int64_t)c * g.N + min(n0 + 16 * j + r16, g.N - 1)]
+                           : g.bs[(min(n0, g.N - 1) >> 7) * g.bs_n + c * g.bs_k + opaque];
+    };
+    auto v8 = [](const uint4& lo, const uint4& hi) {
+        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int em = tid / (4 * NT), en = 4 * (tid % (4 * NT));    // this thread's row and first column of the tile
+    const bool owner = tid < MT * NT * 64;
+    Operands o;
+    if (wave < nch) load(wave, o);
+    for (int r = 0; r * NW < nch; r++) {
+        const int c = r * NW + wave;
+        float* slot = lds + ((r & 1) * NW + wave) * (L::P + L::S);
+        if (c < nch) {
+            v8i a[MT], b[NT];
+            float s[MT];
+            if constexpr (X) {
+                float f[32];
+                uint32_t m = 0;
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const uint32_t q[4] = {o.xv[u].x, o.xv[u].y, o.xv[u].z, o.xv[u].w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        f[8 * u + 2 * e] = bf16_to_f32(q[e] & 0xFFFFu);
+                        f[8 * u + 2 * e + 1] = bf16_to_f32(q[e] >> 16);
+                        m = max(m, max(mag_bits(f[8 * u + 2 * e]), mag_bits(f[8 * u + 2 * e + 1])));
+                    }
+                }
+                m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+                m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+                const float sc = group_scale(m);
+                s[0] = sc;
+                // scales far from the ends of the range: the short division gives the same quotients
+                if (sc > 0x1p-80f && sc < 0x1p80f) {
+                    const float y = 1.0f / sc;
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        a[0][u] = (int)(e4m3x2(quotient(f[4 * u], sc, y), quotient(f[4 * u + 1], sc, y)) |
+                                        (e4m3x2(quotient(f[4 * u + 2], sc, y), quotient(f[4 * u + 3], sc, y)) << 16));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; e++) acc[i][j][e] = fmaf(sa, p[e], acc[i][j][e]);
+                    for (int u = 0; u < 8; u++) a[0][u] = (int)codes4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3], sc);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < MT; i++) a[i] = v8(o.a[i][0], o.a[i][1]), s[i] = o.sa[i];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; j++) b[j] = v8(o.b[j][0], o.b[j][1]);
+            if (kq == 0) {
+#pragma unroll
+                for (int i = 0; i < MT; i++) slot[L::P + 16 * i + r16] = ROWS ? s[i] : s[i] * o.sb[0];
+                if constexpr (ROWS) {
+#pragma unroll
+                    for (int j = 0; j < NT; j++) slot[L::P + 16 * MT + 16 * j + r16] = o.sb[j];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    const v4f p = mfma_e4m3(b[j], a[i]);
+                    *reinterpret_cast<float4*>(slot + (16 * i + r16) * (16 * NT + 4) + 16 * j + 4 * kq) =
+                        make_float4(p[0], p[1], p[2], p[3]);
+                }
+            if (c + NW < nch) load(c + NW, o);
+        }
+        __syncthreads();     // (two rounds' slots: a round is read before its slots are written again)
+        if (owner) {
+            const float* p = lds + (r & 1) * NW * (L::P + L::S);
+            auto add = [&](float4 v, float s, float4 b) {
+                if constexpr (ROWS) {
+                    acc[0] = fmaf(s * b.x, v.x, acc[0]);
+                    acc[1] = fmaf(s * b.y, v.y, acc[1]);
+                    acc[2] = fmaf(s * b.z, v.z, acc[2]);
+                    acc[3] = fmaf(s * b.w, v.w, acc[3]);
+                } else {
+                    acc[0] = fmaf(s, v.x, acc[0]);
+                    acc[1] = fmaf(s, v.y, acc[1]);
+                    acc[2] = fmaf(s, v.z, acc[2]);
+                    acc[3] = fmaf(s, v.w, acc[3]);
+                }
+            };
+            auto product = [&](int w) { return *reinterpret_cast<const float4*>(p + w * (L::P + L::S) + em * (16 * NT + 4) + en); };
+            auto scale = [&](int w) { return p[w * (L::P + L::S) + L::P + em]; };
+            auto rows = [&](int w) {
+                return ROWS ? *reinterpret_cast<const float4*>(p + w * (L::P + L::S) + L::P + 16 * MT + en) : float4{};
+            };
+            const int n = nch - r * NW;
+            if (n >= NW) {
+                // eight chunks' values read together: an add then waits for none of its own
+#pragma unroll
+                for (int w0 = 0; w0 < NW; w0 += 8) {
+                    float4 v[8], b[8];
+                    float s[8];
+#pragma unroll
+                    for (int w = 0; w < 8; w++) v[w] = product(w0 + w), s[w] = scale(w0 + w), b[w] = rows(w0 + w);
+#pragma unroll
+                    for (int w = 0; w < 8; w++) add(v[w], s[w], b[w]);
+                }
+            } else {
+                for (int w = 0; w < n; w++) add(product(w), scale(w), rows(w));
             }
         }
     }
+    const int m = m0 + em, n = n0 + en;
+    if (!owner || m >= g.M) return;
 #pragma unroll
-    for (int i = 0; i < MI; i++) {
-        const int m = m0 + arow + 16 * i;
-        if (m >= g.M) continue;
-#pragma unroll
-        for (int j = 0; j < NI; j++) {
-            const int n = n0 + wn * NI * 16 + 16 * j + 4 * kq, nv = min(4, g.N - n);
-            if (nv <= 0) continue;
-            v4f v = acc[i][j];
-            if (g.c_bf16) {
-                uint16_t* o = static_cast<uint16_t*>(g.c) + (int64_t)m * g.ldc + n;
-                if (g.accumulate)
-                    for (int e = 0; e < nv; e++) v[e] += bf16_to_f32(o[e]);
-                const uint32_t lo = bf16x2(v[0], v[1]), hi = bf16x2(v[2], v[3]);
-                if (g.vec && nv == 4) *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
-                else
-                    for (int e = 0; e < nv; e++) o[e] = (uint16_t)((e & 2 ? hi : lo) >> (16 * (e & 1)));
-            } else {
-                float* o = static_cast<float*>(g.c) + (int64_t)m * g.ldc + n;
-                if (g.accumulate)
-                    for (int e = 0; e < nv; e++) v[e] += o[e];
-                if (g.vec && nv == 4) *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-                else
-                    for (int e = 0; e < nv; e++) o[e] = v[e];
-            }
+    for (int e = 0; e < 4; e++) {
+        if (n + e >= g.N) break;
+        if (g.c_bf16) {
+            uint16_t* o = static_cast<uint16_t*>(g.c) + (int64_t)m * g.ldc + n + e;
+            const uint32_t b = bf16x2(acc[e], 0.0f);
+            *o = g.accumulate ? (uint16_t)bf16x2(bf16_to_f32(*o) + bf16_to_f32(b & 0xFFFFu), 0.0f) : (uint16_t)b;
+        } else {
+            float* o = static_cast<float*>(g.c) + (int64_t)m * g.ldc + n + e;
+            *o = g.accumulate ? *o + acc[e] : acc[e];
         }
     }
 }
@@ -398,13 +709,67 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t s)
         if (e != hipSuccess) return e;
     }
     const int tm = (g.M + L::BM - 1) / L::BM, tn = (g.N + L::BN - 1) / L::BN;
+    if ((int64_t)tm * tn > INT32_MAX / 8) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(64 * L::NW), L::BYTES, s, g, tm, tn);
     return hipGetLastError();
 }
 
-hipError_t run_gemm(const GemmArgs& g, bool rows, hipStream_t s)
+template <int MT, int NT, int NW, bool ROWS, bool X>
+hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nullptr, int64_t ldx = 0, int kx = 0)
 {
-    return rows ? launch_gemm<2, 2, 2, 2, 3, true>(g, s) : launch_gemm<2, 2, 2, 2, 3, false>(g, s);
+    using L = SplitLds<MT, NT, NW, ROWS, X>;
+    const auto kernel = k_fp8_split<MT, NT, NW, ROWS, X>;
+    if (L::BYTES > 65536) {
+        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid((unsigned)((g.N + 16 * NT - 1) / (16 * NT)), (unsigned)((g.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), L::BYTES, s, g, x, ldx, kx);
+    return hipGetLastError();
+}
+
+// The product's variants.  A call takes the one of the least modelled time, base
+// + slope * ceil(tiles / 256) us: measured at K = 4096 over M = 1 .. 8192 with
+// N = 4096 and 1024, where the model is within 10%, and nearly proportional to
+// K, so the order holds.  A round is one tile per CU.
+//                 tiles   us     1 round   2 rounds   4 rounds
+//   k_fp8_split   16x16          6.6       10.2       17.8
+//   k_fp8_gemm    16x64          9.3       12.1       20.4
+//                 32x64          10.1      13.3       22.6
+//                 64x64          14.6      18.1       31.9
+//                 128x128        24.2      39.5       77.1
+//                 256x256        68.3      131
+struct Variant {
+    int bm, bn;
+    float base, slope;
+};
+constexpr Variant kVariants[] = {{16, 16, 3.0f, 3.6f}, {16, 64, 6.0f, 3.5f},    {32, 64, 6.4f, 3.9f},
+                                 {64, 64, 8.5f, 5.7f}, {128, 128, 5.0f, 18.0f}, {256, 256, 3.0f, 64.0f}};
+int choose_variant(int64_t M, int64_t N)
+{
+    int best = 0;
+    float least = 0.0f;
+    for (int v = 0; v < 6; v++) {
+        const Variant& k = kVariants[v];
+        const int64_t tiles = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn);
+        const float us = k.base + k.slope * (float)((tiles + 255) / 256);
+        if (v == 0 || us < least) best = v, least = us;
+    }
+    return best;
+}
+
+template <bool ROWS>
+hipError_t run_gemm(const GemmArgs& g, hipStream_t s)
+{
+    switch (choose_variant(g.M, g.N)) {
+    case 0: return launch_split<1, 1, 8, ROWS, false>(g, s);
+    case 1: return launch_gemm<1, 4, 1, 1, 4, ROWS>(g, s);
+    case 2: return launch_gemm<2, 2, 1, 2, 4, ROWS>(g, s);
+    case 3: return launch_gemm<2, 2, 2, 2, 3, ROWS>(g, s);
+    case 4: return launch_gemm<2, 2, 4, 4, 2, ROWS>(g, s);
+    default: return launch_gemm<2, 4, 8, 4, 2, ROWS>(g, s);
+    }
 }
 
 bool type_ok(int t) { return t == V4MOE_TYPE_F32 || t == V4MOE_TYPE_BF16; }
@@ -503,8 +868,9 @@ __attribute__((visibility("default"))) int moe_fp8_gemm(const v4moe_gemm* p, con
     if (!device_ready()) return V4MOE_EDEVICE;
     const bool bf16 = p->c_type == V4MOE_TYPE_BF16, rows = p->b_scale == V4MOE_SCALE_ROW;
     const GemmArgs g{p->M, p->N, p->K, a, p->lda, as, b, p->ldb, bs, p->bs_n, p->bs_k, c, p->ldc, bf16, p->accumulate != 0,
-                     p->ldc % 4 == 0 && aligned_to(c, bf16 ? 8 : 16)};
-    return run_gemm(g, rows, static_cast<hipStream_t>(stream)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+                     p->ldc % (bf16 ? 8 : 4) == 0 && aligned_to(c, 16)};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return (rows ? run_gemm<true>(g, s) : run_gemm<false>(g, s)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }
 
 __attribute__((visibility("default"))) size_t moe_fp8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K,
@@ -528,10 +894,18 @@ __attribute__((visibility("default"))) int moe_fp8_linear(int32_t M, const void*
     if (!aligned_to(workspace, 16)) return V4MOE_EALIGN;
     const LinearLayout L = linear_layout(M, N, K, false);
     if (ws_bytes < L.total) return V4MOE_EWORKSPACE;
+    const int K16 = (int)up16(K), y_bf16 = y_type == V4MOE_TYPE_BF16;
+    if (x_type == V4MOE_TYPE_BF16 && K % 8 == 0 && ldx % 8 == 0 && aligned_to(x, 16) && choose_variant(M, N) == 0) {
+        // few rows: the product quantises x itself
+        if (!device_ready()) return V4MOE_EDEVICE;
+        const GemmArgs g{M, N, K16, nullptr, 0, nullptr, w->q, K16, w->blk, chunks(K), 1, y, ldy, y_bf16, 0, 0};
+        return launch_split<1, 1, 8, false, true>(g, static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(x), ldx,
+                                                  K) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+    }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* xs = reinterpret_cast<float*>(ws + L.xs);
     if (const int rc = moe_fp8_quantize(M, K, x, x_type, ldx, ws + L.xq, xs, nullptr, nullptr, stream)) return rc;
-    const v4moe_gemm g{M, N, (int32_t)up16(K), V4MOE_SCALE_BLOCK, y_type, 0, up16(K), up16(K), ldy, chunks(K), 1};
+    const v4moe_gemm g{M, N, K16, V4MOE_SCALE_BLOCK, y_type, 0, K16, K16, ldy, chunks(K), 1};
     return moe_fp8_gemm(&g, ws + L.xq, xs, w->q, w->blk, y, stream);
 }
 

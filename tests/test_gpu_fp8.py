@@ -130,7 +130,8 @@ def operand(seed, R, C, pad=0, wide=False):
 
 GEMMS = [(1, 1, 16), (1, 64, 128), (2, 17, 144), (5, 300, 1008), (16, 128, 2048), (17, 129, 256), (33, 48, 4096),
          (64, 256, 512), (65, 1000, 384), (100, 31, 112), (128, 512, 640), (129, 257, 272), (200, 384, 128),
-         (300, 640, 1040), (513, 514, 528), (700, 1030, 256), (1100, 900, 384), (2050, 1300, 160)]
+         (300, 640, 1040), (513, 514, 528), (700, 1030, 256), (1100, 900, 384), (2050, 1300, 160), (1, 2000, 2064),
+         (20, 1500, 272), (70, 2200, 1200), (300, 3000, 256), (1000, 3100, 144), (4100, 4000, 400)]
 
 
 @pytest.mark.parametrize("rows", [False, True])
@@ -160,7 +161,7 @@ def test_gemm(shape, wide, rows):
             assert torch.equal(acc, out + out)
 
 
-@pytest.mark.parametrize("shape", [(2050, 1300, 1056), (1100, 257, 4096)], ids=str)
+@pytest.mark.parametrize("shape", [(2050, 1300, 1056), (1100, 257, 4096), (4352, 4096, 656)], ids=str)
 @pytest.mark.parametrize("rows", [False, True])
 def test_row_does_not_depend_on_the_batch(shape, rows):
     M, N, K = shape
@@ -168,7 +169,9 @@ def test_row_does_not_depend_on_the_batch(shape, rows):
     b, sb = operand(2, N, K, 0, True)
     sb = sb.t().contiguous() if rows else sb[::128].contiguous()
     full = v4moe.fp8_gemm(a, sa.t().contiguous(), b, sb, rows, out=torch.empty(M, N, device=DEV))
-    for lo, n in ((0, 1), (7, 5), (100, 16), (90, 33), (11, 64), (500, 100), (0, 200), (64, 400), (30, 700)):
+    for lo, n in ((0, 1), (7, 5), (100, 16), (90, 33), (11, 64), (500, 100), (0, 200), (64, 400), (30, 700), (1000, 3000)):
+        if lo + n > M:
+            continue
         part = v4moe.fp8_gemm(a[lo:lo + n], sa[lo:lo + n].t().contiguous(), b, sb, rows, out=torch.empty(n, N, device=DEV))
         assert torch.equal(part, full[lo:lo + n]), (lo, n)
 
@@ -213,6 +216,22 @@ def test_linear(shape, type):
     ref, tol = gemm_ref(qy.to(DEV), sy.to(DEV), qx.to(DEV), sx.to(DEV), True)
     assert bool(((dw.double() - ref).abs() <= bar(ref, tol, torch.bfloat16)).all())
     assert bool(((dw32.double() - 1 - ref).abs() <= bar(ref, tol, torch.float32) + 2.0 ** -23 * (1 + ref.abs())).all())
+
+
+@pytest.mark.parametrize("shape", [(1, 2048, 2048), (16, 256, 4096), (9, 64, 8), (40, 512, 1000), (5, 33, 1048)], ids=str)
+def test_linear_of_few_rows(shape):
+    """bf16 rows at 16-byte addresses are quantised inside the product; others beforehand: the same bits."""
+    M, N, K = shape
+    x = source(7, M, K, torch.bfloat16)
+    x[0, 0] = 1e-30
+    w = v4moe.fp8_weights(source(8, N, K, torch.float32))
+    moved = torch.empty(M * K + 1, dtype=torch.bfloat16, device=DEV)[1:].view(M, K).copy_(x)
+    assert torch.equal(v4moe.fp8_linear(x, w), v4moe.fp8_linear(moved, w))
+    tiny = (x.float() * 1e-33).to(torch.bfloat16)      # scales down to subnormal numbers
+    assert torch.equal(v4moe.fp8_linear(tiny, w), v4moe.fp8_linear(moved.copy_(tiny), w))
+    x[0, K - 1] = math.inf
+    y = v4moe.fp8_linear(x, w)
+    assert bool(y[0].isnan().all()) and not y[1:].isnan().any()
 
 
 def test_gradient_against_differences():
