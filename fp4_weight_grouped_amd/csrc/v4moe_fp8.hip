@@ -34,23 +34,28 @@ __device__ __forceinline__ float load_f32<float>(const float* p) { return *p; }
 template <>
 __device__ __forceinline__ float load_f32<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
 
-// Eight consecutive elements, `n` of them inside the array (the rest read as
-// zero); vec: the address is 16-byte aligned.
+// Sixteen bytes at any element's address, in one access: unaligned ones are the
+// hardware's to split.
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef v4u v4u_any __attribute__((aligned(2)));
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&f)[8])
+__device__ __forceinline__ v4u load16(const T* p) { return *reinterpret_cast<const v4u_any*>(p); }
+
+// Eight consecutive elements, `n` of them inside the array (the rest read as zero).
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, float (&f)[8])
 {
-    if (vec && n >= 8) {
+    if (n >= 8) {
+        const v4u v = load16(p);
         if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            const v4u w = load16(p + 4);
+#pragma unroll
+            for (int u = 0; u < 4; u++) f[u] = __uint_as_float(v[u]), f[4 + u] = __uint_as_float(w[u]);
         } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(p);
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int u = 0; u < 4; u++) {
-                f[2 * u] = bf16_to_f32(q[u] & 0xFFFFu);
-                f[2 * u + 1] = bf16_to_f32(q[u] >> 16);
+                f[2 * u] = bf16_to_f32(v[u] & 0xFFFFu);
+                f[2 * u + 1] = bf16_to_f32(v[u] >> 16);
             }
         }
     } else {
@@ -70,108 +75,190 @@ __device__ __forceinline__ float group_scale(uint32_t mag)
     return s > 0.0f ? s : 1.0f;
 }
 
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s)
+// E4M3 codes of x / s, the quotient rounded to fp32 first.  A scale well inside
+// the normal range takes y = 1/s rounded, then two corrections of x y by its
+// exact residual, which give the rounded quotient (half the instructions of a
+// division); the others divide; a NaN scale gives codes 0.
+struct Divisor {
+    float s, y;
+    bool quick;
+    __device__ __forceinline__ explicit Divisor(float scale) : s(scale), y(1.0f / scale), quick(scale > 0x1p-80f && scale < 0x1p80f) {}
+    __device__ __forceinline__ float corrected(float x) const
+    {
+        // (residuals as q s - x: where they vanish the quotient keeps its sign, a zero's too)
+        float q = x * y;
+        q = fmaf(-fmaf(q, s, -x), y, q);
+        return fmaf(-fmaf(q, s, -x), y, q);
+    }
+    __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) const
+    {
+        if (quick) return e4m3x2(corrected(a), corrected(b)) | (e4m3x2(corrected(c), corrected(d)) << 16);
+        if (s != s) return 0u;
+        return e4m3x2(a / s, b / s) | (e4m3x2(c / s, d / s) << 16);
+    }
+};
+
+// Groups along rows: x [R][C] -> q [R][ldq] (up to C rounded up to 16, zeros
+// past C), s [ceil(C/128)][R].  Sixteen lanes per group, eight elements each.
+// HBM-bound: x read once, a byte written per element.
+template <typename T>
+__global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, const T* __restrict__ x, int64_t ldx,
+                                                        uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
 {
-    if (s != s) return 0u;
-    return e4m3x2(a / s, b / s) | (e4m3x2(c / s, d / s) << 16);
+    const int nc = (C + 127) / 128;
+    const int64_t group = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int64_t r = group / nc;
+    if (r >= R) return;                                   // whole groups of lanes
+    const int c = (int)(group - r * nc), at = c * 128 + 8 * (threadIdx.x & 15);
+    float f[8];
+    load8(x + r * ldx + min(at, C - 1), C - at, f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < 8; u++) m = max(m, mag_bits(f[u]));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    const Divisor d(group_scale(m));
+    if (at < (C + 15) / 16 * 16)
+        *reinterpret_cast<uint2*>(q + r * ldq + at) = make_uint2(d.codes4(f[0], f[1], f[2], f[3]), d.codes4(f[4], f[5], f[6], f[7]));
+    if ((threadIdx.x & 15) == 0) s[(int64_t)c * R + r] = d.s;
 }
 
-// One 128x128 tile of x [R][C] per block: thread t holds rows 8(t/16) .. +7,
-// columns 8(t%16) .. +7.  Bound by HBM (a read of x, a byte or two written per
-// element); the tile is read once for both orders.
+// Maximum over the 16 lanes of a row, in every lane (quad xor 1, xor 2, half-row
+// mirror, row mirror).
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    auto step = [&](auto ctrl) {
+        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    step(std::integral_constant<int, 0xB1>{});
+    step(std::integral_constant<int, 0x4E>{});
+    step(std::integral_constant<int, 0x141>{});
+    step(std::integral_constant<int, 0x140>{});
+    return v;
+}
+
+// Eight consecutive elements as they are in memory (zeros past the array's end).
+template <typename T>
+struct Raw {
+    v4u w[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int u) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[u >> 2][u & 3]);
+        else return __uint_as_float(u & 1 ? w[0][u >> 1] & 0xFFFF0000u : w[0][u >> 1] << 16);
+    }
+    __device__ __forceinline__ void forget()
+    {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; h++) asm volatile("" : "+v"(w[h]));
+    }
+    __device__ __forceinline__ void load(const T* p, int n)
+    {
+        if (n >= 8) {
+#pragma unroll
+            for (int h = 0; h < (int)sizeof(T) / 2; h++) w[h] = load16(p + 4 * h);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const uint32_t b = u < n ? (sizeof(T) == 4 ? __float_as_uint(load_f32(p + u)) : __float_as_uint(load_f32(p + u)) >> 16) : 0u;
+                if constexpr (sizeof(T) == 4) w[u >> 2][u & 3] = b;
+                else w[0][u >> 1] = u & 1 ? w[0][u >> 1] | (b << 16) : b;
+            }
+        }
+    }
+};
+
+// One 128x128 tile of x [R][C] per block, read once for both orders: thread t
+// holds rows 8(t/16) .. +7, columns 8(t%16) .. +7 as they are in memory.  Bound by
+// its own latency and VALU work next to HBM: 8192x4096 bf16 by columns 28 us
+// (3.6 TB/s), 8192x2048 in both orders 27 us, 16384x4096 fp32 weights 87 us (4.6
+// TB/s).  What it is sensitive to is the blocks per CU (five): with the elements
+// kept as floats (three blocks) 32 / 35 us, with the next tile's loads out a
+// tile ahead (two) 34 / 34 us; without the residual corrections, or with the
+// stores of qt in one stretch of memory, 30 / 29 us at two blocks.
 //   ROWS: q [R][ldq], s [ceil(C/128)][R]: groups of 128 columns of a row
 //   COLS: qt [C][ldqt], st [ceil(R/128)][C]: groups of 128 rows of a column
 //   BLOCK: q, qt, s [ceil(R/128)][ceil(C/128)]: one group per tile
 // Rows of q are written up to C rounded up to 16, zeros past C (qt likewise).
 enum { kQuantRows = 1, kQuantCols = 2, kQuantBlock = 4 };
 template <typename T, int MODE>
-__global__ __launch_bounds__(256) void k_fp8_quant(int R, int C, const T* __restrict__ x, int64_t ldx, int vec,
+__global__ __launch_bounds__(256) void k_fp8_quant(int R, int C, const T* __restrict__ x, int64_t ldx,
                                                    uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s,
                                                    uint8_t* __restrict__ qt, int64_t ldqt, float* __restrict__ st)
 {
-    __shared__ uint32_t mx[4][128];
-    __shared__ __align__(16) uint8_t tq[128][144];
+    __shared__ __align__(16) uint32_t mx[4][128];
+    __shared__ __align__(16) uint8_t tq[128 * 128];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int c0 = blockIdx.x * 128, r0 = blockIdx.y * 128;
     const int rt = 8 * (t >> 4), ct = 8 * (t & 15);
-    const int nc = C - c0 - ct;                        // columns of this thread inside x
-    float f[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int r = r0 + rt + i;
-        load8(x + (int64_t)min(r, R - 1) * ldx + min(c0 + ct, C - 1), r < R ? nc : 0, vec, f[i]);
-    }
     const int cpad = (C + 15) / 16 * 16, rpad = (R + 15) / 16 * 16;
+    const int nx = (C + 127) / 128;
+    const int tile = blockIdx.x, by = tile / nx, bx = tile % nx, r0 = by * 128, c0 = bx * 128;
+    Raw<T> f[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        f[i].load(x + (int64_t)min(r0 + rt + i, R - 1) * ldx + min(c0 + ct, C - 1), r0 + rt + i < R ? C - c0 - ct : 0);
+    auto store_row = [&](int i, const Divisor& d) {
+        if (r0 + rt + i < R && c0 + ct < cpad)
+            *reinterpret_cast<uint2*>(q + (int64_t)(r0 + rt + i) * ldq + c0 + ct) =
+                make_uint2(d.codes4(f[i][0], f[i][1], f[i][2], f[i][3]), d.codes4(f[i][4], f[i][5], f[i][6], f[i][7]));
+    };
     if constexpr (MODE & kQuantRows) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             uint32_t m = 0;
 #pragma unroll
             for (int u = 0; u < 8; u++) m = max(m, mag_bits(f[i][u]));
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-            const float sc = group_scale(m);
-            const int r = r0 + rt + i;
-            if (r < R) {
-                if (c0 + ct < cpad)
-                    *reinterpret_cast<uint2*>(q + (int64_t)r * ldq + c0 + ct) =
-                        make_uint2(codes4(f[i][0], f[i][1], f[i][2], f[i][3], sc),
-                                   codes4(f[i][4], f[i][5], f[i][6], f[i][7], sc));
-                if ((t & 15) == 0) s[(int64_t)blockIdx.x * R + r] = sc;
-            }
+            const Divisor d(group_scale(row_max(m)));
+            store_row(i, d);
+            if ((t & 15) == 0 && r0 + rt + i < R) s[(int64_t)bx * R + r0 + rt + i] = d.s;
         }
     }
-    if constexpr (MODE & (kQuantCols | kQuantBlock)) {
-        uint32_t m[8];
+    uint32_t m[8];
+    // (the columns convert the elements again: kept as floats from the rows, twice the registers would halve the blocks per CU)
 #pragma unroll
-        for (int u = 0; u < 8; u++) {
-            m[u] = 0;
+    for (int i = 0; i < 8; i++) f[i].forget();
 #pragma unroll
-            for (int i = 0; i < 8; i++) m[u] = max(m[u], mag_bits(f[i][u]));
-            m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 16));
-            m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 32));
-            if (lane < 16) mx[wave][ct + u] = m[u];
-        }
-        __syncthreads();
-        float sc[8];
-        if constexpr (MODE & kQuantBlock) {
-            uint32_t b = max(max(mx[0][lane], mx[1][lane]), max(mx[2][lane], mx[3][lane]));
-            b = max(b, max(max(mx[0][64 + lane], mx[1][64 + lane]), max(mx[2][64 + lane], mx[3][64 + lane])));
+    for (int u = 0; u < 8; u++) {
+        m[u] = 0;
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) b = max(b, (uint32_t)__shfl_xor((int)b, o));
+        for (int i = 0; i < 8; i++) m[u] = max(m[u], mag_bits(f[i][u]));
+        m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 16));
+        m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 32));
+    }
+    if (lane < 16) {
+        *reinterpret_cast<uint4*>(&mx[wave][ct]) = make_uint4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<uint4*>(&mx[wave][ct + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+    }
+    __syncthreads();
+    uint32_t all = 0;
+    if constexpr (MODE & kQuantBlock) {
+        all = max(max(mx[0][lane], mx[1][lane]), max(mx[2][lane], mx[3][lane]));
+        all = max(all, max(max(mx[0][64 + lane], mx[1][64 + lane]), max(mx[2][64 + lane], mx[3][64 + lane])));
 #pragma unroll
-            for (int u = 0; u < 8; u++) sc[u] = group_scale(b);
-            if (t == 0) s[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sc[0];
+        for (int o = 1; o < 64; o <<= 1) all = max(all, (uint32_t)__shfl_xor((int)all, o));
+        const Divisor d(group_scale(all));
+        if (t == 0) s[tile] = d.s;
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (r0 + rt + i < R && c0 + ct < cpad)
-                    *reinterpret_cast<uint2*>(q + (int64_t)(r0 + rt + i) * ldq + c0 + ct) =
-                        make_uint2(codes4(f[i][0], f[i][1], f[i][2], f[i][3], sc[0]),
-                                   codes4(f[i][4], f[i][5], f[i][6], f[i][7], sc[0]));
-        } else {
+        for (int i = 0; i < 8; i++) store_row(i, d);
+    }
+    // The codes transposed through LDS: column c's row holds sixteen units of
+    // eight rows, XORed by c/8, so that the sixteen columns a store covers lie
+    // in different banks; then 16-byte stores along the rows of qt.
 #pragma unroll
-            for (int u = 0; u < 8; u++)
-                sc[u] = group_scale(max(max(mx[0][ct + u], mx[1][ct + u]), max(mx[2][ct + u], mx[3][ct + u])));
-            if (lane < 16 && wave == 0) {
+    for (int u = 0; u < 8; u++) {
+        const int c = ct + u;
+        const Divisor d(group_scale(MODE & kQuantBlock ? all : max(max(mx[0][c], mx[1][c]), max(mx[2][c], mx[3][c]))));
+        if ((MODE & kQuantCols) && wave == 0 && lane < 16 && c0 + c < C) st[(int64_t)by * C + c0 + c] = d.s;
+        *reinterpret_cast<uint2*>(tq + c * 128 + ((t >> 4) ^ (t & 15)) * 8) =
+            make_uint2(d.codes4(f[0][u], f[1][u], f[2][u], f[3][u]), d.codes4(f[4][u], f[5][u], f[6][u], f[7][u]));
+    }
+    __syncthreads();
 #pragma unroll
-                for (int u = 0; u < 8; u++)
-                    if (u < nc) st[(int64_t)blockIdx.y * C + c0 + ct + u] = sc[u];
-            }
-        }
-        // the codes transposed through LDS, then 16-byte stores along the rows
-#pragma unroll
-        for (int u = 0; u < 8; u++)
-            *reinterpret_cast<uint2*>(&tq[ct + u][rt]) =
-                make_uint2(codes4(f[0][u], f[1][u], f[2][u], f[3][u], sc[u]),
-                           codes4(f[4][u], f[5][u], f[6][u], f[7][u], sc[u]));
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int p = i * 256 + t, c = p >> 3, seg = p & 7;
-            if (c0 + c < C && r0 + 16 * seg < rpad)
-                *reinterpret_cast<uint4*>(qt + (int64_t)(c0 + c) * ldqt + r0 + 16 * seg) =
-                    *reinterpret_cast<const uint4*>(&tq[c][16 * seg]);
-        }
+    for (int i = 0; i < 4; i++) {
+        const int p = i * 256 + t, c = p >> 3, seg = p & 7, x8 = c >> 3;
+        uint4 v = *reinterpret_cast<const uint4*>(tq + c * 128 + (seg ^ (x8 >> 1)) * 16);
+        if (x8 & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+        if (c0 + c < C && r0 + 16 * seg < rpad)
+            *reinterpret_cast<uint4*>(qt + (int64_t)(c0 + c) * ldqt + r0 + 16 * seg) = v;
     }
 }
 
@@ -184,7 +271,7 @@ struct GemmArgs {
     const uint8_t* b; int64_t ldb; const float* bs;     // B [N][ldb]
     int64_t bs_n, bs_k;                                  // block scales: bs[(n/128)*bs_n + c*bs_k]; ROWS: bs [c][N]
     void* c; int64_t ldc;
-    int c_bf16, accumulate, vec;                         // vec: C rows allow 16-byte stores
+    int c_bf16, accumulate;
 };
 
 // Both operands E4M3, no hardware scale (E8M0 127 = 2^0).  Weights (rows of B)
@@ -227,8 +314,8 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* st
             const int m = m0 + 16 * i + r, n = n0 + sg * PER;
             if (m >= g.M || n >= g.N) continue;
             T* o = c + (int64_t)m * g.ldc + n;
-            if (g.vec && n + PER <= g.N && !g.accumulate) {
-                *reinterpret_cast<uint4*>(o) = v;
+            if (n + PER <= g.N && !g.accumulate) {
+                *reinterpret_cast<v4u_any*>(o) = v4u{v.x, v.y, v.z, v.w};
                 continue;
             }
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -456,15 +543,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
     else store_tile<MI, NI>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
 }
 
-// x / s rounded once to fp32: y = 1/s rounded, then two corrections by the
-// exact residual.  Needs s and the quotient well inside the normal range.
-__device__ __forceinline__ float quotient(float x, float s, float y)
-{
-    float q = x * y;
-    q = fmaf(fmaf(-q, s, x), y, q);
-    return fmaf(fmaf(-q, s, x), y, q);
-}
-
 // Few rows: the chunks of a tile of (16 MT) x (16 NT) are spread over the NW
 // waves of a block, each loading its operands straight into registers, so that
 // a block's whole stretch of weights is in flight at once and nothing waits
@@ -507,7 +585,6 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_split(GemmArgs g, const uint16_
         float sa[MT], sb[ROWS ? NT : 1];
     };
     // this lane's segments kq and 4 + kq of chunk c, zeros past the end (by their address: no branch between loads)
-    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
     typedef const __attribute__((address_space(1))) v4u* gptr;
     const gptr zeros = (gptr)&g_zeros[lane];
     auto fetch = [&](bool in, const void* p) {
@@ -575,19 +652,10 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_split(GemmArgs g, const uint16_
                 }
                 m = max(m, (uint32_t)__shfl_xor((int)m, 16));
                 m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-                const float sc = group_scale(m);
-                s[0] = sc;
-                // scales far from the ends of the range: the short division gives the same quotients
-                if (sc > 0x1p-80f && sc < 0x1p80f) {
-                    const float y = 1.0f / sc;
+                const Divisor d(group_scale(m));
+                s[0] = d.s;
 #pragma unroll
-                    for (int u = 0; u < 8; u++)
-                        a[0][u] = (int)(e4m3x2(quotient(f[4 * u], sc, y), quotient(f[4 * u + 1], sc, y)) |
-                                        (e4m3x2(quotient(f[4 * u + 2], sc, y), quotient(f[4 * u + 3], sc, y)) << 16));
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 8; u++) a[0][u] = (int)codes4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3], sc);
-                }
+                for (int u = 0; u < 8; u++) a[0][u] = (int)d.codes4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
             } else {
 #pragma unroll
                 for (int i = 0; i < MT; i++) a[i] = v8(o.a[i][0], o.a[i][1]), s[i] = o.sa[i];
@@ -675,14 +743,18 @@ template <typename T>
 hipError_t launch_quant(int mode, int R, int C, const T* x, int64_t ldx, uint8_t* q, int64_t ldq, float* s, uint8_t* qt,
                         int64_t ldqt, float* st, hipStream_t stream)
 {
-    const int vec = aligned_to(x, 16) && ldx % (16 / (int)sizeof(T)) == 0;
-    const dim3 grid((unsigned)chunks(C), (unsigned)chunks(R));
+    if (mode == kQuantRows) {
+        hipLaunchKernelGGL(k_fp8_quant_rows<T>, dim3((unsigned)((R * chunks(C) + 15) / 16)), dim3(256), 0, stream, R, C, x, ldx,
+                           q, ldq, s);
+        return hipGetLastError();
+    }
+    const int64_t tiles = chunks(C) * chunks(R);
+    const dim3 grid((unsigned)tiles);
     auto run = [&](auto m) {
-        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), grid, dim3(256), 0, stream, R, C, x, ldx, vec, q, ldq, s,
-                           qt, ldqt, st);
+        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), grid, dim3(256), 0, stream, R, C, x, ldx, q, ldq, s, qt, ldqt,
+                           st);
     };
     switch (mode) {
-    case kQuantRows: run(std::integral_constant<int, kQuantRows>{}); break;
     case kQuantCols: run(std::integral_constant<int, kQuantCols>{}); break;
     case kQuantRows | kQuantCols: run(std::integral_constant<int, kQuantRows | kQuantCols>{}); break;
     default: run(std::integral_constant<int, kQuantBlock>{}); break;
@@ -867,8 +939,7 @@ __attribute__((visibility("default"))) int moe_fp8_gemm(const v4moe_gemm* p, con
     if (!aligned_to(a, 16) || !aligned_to(b, 16) || !aligned_to(as, 4) || !aligned_to(bs, 4)) return V4MOE_EALIGN;
     if (!device_ready()) return V4MOE_EDEVICE;
     const bool bf16 = p->c_type == V4MOE_TYPE_BF16, rows = p->b_scale == V4MOE_SCALE_ROW;
-    const GemmArgs g{p->M, p->N, p->K, a, p->lda, as, b, p->ldb, bs, p->bs_n, p->bs_k, c, p->ldc, bf16, p->accumulate != 0,
-                     p->ldc % (bf16 ? 8 : 4) == 0 && aligned_to(c, 16)};
+    const GemmArgs g{p->M, p->N, p->K, a, p->lda, as, b, p->ldb, bs, p->bs_n, p->bs_k, c, p->ldc, bf16, p->accumulate != 0};
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return (rows ? run_gemm<true>(g, s) : run_gemm<false>(g, s)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }
@@ -898,7 +969,7 @@ __attribute__((visibility("default"))) int moe_fp8_linear(int32_t M, const void*
     if (x_type == V4MOE_TYPE_BF16 && K % 8 == 0 && ldx % 8 == 0 && aligned_to(x, 16) && choose_variant(M, N) == 0) {
         // few rows: the product quantises x itself
         if (!device_ready()) return V4MOE_EDEVICE;
-        const GemmArgs g{M, N, K16, nullptr, 0, nullptr, w->q, K16, w->blk, chunks(K), 1, y, ldy, y_bf16, 0, 0};
+        const GemmArgs g{M, N, K16, nullptr, 0, nullptr, w->q, K16, w->blk, chunks(K), 1, y, ldy, y_bf16, 0};
         return launch_split<1, 1, 8, false, true>(g, static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(x), ldx,
                                                   K) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
     }
