@@ -24,15 +24,45 @@ namespace {
 constexpr float kMask = 1e30f;
 constexpr float kInf = __builtin_inff();
 
-template <typename T>
-__device__ __forceinline__ float load_logit(const T* p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float* p) { return *p; }
-template <>
-__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
-
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16_t)bf16x2(v, 0.0f); }
+// EPL consecutive logits of a row from expert e0 on, -inf past E: one access
+// where the row has them all (at any element's address).
+template <typename T, int EPL>
+__device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (&z)[EPL])
+{
+    typedef T vec __attribute__((ext_vector_type(EPL)));
+    typedef vec vec_any __attribute__((aligned(sizeof(T))));
+    auto f32 = [](T v) {
+        if constexpr (sizeof(T) == 4) return (float)v;
+        else return bf16_to_f32(v);
+    };
+    if (e0 + EPL <= E) {
+        const vec v = *reinterpret_cast<const vec_any*>(row + e0);
+#pragma unroll
+        for (int q = 0; q < EPL; q++) z[q] = f32(v[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < EPL; q++) z[q] = e0 + q < E ? f32(row[e0 + q]) : -kInf;
+    }
+}
+template <typename T, int EPL>
+__device__ __forceinline__ void store_logits(T* row, int e0, int E, const float (&z)[EPL])
+{
+    typedef T vec __attribute__((ext_vector_type(EPL)));
+    typedef vec vec_any __attribute__((aligned(sizeof(T))));
+    vec v;
+#pragma unroll
+    for (int q = 0; q < EPL; q++) {
+        if constexpr (sizeof(T) == 4) v[q] = z[q];
+        else v[q] = (T)bf16x2(z[q], 0.0f);
+    }
+    if (e0 + EPL <= E) {
+        *reinterpret_cast<vec_any*>(row + e0) = v;
+    } else {
+#pragma unroll
+        for (int q = 0; q < EPL; q++)
+            if (e0 + q < E) row[e0 + q] = v[q];
+    }
+}
 
 // -inf for a masked logit, and for NaN
 __device__ __forceinline__ float clean(float z) { return z > -kMask ? fminf(z, kMask) : -kInf; }
@@ -40,11 +70,43 @@ __device__ __forceinline__ float clean(float z) { return z > -kMask ? fminf(z, k
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 __device__ __forceinline__ float sqrt_softplus(float z) { return sqrtf(fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z)))); }
 
-__device__ __forceinline__ float wave_max(float v)
+// One step of a reduction over lanes: v as lane pattern CTRL brings it (DPP),
+// `none` where it brings nothing.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
+}
+// Maximum over the wave, as a scalar: inside the rows of 16 lanes (quad xor 1,
+// xor 2, half-row mirror, mirror), then row 0 into 1 and 2 into 3, then 1 into 3.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = max(v, dpp<0xB1>(0, v));
+    v = max(v, dpp<0x4E>(0, v));
+    v = max(v, dpp<0x141>(0, v));
+    v = max(v, dpp<0x140>(0, v));
+    v = max(v, dpp<0x142, 0xA>(0, v));
+    v = max(v, dpp<0x143, 0xC>(0, v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// Sum over the 16 lanes of a row, in every one of them.
+__device__ __forceinline__ float row_sum(float v)
+{
+    auto add = [&](uint32_t o) { v += __uint_as_float(o); };
+    add(dpp<0xB1>(0, __float_as_uint(v)));
+    add(dpp<0x4E>(0, __float_as_uint(v)));
+    add(dpp<0x141>(0, __float_as_uint(v)));
+    add(dpp<0x140>(0, __float_as_uint(v)));
     return v;
+}
+__device__ __forceinline__ float from_lane(float v, int lane)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = row_sum(v);
+    return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
 __device__ __forceinline__ double wave_sum(double v)
 {
@@ -53,112 +115,144 @@ __device__ __forceinline__ double wave_sum(double v)
     return v;
 }
 
-// z -> scores, in place; lane l holds experts l + 64q.  Softmax leaves the
-// maximum and the sum in m and total.
-template <int NQ>
-__device__ __forceinline__ void scores(int score, float (&z)[NQ], float& m, float& total)
+// Order-preserving map of floats (no NaN) to unsigned integers; -inf is kNone.
+constexpr uint32_t kNone = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t order_of(float f)
 {
-    if (score == V4MOE_SCORE_SOFTMAX) {
-        m = -kInf;
-#pragma unroll
-        for (int q = 0; q < NQ; q++) m = fmaxf(m, z[q]);
-        m = wave_max(m);
-        m = m == -kInf ? 0.0f : m;
-        double sum = 0.0;
-#pragma unroll
-        for (int q = 0; q < NQ; q++) {
-            z[q] = expf(z[q] - m);
-            sum += (double)z[q];
-        }
-        total = (float)wave_sum(sum);
-#pragma unroll
-        for (int q = 0; q < NQ; q++) z[q] = total > 0.0f ? z[q] / total : 0.0f;
-    } else {
-#pragma unroll
-        for (int q = 0; q < NQ; q++)
-            z[q] = score == V4MOE_SCORE_SIGMOID ? sigmoid(z[q]) : sqrt_softplus(z[q]);
-    }
+    const uint32_t u = __float_as_uint(f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float float_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o); }
 
-// Larger key first, then the lower id.
-__device__ __forceinline__ bool ahead(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
-
-// One wave per token; lane l holds experts l + 64q, q < NQ.
-template <typename T, int NQ>
+// One wave per token; lane l holds experts l EPL .. + EPL - 1, so that of equal
+// keys the lowest lane has the lowest id.  Each lane keeps its best key not yet
+// picked; a round takes the maximum over the wave (DPP), the first lane that
+// has it, and only that lane looks for its next best.  The groups' two largest
+// keys are found by 64 / groups lanes each, over keys staged in LDS, as groups
+// need not end with a lane.  Bound by the instructions a token takes, most of
+// them in the rounds and the scores' exponentials and divisions.
+template <typename T, int EPL>
 __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
                                               const float* __restrict__ bias, int32_t* __restrict__ ids,
                                               float* __restrict__ w)
 {
-    __shared__ float keys[4][NQ * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ uint32_t staged[4][EPL * 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int t = blockIdx.x * 4 + wave;
-    const bool on = t < g.T;
-    const T* row = logits + (int64_t)(on ? t : 0) * ld;
-    float s[NQ], key[NQ];
-    bool masked[NQ];
+    if (t >= g.T) return;
+    const int e0 = lane * EPL;
+    float s[EPL];
+    uint32_t key[EPL];
+    load_logits<T, EPL>(logits + (int64_t)t * ld, e0, g.E, s);
+    uint32_t valid = 0;
 #pragma unroll
-    for (int q = 0; q < NQ; q++) {
-        const int e = lane + 64 * q;
-        s[q] = e < g.E ? clean(load_logit(row + e)) : -kInf;
-        masked[q] = s[q] == -kInf;
+    for (int q = 0; q < EPL; q++) {
+        s[q] = clean(s[q]);
+        valid |= (s[q] != -kInf ? 1u : 0u) << q;
     }
-    float m = 0.0f, total = 0.0f;
-    scores<NQ>(g.score, s, m, total);
+    if (g.score == V4MOE_SCORE_SOFTMAX) {
+        uint32_t best = kNone;
 #pragma unroll
-    for (int q = 0; q < NQ; q++) {
-        const int e = lane + 64 * q;
-        const float k = bias && e < g.E ? s[q] + bias[e] : s[q];
-        key[q] = masked[q] || k != k ? -kInf : k;
+        for (int q = 0; q < EPL; q++) best = max(best, order_of(s[q]));
+        best = wave_max(best);
+        const float m = best == kNone ? 0.0f : float_of(best);
+        double sum = 0.0;
+#pragma unroll
+        for (int q = 0; q < EPL; q++) {
+            s[q] = expf(s[q] - m);
+            sum += (double)s[q];
+        }
+        const float total = (float)wave_sum(sum);
+#pragma unroll
+        for (int q = 0; q < EPL; q++) s[q] = total > 0.0f ? s[q] / total : 0.0f;
+    } else if (g.score == V4MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int q = 0; q < EPL; q++) s[q] = sigmoid(s[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < EPL; q++) s[q] = sqrt_softplus(s[q]);
+    }
+    float b[EPL];
+#pragma unroll
+    for (int q = 0; q < EPL; q++) b[q] = 0.0f;
+    if (bias) load_logits<float, EPL>(bias, e0, g.E, b);
+#pragma unroll
+    for (int q = 0; q < EPL; q++) {
+        const float k = bias ? s[q] + b[q] : s[q];
+        key[q] = (valid >> q) & 1 && k == k ? order_of(k) : kNone;
     }
     if (g.groups > 1) {
-        // lane i < groups: group i's value, then its rank among the groups
         const int size = g.E / g.groups;
+        // 2^shift lanes per group: lane i of them takes the group's keys i, i + 2^shift, ...
+        const int shift = 6 - (32 - __builtin_clz(g.groups - 1)), per = 1 << shift;
+        const int mine = lane >> shift;
 #pragma unroll
-        for (int q = 0; q < NQ; q++) keys[wave][lane + 64 * q] = key[q];
-        __syncthreads();
-        float a = -kInf, b = -kInf;
-        if (lane < g.groups)
-            for (int i = 0; i < size; i++) {
-                const float k = keys[wave][lane * size + i];
-                b = fmaxf(b, fminf(a, k));
-                a = fmaxf(a, k);
+        for (int q = 0; q < EPL; q++) staged[wave][e0 + q] = key[q];
+        __builtin_amdgcn_wave_barrier();
+        uint32_t a = kNone, c = kNone;              // largest and second of the group
+        if (mine < g.groups)
+            for (int i = lane & (per - 1); i < size; i += per) {
+                const uint32_t k = staged[wave][mine * size + i];
+                c = max(c, min(a, k));
+                a = max(a, k);
             }
-        const float v = b == -kInf ? a : a + b;
+        for (int o = 1; o < per; o <<= 1) {
+            const uint32_t oa = (uint32_t)__shfl_xor((int)a, o), oc = (uint32_t)__shfl_xor((int)c, o);
+            c = max(min(a, oa), max(c, oc));
+            a = max(a, oa);
+        }
+        const uint32_t v = c == kNone ? a : order_of(float_of(a) + float_of(c));
         int rank = 0;
-        for (int o = 0; o < g.groups; o++) rank += ahead(__shfl(v, o), o, v, lane);
-        const uint64_t kept = __ballot(lane < g.groups && rank < g.topk_groups);
+        for (int o = 0; o < g.groups; o++) {
+            const uint32_t u = (uint32_t)__builtin_amdgcn_readlane((int)v, o << shift);
+            rank += (o < mine ? u >= v : u > v) ? 1 : 0;
+        }
+        const uint64_t kept = __ballot(mine < g.groups && rank < g.topk_groups);
+        const float inv = 1.0f / (float)size;
 #pragma unroll
-        for (int q = 0; q < NQ; q++) {
-            const int e = lane + 64 * q;
-            if (e < g.E && !((kept >> (e / size)) & 1)) key[q] = -kInf;
+        for (int q = 0; q < EPL; q++) {
+            const int group = min((int)(((float)(e0 + q) + 0.5f) * inv), g.groups - 1);     // (e0 + q) / size: exact below 2^20
+            if (!((kept >> (group << shift)) & 1)) key[q] = kNone;
         }
     }
-    // topk rounds of a wave maximum; a picked expert leaves by its id
+    uint32_t best = kNone, taken = 0;
+    int at = 0;
+    float bs = 0.0f;
+    auto rescan = [&]() {
+        best = kNone;
+#pragma unroll
+        for (int q = 0; q < EPL; q++)
+            if (key[q] > best) best = key[q], at = q, bs = s[q];
+    };
+    rescan();
     float my_s = 0.0f;
-    int my_e = 0;
-    uint32_t taken = 0;
-    for (int j = 0; j < g.topk; j++) {
-        float bk = -kInf, bs = 0.0f;
-        int be = 1 << 30;
+    int my_e = 0, j = 0;
+    for (; j < g.topk; j++) {
+        const uint32_t m = wave_max(best);
+        if (m == kNone) break;
+        const int src = __builtin_ctzll(__ballot(best == m));
+        const int e = src * EPL + __builtin_amdgcn_readlane(at, src);
+        const float ps = from_lane(bs, src);
+        if (lane == j) my_e = e, my_s = ps;
+        if (lane == src) {
+            taken |= 1u << at;
 #pragma unroll
-        for (int q = 0; q < NQ; q++) {
-            const int e = lane + 64 * q;
-            if (e < g.E && !((taken >> q) & 1) && ahead(key[q], e, bk, be)) bk = key[q], bs = s[q], be = e;
+            for (int q = 0; q < EPL; q++)
+                if (q == at) key[q] = kNone;
+            rescan();
         }
-        for (int o = 1; o < 64; o <<= 1) {
-            const float ok = __shfl_xor(bk, o), os = __shfl_xor(bs, o);
-            const int oe = __shfl_xor(be, o);
-            if (ahead(ok, oe, bk, be)) bk = ok, bs = os, be = oe;
-        }
-        if ((be & 63) == lane) taken |= 1u << (be >> 6);
-        if (lane == j) my_e = be, my_s = bk == -kInf ? 0.0f : bs;
     }
-    float sum = 1.0f;
-    if (g.renorm) {
-        sum = 0.0f;
-        for (int j = 0; j < g.topk; j++) sum += __shfl(my_s, j);
+    // fewer unmasked experts than slots: the lowest others, weight 0
+    for (; j < g.topk; j++) {
+        const uint32_t free = ~taken & ((1u << EPL) - 1);
+        const int q = free ? __builtin_ctz(free) : EPL;
+        const int src = __builtin_ctzll(__ballot(q < EPL && e0 + q < g.E));
+        const int e = src * EPL + __builtin_amdgcn_readlane(q, src);
+        if (lane == j) my_e = e, my_s = 0.0f;
+        if (lane == src) taken |= 1u << q;
     }
-    if (on && lane < g.topk) {
+    const float sum = g.renorm ? row_sum(my_s) : 1.0f;       // (topk <= 16: lanes past it hold 0)
+    if (lane < g.topk) {
         ids[(int64_t)t * g.topk + lane] = my_e;
         w[(int64_t)t * g.topk + lane] = (sum > 0.0f ? my_s / sum : 0.0f) * g.scale;
     }
@@ -171,44 +265,67 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
 //   dz = ds s (1 - s) | ds sigmoid(z) / (2 s) | p_e (ds_e [picked] - sum_j ds_j p_j),
 // the softmax's last sum zero where the weights are renormalised, which leaves
 // only the picked logits and, as p_j / S = e_j / (sum of the picked e),
-// no need of the others.
-template <typename T, int NQ>
+// no need of the others.  One wave per token, lane j < topk its slot j; the
+// picked logits' parts reach the lanes that write them through LDS.  Bound by HBM
+// where the softmax reaches every logit (read and written once), by the rows'
+// writes elsewhere.
+template <typename T, int EPL>
 __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
                                                        const int32_t* __restrict__ ids, const float* __restrict__ w,
                                                        const float* __restrict__ dw, T* __restrict__ dl, int64_t ldd)
 {
-    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
+    __shared__ __align__(16) float staged[4][EPL * 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int t = blockIdx.x * 4 + wave;
     if (t >= g.T) return;
+    const int e0 = lane * EPL;
     const T* row = logits + (int64_t)t * ld;
+    const bool soft = g.score == V4MOE_SCORE_SOFTMAX, dense = soft && !g.renorm;
+    float p[EPL];
+    if (dense) load_logits<T, EPL>(row, e0, g.E, p);
     const bool slot = lane < g.topk;
     const int64_t at = (int64_t)t * g.topk + lane;
     const int my_e = slot ? ids[at] : -1;
     const bool valid = my_e >= 0 && my_e < g.E;      // an id out of range (an input error) gets no gradient
     const bool live = valid && w[at] != 0.0f;
     const float my_dw = live ? dw[at] : 0.0f;
-    const float z = live ? clean(load_logit(row + my_e)) : -kInf;
-    const bool soft = g.score == V4MOE_SCORE_SOFTMAX, dense = soft && !g.renorm;
-    float p[NQ];
-#pragma unroll
-    for (int q = 0; q < NQ; q++) p[q] = 0.0f;
+    float z = -kInf;
+    if (live) {
+        if constexpr (sizeof(T) == 4) z = clean(row[my_e]);
+        else z = clean(bf16_to_f32(row[my_e]));
+    }
     float m = 0.0f, total = 1.0f;
-    if (dense) {
+    if (soft) {
+        uint32_t best = order_of(z);
+        if (dense) {
 #pragma unroll
-        for (int q = 0; q < NQ; q++) {
-            const int e = lane + 64 * q;
-            p[q] = e < g.E ? clean(load_logit(row + e)) : -kInf;
+            for (int q = 0; q < EPL; q++) {
+                p[q] = clean(p[q]);
+                best = max(best, order_of(p[q]));
+            }
         }
-        scores<NQ>(g.score, p, m, total);
-    } else if (soft) {
-        m = wave_max(z);
+        best = wave_max(best);
+        m = best == kNone ? 0.0f : float_of(best);
+    }
+    if (dense) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < EPL; q++) {
+            p[q] = expf(p[q] - m);
+            sum += p[q];
+        }
+        total = wave_sum(sum);
+        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+        for (int q = 0; q < EPL; q++) p[q] *= inv;
     }
     float s = 0.0f;
     if (live) s = soft ? expf(z - m) / total : g.score == V4MOE_SCORE_SIGMOID ? sigmoid(z) : sqrt_softplus(z);
     float ds = live ? g.scale * my_dw : 0.0f;
     if (g.renorm) {
-        float S = 0.0f, d = 0.0f;
-        for (int j = 0; j < g.topk; j++) S += __shfl(s, j);
-        for (int j = 0; j < g.topk; j++) d += __shfl(s, j) * (my_dw - __shfl(my_dw, j));
+        const float S = row_sum(s);                  // (lanes past topk <= 16 hold 0)
+        float d = 0.0f;
+        for (int j = 0; j < g.topk; j++) d += from_lane(s, j) * (my_dw - from_lane(my_dw, j));
         ds = live && S > 0.0f ? g.scale * (d / S) / S : 0.0f;
     }
     float dz;
@@ -216,27 +333,17 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
     else if (g.score == V4MOE_SCORE_SIGMOID) dz = ds * s * (1.0f / (1.0f + expf(z)));
     else dz = ds * sigmoid(z) / (2.0f * s);
     if (!live || s == 0.0f) dz = 0.0f;
-    if (dense) {
-        float dot = 0.0f;
-        for (int j = 0; j < g.topk; j++) dot += __shfl(dz, j);
+    float* st = staged[wave];
+    const float dot = dense ? from_lane(row_sum(dz), 0) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < NQ; q++) p[q] = -p[q] * dot;
-    }
-    for (int j = 0; j < g.topk; j++) {
-        const int e = __shfl(valid ? my_e : -1, j);
-        const float v = __shfl(dz, j);
-        if (e >= 0 && (e & 63) == lane) {
+    for (int q = 0; q < EPL; q++) st[e0 + q] = dense ? -p[q] * dot : 0.0f;
+    __builtin_amdgcn_wave_barrier();
+    if (valid) st[my_e] += dz;                       // (ids of a row are distinct)
+    __builtin_amdgcn_wave_barrier();
+    float out[EPL];
 #pragma unroll
-            for (int q = 0; q < NQ; q++)
-                if (q == (e >> 6)) p[q] += v;
-        }
-    }
-    T* out = dl + (int64_t)t * ldd;
-#pragma unroll
-    for (int q = 0; q < NQ; q++) {
-        const int e = lane + 64 * q;
-        if (e < g.E) store_logit(out + e, p[q]);
-    }
+    for (int q = 0; q < EPL; q++) out[q] = st[e0 + q];
+    store_logits<T, EPL>(dl + (int64_t)t * ldd, e0, g.E, out);
 }
 
 // calls f with the number of 64-expert steps of a row
