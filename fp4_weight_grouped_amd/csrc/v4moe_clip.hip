@@ -5,10 +5,12 @@
 //   out = g * coef (rounded once to the gradient's type)
 // Squares are summed in fp64: nothing overflows or vanishes that fp32 holds,
 // and at the rate the gradients arrive from HBM the conversion and the fma
-// are hidden.  No atomics: a block sums the chunks b, b + grid, ... in order
-// and one thread per partial adds them in a fixed tree, so the norm is the same
-// bits on every run.  Bound by HBM: every gradient is read for the norm, and
-// read again and written once the norm is known.
+// are hidden.  No atomics: a block sums the chunks b, b + grid, ... in order,
+// a fixed tree adds the blocks' sums, and every block that scales adds them
+// again in the same tree, so the norm is the same bits everywhere and on every
+// run.  Bound by HBM: every gradient is read for the norm, and read again and
+// written once the norm is known (the last of them still from the memory-side
+// cache, as the second pass goes backwards).
 #include "v4moe.h"
 #include "v4moe_device.h"
 #include "v4moe_internal.h"
@@ -20,9 +22,9 @@ namespace v4moe {
 namespace {
 
 constexpr int kTensors = 96;          // tensors per launch: their table travels in the kernel's arguments (< 4 KiB)
-constexpr int kChunk = 16384;         // elements per chunk: one block's unit of work
-constexpr int kMaxBlocks = 2048;      // partial sums per launch
+constexpr int kMaxBlocks = 2048;      // partial sums per launch: eight blocks a CU
 constexpr int64_t kMaxElements = 1ll << 36;   // of a tensor: a launch's chunks then fit 31 bits
+constexpr int kThreads = 256;
 
 struct Entry {
     const void* g;
@@ -33,55 +35,111 @@ struct Entry {
 };
 struct Table {
     Entry e[kTensors];
-    int32_t count, chunks;
+    int32_t count, chunks, chunk;     // chunk: elements of one, a block's unit of work
 };
-static_assert(sizeof(Table) < 3584, "kernel arguments");
+static_assert(sizeof(Table) < 3584 && sizeof(Entry) == 32, "kernel arguments");
 
-// The tensor chunk c belongs to.
-__device__ __forceinline__ int find(const Table& t, int c)
+// The table in LDS: the arguments lie in host memory, and each dependent read
+// of them (a search takes seven) would wait for it.
+__device__ __forceinline__ void stage_table(const Table& t, Entry* lds)
 {
-    int lo = 0, hi = t.count - 1;
+    if ((int)threadIdx.x < t.count) lds[threadIdx.x] = t.e[threadIdx.x];
+    __syncthreads();
+}
+// The tensor chunk c belongs to.
+__device__ __forceinline__ int find(const Entry* e, int count, int c)
+{
+    int lo = 0, hi = count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (t.e[mid].first <= c) lo = mid;
+        if (e[mid].first <= c) lo = mid;
         else hi = mid - 1;
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Sixteen bytes at any element's address, in one access: unaligned ones are the
+// hardware's to split.
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef v4u v4u_any __attribute__((aligned(2)));
 template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return (uint16_t)bf16x2(v, 0.0f); }
+__device__ __forceinline__ float element(const v4u& v, int i)
+{
+    if constexpr (sizeof(T) == 4) return __uint_as_float(v[i]);
+    else return __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+}
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_to_f32(v); }
 
 template <typename T>
-__device__ __forceinline__ double sum_squares(const T* p, int n)
+__device__ __forceinline__ void sum_squares(const T* p, int n, double (&s)[4])
 {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += 256) {
-        const double v = (double)to_f32(p[i]);
-        s = fma(v, v, s);
+    constexpr int V = 16 / sizeof(T), U = 4;             // elements per access, accesses in flight
+    const int nv = n / V;
+    int i = threadIdx.x;
+    for (; i + (U - 1) * kThreads < nv; i += U * kThreads) {
+        v4u v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) v[u] = *reinterpret_cast<const v4u_any*>(p + (int64_t)(i + u * kThreads) * V);
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int k = 0; k < V; k++) {
+                const double d = (double)element<T>(v[u], k);
+                s[k & 3] = fma(d, d, s[k & 3]);
+            }
     }
-    return s;
+    for (; i < nv; i += kThreads) {
+        const v4u v = *reinterpret_cast<const v4u_any*>(p + (int64_t)i * V);
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+            const double d = (double)element<T>(v, k);
+            s[k & 3] = fma(d, d, s[k & 3]);
+        }
+    }
+    if ((int)threadIdx.x < n - nv * V) {
+        const double d = (double)to_f32(p[nv * V + threadIdx.x]);
+        s[0] = fma(d, d, s[0]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ v4u scaled(const v4u& v, float coef)
+{
+    v4u r;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        if constexpr (sizeof(T) == 4) r[k] = __float_as_uint(element<T>(v, k) * coef);
+        else r[k] = bf16x2(element<T>(v, 2 * k) * coef, element<T>(v, 2 * k + 1) * coef);
+    }
+    return r;
 }
 template <typename T>
 __device__ __forceinline__ void scale_to(const T* p, T* o, int n, float coef)
 {
-    for (int i = threadIdx.x; i < n; i += 256) o[i] = from_f32<T>(to_f32(p[i]) * coef);
+    constexpr int V = 16 / sizeof(T), U = 4;
+    const int nv = n / V;
+    int i = threadIdx.x;
+    for (; i + (U - 1) * kThreads < nv; i += U * kThreads) {
+        v4u v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) v[u] = *reinterpret_cast<const v4u_any*>(p + (int64_t)(i + u * kThreads) * V);
+#pragma unroll
+        for (int u = 0; u < U; u++) *reinterpret_cast<v4u_any*>(o + (int64_t)(i + u * kThreads) * V) = scaled<T>(v[u], coef);
+    }
+    for (; i < nv; i += kThreads)
+        *reinterpret_cast<v4u_any*>(o + (int64_t)i * V) = scaled<T>(*reinterpret_cast<const v4u_any*>(p + (int64_t)i * V), coef);
+    if ((int)threadIdx.x < n - nv * V) {
+        const int at = nv * V + threadIdx.x;
+        const float f = to_f32(p[at]) * coef;
+        if constexpr (sizeof(T) == 4) o[at] = f;
+        else o[at] = (T)bf16x2(f, 0.0f);
+    }
 }
 
 // Sum over the block, in every thread; fixed tree.
 __device__ __forceinline__ double block_sum(double v)
 {
-    __shared__ double part[4];
+    __shared__ double part[kThreads / 64];
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
@@ -89,62 +147,78 @@ __device__ __forceinline__ double block_sum(double v)
     return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-__global__ __launch_bounds__(256) void k_grad_squares(Table t, double* __restrict__ partial)
+__global__ __launch_bounds__(kThreads) void k_grad_squares(Table t, double* __restrict__ partial)
 {
-    double s = 0.0;
+    __shared__ Entry tab[kTensors];
+    stage_table(t, tab);
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const Entry& e = t.e[find(t, c)];
-        const int64_t at = (int64_t)(c - e.first) * kChunk;
-        const int n = (int)min((int64_t)kChunk, e.n - at);
-        s += e.bf16 ? sum_squares(static_cast<const uint16_t*>(e.g) + at, n)
-                    : sum_squares(static_cast<const float*>(e.g) + at, n);
+        const Entry& e = tab[find(tab, t.count, c)];
+        const int64_t at = (int64_t)(c - e.first) * t.chunk;
+        const int n = (int)min((int64_t)t.chunk, e.n - at);
+        if (e.bf16) sum_squares(static_cast<const uint16_t*>(e.g) + at, n, s);
+        else sum_squares(static_cast<const float*>(e.g) + at, n, s);
     }
-    s = block_sum(s);
-    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+    const double v = block_sum((s[0] + s[1]) + (s[2] + s[3]));
+    if (threadIdx.x == 0) partial[blockIdx.x] = v;
 }
 
-__global__ __launch_bounds__(256) void k_grad_norm(int n, const double* __restrict__ partial, float* __restrict__ norm)
+// n_partial sums of all launches of k_grad_squares -> the norm, in every block
+// (block 0 of the first launch writes it); then this launch's chunks, last first.
+__global__ __launch_bounds__(kThreads) void k_grad_scale(Table t, int n_partial, const double* __restrict__ partial,
+                                                         float* __restrict__ norm, float max_norm)
 {
+    __shared__ Entry tab[kTensors];
     double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += 256) s += partial[i];
-    s = block_sum(s);
-    if (threadIdx.x == 0) *norm = (float)sqrt(s);
-}
-
-__global__ __launch_bounds__(256) void k_grad_scale(Table t, const float* __restrict__ norm, float max_norm)
-{
+    for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
+    stage_table(t, tab);
+    const float v = (float)sqrt(block_sum(s));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     // a norm that is not finite leaves the gradients as they are: the caller sees it and drops the step
-    const float v = *norm;
     const float coef = v > max_norm && v < __builtin_inff() ? max_norm / v : 1.0f;
-    for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const Entry& e = t.e[find(t, c)];
+    for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+        const Entry& e = tab[find(tab, t.count, c)];
         if (coef == 1.0f && e.out == e.g) continue;
-        const int64_t at = (int64_t)(c - e.first) * kChunk;
-        const int n = (int)min((int64_t)kChunk, e.n - at);
+        const int64_t at = (int64_t)(c - e.first) * t.chunk;
+        const int n = (int)min((int64_t)t.chunk, e.n - at);
         if (e.bf16) scale_to(static_cast<const uint16_t*>(e.g) + at, static_cast<uint16_t*>(e.out) + at, n, coef);
         else scale_to(static_cast<const float*>(e.g) + at, static_cast<float*>(e.out) + at, n, coef);
     }
 }
 
+// Elements per chunk for a list of `total`: a power of two of 1024 (one access
+// per thread) to 65536, so that a small list still makes a block per CU and a
+// large one spends its time in the unrolled loop.
+int chunk_of(int64_t total)
+{
+    int chunk = 1024;
+    while (chunk < 65536 && total / chunk > 2 * kMaxBlocks) chunk *= 2;
+    return chunk;
+}
+
 // Splits a list into launches of at most kTensors entries; f(table, blocks)
-// returns false to stop.
+// returns false to stop.  An empty list gives one empty table.
 template <typename F>
 bool for_tables(int32_t count, const v4moe_tensor* t, F f)
 {
+    int64_t total = 0;
+    for (int32_t i = 0; i < count; i++) total += t[i].n;
+    const int chunk = chunk_of(total);
     int32_t i = 0;
-    while (i < count) {
-        Table tab{};
+    do {
+        Table tab;
         int64_t chunks = 0;
+        tab.count = 0;
         for (; i < count && tab.count < kTensors; i++) {
             if (t[i].n == 0) continue;
             tab.e[tab.count++] = Entry{t[i].g, t[i].out ? t[i].out : const_cast<void*>(t[i].g), t[i].n, (int32_t)chunks,
                                        t[i].type == V4MOE_TYPE_BF16};
-            chunks += (t[i].n + kChunk - 1) / kChunk;
+            chunks += (t[i].n + chunk - 1) / chunk;
         }
-        if (tab.count == 0) break;
         tab.chunks = (int32_t)chunks;
-        if (!f(tab, (int)(chunks < kMaxBlocks ? chunks : kMaxBlocks))) return false;
-    }
+        tab.chunk = chunk;
+        if (!f(tab, (int)(chunks < 1 ? 1 : chunks < kMaxBlocks ? chunks : kMaxBlocks))) return false;
+    } while (i < count);
     return true;
 }
 
@@ -162,7 +236,7 @@ int check_tensors(int32_t count, const v4moe_tensor* t)
     return V4MOE_OK;
 }
 
-size_t partials(int32_t count) { return (size_t)((count + kTensors - 1) / kTensors) * kMaxBlocks; }
+size_t partials(int32_t count) { return (size_t)(count / kTensors + 1) * kMaxBlocks; }
 
 }  // namespace
 
@@ -174,7 +248,7 @@ extern "C" {
 
 __attribute__((visibility("default"))) size_t moe_clip_workspace_bytes(int32_t count)
 {
-    return count < 0 || count > (1 << 20) ? 0 : (count == 0 ? 256 : partials(count) * sizeof(double));
+    return count < 0 || count > (1 << 20) ? 0 : partials(count) * sizeof(double);
 }
 
 __attribute__((visibility("default"))) int moe_clip_grads(int32_t count, const v4moe_tensor* tensors, float max_norm,
@@ -191,15 +265,14 @@ __attribute__((visibility("default"))) int moe_clip_grads(int32_t count, const v
     int used = 0;
     auto launched = []() { return hipGetLastError() == hipSuccess; };
     if (!for_tables(count, tensors, [&](const Table& t, int blocks) {
-            hipLaunchKernelGGL(k_grad_squares, dim3(blocks), dim3(256), 0, s, t, part + used);
+            hipLaunchKernelGGL(k_grad_squares, dim3(blocks), dim3(kThreads), 0, s, t, part + used);
             used += blocks;
             return launched();
         }))
         return V4MOE_ELAUNCH;
-    hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(256), 0, s, used, part, norm);
-    if (!launched()) return V4MOE_ELAUNCH;
     if (!for_tables(count, tensors, [&](const Table& t, int blocks) {
-            hipLaunchKernelGGL(k_grad_scale, dim3(blocks), dim3(256), 0, s, t, norm, max_norm);
+            hipLaunchKernelGGL(k_grad_scale, dim3(blocks), dim3(kThreads), 0, s, t, used, part, norm, max_norm);
+            norm = nullptr;
             return launched();
         }))
         return V4MOE_ELAUNCH;

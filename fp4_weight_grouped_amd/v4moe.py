@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import re
 from typing import Optional
@@ -297,14 +298,11 @@ def moe_time_next_ffn(start_event, stop_event):
 
 
 # ---- operators next to the layer ---------------------------------------------------------------
+# These wrap launches of a few microseconds, so the checks are plain attribute reads, the stream
+# comes from the runtime without a Stream object, and pointers travel as integers.
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
-
-
-def _type(t: torch.Tensor) -> int:
-    try:
-        return _TYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"float32 or bfloat16 expected, got {t.dtype}") from None
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _require(ok: bool, what: str):
@@ -312,17 +310,46 @@ def _require(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dtype=None):
+def _type(t: torch.Tensor) -> int:
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"float32 or bfloat16 expected, got {t.dtype}")
+    return ty
+
+
+def _on_device(t: torch.Tensor, what: str) -> int:
+    """The current stream, after checking that t is on the current GPU."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a GPU")
+    i = t.device.index
+    if i != _current_device():
+        raise ValueError(f"{what} is on GPU {i}, which is not the current device")
+    return _raw_stream(i)
+
+
+def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dtype=None) -> int:
     """t's leading dimension, after checking that it is [rows][cols] with contiguous columns on a GPU."""
-    _require(t.is_cuda, f"{what} must be on a GPU")
-    _require(t.shape == (rows, cols), f"{what} must be [{rows}][{cols}], got {list(t.shape)}")
-    _require(dtype is None or t.dtype == dtype, f"{what} must be {dtype}, got {t.dtype}")
-    st = t.stride()
-    _require(cols <= 1 or st[1] == 1, f"{what} must have contiguous rows")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a GPU")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must be [{rows}][{cols}], got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    ld, st = t.stride()
+    if st != 1 and cols > 1:
+        raise ValueError(f"{what} must have contiguous rows")
     if rows <= 1:
         return cols
-    _require(st[0] >= cols, f"{what} must not have overlapping rows")
-    return st[0]
+    if ld < cols:
+        raise ValueError(f"{what} must not have overlapping rows")
+    return ld
+
+
+def _dense(t: torch.Tensor, shape: tuple, dtype, what: str) -> int:
+    """t's address, after checking that it is contiguous, of this shape and type, on a GPU."""
+    if not (t.is_cuda and t.shape == shape and t.dtype == dtype and t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)} on a GPU, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
 
 
 def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Optional[torch.Tensor] = None,
@@ -331,13 +358,13 @@ def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Opti
     Returns (topk_ids int32 [T][topk], topk_w fp32 [T][topk]).  See moe_gate in include/v4moe.h."""
     T, E = logits.shape
     ld = _matrix(logits, T, E, "logits")
-    if bias is not None:
-        _require(bias.is_cuda and bias.shape == (E,) and bias.dtype == torch.float32 and bias.is_contiguous(),
-                 f"bias must be contiguous float32 [{E}] on a GPU")
+    stream = _on_device(logits, "logits")
+    b = None if bias is None else _dense(bias, (E,), torch.float32, "bias")
     g = GateC(T, E, topk, score, groups, topk_groups, 1 if renorm else 0, scale)
-    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-    _check(lib().moe_gate(ctypes.byref(g), _p(logits), _type(logits), ld, _p(bias), _p(ids), _p(w), _stream()))
+    dev = logits.device
+    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    w = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    _check(lib().moe_gate(ctypes.byref(g), logits.data_ptr(), _type(logits), ld, b, ids.data_ptr(), w.data_ptr(), stream))
     return ids, w
 
 
@@ -346,14 +373,15 @@ def gate_backward(logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Te
     """dL/dlogits [T][E] (the logits' type) from dw = dL/dtopk_w and gate()'s outputs."""
     T, E = logits.shape
     ld = _matrix(logits, T, E, "logits")
+    stream = _on_device(logits, "logits")
     k = topk_ids.shape[1]
-    for t, name, dt in ((topk_ids, "topk_ids", torch.int32), (topk_w, "topk_w", torch.float32), (dw, "dw", torch.float32)):
-        _matrix(t, T, k, name, dt)
-        _require(t.is_contiguous(), f"{name} must be contiguous")
+    ids = _dense(topk_ids, (T, k), torch.int32, "topk_ids")
+    w = _dense(topk_w, (T, k), torch.float32, "topk_w")
+    d = _dense(dw, (T, k), torch.float32, "dw")
     g = GateC(T, E, k, score, 1, 1, 1 if renorm else 0, scale)
     dl = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _check(lib().moe_gate_backward(ctypes.byref(g), _p(logits), _type(logits), ld, _p(topk_ids), _p(topk_w), _p(dw),
-                                   _p(dl), E, _stream()))
+    _check(lib().moe_gate_backward(ctypes.byref(g), logits.data_ptr(), _type(logits), ld, ids, w, d, dl.data_ptr(), E,
+                                   stream))
     return dl
 
 
@@ -375,23 +403,23 @@ class FP8Matrix:
     blk: torch.Tensor   # float32 [ceil(N/128)][ceil(K/128)]
 
     def c(self) -> FP8MatC:
-        for t, shape, dt in ((self.q, (self.N, _up16(self.K)), torch.uint8), (self.qt, (self.K, _up16(self.N)), torch.uint8),
-                             (self.blk, (_chunks(self.N), _chunks(self.K)), torch.float32)):
-            _require(t.is_cuda and t.shape == shape and t.dtype == dt and t.is_contiguous(),
-                     f"an FP8Matrix part must be contiguous {dt} {list(shape)} on a GPU, got {t.dtype} {list(t.shape)}")
-        return FP8MatC(self.N, self.K, self.q.data_ptr(), self.qt.data_ptr(), self.blk.data_ptr())
+        N, K = self.N, self.K
+        return FP8MatC(N, K, _dense(self.q, (N, _up16(K)), torch.uint8, "q"),
+                       _dense(self.qt, (K, _up16(N)), torch.uint8, "qt"),
+                       _dense(self.blk, (_chunks(N), _chunks(K)), torch.float32, "blk"))
 
 
 def fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False):
     """E4M3 codes of x [M][K] and their scales: (q, s) by rows and / or (qt, st) by columns, None where not asked."""
     M, K = x.shape
     ld = _matrix(x, M, K, "x")
+    stream = _on_device(x, "x")
     dev = x.device
     q = torch.empty((M, _up16(K)), dtype=torch.uint8, device=dev) if rows else None
     s = torch.empty((_chunks(K), M), dtype=torch.float32, device=dev) if rows else None
     qt = torch.empty((K, _up16(M)), dtype=torch.uint8, device=dev) if cols else None
     st = torch.empty((_chunks(M), K), dtype=torch.float32, device=dev) if cols else None
-    _check(lib().moe_fp8_quantize(M, K, _p(x), _type(x), ld, _p(q), _p(s), _p(qt), _p(st), _stream()))
+    _check(lib().moe_fp8_quantize(M, K, x.data_ptr(), _type(x), ld, _p(q), _p(s), _p(qt), _p(st), stream))
     return q, s, qt, st
 
 
@@ -399,11 +427,13 @@ def fp8_weights(w: torch.Tensor) -> FP8Matrix:
     """E4M3 codes of a weight [N][K] (fp32 or bf16) in both orders, a scale for each 128x128 block."""
     N, K = w.shape
     ld = _matrix(w, N, K, "w")
+    stream = _on_device(w, "w")
     dev = w.device
     m = FP8Matrix(N, K, torch.empty((N, _up16(K)), dtype=torch.uint8, device=dev),
                   torch.empty((K, _up16(N)), dtype=torch.uint8, device=dev),
                   torch.empty((_chunks(N), _chunks(K)), dtype=torch.float32, device=dev))
-    _check(lib().moe_fp8_quantize_weights(N, K, _p(w), _type(w), ld, _p(m.q), _p(m.qt), _p(m.blk), _stream()))
+    _check(lib().moe_fp8_quantize_weights(N, K, w.data_ptr(), _type(w), ld, m.q.data_ptr(), m.qt.data_ptr(),
+                                          m.blk.data_ptr(), stream))
     return m
 
 
@@ -412,57 +442,67 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     """a [M][K] times b [N][K] transposed, E4M3 codes (K a multiple of 16) with scales a_scale [ceil(K/128)][M] and
     b_scale: [ceil(N/128)][ceil(K/128)] (any strides), or with ``rows`` [ceil(K/128)][N].  out: [M][N], bf16 by default."""
     (M, K), N = a.shape, b.shape[0]
+    stream = _on_device(a, "a")
     lda, ldb = _matrix(a, M, K, "a", torch.uint8), _matrix(b, N, K, "b", torch.uint8)
     n = _chunks(K)
-    _matrix(a_scale, n, M, "a_scale", torch.float32)
-    _require(a_scale.is_contiguous(), "a_scale must be contiguous")
+    sa = _dense(a_scale, (n, M), torch.float32, "a_scale")
     if rows:
-        _matrix(b_scale, n, N, "b_scale", torch.float32)
-        _require(b_scale.is_contiguous(), "b_scale must be contiguous")
+        sb, bs = _dense(b_scale, (n, N), torch.float32, "b_scale"), (0, 0)
     else:
         _require(b_scale.is_cuda and b_scale.shape == (_chunks(N), n) and b_scale.dtype == torch.float32,
                  f"b_scale must be float32 [{_chunks(N)}][{n}] on a GPU")
+        sb, bs = b_scale.data_ptr(), b_scale.stride()
     if out is None:
         _require(not accumulate, "accumulate needs out")
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     ldc = _matrix(out, M, N, "out")
-    bs = (0, 0) if rows else b_scale.stride()
     g = GemmC(M, N, K, SCALE_ROW if rows else SCALE_BLOCK, _type(out), 1 if accumulate else 0, lda, ldb, ldc, bs[0], bs[1])
-    _check(lib().moe_fp8_gemm(ctypes.byref(g), _p(a), _p(a_scale), _p(b), _p(b_scale), _p(out), _stream()))
+    _check(lib().moe_fp8_gemm(ctypes.byref(g), a.data_ptr(), sa, b.data_ptr(), sb, out.data_ptr(), stream))
     return out
+
+
+@functools.lru_cache(maxsize=4096)
+def moe_fp8_linear_workspace_bytes(M: int, N: int, K: int, backward: int) -> int:
+    return int(lib().moe_fp8_linear_workspace_bytes(M, N, K, backward))
 
 
 def fp8_linear(x: torch.Tensor, w: FP8Matrix, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = x W^T: x [M][K] bf16 or fp32, quantised by rows; y [M][N] (bf16 unless ``out`` says otherwise)."""
-    M = x.shape[0]
-    ldx = _matrix(x, M, w.K, "x")
+    M, N, K = x.shape[0], w.N, w.K
+    ldx = _matrix(x, M, K, "x")
+    stream = _on_device(x, "x")
+    dev = x.device
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.bfloat16, device=x.device)
-    ldy = _matrix(out, M, w.N, "out")
+        out, ldy, ty = torch.empty((M, N), dtype=torch.bfloat16, device=dev), N, TYPE_BF16
+    else:
+        ldy, ty = _matrix(out, M, N, "out"), _type(out)
     c = w.c()
-    n = lib().moe_fp8_linear_workspace_bytes(M, w.N, w.K, 0)
-    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
-    _check(lib().moe_fp8_linear(M, _p(x), _type(x), ldx, ctypes.byref(c), _p(out), _type(out), ldy, _p(ws), n, _stream()))
+    n = moe_fp8_linear_workspace_bytes(M, N, K, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib().moe_fp8_linear(M, x.data_ptr(), _type(x), ldx, ctypes.byref(c), out.data_ptr(), ty, ldy, ws.data_ptr(), n,
+                                stream))
     return out
 
 
 def fp8_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: FP8Matrix, dx: Optional[torch.Tensor] = None,
                         dw: Optional[torch.Tensor] = None, accumulate: bool = False):
     """Gradients of fp8_linear: (dx [M][K], dw [N][K]), bf16 unless given; accumulate adds to the given dw."""
-    M = x.shape[0]
-    ldx, lddy = _matrix(x, M, w.K, "x"), _matrix(dy, M, w.N, "dy")
+    M, N, K = x.shape[0], w.N, w.K
+    ldx, lddy = _matrix(x, M, K, "x"), _matrix(dy, M, N, "dy")
+    stream = _on_device(x, "x")
+    dev = x.device
     _require(dw is not None or not accumulate, "accumulate needs dw")
     if dx is None:
-        dx = torch.empty((M, w.K), dtype=torch.bfloat16, device=x.device)
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
     if dw is None:
-        dw = torch.empty((w.N, w.K), dtype=torch.bfloat16, device=x.device)
-    lddx, lddw = _matrix(dx, M, w.K, "dx"), _matrix(dw, w.N, w.K, "dw")
+        dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+    lddx, lddw = _matrix(dx, M, K, "dx"), _matrix(dw, N, K, "dw")
     c = w.c()
-    n = lib().moe_fp8_linear_workspace_bytes(M, w.N, w.K, 1)
-    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
-    _check(lib().moe_fp8_linear_backward(M, _p(x), _type(x), ldx, _p(dy), _type(dy), lddy, ctypes.byref(c), _p(dx),
-                                         _type(dx), lddx, _p(dw), _type(dw), lddw, 1 if accumulate else 0, _p(ws), n,
-                                         _stream()))
+    n = moe_fp8_linear_workspace_bytes(M, N, K, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib().moe_fp8_linear_backward(M, x.data_ptr(), _type(x), ldx, dy.data_ptr(), _type(dy), lddy, ctypes.byref(c),
+                                         dx.data_ptr(), _type(dx), lddx, dw.data_ptr(), _type(dw), lddw,
+                                         1 if accumulate else 0, ws.data_ptr(), n, stream))
     return dx, dw
 
 
@@ -470,22 +510,35 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     """Scales contiguous fp32 / bf16 gradients so that their joint norm is at most max_norm: in place, or into the
     tensors of ``out`` (same shapes and types).  Returns the norm before (fp32, on the GPU, no synchronisation)."""
     grads = list(grads)
-    outs = grads if out is None else list(out)
-    _require(len(outs) == len(grads), "out must match grads")
-    _require(len(grads) > 0, "no gradients")
+    n = len(grads)
+    _require(n > 0, "no gradients")
+    stream = _on_device(grads[0], "gradients")
     dev = grads[0].device
-    table = (TensorC * len(grads))()
-    for e, g, o in zip(table, grads, outs):
-        _require(g.is_cuda and g.device == dev and g.is_contiguous(), "gradients must be contiguous on one GPU")
-        if o is not g:
-            _require(o.device == dev and o.is_contiguous() and o.shape == g.shape and o.dtype == g.dtype,
-                     "out must match grads")
-        e.g, e.out, e.n, e.type = g.data_ptr(), o.data_ptr(), g.numel(), _type(g)
+    flat = []           # v4moe_tensor is four 64-bit words: g, out, n, type
+    for g in grads:
+        if g.device != dev or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous on one GPU")
+        p = g.data_ptr()
+        flat += (p, p, g.numel(), _type(g))
+    if out is not None:
+        out = list(out)
+        _require(len(out) == n, "out must match grads")
+        for g, o in zip(grads, out):
+            if o.dtype != g.dtype or o.shape != g.shape or o.device != dev or not o.is_contiguous():
+                raise ValueError("out must match grads")
+        flat[1::4] = [o.data_ptr() for o in out]
+    table = (ctypes.c_int64 * (4 * n))(*flat)
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    n = lib().moe_clip_workspace_bytes(len(grads))
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _check(lib().moe_clip_grads(len(grads), table, max_norm, _p(norm), _p(ws), n, _stream()))
+    size = _clip_workspace_bytes(n)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _check(lib().moe_clip_grads(n, ctypes.cast(table, ctypes.POINTER(TensorC)), max_norm, norm.data_ptr(), ws.data_ptr(),
+                                size, stream))
     return norm
+
+
+@functools.lru_cache(maxsize=1024)
+def _clip_workspace_bytes(count: int) -> int:
+    return int(lib().moe_clip_workspace_bytes(count))
 
 
 # ---- conveniences for callers holding host (numpy) weights ----------------------------------
