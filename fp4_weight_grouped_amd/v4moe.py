@@ -9,6 +9,7 @@ no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import dataclasses
 import functools
@@ -132,7 +133,7 @@ def lib():
                                               _i64, _i32, _vp, _sz, _vp]
         L.moe_clip_workspace_bytes.argtypes = [_i32]
         L.moe_clip_workspace_bytes.restype = _sz
-        L.moe_clip_grads.argtypes = [_i32, ctypes.POINTER(TensorC), _f32, _vp, _vp, _sz, _vp]
+        L.moe_clip_grads.argtypes = [_i32, _vp, _f32, _vp, _vp, _sz, _vp]
         L.moe_time_next_ffn.argtypes = [_vp, _vp]
         L.moe_time_next_ffn.restype = None
         for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
@@ -515,24 +516,27 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     stream = _on_device(grads[0], "gradients")
     dev = grads[0].device
     flat = []           # v4moe_tensor is four 64-bit words: g, out, n, type
-    for g in grads:
-        if g.device != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous on one GPU")
-        p = g.data_ptr()
-        flat += (p, p, g.numel(), _type(g))
-    if out is not None:
+    if out is None:
+        for g in grads:
+            if g.device != dev or not g.is_contiguous():
+                raise ValueError("gradients must be contiguous on one GPU")
+            p = g.data_ptr()
+            flat += (p, p, g.numel(), _type(g))
+    else:
         out = list(out)
         _require(len(out) == n, "out must match grads")
         for g, o in zip(grads, out):
-            if o.dtype != g.dtype or o.shape != g.shape or o.device != dev or not o.is_contiguous():
+            m = g.numel()
+            if g.device != dev or not g.is_contiguous():
+                raise ValueError("gradients must be contiguous on one GPU")
+            if o.dtype != g.dtype or o.numel() != m or o.device != dev or not o.is_contiguous():
                 raise ValueError("out must match grads")
-        flat[1::4] = [o.data_ptr() for o in out]
-    table = (ctypes.c_int64 * (4 * n))(*flat)
+            flat += (g.data_ptr(), o.data_ptr(), m, _type(g))
+    table = array.array("q", flat)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     size = _clip_workspace_bytes(n)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _check(lib().moe_clip_grads(n, ctypes.cast(table, ctypes.POINTER(TensorC)), max_norm, norm.data_ptr(), ws.data_ptr(),
-                                size, stream))
+    _check(lib().moe_clip_grads(n, table.buffer_info()[0], max_norm, norm.data_ptr(), ws.data_ptr(), size, stream))
     return norm
 
 
