@@ -246,15 +246,16 @@ namespace v4moe {
 
 bool device_ready() { return device_info() != nullptr; }
 
-// The layer forward on a given workspace (moe_layer_forward and
-// moe_layer_forward_noalloc).
+// The layer forward on a given workspace (moe_layer_forward,
+// moe_layer_forward_noalloc and, with mode kRouteGiven, moe_routed_forward:
+// topk_ids and topk_w are then inputs).
 int layer_forward_ws(
     const v4moe_dims* d, const uint16_t* x, const float* w_router, const float* bias, int32_t mode,
     const int64_t* token_ids, const v4moe_experts* w, int32_t* topk_ids, float* topk_w,
     int32_t* expert_offsets, uint16_t* out, void* workspace, size_t ws_bytes, void* stream)
 {
     if (!dims_ok(d)) return V4MOE_EDIMS;
-    if (mode != V4MOE_ROUTE_LEARNED && mode != V4MOE_ROUTE_HASH) return V4MOE_EDIMS;
+    if (mode != V4MOE_ROUTE_LEARNED && mode != V4MOE_ROUTE_HASH && mode != kRouteGiven) return V4MOE_EDIMS;
     if (!expert_offsets) return V4MOE_ENULL;
     if (d->T == 0) {
         // an empty batch: only the offsets (E+1 zeros) are written
@@ -282,7 +283,8 @@ int layer_forward_ws(
     // device code, same results).  Decode-sized batches: the router also
     // writes the FP8 dispatch payload.
     const bool fuse = perm_tiles_one_block(d->T, d->topk, d->E);
-    if (launch_route(d->T, d->H, d->E, d->topk, x, w_router, bias, mode, token_ids, topk_ids, topk_w,
+    if (mode != kRouteGiven &&
+        launch_route(d->T, d->H, d->E, d->topk, x, w_router, bias, mode, token_ids, topk_ids, topk_w,
                      reinterpret_cast<float*>(ws + L.z), s, xq, xs) != hipSuccess)
         return V4MOE_ELAUNCH;
     if (!route_writes_payload(d->T, d->H, d->E, mode) && launch_quant_x(d->T, d->H, x, xq, xs, s) != hipSuccess)
@@ -301,6 +303,142 @@ int layer_forward_ws(
     if (launch_combine(d->T, d->H, d->topk, y, topk_w, out, s) != hipSuccess) return V4MOE_ELAUNCH;
     return V4MOE_OK;
 }
+
+namespace {
+
+// The layer backward (moe_layer_backward and, with mode kRouteGiven and the
+// routing in given_ids and given_w, moe_routed_backward).
+int layer_backward(
+    const v4moe_dims* d, const uint16_t* x, const float* w_router, const float* bias, int32_t mode,
+    const int64_t* token_ids, const int32_t* given_ids, const float* given_w, const v4moe_experts* w, const uint8_t* wt_gu, const uint8_t* wt_d,
+    const uint16_t* dout, float* dx, float* dw, float* dWg, float* dWu, float* dWd, void* workspace,
+    size_t ws_bytes, void* stream)
+{
+    if (!dims_ok(d)) return V4MOE_EDIMS;
+    if (mode != V4MOE_ROUTE_LEARNED && mode != V4MOE_ROUTE_HASH && mode != kRouteGiven) return V4MOE_EDIMS;
+    if (!w || !wt_gu || !wt_d || !dWu || !dWd || !workspace || (gated(d) && !dWg)) return V4MOE_ENULL;
+    if ((gated(d) && !mat_ok(w->gate)) || !mat_ok(w->up) || !mat_ok(w->down)) return V4MOE_ENULL;
+    if (d->T > 0 && (!x || !dout || !dx || !dw || (mode == V4MOE_ROUTE_LEARNED && !w_router) ||
+                     (mode == kRouteGiven && (!given_ids || !given_w))))
+        return V4MOE_ENULL;
+    for (const void* p : {(const void*)x, (const void*)dout, (const void*)dx, (const void*)wt_gu, (const void*)wt_d,
+                          (const void*)dWu, (const void*)dWd, (const void*)dWg, (const void*)workspace})
+        if (p && !aligned16(p)) return V4MOE_EALIGN;
+    if (mode == V4MOE_ROUTE_LEARNED && d->T > 0 && !aligned16(w_router)) return V4MOE_EALIGN;
+    const BwdLayout B = bwd_layout(d);
+    if (ws_bytes < B.total) return V4MOE_EWORKSPACE;
+    DeviceInfo* di = device_info();
+    if (!di) return V4MOE_EDEVICE;
+    hipStream_t s = as_stream(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Layout& L = B.F;
+    const int T = d->T, H = d->H, I = d->I, E = d->E, k = d->topk, gI = B.gI;
+    auto at = [&](size_t off) { return ws + off; };
+    int32_t* own_ids = reinterpret_cast<int32_t*>(at(B.ids));
+    float* own_w = reinterpret_cast<float*>(at(B.w));
+    const int32_t* ids = mode == kRouteGiven ? given_ids : own_ids;
+    const float* wts = mode == kRouteGiven ? given_w : own_w;
+    int32_t* offsets = reinterpret_cast<int32_t*>(at(B.off));
+    uint8_t* xq = at(L.xq);
+    float* xs = reinterpret_cast<float*>(at(L.xs));
+    int32_t* sp = reinterpret_cast<int32_t*>(at(L.sorted_pair));
+    int32_t* pp = reinterpret_cast<int32_t*>(at(L.pair_pos));
+    int32_t* padoff = reinterpret_cast<int32_t*>(at(B.padoff));
+    if (T > 0) {
+        // the forward again, keeping what the backward needs (G, U; hq, hs; Y)
+        if (mode != kRouteGiven && launch_route(T, H, E, k, x, w_router, bias, mode, token_ids, own_ids, own_w,
+                                                reinterpret_cast<float*>(at(L.z)), s) != hipSuccess)
+            return V4MOE_ELAUNCH;
+        if (launch_quant_x(T, H, x, xq, xs, s) != hipSuccess) return V4MOE_ELAUNCH;
+        if (launch_permute(T, k, E, ids, offsets, sp, pp, reinterpret_cast<int32_t*>(at(L.hist)), s) != hipSuccess)
+            return V4MOE_ELAUNCH;
+        uint16_t* y = reinterpret_cast<uint16_t*>(at(L.y));
+        FfnArgs a = ffn_args(d, L, ws, xq, xs, offsets, sp, w, y);
+        a.g_out = gated(d) ? reinterpret_cast<float*>(at(B.g)) : nullptr;
+        a.u_out = reinterpret_cast<float*>(at(B.u));
+        int rc = run_ffn(d, L, a, ws, L.MT < 8, di, s);   // as in moe_layer_forward
+        if (rc) return rc;
+        uint16_t* dys = reinterpret_cast<uint16_t*>(at(B.dys));
+        if (launch_bwd_combine(T, H, k, dout, wts, y, pp, dys, dw, s) != hipSuccess) return V4MOE_ELAUNCH;
+        // m-tiles of B.bm rows over the experts' row segments
+        FfnArgs b = a;
+        b.ctrl = reinterpret_cast<int32_t*>(at(B.bctrl));
+        b.done1 = reinterpret_cast<int32_t*>(at(B.bdone1));
+        int32_t* bmte = reinterpret_cast<int32_t*>(at(B.bmt_expert));
+        int32_t* bmtr = reinterpret_cast<int32_t*>(at(B.bmt_row0));
+        if (launch_build_tiles(E, B.bm / 16, 1, 1, 0, 1, b, bmte, bmtr, nullptr, s) != hipSuccess)
+            return V4MOE_ELAUNCH;
+        BgemmArgs g{};
+        g.I = I; g.H = H; g.act = d->act;
+        g.mt_expert = bmte; g.mt_row0 = bmtr; g.ctrl = b.ctrl; g.offsets = offsets;
+        g.g = a.g_out; g.u = a.u_out;
+        uint16_t* dgu = reinterpret_cast<uint16_t*>(at(B.dgu));
+        g.dgu = dgu;
+        float* dxs = reinterpret_cast<float*>(at(B.dxs));
+        g.dxs = dxs;
+        // dh = Wd^T dY, activation derivative -> dG, dU
+        g.N = I; g.K = H; g.A = dys; g.lda = H; g.Bq = wt_d; g.ldb = H; g.b_expert = (size_t)I * H;
+        g.blk0 = w->down.blk;
+        if (launch_bgemm(BG_DGRAD2, B.bm, g, B.n_mt4, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+        // dx per row = [Wg Wu]^T [dG dU]
+        g.N = H; g.K = gI; g.A = dgu; g.lda = gI; g.Bq = wt_gu; g.ldb = gI; g.b_expert = (size_t)H * gI;
+        g.blk0 = gated(d) ? w->gate.blk : w->up.blk;
+        g.blk1 = w->up.blk;
+        if (launch_bgemm(BG_DGRAD1, B.bm, g, B.n_mt4, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+        if (launch_bwd_unpermute(T, H, k, pp, dxs, dx, s) != hipSuccess) return V4MOE_ELAUNCH;
+        // transposed operands of the weight gradients
+        if (launch_pad_offsets(E, offsets, padoff, s) != hipSuccess) return V4MOE_ELAUNCH;
+        const int P = T * k, maxc = P + 32 * E;
+        uint16_t* dyT = reinterpret_cast<uint16_t*>(at(B.dyT));
+        uint16_t* dguT = reinterpret_cast<uint16_t*>(at(B.dguT));
+        uint16_t* xT = reinterpret_cast<uint16_t*>(at(B.xT));
+        uint16_t* hT = reinterpret_cast<uint16_t*>(at(B.hT));
+        if (launch_bwd_transpose(0, H, E, k, maxc, offsets, padoff, sp, dys, nullptr, nullptr, 0, dyT, B.ldd, s) !=
+                hipSuccess ||
+            launch_bwd_transpose(0, gI, E, k, maxc, offsets, padoff, sp, dgu, nullptr, nullptr, 0, dguT, B.ldd, s) !=
+                hipSuccess ||
+            launch_bwd_transpose(1, H, E, k, maxc, offsets, padoff, sp, nullptr, xq, xs, H / 128, xT, B.ldd, s) !=
+                hipSuccess ||
+            launch_bwd_transpose(2, I, E, k, maxc, offsets, padoff, sp, nullptr, at(L.hq),
+                                 reinterpret_cast<const float*>(at(L.hs)), hs_stride(I), hT, B.ldd, s) != hipSuccess)
+            return V4MOE_ELAUNCH;
+        BgemmArgs wg{};
+        wg.offsets = offsets; wg.padoff = padoff;
+        wg.lda = wg.ldb = B.ldd;
+        // weight gradients: with the same batch rule as the dgrads' tiles
+        // (about 64 rows per expert or more), the kernel that holds B in registers
+        wg.M = H; wg.N = I; wg.A = dyT; wg.B = hT; wg.dW = dWd;
+        if (launch_bgemm(BG_WGRAD, B.bm, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+        wg.M = I; wg.N = H; wg.B = xT;
+        if (gated(d)) {
+            wg.A = dguT; wg.dW = dWg;
+            if (launch_bgemm(BG_WGRAD, B.bm, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+        }
+        wg.A = dguT + (gated(d) ? (size_t)I * B.ldd : 0); wg.dW = dWu;
+        if (launch_bgemm(BG_WGRAD, B.bm, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+    } else {
+        // no tokens: every weight gradient is zero
+        if (launch_fill_i32(offsets, 0, E + 1, s) != hipSuccess) return V4MOE_ELAUNCH;
+        if (launch_pad_offsets(E, offsets, padoff, s) != hipSuccess) return V4MOE_ELAUNCH;
+        uint16_t* dyT = reinterpret_cast<uint16_t*>(at(B.dyT));
+        BgemmArgs wg{};
+        wg.offsets = offsets; wg.padoff = padoff;
+        wg.lda = wg.ldb = B.ldd;
+        wg.A = dyT; wg.B = dyT;
+        wg.M = H; wg.N = I; wg.dW = dWd;
+        if (launch_bgemm(BG_WGRAD, 64, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+        wg.M = I; wg.N = H;
+        if (gated(d)) {
+            wg.dW = dWg;
+            if (launch_bgemm(BG_WGRAD, 64, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+        }
+        wg.dW = dWu;
+        if (launch_bgemm(BG_WGRAD, 64, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
+    }
+    return V4MOE_OK;
+}
+
+}  // namespace
 
 }  // namespace v4moe
 
@@ -426,6 +564,7 @@ __attribute__((visibility("default"))) int moe_layer_forward(
     const int64_t* token_ids, const v4moe_experts* w, int32_t* topk_ids, float* topk_w,
     int32_t* expert_offsets, uint16_t* out, void* workspace, size_t ws_bytes, void* stream)
 {
+    if (mode == kRouteGiven) return V4MOE_EDIMS;
     return v4moe::layer_forward_ws(d, x, w_router, bias, mode, token_ids, w, topk_ids, topk_w, expert_offsets, out,
                                    workspace, ws_bytes, stream);
 }
@@ -536,124 +675,29 @@ __attribute__((visibility("default"))) int moe_layer_backward(
     const uint16_t* dout, float* dx, float* dw, float* dWg, float* dWu, float* dWd, void* workspace,
     size_t ws_bytes, void* stream)
 {
-    if (!dims_ok(d)) return V4MOE_EDIMS;
-    if (mode != V4MOE_ROUTE_LEARNED && mode != V4MOE_ROUTE_HASH) return V4MOE_EDIMS;
-    if (!w || !wt_gu || !wt_d || !dWu || !dWd || !workspace || (gated(d) && !dWg)) return V4MOE_ENULL;
-    if ((gated(d) && !mat_ok(w->gate)) || !mat_ok(w->up) || !mat_ok(w->down)) return V4MOE_ENULL;
-    if (d->T > 0 && (!x || !dout || !dx || !dw || (mode == V4MOE_ROUTE_LEARNED && !w_router))) return V4MOE_ENULL;
-    for (const void* p : {(const void*)x, (const void*)dout, (const void*)dx, (const void*)wt_gu, (const void*)wt_d,
-                          (const void*)dWu, (const void*)dWd, (const void*)dWg, (const void*)workspace})
-        if (p && !aligned16(p)) return V4MOE_EALIGN;
-    if (mode == V4MOE_ROUTE_LEARNED && d->T > 0 && !aligned16(w_router)) return V4MOE_EALIGN;
-    const BwdLayout B = bwd_layout(d);
-    if (ws_bytes < B.total) return V4MOE_EWORKSPACE;
-    DeviceInfo* di = device_info();
-    if (!di) return V4MOE_EDEVICE;
-    hipStream_t s = as_stream(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const Layout& L = B.F;
-    const int T = d->T, H = d->H, I = d->I, E = d->E, k = d->topk, gI = B.gI;
-    auto at = [&](size_t off) { return ws + off; };
-    int32_t* ids = reinterpret_cast<int32_t*>(at(B.ids));
-    float* wts = reinterpret_cast<float*>(at(B.w));
-    int32_t* offsets = reinterpret_cast<int32_t*>(at(B.off));
-    uint8_t* xq = at(L.xq);
-    float* xs = reinterpret_cast<float*>(at(L.xs));
-    int32_t* sp = reinterpret_cast<int32_t*>(at(L.sorted_pair));
-    int32_t* pp = reinterpret_cast<int32_t*>(at(L.pair_pos));
-    int32_t* padoff = reinterpret_cast<int32_t*>(at(B.padoff));
-    if (T > 0) {
-        // the forward again, keeping what the backward needs (G, U; hq, hs; Y)
-        if (launch_route(T, H, E, k, x, w_router, bias, mode, token_ids, ids, wts,
-                         reinterpret_cast<float*>(at(L.z)), s) != hipSuccess)
-            return V4MOE_ELAUNCH;
-        if (launch_quant_x(T, H, x, xq, xs, s) != hipSuccess) return V4MOE_ELAUNCH;
-        if (launch_permute(T, k, E, ids, offsets, sp, pp, reinterpret_cast<int32_t*>(at(L.hist)), s) != hipSuccess)
-            return V4MOE_ELAUNCH;
-        uint16_t* y = reinterpret_cast<uint16_t*>(at(L.y));
-        FfnArgs a = ffn_args(d, L, ws, xq, xs, offsets, sp, w, y);
-        a.g_out = gated(d) ? reinterpret_cast<float*>(at(B.g)) : nullptr;
-        a.u_out = reinterpret_cast<float*>(at(B.u));
-        int rc = run_ffn(d, L, a, ws, L.MT < 8, di, s);   // as in moe_layer_forward
-        if (rc) return rc;
-        uint16_t* dys = reinterpret_cast<uint16_t*>(at(B.dys));
-        if (launch_bwd_combine(T, H, k, dout, wts, y, pp, dys, dw, s) != hipSuccess) return V4MOE_ELAUNCH;
-        // m-tiles of B.bm rows over the experts' row segments
-        FfnArgs b = a;
-        b.ctrl = reinterpret_cast<int32_t*>(at(B.bctrl));
-        b.done1 = reinterpret_cast<int32_t*>(at(B.bdone1));
-        int32_t* bmte = reinterpret_cast<int32_t*>(at(B.bmt_expert));
-        int32_t* bmtr = reinterpret_cast<int32_t*>(at(B.bmt_row0));
-        if (launch_build_tiles(E, B.bm / 16, 1, 1, 0, 1, b, bmte, bmtr, nullptr, s) != hipSuccess)
-            return V4MOE_ELAUNCH;
-        BgemmArgs g{};
-        g.I = I; g.H = H; g.act = d->act;
-        g.mt_expert = bmte; g.mt_row0 = bmtr; g.ctrl = b.ctrl; g.offsets = offsets;
-        g.g = a.g_out; g.u = a.u_out;
-        uint16_t* dgu = reinterpret_cast<uint16_t*>(at(B.dgu));
-        g.dgu = dgu;
-        float* dxs = reinterpret_cast<float*>(at(B.dxs));
-        g.dxs = dxs;
-        // dh = Wd^T dY, activation derivative -> dG, dU
-        g.N = I; g.K = H; g.A = dys; g.lda = H; g.Bq = wt_d; g.ldb = H; g.b_expert = (size_t)I * H;
-        g.blk0 = w->down.blk;
-        if (launch_bgemm(BG_DGRAD2, B.bm, g, B.n_mt4, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-        // dx per row = [Wg Wu]^T [dG dU]
-        g.N = H; g.K = gI; g.A = dgu; g.lda = gI; g.Bq = wt_gu; g.ldb = gI; g.b_expert = (size_t)H * gI;
-        g.blk0 = gated(d) ? w->gate.blk : w->up.blk;
-        g.blk1 = w->up.blk;
-        if (launch_bgemm(BG_DGRAD1, B.bm, g, B.n_mt4, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-        if (launch_bwd_unpermute(T, H, k, pp, dxs, dx, s) != hipSuccess) return V4MOE_ELAUNCH;
-        // transposed operands of the weight gradients
-        if (launch_pad_offsets(E, offsets, padoff, s) != hipSuccess) return V4MOE_ELAUNCH;
-        const int P = T * k, maxc = P + 32 * E;
-        uint16_t* dyT = reinterpret_cast<uint16_t*>(at(B.dyT));
-        uint16_t* dguT = reinterpret_cast<uint16_t*>(at(B.dguT));
-        uint16_t* xT = reinterpret_cast<uint16_t*>(at(B.xT));
-        uint16_t* hT = reinterpret_cast<uint16_t*>(at(B.hT));
-        if (launch_bwd_transpose(0, H, E, k, maxc, offsets, padoff, sp, dys, nullptr, nullptr, 0, dyT, B.ldd, s) !=
-                hipSuccess ||
-            launch_bwd_transpose(0, gI, E, k, maxc, offsets, padoff, sp, dgu, nullptr, nullptr, 0, dguT, B.ldd, s) !=
-                hipSuccess ||
-            launch_bwd_transpose(1, H, E, k, maxc, offsets, padoff, sp, nullptr, xq, xs, H / 128, xT, B.ldd, s) !=
-                hipSuccess ||
-            launch_bwd_transpose(2, I, E, k, maxc, offsets, padoff, sp, nullptr, at(L.hq),
-                                 reinterpret_cast<const float*>(at(L.hs)), hs_stride(I), hT, B.ldd, s) != hipSuccess)
-            return V4MOE_ELAUNCH;
-        BgemmArgs wg{};
-        wg.offsets = offsets; wg.padoff = padoff;
-        wg.lda = wg.ldb = B.ldd;
-        // weight gradients: with the same batch rule as the dgrads' tiles
-        // (about 64 rows per expert or more), the kernel that holds B in registers
-        wg.M = H; wg.N = I; wg.A = dyT; wg.B = hT; wg.dW = dWd;
-        if (launch_bgemm(BG_WGRAD, B.bm, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-        wg.M = I; wg.N = H; wg.B = xT;
-        if (gated(d)) {
-            wg.A = dguT; wg.dW = dWg;
-            if (launch_bgemm(BG_WGRAD, B.bm, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-        }
-        wg.A = dguT + (gated(d) ? (size_t)I * B.ldd : 0); wg.dW = dWu;
-        if (launch_bgemm(BG_WGRAD, B.bm, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-    } else {
-        // no tokens: every weight gradient is zero
-        if (launch_fill_i32(offsets, 0, E + 1, s) != hipSuccess) return V4MOE_ELAUNCH;
-        if (launch_pad_offsets(E, offsets, padoff, s) != hipSuccess) return V4MOE_ELAUNCH;
-        uint16_t* dyT = reinterpret_cast<uint16_t*>(at(B.dyT));
-        BgemmArgs wg{};
-        wg.offsets = offsets; wg.padoff = padoff;
-        wg.lda = wg.ldb = B.ldd;
-        wg.A = dyT; wg.B = dyT;
-        wg.M = H; wg.N = I; wg.dW = dWd;
-        if (launch_bgemm(BG_WGRAD, 64, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-        wg.M = I; wg.N = H;
-        if (gated(d)) {
-            wg.dW = dWg;
-            if (launch_bgemm(BG_WGRAD, 64, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-        }
-        wg.dW = dWu;
-        if (launch_bgemm(BG_WGRAD, 64, wg, 0, E, s) != hipSuccess) return V4MOE_ELAUNCH;
-    }
-    return V4MOE_OK;
+    if (mode == kRouteGiven) return V4MOE_EDIMS;
+    return layer_backward(d, x, w_router, bias, mode, token_ids, nullptr, nullptr, w, wt_gu, wt_d, dout, dx, dw, dWg, dWu,
+                          dWd, workspace, ws_bytes, stream);
+}
+
+__attribute__((visibility("default"))) int moe_routed_forward(const v4moe_dims* d, const uint16_t* x,
+                                                              const int32_t* topk_ids, const float* topk_w,
+                                                              const v4moe_experts* w, int32_t* expert_offsets,
+                                                              uint16_t* out, void* workspace, size_t ws_bytes,
+                                                              void* stream)
+{
+    // (with the routing given, the layer only reads it)
+    return v4moe::layer_forward_ws(d, x, nullptr, nullptr, kRouteGiven, nullptr, w, const_cast<int32_t*>(topk_ids),
+                                   const_cast<float*>(topk_w), expert_offsets, out, workspace, ws_bytes, stream);
+}
+
+__attribute__((visibility("default"))) int moe_routed_backward(
+    const v4moe_dims* d, const uint16_t* x, const int32_t* topk_ids, const float* topk_w, const v4moe_experts* w,
+    const uint8_t* wt_gu, const uint8_t* wt_d, const uint16_t* dout, float* dx, float* dw, float* dWg, float* dWu,
+    float* dWd, void* workspace, size_t ws_bytes, void* stream)
+{
+    return layer_backward(d, x, nullptr, nullptr, kRouteGiven, nullptr, topk_ids, topk_w, w, wt_gu, wt_d, dout, dx, dw,
+                          dWg, dWu, dWd, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

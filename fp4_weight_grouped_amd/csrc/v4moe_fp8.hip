@@ -146,6 +146,7 @@ struct Raw {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[u >> 2][u & 3]);
         else return __uint_as_float(u & 1 ? w[0][u >> 1] & 0xFFFF0000u : w[0][u >> 1] << 16);
     }
+    // the compiler takes the words for new ones
     __device__ __forceinline__ void forget()
     {
 #pragma unroll
@@ -168,33 +169,35 @@ struct Raw {
 };
 
 // One 128x128 tile of x [R][C] per block, read once for both orders: thread t
-// holds rows 8(t/16) .. +7, columns 8(t%16) .. +7 as they are in memory.  Bound by
-// its own latency and VALU work next to HBM: 8192x4096 bf16 by columns 28 us
-// (3.6 TB/s), 8192x2048 in both orders 27 us, 16384x4096 fp32 weights 87 us (4.6
-// TB/s).  What it is sensitive to is the blocks per CU (five): with the elements
-// kept as floats (three blocks) 32 / 35 us, with the next tile's loads out a
-// tile ahead (two) 34 / 34 us; without the residual corrections, or with the
-// stores of qt in one stretch of memory, 30 / 29 us at two blocks.
+// holds rows 4(t/16) .. +3, columns 8(t%16) .. +7 as they are in memory.  Bound by
+// the tile's own latency and VALU work beside HBM: 8192x4096 bf16 by columns 25 us
+// (4.0 TB/s), 8192x2048 in both orders 27 us, 16384x4096 fp32 weights 84 us (4.8
+// TB/s).  Waves per CU are what helps: eight rows per thread (five blocks of four
+// waves) took 28 / 27 / 87 us, with the elements kept as floats (three blocks)
+// 32 / 35, with the next tile's loads out a tile ahead (two blocks) 34 / 34;
+// without the residual corrections, or with the stores of qt in one stretch, the
+// last took 30 / 29.
 //   ROWS: q [R][ldq], s [ceil(C/128)][R]: groups of 128 columns of a row
 //   COLS: qt [C][ldqt], st [ceil(R/128)][C]: groups of 128 rows of a column
 //   BLOCK: q, qt, s [ceil(R/128)][ceil(C/128)]: one group per tile
 // Rows of q are written up to C rounded up to 16, zeros past C (qt likewise).
 enum { kQuantRows = 1, kQuantCols = 2, kQuantBlock = 4 };
 template <typename T, int MODE>
-__global__ __launch_bounds__(256) void k_fp8_quant(int R, int C, const T* __restrict__ x, int64_t ldx,
+__global__ __launch_bounds__(512) void k_fp8_quant(int R, int C, const T* __restrict__ x, int64_t ldx,
                                                    uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s,
                                                    uint8_t* __restrict__ qt, int64_t ldqt, float* __restrict__ st)
 {
-    __shared__ __align__(16) uint32_t mx[4][128];
+    constexpr int NR = 4, NW = 8;                      // rows per thread, waves
+    __shared__ __align__(16) uint32_t mx[NW][128];
     __shared__ __align__(16) uint8_t tq[128 * 128];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int rt = 8 * (t >> 4), ct = 8 * (t & 15);
+    const int rt = NR * (t >> 4), ct = 8 * (t & 15);
     const int cpad = (C + 15) / 16 * 16, rpad = (R + 15) / 16 * 16;
     const int nx = (C + 127) / 128;
     const int tile = blockIdx.x, by = tile / nx, bx = tile % nx, r0 = by * 128, c0 = bx * 128;
-    Raw<T> f[8];
+    Raw<T> f[NR];
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+    for (int i = 0; i < NR; i++)
         f[i].load(x + (int64_t)min(r0 + rt + i, R - 1) * ldx + min(c0 + ct, C - 1), r0 + rt + i < R ? C - c0 - ct : 0);
     auto store_row = [&](int i, const Divisor& d) {
         if (r0 + rt + i < R && c0 + ct < cpad)
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(256) void k_fp8_quant(int R, int C, const T* __rest
     };
     if constexpr (MODE & kQuantRows) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < NR; i++) {
             uint32_t m = 0;
 #pragma unroll
             for (int u = 0; u < 8; u++) m = max(m, mag_bits(f[i][u]));
@@ -213,14 +216,14 @@ __global__ __launch_bounds__(256) void k_fp8_quant(int R, int C, const T* __rest
         }
     }
     uint32_t m[8];
-    // (the columns convert the elements again: kept as floats from the rows, twice the registers would halve the blocks per CU)
+    // (the columns convert the elements anew: kept as floats they would cost two blocks of the CU's four)
 #pragma unroll
-    for (int i = 0; i < 8; i++) f[i].forget();
+    for (int i = 0; i < NR; i++) f[i].forget();
 #pragma unroll
     for (int u = 0; u < 8; u++) {
         m[u] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; i++) m[u] = max(m[u], mag_bits(f[i][u]));
+        for (int i = 0; i < NR; i++) m[u] = max(m[u], mag_bits(f[i][u]));
         m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 16));
         m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 32));
     }
@@ -229,36 +232,52 @@ __global__ __launch_bounds__(256) void k_fp8_quant(int R, int C, const T* __rest
         *reinterpret_cast<uint4*>(&mx[wave][ct + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
     }
     __syncthreads();
+    auto column = [&](int c) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < NW; i++) v = max(v, mx[i][c]);
+        return v;
+    };
     uint32_t all = 0;
     if constexpr (MODE & kQuantBlock) {
-        all = max(max(mx[0][lane], mx[1][lane]), max(mx[2][lane], mx[3][lane]));
-        all = max(all, max(max(mx[0][64 + lane], mx[1][64 + lane]), max(mx[2][64 + lane], mx[3][64 + lane])));
+        all = max(column(lane), column(64 + lane));
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) all = max(all, (uint32_t)__shfl_xor((int)all, o));
         const Divisor d(group_scale(all));
         if (t == 0) s[tile] = d.s;
 #pragma unroll
-        for (int i = 0; i < 8; i++) store_row(i, d);
+        for (int i = 0; i < NR; i++) store_row(i, d);
+    } else {
+        // each column's maximum once, by one thread
+        if (t < 128) {
+            const uint32_t v = column(t);
+            mx[0][t] = v;
+            if (c0 + t < C) st[(int64_t)by * C + c0 + t] = group_scale(v);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint4 v = *reinterpret_cast<const uint4*>(&mx[0][ct + 4 * h]);
+            m[4 * h] = v.x; m[4 * h + 1] = v.y; m[4 * h + 2] = v.z; m[4 * h + 3] = v.w;
+        }
     }
-    // The codes transposed through LDS: column c's row holds sixteen units of
-    // eight rows, XORed by c/8, so that the sixteen columns a store covers lie
-    // in different banks; then 16-byte stores along the rows of qt.
+    // The codes transposed through LDS: column c's 128 bytes, their 16-byte
+    // segments XORed by c/8 so that the columns a store covers spread over the
+    // banks; then 16-byte stores along the rows of qt.
 #pragma unroll
     for (int u = 0; u < 8; u++) {
-        const int c = ct + u;
-        const Divisor d(group_scale(MODE & kQuantBlock ? all : max(max(mx[0][c], mx[1][c]), max(mx[2][c], mx[3][c]))));
-        if ((MODE & kQuantCols) && wave == 0 && lane < 16 && c0 + c < C) st[(int64_t)by * C + c0 + c] = d.s;
-        *reinterpret_cast<uint2*>(tq + c * 128 + ((t >> 4) ^ (t & 15)) * 8) =
-            make_uint2(d.codes4(f[0][u], f[1][u], f[2][u], f[3][u]), d.codes4(f[4][u], f[5][u], f[6][u], f[7][u]));
+        const int c = ct + u, r4 = t >> 4;
+        const Divisor d(group_scale(MODE & kQuantBlock ? all : m[u]));
+        *reinterpret_cast<uint32_t*>(tq + c * 128 + (((r4 >> 2) ^ (c >> 3 & 7)) * 16) + (r4 & 3) * 4) =
+            d.codes4(f[0][u], f[1][u], f[2][u], f[3][u]);
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int p = i * 256 + t, c = p >> 3, seg = p & 7, x8 = c >> 3;
-        uint4 v = *reinterpret_cast<const uint4*>(tq + c * 128 + (seg ^ (x8 >> 1)) * 16);
-        if (x8 & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+    for (int i = 0; i < 2; i++) {
+        const int p = i * 512 + t, c = p >> 3, seg = p & 7;
         if (c0 + c < C && r0 + 16 * seg < rpad)
-            *reinterpret_cast<uint4*>(qt + (int64_t)(c0 + c) * ldqt + r0 + 16 * seg) = v;
+            *reinterpret_cast<uint4*>(qt + (int64_t)(c0 + c) * ldqt + r0 + 16 * seg) =
+                *reinterpret_cast<const uint4*>(tq + c * 128 + ((seg ^ (c >> 3 & 7)) * 16));
     }
 }
 
@@ -751,7 +770,7 @@ hipError_t launch_quant(int mode, int R, int C, const T* x, int64_t ldx, uint8_t
     const int64_t tiles = chunks(C) * chunks(R);
     const dim3 grid((unsigned)tiles);
     auto run = [&](auto m) {
-        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), grid, dim3(256), 0, stream, R, C, x, ldx, q, ldq, s, qt, ldqt,
+        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), grid, dim3(512), 0, stream, R, C, x, ldx, q, ldq, s, qt, ldqt,
                            st);
     };
     switch (mode) {

@@ -136,7 +136,10 @@ void* noalloc_scratch(int dev);
 // Device set-up of the library (gfx950 check, occupancy, scratch address) for
 // the current device; false if the device is unusable.
 bool device_ready();
-// moe_layer_forward on the given workspace (both layer-forward entry points).
+// Routing mode of the entry points that take the routing from the caller (not
+// one a caller passes).
+constexpr int32_t kRouteGiven = -1;
+// moe_layer_forward on the given workspace (the layer-forward entry points).
 int layer_forward_ws(const v4moe_dims* d, const uint16_t* x, const float* w_router, const float* bias,
                      int32_t mode, const int64_t* token_ids, const v4moe_experts* w, int32_t* topk_ids,
                      float* topk_w, int32_t* expert_offsets, uint16_t* out, void* workspace, size_t ws_bytes,

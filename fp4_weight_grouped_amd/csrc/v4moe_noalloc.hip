@@ -48,7 +48,7 @@ __attribute__((visibility("default"))) int moe_layer_forward_noalloc(
     int32_t* expert_offsets, uint16_t* out, void* stream)
 {
     const size_t need = moe_workspace_bytes(d);
-    if (need == 0) return V4MOE_EDIMS;
+    if (need == 0 || mode == v4moe::kRouteGiven) return V4MOE_EDIMS;
     if (need > v4moe::kScratchBytes) return V4MOE_EWORKSPACE;
     if (!v4moe::device_ready()) return V4MOE_EDEVICE;
     int dev = -1;

@@ -134,12 +134,15 @@ def lib():
         L.moe_clip_workspace_bytes.argtypes = [_i32]
         L.moe_clip_workspace_bytes.restype = _sz
         L.moe_clip_grads.argtypes = [_i32, _vp, _f32, _vp, _vp, _sz, _vp]
+        EP = ctypes.POINTER(ExpertsC)
+        L.moe_routed_forward.argtypes = [_DP, _vp, _vp, _vp, EP, _vp, _vp, _vp, _sz, _vp]
+        L.moe_routed_backward.argtypes = [_DP, _vp, _vp, _vp, EP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
         L.moe_time_next_ffn.argtypes = [_vp, _vp]
         L.moe_time_next_ffn.restype = None
         for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
                   "moe_layer_forward_noalloc",
                   "moe_prepack_weights", "moe_dequant_fp8", "moe_quantize_weights", "moe_transpose_weights",
-                  "moe_layer_backward", "moe_gate", "moe_gate_backward", "moe_fp8_quantize",
+                  "moe_layer_backward", "moe_routed_forward", "moe_routed_backward", "moe_gate", "moe_gate_backward", "moe_fp8_quantize",
                   "moe_fp8_quantize_weights", "moe_fp8_gemm", "moe_fp8_linear", "moe_fp8_linear_backward",
                   "moe_clip_grads"):
             getattr(L, f).restype = ctypes.c_int
@@ -289,6 +292,20 @@ def moe_layer_backward(d: Dims, x, w_router, bias, mode, token_ids, experts: Dev
     _check(lib().moe_layer_backward(ctypes.byref(d), _p(x), _p(w_router), _p(bias), mode, _p(token_ids),
                                     ctypes.byref(ex), _p(wt_gu), _p(wt_d), _p(dout), _p(dx), _p(dw), _p(dWg),
                                     _p(dWu), _p(dWd), _p(workspace), workspace.numel(), _stream()))
+
+
+def moe_routed_forward(d: Dims, x, topk_ids, topk_w, experts: DeviceExperts, expert_offsets, out, workspace):
+    ex = experts.c()
+    _check(lib().moe_routed_forward(ctypes.byref(d), _p(x), _p(topk_ids), _p(topk_w), ctypes.byref(ex),
+                                    _p(expert_offsets), _p(out), _p(workspace), workspace.numel(), _stream()))
+
+
+def moe_routed_backward(d: Dims, x, topk_ids, topk_w, experts: DeviceExperts, wt_gu, wt_d, dout, dx, dw, dWg, dWu, dWd,
+                        workspace):
+    ex = experts.c()
+    _check(lib().moe_routed_backward(ctypes.byref(d), _p(x), _p(topk_ids), _p(topk_w), ctypes.byref(ex), _p(wt_gu),
+                                     _p(wt_d), _p(dout), _p(dx), _p(dw), _p(dWg), _p(dWu), _p(dWd), _p(workspace),
+                                     workspace.numel(), _stream()))
 
 
 def moe_time_next_ffn(start_event, stop_event):
@@ -609,6 +626,11 @@ class MoELayer:
                           self.workspace(T))
         return out, ids, w, off
 
+    def set_experts(self, experts: DeviceExperts):
+        """Another version of the (packed) expert weights, e.g. after an optimizer step."""
+        self.experts = experts
+        self._wt = None
+
     def transposed_weights(self):
         """The transposed FP8 weight values (E4M3 bytes) the backward reads (made once)."""
         if getattr(self, "_wt", None) is None:
@@ -625,21 +647,45 @@ class MoELayer:
         """Gradients of sum(dout * out): dict(dx [T][H], dw [T][k], dWg / dWu [E][I][H], dWd [E][H][I])
         (fp32; dWg absent gate-less).  ``grads`` may hold preallocated outputs."""
         T = x.shape[0]
-        d = self.dims(T)
+        d, g = self.dims(T), grads or self._gradients(T)
+        wt_gu, wt_d = self.transposed_weights()
+        moe_layer_backward(d, x, self.w_router, bias, mode, token_ids, self.experts, wt_gu, wt_d, dout,
+                           g["dx"], g["dw"], g.get("dWg"), g["dWu"], g["dWd"], self._backward_workspace(d))
+        return g
+
+    def _gradients(self, T: int):
         dev = self.device
         gated = self.act == ACT_SWIGLU
-        g = grads or dict(
+        return dict(
             dx=torch.empty((T, self.H), dtype=torch.float32, device=dev),
             dw=torch.empty((T, self.topk), dtype=torch.float32, device=dev),
             dWu=torch.empty((self.E, self.I, self.H), dtype=torch.float32, device=dev),
             dWd=torch.empty((self.E, self.H, self.I), dtype=torch.float32, device=dev),
             **({"dWg": torch.empty((self.E, self.I, self.H), dtype=torch.float32, device=dev)} if gated else {}))
+
+    def _backward_workspace(self, d: Dims):
         n = moe_backward_workspace_bytes(d)
         if getattr(self, "_bws", None) is None or self._bws.numel() < n:
-            self._bws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+            self._bws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+        return self._bws
+
+    def forward_routed(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, out=None):
+        """The layer with the routing given (gate()'s outputs).  Returns (out bf16 bits [T][H], expert_offsets)."""
+        T = x.shape[0]
+        off = torch.empty(self.E + 1, dtype=torch.int32, device=self.device)
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.int16, device=self.device)
+        moe_routed_forward(self.dims(T), x, topk_ids, topk_w, self.experts, off, out, self.workspace(T))
+        return out, off
+
+    def backward_routed(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, dout: torch.Tensor,
+                        grads=None):
+        """backward() with the routing given; its dw is what gate_backward() takes."""
+        T = x.shape[0]
+        d, g = self.dims(T), grads or self._gradients(T)
         wt_gu, wt_d = self.transposed_weights()
-        moe_layer_backward(d, x, self.w_router, bias, mode, token_ids, self.experts, wt_gu, wt_d, dout,
-                           g["dx"], g["dw"], g.get("dWg"), g["dWu"], g["dWd"], self._bws)
+        moe_routed_backward(d, x, topk_ids, topk_w, self.experts, wt_gu, wt_d, dout, g["dx"], g["dw"], g.get("dWg"),
+                            g["dWu"], g["dWd"], self._backward_workspace(d))
         return g
 
     def forward_unfused(self, x: torch.Tensor, bias=None, mode=ROUTE_LEARNED, token_ids=None):

@@ -357,6 +357,18 @@ int moe_gate_backward(const v4moe_gate* g, const void* logits, int32_t type, int
                       const int32_t* topk_ids, const float* topk_w, const float* dw, void* dlogits,
                       int64_t ldd, void* stream);
 
+/* moe_layer_forward and moe_layer_backward with the routing given (moe_gate's
+ * outputs: topk_ids int32 [T][topk], distinct per token and in [0, E); topk_w fp32
+ * [T][topk], any values) instead of computed from x.  Same kernels, workspaces
+ * (moe_workspace_bytes, moe_backward_workspace_bytes) and results as with that routing. */
+int moe_routed_forward(const v4moe_dims* d, const uint16_t* x, const int32_t* topk_ids,
+                       const float* topk_w, const v4moe_experts* w, int32_t* expert_offsets,
+                       uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
+int moe_routed_backward(const v4moe_dims* d, const uint16_t* x, const int32_t* topk_ids,
+                        const float* topk_w, const v4moe_experts* w, const uint8_t* wt_gu,
+                        const uint8_t* wt_d, const uint16_t* dout, float* dx, float* dw, float* dWg,
+                        float* dWu, float* dWd, void* workspace, size_t ws_bytes, void* stream);
+
 /* E4M3 codes of x [M][K] (fp32 or bf16) with an fp32 scale for each group of
  * 128: s = fp32(amax / 448) (1 where that is 0), code = E4M3(fp32(x / s)),
  * nearest even, saturating.  A group holding an infinity or NaN gets scale NaN and
