@@ -23,6 +23,15 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
+@pytest.fixture(autouse=True)
+def _float32():
+    """Other modules set another default type when they are collected."""
+    old = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(old)
+
+
 def up(n, m):
     return (n + m - 1) // m * m
 
