@@ -306,7 +306,7 @@ __device__ __forceinline__ v4f mfma_e4m3(v8i w, v8i x)
 // 16 rows): a lane's four columns become 16-byte stores along the rows, whole
 // lines where a row's part is one (straight from the registers the stores cost
 // 22 us of 139 at 8192 x 4096).  16-byte segments XOR-swizzled by the row.
-template <int MI, int NI, typename T>
+template <bool STREAM, int MI, int NI, typename T>
 __device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* stage, T* __restrict__ c, const GemmArgs& g,
                                            int m0, int n0)
 {
@@ -334,7 +334,9 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* st
             if (m >= g.M || n >= g.N) continue;
             T* o = c + (int64_t)m * g.ldc + n;
             if (n + PER <= g.N && !g.accumulate) {
-                *reinterpret_cast<v4u_any*>(o) = v4u{v.x, v.y, v.z, v.w};
+                const v4u w4 = {v.x, v.y, v.z, v.w};
+                if (STREAM) __builtin_nontemporal_store(w4, reinterpret_cast<v4u_any*>(o));
+                else *reinterpret_cast<v4u_any*>(o) = w4;
                 continue;
             }
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -558,8 +560,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
     __syncthreads();   // every wave is done with the ring: it becomes staging space
     uint8_t* stage = smem + wave * (2 * 16 * NI * 16 * 4);
     const int mw = m0 + wm * MI * 16, nw = n0 + wn * NI * 16;
-    if (g.c_bf16) store_tile<MI, NI>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
-    else store_tile<MI, NI>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
+    constexpr bool STREAM = L::BM * L::BN >= 128 * 128;
+    if (g.c_bf16) store_tile<STREAM, MI, NI>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
+    else store_tile<STREAM, MI, NI>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
 }
 
 // Few rows: the chunks of a tile of (16 MT) x (16 NT) are spread over the NW
