@@ -132,12 +132,6 @@ __device__ __forceinline__ void dma16(const void* g, uint32_t lds_base)
                  :: "v"(g), "s"(lds_base) : "memory", "m0");
 }
 
-__device__ __forceinline__ void dma4(const void* g, uint32_t lds_base)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
-                 :: "v"(g), "s"(lds_base) : "memory", "m0");
-}
-
 // Direct-to-LDS copies: each lane moves 16 (or 4) bytes from its own global
 // address to lds_base + lane*16 (lane*4); lds_base is wave-uniform (M0).  As
 // inline asm they are invisible to the compiler's wait insertion, which would

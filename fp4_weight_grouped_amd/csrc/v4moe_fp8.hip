@@ -355,19 +355,19 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* st
     }
 }
 
-template <int WM, int WN, int MI, int NI, int NS, bool ROWS>
+template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
 struct GemmTile {
     static constexpr int NW = WM * WN, BM = WM * MI * 16, BN = WN * NI * 16;
     static constexpr int AJ = (BM / 8 + NW - 1) / NW, BJ = (BN / 8 + NW - 1) / NW;    // 1 KiB pieces per wave
     static constexpr int AS = (BM + 63) / 64, BS = ROWS ? (BN + 63) / 64 : 0;         // 64-scale pieces
     static constexpr int SJ = (AS + BS + NW - 1) / NW;
-    static constexpr int OPS = AJ + BJ + SJ;                                           // copies per wave and stage
+    static constexpr int OPS = AJ + BJ + SJ;                                           // copies per wave and chunk
     static constexpr int A_OFF = 0, B_OFF = BM * 128, S_OFF = B_OFF + BN * 128;
-    static constexpr int STAGE = S_OFF + (AS + BS) * 256;
+    static constexpr int CHUNK = S_OFF + (AS + BS) * 256, STAGE = KC * CHUNK;
     static constexpr int BYTES = NS * STAGE;
     static_assert(NW * 2 * 16 * NI * 16 * 4 <= BYTES, "staging of C fits the ring");
     static_assert(NW > 1, "the barrier, not only the order of one wave, frees a slot");
-    static_assert(OPS * (NS - 1) < 64 && NS >= 2, "vmcnt range");
+    static_assert(OPS * KC * (NS - 1) < 64 && NS >= 2, "vmcnt range");
     static_assert(NI * 16 <= 128 && 128 % (NI * 16) == 0, "a wave's rows of B lie in one 128-row block");
 };
 
@@ -385,13 +385,13 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& 
 }
 
 // A tile of C per block: WM x WN waves, each with MI x NI tiles of 16x16.
-// Operand rows are staged in LDS, a chunk of 128 per stage, by direct-to-LDS
-// copies NS-1 stages ahead; 16-byte segments are XOR-swizzled by (row/2)%8, so
+// Operand rows are staged in LDS, KC chunks of 128 per stage (and barrier), by
+// direct-to-LDS copies NS-1 stages ahead; 16-byte segments are XOR-swizzled by (row/2)%8, so
 // the 16 rows of an operand read hit distinct banks.
-template <int WM, int WN, int MI, int NI, int NS, bool ROWS>
+template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
 __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles_m, int tiles_n)
 {
-    using L = GemmTile<WM, WN, MI, NI, NS, ROWS>;
+    using L = GemmTile<WM, WN, MI, NI, NS, KC, ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int tm, tn;
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
     }
     // this wave's copies of chunk c into the slot of chunk `at`; tail: the last, shorter chunk, zeros past its end
     auto issue = [&](int at, int c, auto tail) {
-        const uint32_t slot = lds0 + (uint32_t)(at % NS) * L::STAGE;
+        const uint32_t slot = lds0 + (uint32_t)(at / KC % NS) * L::STAGE + (uint32_t)(at % KC) * L::CHUNK;
         const uint8_t *ac = abase + (int64_t)c * 128, *bc = bbase + (int64_t)c * 128;
         auto copy = [&](const uint8_t* base, uint32_t off, int p, uint32_t to) {
             const uint32_t dst = __builtin_amdgcn_readfirstlane(to);
@@ -470,14 +470,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
         const uint4 y = *reinterpret_cast<const uint4*>(st + hi + tile * 2048);
         return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
     };
-    v8i af[2], bf[NI];
+    // Small wave tiles have all of a chunk's operands in registers, large ones two row tiles of A.
+    constexpr bool SMALL = MI * NI <= 4;
+    v8i af[SMALL && MI > 2 ? MI : 2], bf[NI];
     float sa[MI], bs = 1.0f;
     float4 br[ROWS ? NI : 1];
     v4f p[NI];
     // operands that every step of chunk c needs, and its first row tile
     auto open = [&](int c) {
-        const uint8_t* st = smem + (c % NS) * L::STAGE;
-        af[0] = frag(st, alo, ahi, 0);
+        const uint8_t* st = smem + (c / KC % NS) * L::STAGE + (c % KC) * L::CHUNK;
+#pragma unroll
+        for (int i = 0; i < (SMALL ? MI : 1); i++) af[i] = frag(st, alo, ahi, i);
 #pragma unroll
         for (int j = 0; j < NI; j++) bf[j] = frag(st, blo, bhi, j);
 #pragma unroll
@@ -491,22 +494,47 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
             bs_next = bsp[min(c + 1, nch - 1) * g.bs_k];
         }
     };
-    auto add = [&](int i, int j, float s, float4 r) {
+    auto add_to = [&](v4f& a, const v4f& v, float s, float4 r) {
         if constexpr (ROWS) {
-            acc[i][j][0] = fmaf(s * r.x, p[j][0], acc[i][j][0]);
-            acc[i][j][1] = fmaf(s * r.y, p[j][1], acc[i][j][1]);
-            acc[i][j][2] = fmaf(s * r.z, p[j][2], acc[i][j][2]);
-            acc[i][j][3] = fmaf(s * r.w, p[j][3], acc[i][j][3]);
+            a[0] = fmaf(s * r.x, v[0], a[0]);
+            a[1] = fmaf(s * r.y, v[1], a[1]);
+            a[2] = fmaf(s * r.z, v[2], a[2]);
+            a[3] = fmaf(s * r.w, v[3], a[3]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][j][e] = fmaf(s, p[j][e], acc[i][j][e]);
+            for (int e = 0; e < 4; e++) a[e] = fmaf(s, v[e], a[e]);
         }
     };
+    auto add = [&](int i, int j, float s, float4 r) { add_to(acc[i][j], p[j], s, r); };
     // Products of chunk c, whose operands open() has begun: row tile i's go out
     // while the previous tile's are added; mid() runs once every operand is in
     // registers, next() once the last products are out.
+    // (a small tile reads the next chunk's operands before its own products, which cover their latency)
     auto chunk = [&](int c, auto mid, auto next) {
-        const uint8_t* st = smem + (c % NS) * L::STAGE;
+        if constexpr (SMALL) {
+            mid();
+            v8i a0[MI], b0[NI];
+            float s0[MI];
+            float4 r0[ROWS ? NI : 1];
+#pragma unroll
+            for (int i = 0; i < MI; i++) a0[i] = af[i], s0[i] = sa[i] * bs;
+#pragma unroll
+            for (int j = 0; j < NI; j++) b0[j] = bf[j];
+#pragma unroll
+            for (int j = 0; j < (ROWS ? NI : 1); j++) r0[j] = br[j];
+            next();
+            v4f v[MI][NI];
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+#pragma unroll
+                for (int j = 0; j < NI; j++) v[i][j] = mfma_e4m3(b0[j], a0[i]);
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+#pragma unroll
+                for (int j = 0; j < NI; j++) add_to(acc[i][j], v[i][j], s0[i], r0[ROWS ? j : 0]);
+            return;
+        }
+        const uint8_t* st = smem + (c / KC % NS) * L::STAGE + (c % KC) * L::CHUNK;
 #pragma unroll
         for (int i = 0; i < MI - 1; i++) {
             af[(i + 1) & 1] = frag(st, alo, ahi, i + 1);
@@ -532,20 +560,32 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
     const std::false_type whole;
     const std::true_type tail;
     const int full = g.K >> 7;
+    auto issue_stage = [&](int g0) {
+#pragma unroll
+        for (int k = 0; k < KC; k++) issue(g0 * KC + k, min(g0 * KC + k, full - 1), whole);
+    };
     if (full > 0) {
 #pragma unroll
-        for (int c = 0; c < NS; c++) issue(c, min(c, full - 1), whole);
-        wait_vm<L::OPS * (NS - 1)>();
+        for (int g0 = 0; g0 < NS; g0++) issue_stage(g0);
+        wait_vm<L::OPS * KC * (NS - 1)>();
         __syncthreads();
         open(0);
     }
-    // The barrier in a chunk frees its slot and makes the next stage whole: only
-    // copies of later stages are then out.  Copies past the last stage fetch it
-    // again, into slots that are not read any more.
-    for (int c = 0; c < full - 1; c++)
-        chunk(c, [&]() { wait_vm<L::OPS * (NS - 2)>(); __syncthreads(); },
-              [&]() { issue(c, min(c + NS, full - 1), whole); open(c + 1); });
-    for (int c = full > 0 ? full - 1 : 0; c < nch; c++) {
+    // The barrier in a stage's last chunk frees its slot and makes the next stage
+    // whole: only copies of later stages are then out.  Copies past the last chunk
+    // fetch it again, into slots that are not read any more.
+    const int stages = (full + KC - 1) / KC;
+    int c = 0;
+    for (int g0 = 0; g0 < stages - 1; g0++) {
+#pragma unroll
+        for (int k = 0; k < KC - 1; k++, c++) chunk(c, []() {}, [&]() { open(c + 1); });
+        chunk(c, [&]() { wait_vm<L::OPS * KC * (NS - 2)>(); __syncthreads(); },
+              [&]() { issue_stage(g0 + NS); open(c + 1); });
+        c++;
+    }
+    if (KC > 1)
+        for (; c < full - 1; c++) chunk(c, []() {}, [&]() { open(c + 1); });
+    for (; c < nch; c++) {
         if (c == full) {
             wait_vm<0>();
             __syncthreads();
@@ -792,11 +832,11 @@ hipError_t run_quant(int mode, int R, int C, const void* x, int type, int64_t ld
     return launch_quant(mode, R, C, static_cast<const uint16_t*>(x), ldx, q, ldq, s, qt, ldqt, st, stream);
 }
 
-template <int WM, int WN, int MI, int NI, int NS, bool ROWS>
+template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t s)
 {
-    using L = GemmTile<WM, WN, MI, NI, NS, ROWS>;
-    const auto kernel = k_fp8_gemm<WM, WN, MI, NI, NS, ROWS>;
+    using L = GemmTile<WM, WN, MI, NI, NS, KC, ROWS>;
+    const auto kernel = k_fp8_gemm<WM, WN, MI, NI, NS, KC, ROWS>;
     if (L::BYTES > 65536) {
         static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
@@ -831,15 +871,24 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 //   k_fp8_split   16x16          6.6       10.2       17.8
 //   k_fp8_gemm    16x64          9.3       12.1       20.4
 //                 32x64          10.1      13.3       22.6
-//                 64x64          14.6      18.1       31.9
-//                 128x128        24.2      39.5       77.1
-//                 256x256        68.3      131
+//                 64x64          12.7      17.0       30.5
+//                 128x128        22.9      39.5       77.1
+//                 256x256        66        128
+// What bounds them: the small tiles the bytes of their operands through a CU's
+// vector memory path (the 32x64 tiles of 128x4096x4096 move 0.4 MB a CU in about 7
+// of their 10 us; deeper rings, two to four chunks a stage and scales through
+// LDS left that as it was), the large ones the matrix pipe next to the copies.
+// At 8192x4096x4096 (128 us, 2.15 PFLOP/s, clock 2.1 GHz, matrix pipe 47% busy)
+// copies of the kernel that leave work out take: no stores of C 115 us, no
+// copies into LDS 104, no scaling of the chunk sums 116, neither 87, and without
+// operand reads too 81 us, which is the products (65 us at the pipe's rate) and the
+// ends of the tiles.  64x64 takes two chunks a stage (one: 13.1 / 18.8 / 32.3 us).
 struct Variant {
     int bm, bn;
     float base, slope;
 };
 constexpr Variant kVariants[] = {{16, 16, 3.0f, 3.6f}, {16, 64, 6.0f, 3.5f},    {32, 64, 6.4f, 3.9f},
-                                 {64, 64, 8.5f, 5.7f}, {128, 128, 5.0f, 18.0f}, {256, 256, 3.0f, 64.0f}};
+                                 {64, 64, 7.0f, 5.7f}, {128, 128, 4.5f, 18.0f}, {256, 256, 3.0f, 62.0f}};
 int choose_variant(int64_t M, int64_t N)
 {
     int best = 0;
@@ -858,11 +907,11 @@ hipError_t run_gemm(const GemmArgs& g, hipStream_t s)
 {
     switch (choose_variant(g.M, g.N)) {
     case 0: return launch_split<1, 1, 8, ROWS, false>(g, s);
-    case 1: return launch_gemm<1, 4, 1, 1, 4, ROWS>(g, s);
-    case 2: return launch_gemm<2, 2, 1, 2, 4, ROWS>(g, s);
-    case 3: return launch_gemm<2, 2, 2, 2, 3, ROWS>(g, s);
-    case 4: return launch_gemm<2, 2, 4, 4, 2, ROWS>(g, s);
-    default: return launch_gemm<2, 4, 8, 4, 2, ROWS>(g, s);
+    case 1: return launch_gemm<1, 4, 1, 1, 4, 1, ROWS>(g, s);
+    case 2: return launch_gemm<2, 2, 1, 2, 4, 1, ROWS>(g, s);
+    case 3: return launch_gemm<2, 2, 2, 2, 2, 2, ROWS>(g, s);
+    case 4: return launch_gemm<2, 2, 4, 4, 2, 1, ROWS>(g, s);
+    default: return launch_gemm<2, 4, 8, 4, 2, 1, ROWS>(g, s);
     }
 }
 
