@@ -128,8 +128,9 @@ __device__ __forceinline__ float float_of(uint32_t o) { return __uint_as_float(o
 // keys the lowest lane has the lowest id.  Each lane keeps its best key not yet
 // picked; a round takes the maximum over the wave (DPP), the first lane that
 // has it, and only that lane looks for its next best.  The groups' two largest
-// keys are found by 64 / groups lanes each, over keys staged in LDS, as groups
-// need not end with a lane.  Bound by the instructions a token takes, most of
+// keys are found by 64 / groups lanes each: the lanes that hold them where the
+// experts fill the wave and the groups are a power of two, otherwise over
+// keys staged in LDS, as groups need not end with a lane.  Bound by the instructions a token takes, most of
 // them in the rounds and the scores' exponentials and divisions.
 template <typename T, int EPL>
 __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
@@ -183,36 +184,51 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
     }
     if (g.groups > 1) {
         const int size = g.E / g.groups;
-        // 2^shift lanes per group: lane i of them takes the group's keys i, i + 2^shift, ...
+        // 2^shift lanes per group, the group's two largest keys in each of them
         const int shift = 6 - (32 - __builtin_clz(g.groups - 1)), per = 1 << shift;
         const int mine = lane >> shift;
-#pragma unroll
-        for (int q = 0; q < EPL; q++) staged[wave][e0 + q] = key[q];
-        __builtin_amdgcn_wave_barrier();
-        uint32_t a = kNone, c = kNone;              // largest and second of the group
-        if (mine < g.groups)
-            for (int i = lane & (per - 1); i < size; i += per) {
-                const uint32_t k = staged[wave][mine * size + i];
-                c = max(c, min(a, k));
-                a = max(a, k);
-            }
-        for (int o = 1; o < per; o <<= 1) {
-            const uint32_t oa = (uint32_t)__shfl_xor((int)a, o), oc = (uint32_t)__shfl_xor((int)c, o);
+        uint32_t a = kNone, c = kNone;              // largest and second
+        auto merge = [&](uint32_t oa, uint32_t oc) {
             c = max(min(a, oa), max(c, oc));
             a = max(a, oa);
+        };
+        const bool own = g.E == 64 * EPL && (g.groups & (g.groups - 1)) == 0;      // those lanes hold the group's keys
+        if (own) {
+#pragma unroll
+            for (int q = 0; q < EPL; q++) merge(key[q], kNone);
+        } else {
+            // lane i of them takes the group's keys i, i + 2^shift, ... out of LDS
+#pragma unroll
+            for (int q = 0; q < EPL; q++) staged[wave][e0 + q] = key[q];
+            __builtin_amdgcn_wave_barrier();
+            if (mine < g.groups)
+                for (int i = lane & (per - 1); i < size; i += per) merge(staged[wave][mine * size + i], kNone);
         }
+        if (per > 1) merge(dpp<0xB1>(kNone, a), dpp<0xB1>(kNone, c));
+        if (per > 2) merge(dpp<0x4E>(kNone, a), dpp<0x4E>(kNone, c));
+        if (per > 4) merge(dpp<0x141>(kNone, a), dpp<0x141>(kNone, c));
+        if (per > 8) merge(dpp<0x140>(kNone, a), dpp<0x140>(kNone, c));
+        if (per > 16) merge((uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)c, 16));
         const uint32_t v = c == kNone ? a : order_of(float_of(a) + float_of(c));
         int rank = 0;
+#pragma unroll 4
         for (int o = 0; o < g.groups; o++) {
             const uint32_t u = (uint32_t)__builtin_amdgcn_readlane((int)v, o << shift);
-            rank += (o < mine ? u >= v : u > v) ? 1 : 0;
+            rank += u >= v + (o < mine ? 0u : 1u) ? 1 : 0;      // larger, or as large with a lower number
         }
         const uint64_t kept = __ballot(mine < g.groups && rank < g.topk_groups);
-        const float inv = 1.0f / (float)size;
+        if (own) {
+            if (!((kept >> lane) & 1)) {
 #pragma unroll
-        for (int q = 0; q < EPL; q++) {
-            const int group = min((int)(((float)(e0 + q) + 0.5f) * inv), g.groups - 1);     // (e0 + q) / size: exact below 2^20
-            if (!((kept >> (group << shift)) & 1)) key[q] = kNone;
+                for (int q = 0; q < EPL; q++) key[q] = kNone;
+            }
+        } else {
+            const float inv = 1.0f / (float)size;
+#pragma unroll
+            for (int q = 0; q < EPL; q++) {
+                const int group = min((int)(((float)(e0 + q) + 0.5f) * inv), g.groups - 1);     // (e0 + q) / size: exact below 2^20
+                if (!((kept >> (group << shift)) & 1)) key[q] = kNone;
+            }
         }
     }
     uint32_t best = kNone, taken = 0;
