@@ -832,16 +832,26 @@ hipError_t run_quant(int mode, int R, int C, const void* x, int type, int64_t ld
     return launch_quant(mode, R, C, static_cast<const uint16_t*>(x), ldx, q, ldq, s, qt, ldqt, st, stream);
 }
 
+// Lets a kernel have more than 64 KiB of LDS, once per device.
+hipError_t allow_lds(const void* kernel, int bytes, bool (&done)[kMaxDevices])
+{
+    if (bytes <= 65536) return hipSuccess;
+    int dev = 0;
+    if (const hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
+    if (done[dev]) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    done[dev] = e == hipSuccess;
+    return e;
+}
+
 template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t s)
 {
     using L = GemmTile<WM, WN, MI, NI, NS, KC, ROWS>;
     const auto kernel = k_fp8_gemm<WM, WN, MI, NI, NS, KC, ROWS>;
-    if (L::BYTES > 65536) {
-        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-        if (e != hipSuccess) return e;
-    }
+    static bool allowed[kMaxDevices];
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
     const int tm = (g.M + L::BM - 1) / L::BM, tn = (g.N + L::BN - 1) / L::BN;
     if ((int64_t)tm * tn > INT32_MAX / 8) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(64 * L::NW), L::BYTES, s, g, tm, tn);
@@ -853,11 +863,8 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 {
     using L = SplitLds<MT, NT, NW, ROWS, X>;
     const auto kernel = k_fp8_split<MT, NT, NW, ROWS, X>;
-    if (L::BYTES > 65536) {
-        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-        if (e != hipSuccess) return e;
-    }
+    static bool allowed[kMaxDevices];
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
     const dim3 grid((unsigned)((g.N + 16 * NT - 1) / (16 * NT)), (unsigned)((g.M + 16 * MT - 1) / (16 * MT)));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), L::BYTES, s, g, x, ldx, kx);
     return hipGetLastError();
