@@ -20,6 +20,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 namespace v4moe {
 
 namespace {
@@ -182,19 +184,39 @@ struct Raw {
 //   BLOCK: q, qt, s [ceil(R/128)][ceil(C/128)]: one group per tile
 // Rows of q are written up to C rounded up to 16, zeros past C (qt likewise).
 enum { kQuantRows = 1, kQuantCols = 2, kQuantBlock = 4 };
+template <typename T>
+struct QuantJob {
+    int R, C;
+    const T* x; int64_t ldx;
+    uint8_t* q; int64_t ldq;
+    float* s;
+    uint8_t* qt; int64_t ldqt;
+    float* st;
+    int tiles() const { return (int)(((int64_t)R + 127) / 128 * (((int64_t)C + 127) / 128)); }
+};
+constexpr int kQuantThreads = 512;
+struct QuantLds {
+    __align__(16) uint32_t mx[kQuantThreads / 64][128];
+    __align__(16) uint8_t tq[128 * 128];
+};
 template <typename T, int MODE>
-__global__ __launch_bounds__(512) void k_fp8_quant(int R, int C, const T* __restrict__ x, int64_t ldx,
-                                                   uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s,
-                                                   uint8_t* __restrict__ qt, int64_t ldqt, float* __restrict__ st)
+__device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, QuantLds& lds)
 {
-    constexpr int NR = 4, NW = 8;                      // rows per thread, waves
-    __shared__ __align__(16) uint32_t mx[NW][128];
-    __shared__ __align__(16) uint8_t tq[128 * 128];
+    constexpr int NR = 4, NW = kQuantThreads / 64;      // rows per thread, waves
+    const int R = job.R, C = job.C;
+    const T* __restrict__ x = job.x;
+    uint8_t* __restrict__ q = job.q;
+    float* __restrict__ s = job.s;
+    uint8_t* __restrict__ qt = job.qt;
+    float* __restrict__ st = job.st;
+    const int64_t ldx = job.ldx, ldq = job.ldq, ldqt = job.ldqt;
+    auto& mx = lds.mx;
+    auto& tq = lds.tq;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int rt = NR * (t >> 4), ct = 8 * (t & 15);
     const int cpad = (C + 15) / 16 * 16, rpad = (R + 15) / 16 * 16;
     const int nx = (C + 127) / 128;
-    const int tile = blockIdx.x, by = tile / nx, bx = tile % nx, r0 = by * 128, c0 = bx * 128;
+    const int by = tile / nx, bx = tile % nx, r0 = by * 128, c0 = bx * 128;
     Raw<T> f[NR];
 #pragma unroll
     for (int i = 0; i < NR; i++)
@@ -279,6 +301,22 @@ __global__ __launch_bounds__(512) void k_fp8_quant(int R, int C, const T* __rest
             *reinterpret_cast<uint4*>(qt + (int64_t)(c0 + c) * ldqt + r0 + 16 * seg) =
                 *reinterpret_cast<const uint4*>(tq + c * 128 + ((seg ^ (c >> 3 & 7)) * 16));
     }
+}
+
+template <typename T, int MODE>
+__global__ __launch_bounds__(kQuantThreads) void k_fp8_quant(QuantJob<T> job)
+{
+    __shared__ QuantLds lds;
+    quant_tile<T, MODE>(job, blockIdx.x, lds);
+}
+// The operands of a backward in one launch: the incoming gradient (rows for the
+// data gradient, columns for the weights'), then the activations (columns).
+template <typename T, int MODE>
+__global__ __launch_bounds__(kQuantThreads) void k_fp8_quant_pair(QuantJob<T> a, int tiles_a, QuantJob<T> b)
+{
+    __shared__ QuantLds lds;
+    if ((int)blockIdx.x < tiles_a) quant_tile<T, MODE>(a, blockIdx.x, lds);
+    else quant_tile<T, kQuantCols>(b, blockIdx.x - tiles_a, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -810,17 +848,28 @@ hipError_t launch_quant(int mode, int R, int C, const T* x, int64_t ldx, uint8_t
                            q, ldq, s);
         return hipGetLastError();
     }
-    const int64_t tiles = chunks(C) * chunks(R);
-    const dim3 grid((unsigned)tiles);
+    const QuantJob<T> job{R, C, x, ldx, q, ldq, s, qt, ldqt, st};
     auto run = [&](auto m) {
-        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), grid, dim3(512), 0, stream, R, C, x, ldx, q, ldq, s, qt, ldqt,
-                           st);
+        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), dim3((unsigned)job.tiles()), dim3(kQuantThreads), 0, stream, job);
     };
     switch (mode) {
     case kQuantCols: run(std::integral_constant<int, kQuantCols>{}); break;
     case kQuantRows | kQuantCols: run(std::integral_constant<int, kQuantRows | kQuantCols>{}); break;
     default: run(std::integral_constant<int, kQuantBlock>{}); break;
     }
+    return hipGetLastError();
+}
+
+// dy and x of a backward, of one type; rows: dy's codes by rows too
+template <typename T>
+hipError_t launch_quant_pair(const QuantJob<T>& dy, const QuantJob<T>& x, bool rows, hipStream_t stream)
+{
+    const int a = dy.tiles(), b = x.tiles();
+    if (rows)
+        hipLaunchKernelGGL((k_fp8_quant_pair<T, kQuantRows | kQuantCols>), dim3((unsigned)(a + b)), dim3(kQuantThreads), 0,
+                           stream, dy, a, x);
+    else
+        hipLaunchKernelGGL((k_fp8_quant_pair<T, kQuantCols>), dim3((unsigned)(a + b)), dim3(kQuantThreads), 0, stream, dy, a, x);
     return hipGetLastError();
 }
 
@@ -1080,13 +1129,29 @@ __attribute__((visibility("default"))) int moe_fp8_linear_backward(
     if (ws_bytes < L.total) return V4MOE_EWORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    if (M > 0) {
-        if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, dx ? ws + L.dq : nullptr, dx ? f32(L.ds) : nullptr,
-                                            dw ? ws + L.dt : nullptr, dw ? f32(L.dts) : nullptr, stream))
-            return rc;
-        if (dw)
+    if (M > 0 && dw) {
+        // both operands' columns, and dy's rows, in one launch where they are of one type
+        const bool one = x_type == dy_type;
+        if (!device_ready()) return V4MOE_EDEVICE;
+        const hipStream_t s = static_cast<hipStream_t>(stream);
+        auto both = [&](auto* as) {
+            using T = std::remove_pointer_t<decltype(as)>;
+            const QuantJob<T> a{M, N, static_cast<const T*>(dy), lddy, ws + L.dq, up16(N), f32(L.ds), ws + L.dt, up16(M), f32(L.dts)};
+            const QuantJob<T> b{M, K, static_cast<const T*>(x), ldx, nullptr, 0, nullptr, ws + L.xt, up16(M), f32(L.xts)};
+            return launch_quant_pair(a, b, dx != nullptr, s);
+        };
+        if (one) {
+            const hipError_t e = x_type == V4MOE_TYPE_F32 ? both(static_cast<float*>(nullptr)) : both(static_cast<uint16_t*>(nullptr));
+            if (e != hipSuccess) return V4MOE_ELAUNCH;
+        } else {
+            if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, dx ? ws + L.dq : nullptr, dx ? f32(L.ds) : nullptr,
+                                                ws + L.dt, f32(L.dts), stream))
+                return rc;
             if (const int rc = moe_fp8_quantize(M, K, x, x_type, ldx, nullptr, nullptr, ws + L.xt, f32(L.xts), stream))
                 return rc;
+        }
+    } else if (M > 0) {
+        if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, ws + L.dq, f32(L.ds), nullptr, nullptr, stream)) return rc;
     }
     if (dx && M > 0) {
         // dx = dy W: contraction over N, block (i, c) of W^T is block (c, i) of W
