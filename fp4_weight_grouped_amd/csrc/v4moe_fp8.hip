@@ -920,17 +920,21 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
     return hipGetLastError();
 }
 
-// The product's variants.  A call takes the one of the least modelled time, base
-// + slope * ceil(tiles / 256) us: measured at K = 4096 over M = 1 .. 8192 with
-// N = 4096 and 1024, where the model is within 10%, and nearly proportional to
-// K, so the order holds.  A round is one tile per CU.
-//                 tiles   us     1 round   2 rounds   4 rounds
-//   k_fp8_split   16x16          6.6       10.2       17.8
-//   k_fp8_gemm    16x64          9.3       12.1       20.4
-//                 32x64          10.1      13.3       22.6
-//                 64x64          12.7      17.0       30.5
-//                 128x128        22.9      39.5       77.1
-//                 256x256        66        128
+// The product's variants.  A call takes the one of the least time in this table,
+// by the rounds its tiles make (a round is one tile per CU): microseconds at
+// K = 4096, N = 4096 and M = 16 .. 8192, in a graph of many calls.  Times are nearly
+// proportional to K, so the order holds for others; two blocks of the tiles up to
+// 128x128 share a CU, so that a second round costs less than the first.
+//                 tiles   round 1   2      3      4     each further
+//   k_fp8_split   16x16     6.6    10.2   14.0   17.8   3.7
+//   k_fp8_gemm    16x64     9.2    12.3   16.0   20.3   4.0
+//                 32x64    10.2    13.2   17.4   22.5   4.2
+//                 64x64    12.5    15.7   24.6   29.1   8.4
+//                 128x128  23      34     52     73     19
+//                 256x256  58      124    186    248    62
+// (Tiles between them were timed and lie on or above the line these make: 128x64
+// at 512x4096x4096 17.8 us next to 15.8, at 1024x4096x4096 23.9 next to 24.1;
+// 128x256 at 2048x4096x8192 83.5 next to 84.6.)
 // What bounds them: the small tiles the bytes of their operands through a CU's
 // vector memory path (the 32x64 tiles of 128x4096x4096 move 0.4 MB a CU in about 7
 // of their 10 us; deeper rings, two to four chunks a stage and scales through
@@ -942,18 +946,20 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 // ends of the tiles.  64x64 takes two chunks a stage (one: 13.1 / 18.8 / 32.3 us).
 struct Variant {
     int bm, bn;
-    float base, slope;
+    float us[4], further;
 };
-constexpr Variant kVariants[] = {{16, 16, 3.0f, 3.6f}, {16, 64, 6.0f, 3.5f},    {32, 64, 6.4f, 3.9f},
-                                 {64, 64, 7.0f, 5.7f}, {128, 128, 4.5f, 18.0f}, {256, 256, 3.0f, 62.0f}};
+constexpr Variant kVariants[] = {
+    {16, 16, {6.6f, 10.2f, 14.0f, 17.8f}, 3.7f},   {16, 64, {9.2f, 12.3f, 16.0f, 20.3f}, 4.0f},
+    {32, 64, {10.2f, 13.2f, 17.4f, 22.5f}, 4.2f},  {64, 64, {12.5f, 15.7f, 24.6f, 29.1f}, 8.4f},
+    {128, 128, {23.0f, 34.0f, 52.0f, 73.0f}, 19.0f}, {256, 256, {58.0f, 124.0f, 186.0f, 248.0f}, 62.0f}};
 int choose_variant(int64_t M, int64_t N)
 {
     int best = 0;
     float least = 0.0f;
     for (int v = 0; v < 6; v++) {
         const Variant& k = kVariants[v];
-        const int64_t tiles = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn);
-        const float us = k.base + k.slope * (float)((tiles + 255) / 256);
+        const int64_t tiles = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn), rounds = (tiles + 255) / 256;
+        const float us = rounds <= 4 ? k.us[rounds - 1] : k.us[3] + k.further * (float)(rounds - 4);
         if (v == 0 || us < least) best = v, least = us;
     }
     return best;
