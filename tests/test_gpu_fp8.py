@@ -140,7 +140,8 @@ def operand(seed, R, C, pad=0, wide=False):
 GEMMS = [(1, 1, 16), (1, 64, 128), (2, 17, 144), (5, 300, 1008), (16, 128, 2048), (17, 129, 256), (33, 48, 4096),
          (64, 256, 512), (65, 1000, 384), (100, 31, 112), (128, 512, 640), (129, 257, 272), (200, 384, 128),
          (300, 640, 1040), (513, 514, 528), (700, 1030, 256), (1100, 900, 384), (2050, 1300, 160), (1, 2000, 2064),
-         (20, 1500, 272), (70, 2200, 1200), (300, 3000, 256), (1000, 3100, 144), (4100, 4000, 400)]
+         (20, 1500, 272), (70, 2200, 1200), (300, 3000, 256), (1000, 3100, 144), (4100, 4000, 400),
+         (4001, 3900, 272), (3990, 4090, 400)]
 
 
 @pytest.mark.parametrize("rows", [False, True])
@@ -170,7 +171,7 @@ def test_gemm(shape, wide, rows):
             assert torch.equal(acc, out + out)
 
 
-@pytest.mark.parametrize("shape", [(2050, 1300, 1056), (1100, 257, 4096), (4352, 4096, 656)], ids=str)
+@pytest.mark.parametrize("shape", [(2050, 1300, 1056), (1100, 257, 4096), (4352, 4096, 656), (4001, 3800, 656)], ids=str)
 @pytest.mark.parametrize("rows", [False, True])
 def test_row_does_not_depend_on_the_batch(shape, rows):
     M, N, K = shape
