@@ -43,29 +43,6 @@ typedef v4u v4u_any __attribute__((aligned(2)));
 template <typename T>
 __device__ __forceinline__ v4u load16(const T* p) { return *reinterpret_cast<const v4u_any*>(p); }
 
-// Eight consecutive elements, `n` of them inside the array (the rest read as zero).
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, float (&f)[8])
-{
-    if (n >= 8) {
-        const v4u v = load16(p);
-        if constexpr (sizeof(T) == 4) {
-            const v4u w = load16(p + 4);
-#pragma unroll
-            for (int u = 0; u < 4; u++) f[u] = __uint_as_float(v[u]), f[4 + u] = __uint_as_float(w[u]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                f[2 * u] = bf16_to_f32(v[u] & 0xFFFFu);
-                f[2 * u + 1] = bf16_to_f32(v[u] >> 16);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; u++) f[u] = u < n ? load_f32(p + u) : 0.0f;
-    }
-}
-
 // Magnitudes are compared as their bits: a NaN is then larger than everything.
 __device__ __forceinline__ uint32_t mag_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
 
@@ -78,56 +55,38 @@ __device__ __forceinline__ float group_scale(uint32_t mag)
 }
 
 // E4M3 codes of x / s, the quotient rounded to fp32 first.  A scale well inside
-// the normal range takes y = 1/s rounded, then two corrections of x y by its
-// exact residual, which give the rounded quotient (half the instructions of a
-// division); the others divide; a NaN scale gives codes 0.
+// the normal range takes y = 1/s rounded and one correction of q = x y by its
+// residual: that is within 5/(2 S) of the exact quotient's last place (S the
+// scale's 24-bit integer), so another fp32 than the rounded quotient can only
+// come out beside a rounding boundary of E4M3 for S within 5 of a multiple of
+// 2^20, and for every such S (64 on either side were tried) and every 24-bit x
+// the two are equal.  The others (y = 0) divide; a NaN scale gives codes 0.
 struct Divisor {
     float s, y;
-    bool quick;
-    __device__ __forceinline__ explicit Divisor(float scale) : s(scale), y(1.0f / scale), quick(scale > 0x1p-80f && scale < 0x1p80f) {}
+    __device__ __forceinline__ explicit Divisor(float scale) : s(scale), y(scale > 0x1p-80f && scale < 0x1p80f ? 1.0f / scale : 0.0f) {}
+    __device__ __forceinline__ Divisor(float scale, float inverse) : s(scale), y(inverse) {}
     __device__ __forceinline__ float corrected(float x) const
     {
-        // (residuals as q s - x: where they vanish the quotient keeps its sign, a zero's too)
-        float q = x * y;
-        q = fmaf(-fmaf(q, s, -x), y, q);
+        // (the residual as q s - x: where it vanishes the quotient keeps its sign, a zero's too)
+        const float q = x * y;
         return fmaf(-fmaf(q, s, -x), y, q);
+    }
+    __device__ __forceinline__ uint32_t quick4(float a, float b, float c, float d) const
+    {
+        return e4m3x2(corrected(a), corrected(b)) | (e4m3x2(corrected(c), corrected(d)) << 16);
     }
     __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) const
     {
-        if (quick) return e4m3x2(corrected(a), corrected(b)) | (e4m3x2(corrected(c), corrected(d)) << 16);
+        if (y != 0.0f) return quick4(a, b, c, d);
         if (s != s) return 0u;
         return e4m3x2(a / s, b / s) | (e4m3x2(c / s, d / s) << 16);
     }
 };
 
-// Groups along rows: x [R][C] -> q [R][ldq] (up to C rounded up to 16, zeros
-// past C), s [ceil(C/128)][R].  Sixteen lanes per group, eight elements each.
-// HBM-bound: x read once, a byte written per element.
-template <typename T>
-__global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, const T* __restrict__ x, int64_t ldx,
-                                                        uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
-{
-    const int nc = (C + 127) / 128;
-    const int64_t group = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int64_t r = group / nc;
-    if (r >= R) return;                                   // whole groups of lanes
-    const int c = (int)(group - r * nc), at = c * 128 + 8 * (threadIdx.x & 15);
-    float f[8];
-    load8(x + r * ldx + min(at, C - 1), C - at, f);
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < 8; u++) m = max(m, mag_bits(f[u]));
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-    const Divisor d(group_scale(m));
-    if (at < (C + 15) / 16 * 16)
-        *reinterpret_cast<uint2*>(q + r * ldq + at) = make_uint2(d.codes4(f[0], f[1], f[2], f[3]), d.codes4(f[4], f[5], f[6], f[7]));
-    if ((threadIdx.x & 15) == 0) s[(int64_t)c * R + r] = d.s;
-}
-
-// Maximum over the 16 lanes of a row, in every lane (quad xor 1, xor 2, half-row
-// mirror, row mirror).
-__device__ __forceinline__ uint32_t row_max(uint32_t v)
+// Maximum over lanes by DPP (quad xor 1, xor 2, half-row mirror: 8 lanes; row
+// mirror: 16), in every lane of them.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 {
     auto step = [&](auto ctrl) {
         v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF, false));
@@ -135,14 +94,15 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v)
     step(std::integral_constant<int, 0xB1>{});
     step(std::integral_constant<int, 0x4E>{});
     step(std::integral_constant<int, 0x141>{});
-    step(std::integral_constant<int, 0x140>{});
+    if constexpr (LANES == 16) step(std::integral_constant<int, 0x140>{});
     return v;
 }
 
 // Eight consecutive elements as they are in memory (zeros past the array's end).
 template <typename T>
 struct Raw {
-    v4u w[sizeof(T) / 2];
+    static constexpr int W = sizeof(T) / 2;          // 16-byte words
+    v4u w[W];
     __device__ __forceinline__ float operator[](int u) const
     {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[u >> 2][u & 3]);
@@ -152,13 +112,13 @@ struct Raw {
     __device__ __forceinline__ void forget()
     {
 #pragma unroll
-        for (int h = 0; h < (int)sizeof(T) / 2; h++) asm volatile("" : "+v"(w[h]));
+        for (int h = 0; h < W; h++) asm volatile("" : "+v"(w[h]));
     }
     __device__ __forceinline__ void load(const T* p, int n)
     {
         if (n >= 8) {
 #pragma unroll
-            for (int h = 0; h < (int)sizeof(T) / 2; h++) w[h] = load16(p + 4 * h);
+            for (int h = 0; h < W; h++) w[h] = load16(p + 4 * h);
         } else {
 #pragma unroll
             for (int u = 0; u < 8; u++) {
@@ -170,15 +130,67 @@ struct Raw {
     }
 };
 
+// The largest magnitudes of word i of several Raw: fp32 one per word, bf16 two
+// (their bits compare as integers), so half the instructions.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <typename T>
+__device__ __forceinline__ uint32_t mag_word(uint32_t w) { return w & (sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu); }
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b)
+{
+    if constexpr (sizeof(T) == 4) return max(a, b);
+    else return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// ... and of a word alone, as the bits of an fp32
+template <typename T>
+__device__ __forceinline__ uint32_t word_mag(uint32_t w)
+{
+    if constexpr (sizeof(T) == 4) return w;
+    else return max(w & 0xFFFF0000u, w << 16);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t largest(const Raw<T>& r)
+{
+    uint32_t m = mag_word<T>(r.w[0][0]);
+#pragma unroll
+    for (int i = 1; i < 4 * Raw<T>::W; i++) m = max_word<T>(m, mag_word<T>(r.w[i >> 2][i & 3]));
+    return word_mag<T>(m);
+}
+
+// Groups along rows: x [R][C] -> q [R][ldq] (up to C rounded up to 16, zeros
+// past C), s [ceil(C/128)][R].  Eight lanes per group, sixteen elements each; a
+// block takes 2^lg consecutive groups of a row (at most a wave's eight) and
+// 32 / 2^lg rows.  Bound by HBM: 8192x4096 bf16 19.8 us, 102 MB at 5.1 TB/s, the
+// rate of a copy (sixteen lanes per group, whose scales are then twice the work,
+// and a second correction of each quotient: 23 us, all of them issuing).
+template <typename T>
+__global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, int lg, const T* __restrict__ x, int64_t ldx,
+                                                        uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
+{
+    const int g = threadIdx.x >> 3, r = blockIdx.x * (32 >> lg) + (g >> lg), c = ((int)blockIdx.y << lg) + (g & ((1 << lg) - 1));
+    if (r >= R || c * 128 >= C) return;                   // whole groups of lanes
+    const int at = c * 128 + 16 * (threadIdx.x & 7);
+    Raw<T> f[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) f[h].load(x + (int64_t)r * ldx + min(at + 8 * h, C - 1), C - at - 8 * h);
+    const Divisor d(group_scale(lanes_max<8>(max(largest(f[0]), largest(f[1])))));
+    if (at < C)
+        *reinterpret_cast<uint4*>(q + (int64_t)r * ldq + at) =
+            make_uint4(d.codes4(f[0][0], f[0][1], f[0][2], f[0][3]), d.codes4(f[0][4], f[0][5], f[0][6], f[0][7]),
+                       d.codes4(f[1][0], f[1][1], f[1][2], f[1][3]), d.codes4(f[1][4], f[1][5], f[1][6], f[1][7]));
+    if ((threadIdx.x & 7) == 0) s[(int64_t)c * R + r] = d.s;
+}
+
 // One 128x128 tile of x [R][C] per block, read once for both orders: thread t
 // holds rows 4(t/16) .. +3, columns 8(t%16) .. +7 as they are in memory.  Bound by
-// the tile's own latency and VALU work beside HBM: 8192x4096 bf16 by columns 25 us
-// (4.0 TB/s), 8192x2048 in both orders 27 us, 16384x4096 fp32 weights 84 us (4.8
-// TB/s).  Waves per CU are what helps: eight rows per thread (five blocks of four
-// waves) took 28 / 27 / 87 us, with the elements kept as floats (three blocks)
-// 32 / 35, with the next tile's loads out a tile ahead (two blocks) 34 / 34;
-// without the residual corrections, or with the stores of qt in one stretch, the
-// last took 30 / 29.
+// HBM, next to the tile's own latency and instructions: 16384x4096 fp32 weights
+// 81 us (403 MB, 4.9 TB/s); 8192x2048 bf16 in both orders and 8192x4096 by columns
+// in one launch 35 us (169 MB, 4.9 TB/s).  What helps is waves per CU (eight rows
+// per thread took 47 us for the latter where four took 40, with the elements kept
+// as floats or the next tile's loads out a tile ahead 60) and fewer instructions
+// (40 -> 35: bf16 magnitudes two to an operation, their maxima over lanes by
+// permutes of the vector unit, a column's scale inverted by one thread, one
+// correction of each quotient).
 //   ROWS: q [R][ldq], s [ceil(C/128)][R]: groups of 128 columns of a row
 //   COLS: qt [C][ldqt], st [ceil(R/128)][C]: groups of 128 rows of a column
 //   BLOCK: q, qt, s [ceil(R/128)][ceil(C/128)]: one group per tile
@@ -229,69 +241,91 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
     if constexpr (MODE & kQuantRows) {
 #pragma unroll
         for (int i = 0; i < NR; i++) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int u = 0; u < 8; u++) m = max(m, mag_bits(f[i][u]));
-            const Divisor d(group_scale(row_max(m)));
+            const Divisor d(group_scale(lanes_max<16>(largest(f[i]))));
             store_row(i, d);
             if ((t & 15) == 0 && r0 + rt + i < R) s[(int64_t)bx * R + r0 + rt + i] = d.s;
         }
     }
-    uint32_t m[8];
+    // largest magnitude of each column in the wave's 16 rows, a word's columns together
+    constexpr int NWORD = 4 * Raw<T>::W;
+    uint32_t m[NWORD];
     // (the columns convert the elements anew: kept as floats they would cost two blocks of the CU's four)
 #pragma unroll
     for (int i = 0; i < NR; i++) f[i].forget();
 #pragma unroll
-    for (int u = 0; u < 8; u++) {
-        m[u] = 0;
+    for (int u = 0; u < NWORD; u++) {
+        m[u] = mag_word<T>(f[0].w[u >> 2][u & 3]);
 #pragma unroll
-        for (int i = 0; i < NR; i++) m[u] = max(m[u], mag_bits(f[i][u]));
-        m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 16));
-        m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 32));
+        for (int i = 1; i < NR; i++) m[u] = max_word<T>(m[u], mag_word<T>(f[i].w[u >> 2][u & 3]));
+        // lanes 16 apart (odd rows of 16 for even ones), then 32 apart
+        const auto a = __builtin_amdgcn_permlane16_swap(m[u], m[u], false, false);
+        m[u] = max_word<T>(a[0], a[1]);
+        const auto b = __builtin_amdgcn_permlane32_swap(m[u], m[u], false, false);
+        m[u] = max_word<T>(b[0], b[1]);
     }
     if (lane < 16) {
-        *reinterpret_cast<uint4*>(&mx[wave][ct]) = make_uint4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<uint4*>(&mx[wave][ct + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+        for (int h = 0; h < Raw<T>::W; h++)
+            *reinterpret_cast<uint4*>(&mx[wave][(lane * Raw<T>::W + h) * 4]) = make_uint4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
     }
     __syncthreads();
-    auto column = [&](int c) {
-        uint32_t v = 0;
+    constexpr int WORDS = 128 * sizeof(T) / 4;           // of a tile's row
+    auto word = [&](int c) {
+        uint32_t v = mx[0][c];
 #pragma unroll
-        for (int i = 0; i < NW; i++) v = max(v, mx[i][c]);
+        for (int i = 1; i < NW; i++) v = max_word<T>(v, mx[i][c]);
         return v;
     };
-    uint32_t all = 0;
+    Divisor d8[8] = {Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f),
+                     Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f)};
     if constexpr (MODE & kQuantBlock) {
-        all = max(column(lane), column(64 + lane));
+        uint32_t all = word_mag<T>(word(lane));
+        if constexpr (WORDS == 128) all = max(all, word_mag<T>(word(64 + lane)));
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) all = max(all, (uint32_t)__shfl_xor((int)all, o));
-        const Divisor d(group_scale(all));
-        if (t == 0) s[tile] = d.s;
+        d8[0] = Divisor(group_scale(all));
+        if (t == 0) s[tile] = d8[0].s;
 #pragma unroll
-        for (int i = 0; i < NR; i++) store_row(i, d);
+        for (int i = 0; i < NR; i++) store_row(i, d8[0]);
+#pragma unroll
+        for (int u = 1; u < 8; u++) d8[u] = d8[0];
     } else {
-        // each column's maximum once, by one thread
+        // each column's scale and its inverse once, by one thread
+        uint32_t v = 0;
+        if (t < 128) v = sizeof(T) == 4 ? word(t) : t & 1 ? word(t >> 1) & 0xFFFF0000u : word(t >> 1) << 16;
+        __syncthreads();
         if (t < 128) {
-            const uint32_t v = column(t);
-            mx[0][t] = v;
-            if (c0 + t < C) st[(int64_t)by * C + c0 + t] = group_scale(v);
+            const Divisor d(group_scale(v));
+            mx[0][t] = __float_as_uint(d.s);
+            mx[1][t] = __float_as_uint(d.y);
+            if (c0 + t < C) st[(int64_t)by * C + c0 + t] = d.s;
         }
         __syncthreads();
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const uint4 v = *reinterpret_cast<const uint4*>(&mx[0][ct + 4 * h]);
-            m[4 * h] = v.x; m[4 * h + 1] = v.y; m[4 * h + 2] = v.z; m[4 * h + 3] = v.w;
+            const float4 sc = *reinterpret_cast<const float4*>(&mx[0][ct + 4 * h]), in = *reinterpret_cast<const float4*>(&mx[1][ct + 4 * h]);
+            d8[4 * h] = Divisor(sc.x, in.x);
+            d8[4 * h + 1] = Divisor(sc.y, in.y);
+            d8[4 * h + 2] = Divisor(sc.z, in.z);
+            d8[4 * h + 3] = Divisor(sc.w, in.w);
         }
     }
     // The codes transposed through LDS: column c's 128 bytes, their 16-byte
     // segments XORed by c/8 so that the columns a store covers spread over the
     // banks; then 16-byte stores along the rows of qt.
+    bool quick = true;
 #pragma unroll
-    for (int u = 0; u < 8; u++) {
+    for (int u = 0; u < 8; u++) quick = quick && d8[u].y != 0.0f;
+    auto column = [&](int u, uint32_t codes) {
         const int c = ct + u, r4 = t >> 4;
-        const Divisor d(group_scale(MODE & kQuantBlock ? all : m[u]));
-        *reinterpret_cast<uint32_t*>(tq + c * 128 + (((r4 >> 2) ^ (c >> 3 & 7)) * 16) + (r4 & 3) * 4) =
-            d.codes4(f[0][u], f[1][u], f[2][u], f[3][u]);
+        *reinterpret_cast<uint32_t*>(tq + c * 128 + (((r4 >> 2) ^ (c >> 3 & 7)) * 16) + (r4 & 3) * 4) = codes;
+    };
+    if (quick) {
+#pragma unroll
+        for (int u = 0; u < 8; u++) column(u, d8[u].quick4(f[0][u], f[1][u], f[2][u], f[3][u]));
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; u++) column(u, d8[u].codes4(f[0][u], f[1][u], f[2][u], f[3][u]));
     }
     __syncthreads();
 #pragma unroll
@@ -844,8 +878,10 @@ hipError_t launch_quant(int mode, int R, int C, const T* x, int64_t ldx, uint8_t
                         int64_t ldqt, float* st, hipStream_t stream)
 {
     if (mode == kQuantRows) {
-        hipLaunchKernelGGL(k_fp8_quant_rows<T>, dim3((unsigned)((R * chunks(C) + 15) / 16)), dim3(256), 0, stream, R, C, x, ldx,
-                           q, ldq, s);
+        // groups of a row in a block: a power of two up to eight
+        const int lg = chunks(C) >= 8 ? 3 : chunks(C) >= 4 ? 2 : chunks(C) >= 2 ? 1 : 0, per = 32 >> lg;
+        hipLaunchKernelGGL(k_fp8_quant_rows<T>, dim3((unsigned)((R + per - 1) / per), (unsigned)((chunks(C) + (1 << lg) - 1) >> lg)),
+                           dim3(256), 0, stream, R, C, lg, x, ldx, q, ldq, s);
         return hipGetLastError();
     }
     const QuantJob<T> job{R, C, x, ldx, q, ldq, s, qt, ldqt, st};
