@@ -13,6 +13,7 @@ import array
 import ctypes
 import dataclasses
 import functools
+import operator
 import os
 import re
 from typing import Optional
@@ -328,6 +329,9 @@ def _require(ok: bool, what: str):
         raise ValueError(what)
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _type(t: torch.Tensor) -> int:
     ty = _TYPES.get(t.dtype)
     if ty is None:
@@ -532,24 +536,25 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     _require(n > 0, "no gradients")
     stream = _on_device(grads[0], "gradients")
     dev = grads[0].device
-    flat = []           # v4moe_tensor is four 64-bit words: g, out, n, type
-    if out is None:
-        for g in grads:
-            if g.device != dev or not g.is_contiguous():
-                raise ValueError("gradients must be contiguous on one GPU")
-            p = g.data_ptr()
-            flat += (p, p, g.numel(), _type(g))
-    else:
+
+    def words(tensors):     # addresses, sizes and types, by maps over the list: a small step's time is the host's
+        if not all(map(torch.Tensor.is_contiguous, tensors)) or set(map(torch.Tensor.get_device, tensors)) != {dev.index}:
+            raise ValueError("gradients must be contiguous on one GPU")
+        return (array.array("q", map(torch.Tensor.data_ptr, tensors)), array.array("q", map(torch.Tensor.numel, tensors)),
+                list(map(_dtype_of, tensors)))
+
+    g, sizes, dtypes = words(grads)
+    o = g
+    if out is not None:
         out = list(out)
         _require(len(out) == n, "out must match grads")
-        for g, o in zip(grads, out):
-            m = g.numel()
-            if g.device != dev or not g.is_contiguous():
-                raise ValueError("gradients must be contiguous on one GPU")
-            if o.dtype != g.dtype or o.numel() != m or o.device != dev or not o.is_contiguous():
-                raise ValueError("out must match grads")
-            flat += (g.data_ptr(), o.data_ptr(), m, _type(g))
-    table = array.array("q", flat)
+        o, *same = words(out)
+        _require(same == [sizes, dtypes], "out must match grads")
+    table = array.array("q", bytes(32 * n))     # v4moe_tensor is four 64-bit words: g, out, n, type
+    try:
+        table[0::4], table[1::4], table[2::4], table[3::4] = g, o, sizes, array.array("q", map(_TYPES.__getitem__, dtypes))
+    except KeyError as e:
+        raise TypeError(f"float32 or bfloat16 expected, got {e.args[0]}") from None
     norm = torch.empty((), dtype=torch.float32, device=dev)
     size = _clip_workspace_bytes(n)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
