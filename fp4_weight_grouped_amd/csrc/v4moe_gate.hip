@@ -9,13 +9,15 @@
 //   w_j   = scale * s_j [/ sum of the picked s], 0 where the key is -inf
 // Scores and keys are fp32, every operation rounded once (the library is built
 // without contraction), so the picks are a function of the logits alone.  The
-// softmax's sum is taken in fp64: rounded to fp32 it does not depend on the
-// order of the terms, and so neither do the picks.
+// softmax's sum is taken in fp64, over neighbours, their pairs and so on, which
+// is the same tree however many lanes a token has.
 #include "v4moe.h"
 #include "v4moe_device.h"
 #include "v4moe_internal.h"
 
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 namespace v4moe {
 
@@ -124,46 +126,131 @@ __device__ __forceinline__ uint32_t order_of(float f)
 }
 __device__ __forceinline__ float float_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o); }
 
-// One wave per token; lane l holds experts l EPL .. + EPL - 1, so that of equal
-// keys the lowest lane has the lowest id.  Each lane keeps its best key not yet
-// picked; a round takes the maximum over the wave (DPP), the first lane that
-// has it, and only that lane looks for its next best.  The groups' two largest
-// keys are found by 64 / groups lanes each: the lanes that hold them where the
-// experts fill the wave and the groups are a power of two, otherwise over
-// keys staged in LDS, as groups need not end with a lane.  Bound by the instructions a token takes, most of
-// them in the rounds and the scores' exponentials and divisions.
-template <typename T, int EPL>
+// Maximum over the LPT lanes of a token, in every one of them: the rows of 16
+// by DPP, then rows by permutes that swap them (16 and 32 lanes apart).
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v)
+{
+    v = max(v, dpp<0xB1>(0, v));
+    v = max(v, dpp<0x4E>(0, v));
+    v = max(v, dpp<0x141>(0, v));
+    v = max(v, dpp<0x140>(0, v));
+    if constexpr (LPT >= 32) {
+        const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = max(a[0], a[1]);
+    }
+    if constexpr (LPT >= 64) {
+        const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max(a[0], a[1]);
+    }
+    return v;
+}
+template <int LPT>
+__device__ __forceinline__ double token_sum(double v)
+{
+#pragma unroll
+    for (int o = 1; o < LPT; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+}
+// The lowest set bit of each token's LPT bits.
+template <int LPT>
+__device__ __forceinline__ uint64_t first_of(uint64_t m)
+{
+    if constexpr (LPT == 64) {
+        return m & (0 - m);
+    } else {
+        uint64_t r = 0;
+#pragma unroll
+        for (int i = 0; i < 64; i += LPT) {
+            const uint32_t f = (uint32_t)(m >> i) & (uint32_t)((1ull << LPT) - 1);
+            r |= (uint64_t)(f & (0u - f)) << i;
+        }
+        return r;
+    }
+}
+
+// Sorts N values downwards (Batcher's odd-even merges).
+template <int N>
+__device__ __forceinline__ void sort_down(uint64_t (&k)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+            for (int j = d % p; j + d < N; j += 2 * d)
+#pragma unroll
+                for (int i = 0; i < d; i++) {
+                    const int x = i + j, y = x + d;
+                    if (y < N && x / (2 * p) == y / (2 * p)) {
+                        // (as a mask: one comparison, where the compiler would take a maximum and a minimum)
+                        const bool swap = __builtin_amdgcn_inverse_ballot_w64(__ballot(k[y] > k[x]));
+                        const uint64_t hi = swap ? k[y] : k[x], lo = swap ? k[x] : k[y];
+                        k[x] = hi;
+                        k[y] = lo;
+                    }
+                }
+}
+
+// LPT lanes per token (64 / LPT tokens per wave); a token's lane l holds experts
+// l EPL .. + EPL - 1, so that of equal keys the lowest lane has the lowest id.
+// Each lane sorts its keys once, into LDS; a round takes the maximum over the
+// token's lanes, and the first lane that has it notes the expert and reads its next.
+// The groups' two largest keys are found by LPT / groups lanes each: the lanes
+// that hold them where the experts fill the token's lanes and the groups are a
+// power of two, otherwise over keys staged in LDS, as groups need not end with a
+// lane.  Bound by the instructions a token takes, for a sigmoid half of them the
+// exponentials and divisions of its scores: T = 8192, E = 256, top-8 of four of
+// eight groups 8.5 us, where its 8.9 MB would take 2 (rescanning a lane's keys
+// after each pick, and one token a wave, 10.7; lists in registers 9.3).
+template <typename T, int EPL, int LPT>
 __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
                                               const float* __restrict__ bias, int32_t* __restrict__ ids,
                                               float* __restrict__ w)
 {
-    __shared__ uint32_t staged[4][EPL * 64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = blockIdx.x * 4 + wave;
-    if (t >= g.T) return;
+    constexpr int TOK = 64 / LPT, MAXE = EPL * LPT;
+    __shared__ __align__(16) uint32_t staged_[4][TOK][MAXE];     // keys, then scores
+    __shared__ uint32_t values_[4][TOK][LPT];                    // of the groups
+    __shared__ uint32_t lists_[4][64][EPL + 1];                  // each lane's keys in order
+    __shared__ int32_t picks_[4][TOK][16];
+    const int lane = threadIdx.x & (LPT - 1), tok = (threadIdx.x & 63) / LPT;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), t0 = (blockIdx.x * 4 + wave) * TOK;
+    if (t0 >= g.T) return;
+    const int t = min(t0 + tok, g.T - 1);               // (past the last token: it again, not stored)
+    auto& staged = staged_[wave][tok];
+    auto& values = values_[wave][tok];
+    auto& picks = picks_[wave][tok];
     const int e0 = lane * EPL;
     float s[EPL];
     uint32_t key[EPL];
     load_logits<T, EPL>(logits + (int64_t)t * ld, e0, g.E, s);
-    uint32_t valid = 0;
+    float b[EPL];                                        // what the selection adds: -inf where the logit is masked
+#pragma unroll
+    for (int q = 0; q < EPL; q++) b[q] = 0.0f;
+    if (bias) load_logits<float, EPL>(bias, e0, g.E, b);
 #pragma unroll
     for (int q = 0; q < EPL; q++) {
         s[q] = clean(s[q]);
-        valid |= (s[q] != -kInf ? 1u : 0u) << q;
+        if (s[q] == -kInf) b[q] = -kInf;
     }
     if (g.score == V4MOE_SCORE_SOFTMAX) {
         uint32_t best = kNone;
 #pragma unroll
         for (int q = 0; q < EPL; q++) best = max(best, order_of(s[q]));
-        best = wave_max(best);
+        best = token_max<LPT>(best);
         const float m = best == kNone ? 0.0f : float_of(best);
-        double sum = 0.0;
+        // (pairs of neighbours, their pairs, ...: the same sums however the experts lie over the lanes)
+        double p[EPL];
 #pragma unroll
         for (int q = 0; q < EPL; q++) {
             s[q] = expf(s[q] - m);
-            sum += (double)s[q];
+            p[q] = (double)s[q];
         }
-        const float total = (float)wave_sum(sum);
+#pragma unroll
+        for (int d = 1; d < EPL; d *= 2)
+#pragma unroll
+            for (int q = 0; q < EPL; q += 2 * d) p[q] += p[q + d];
+        const float total = (float)token_sum<LPT>(p[0]);
 #pragma unroll
         for (int q = 0; q < EPL; q++) s[q] = total > 0.0f ? s[q] / total : 0.0f;
     } else if (g.score == V4MOE_SCORE_SIGMOID) {
@@ -173,36 +260,29 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
 #pragma unroll
         for (int q = 0; q < EPL; q++) s[q] = sqrt_softplus(s[q]);
     }
-    float b[EPL];
 #pragma unroll
-    for (int q = 0; q < EPL; q++) b[q] = 0.0f;
-    if (bias) load_logits<float, EPL>(bias, e0, g.E, b);
-#pragma unroll
-    for (int q = 0; q < EPL; q++) {
-        const float k = bias ? s[q] + b[q] : s[q];
-        key[q] = (valid >> q) & 1 && k == k ? order_of(k) : kNone;
-    }
+    for (int q = 0; q < EPL; q++) key[q] = order_of(fmaxf(s[q] + b[q], -kInf));      // (NaN: -inf)
     if (g.groups > 1) {
         const int size = g.E / g.groups;
         // 2^shift lanes per group, the group's two largest keys in each of them
-        const int shift = 6 - (32 - __builtin_clz(g.groups - 1)), per = 1 << shift;
+        const int shift = __builtin_ctz(LPT) - (32 - __builtin_clz(g.groups - 1)), per = 1 << shift;
         const int mine = lane >> shift;
         uint32_t a = kNone, c = kNone;              // largest and second
         auto merge = [&](uint32_t oa, uint32_t oc) {
             c = max(min(a, oa), max(c, oc));
             a = max(a, oa);
         };
-        const bool own = g.E == 64 * EPL && (g.groups & (g.groups - 1)) == 0;      // those lanes hold the group's keys
+        const bool own = g.E == MAXE && (g.groups & (g.groups - 1)) == 0;      // those lanes hold the group's keys
         if (own) {
 #pragma unroll
             for (int q = 0; q < EPL; q++) merge(key[q], kNone);
         } else {
             // lane i of them takes the group's keys i, i + 2^shift, ... out of LDS
 #pragma unroll
-            for (int q = 0; q < EPL; q++) staged[wave][e0 + q] = key[q];
+            for (int q = 0; q < EPL; q++) staged[e0 + q] = key[q];
             __builtin_amdgcn_wave_barrier();
             if (mine < g.groups)
-                for (int i = lane & (per - 1); i < size; i += per) merge(staged[wave][mine * size + i], kNone);
+                for (int i = lane & (per - 1); i < size; i += per) merge(staged[mine * size + i], kNone);
         }
         if (per > 1) merge(dpp<0xB1>(kNone, a), dpp<0xB1>(kNone, c));
         if (per > 2) merge(dpp<0x4E>(kNone, a), dpp<0x4E>(kNone, c));
@@ -210,19 +290,19 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
         if (per > 8) merge(dpp<0x140>(kNone, a), dpp<0x140>(kNone, c));
         if (per > 16) merge((uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)c, 16));
         const uint32_t v = c == kNone ? a : order_of(float_of(a) + float_of(c));
+        if ((lane & (per - 1)) == 0) values[mine] = v;
+        __builtin_amdgcn_wave_barrier();
         int rank = 0;
 #pragma unroll 4
-        for (int o = 0; o < g.groups; o++) {
-            const uint32_t u = (uint32_t)__builtin_amdgcn_readlane((int)v, o << shift);
-            rank += u >= v + (o < mine ? 0u : 1u) ? 1 : 0;      // larger, or as large with a lower number
-        }
-        const uint64_t kept = __ballot(mine < g.groups && rank < g.topk_groups);
+        for (int o = 0; o < g.groups; o++) rank += values[o] >= v + (o < mine ? 0u : 1u) ? 1 : 0;    // larger, or as large with a lower number
+        const bool keep = mine < g.groups && rank < g.topk_groups;
         if (own) {
-            if (!((kept >> lane) & 1)) {
+            if (!keep) {
 #pragma unroll
                 for (int q = 0; q < EPL; q++) key[q] = kNone;
             }
         } else {
+            const uint64_t kept = __ballot(keep) >> (tok * LPT);
             const float inv = 1.0f / (float)size;
 #pragma unroll
             for (int q = 0; q < EPL; q++) {
@@ -231,44 +311,58 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
             }
         }
     }
-    uint32_t best = kNone, taken = 0;
-    int at = 0;
-    float bs = 0.0f;
-    auto rescan = [&]() {
-        best = kNone;
+    // the lane's keys in order, with EPL - 1 - q below each: of equal ones the lowest expert is the largest
+    uint64_t list[EPL];
 #pragma unroll
-        for (int q = 0; q < EPL; q++)
-            if (key[q] > best) best = key[q], at = q, bs = s[q];
-    };
-    rescan();
-    float my_s = 0.0f;
-    int my_e = 0, j = 0;
-    for (; j < g.topk; j++) {
-        const uint32_t m = wave_max(best);
-        if (m == kNone) break;
-        const int src = __builtin_ctzll(__ballot(best == m));
-        const int e = src * EPL + __builtin_amdgcn_readlane(at, src);
-        const float ps = from_lane(bs, src);
-        if (lane == j) my_e = e, my_s = ps;
-        if (lane == src) {
-            taken |= 1u << at;
+    for (int q = 0; q < EPL; q++) {
+        list[q] = (uint64_t)key[q] << 32 | (uint32_t)(EPL - 1 - q);
+        staged[e0 + q] = __float_as_uint(s[q]);
+    }
+    sort_down(list);
+    std::conditional_t<(EPL > 8), uint64_t, uint32_t> order = 0;        // the q of each, four bits
+    uint32_t* next = lists_[wave][threadIdx.x & 63];
 #pragma unroll
-            for (int q = 0; q < EPL; q++)
-                if (q == at) key[q] = kNone;
-            rescan();
+    for (int q = 0; q < EPL; q++) {
+        order |= (decltype(order))(EPL - 1 - (uint32_t)list[q]) << (4 * q);
+        next[q] = (uint32_t)(list[q] >> 32);
+    }
+    next[EPL] = kNone;
+    uint32_t best = (uint32_t)(list[0] >> 32), taken = 0;
+    int picked = 0;
+    for (int j = 0; j < g.topk; j++) {
+        const uint32_t m = token_max<LPT>(best);
+        const uint64_t hit = __ballot(best == m && m != kNone);
+        if (hit == 0) break;
+        if (m != kNone) picked = j + 1;
+        if (__builtin_amdgcn_inverse_ballot_w64(first_of<LPT>(hit))) {
+            const uint32_t q = (uint32_t)order & 15;
+            best = *++next;
+            order >>= 4;
+            picks[j] = e0 + (int)q;
+            taken |= 1u << q;
         }
     }
     // fewer unmasked experts than slots: the lowest others, weight 0
-    for (; j < g.topk; j++) {
-        const uint32_t free = ~taken & ((1u << EPL) - 1);
-        const int q = free ? __builtin_ctz(free) : EPL;
-        const int src = __builtin_ctzll(__ballot(q < EPL && e0 + q < g.E));
-        const int e = src * EPL + __builtin_amdgcn_readlane(q, src);
-        if (lane == j) my_e = e, my_s = 0.0f;
-        if (lane == src) taken |= 1u << q;
+    if (__ballot(picked < g.topk)) {
+        for (int j = 0; j < g.topk; j++) {
+            const uint32_t open = ~taken & ((1u << EPL) - 1);
+            const int q = open ? __builtin_ctz(open) : EPL;
+            const uint64_t hit = __ballot(j >= picked && q < EPL && e0 + q < g.E);
+            if (__builtin_amdgcn_inverse_ballot_w64(first_of<LPT>(hit))) {
+                picks[j] = e0 + q;
+                taken |= 1u << q;
+            }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    int my_e = 0;
+    float my_s = 0.0f;
+    if (lane < g.topk) {
+        my_e = picks[lane];
+        if (lane < picked) my_s = __uint_as_float(staged[my_e]);
     }
     const float sum = g.renorm ? row_sum(my_s) : 1.0f;       // (topk <= 16: lanes past it hold 0)
-    if (lane < g.topk) {
+    if (lane < g.topk && t0 + tok < g.T) {
         ids[(int64_t)t * g.topk + lane] = my_e;
         w[(int64_t)t * g.topk + lane] = (sum > 0.0f ? my_s / sum : 0.0f) * g.scale;
     }
@@ -393,10 +487,29 @@ template <typename T>
 hipError_t launch_gate(const v4moe_gate& g, const void* logits, int64_t ld, const float* bias, int32_t* ids, float* w,
                        hipStream_t s)
 {
-    for_row(g.E, [&](auto n) {
-        hipLaunchKernelGGL((k_gate<T, decltype(n)::value>), dim3((unsigned)((g.T + 3) / 4)), dim3(256), 0, s, g,
-                           static_cast<const T*>(logits), ld, bias, ids, w);
-    });
+    auto run = [&](auto epl, auto lpt) {
+        constexpr int PER = 4 * 64 / decltype(lpt)::value;        // tokens per block
+        hipLaunchKernelGGL((k_gate<T, decltype(epl)::value, decltype(lpt)::value>), dim3((unsigned)((g.T + PER - 1) / PER)),
+                           dim3(256), 0, s, g, static_cast<const T*>(logits), ld, bias, ids, w);
+    };
+    // Several tokens to a wave share its reductions, but each lane then has more experts to itself: one token a
+    // wave until that fills the card (1024 SIMDs, four waves each).  E = 256, eight of four groups' experts, one
+    // and two tokens a wave: T = 1 4.0 and 4.5 us, 2048 5.1 and 5.5, 4096 6.3 and 5.9, 8192 9.7 and 8.5, 20000 19.4
+    // and 16.6; four of 16 lanes, sixteen experts each, 20000 17.5.  E = 128, one and four: 2048 4.6 and 5.5, 4096
+    // 5.5 and 5.6, 8192 7.8 and 6.1.
+    const bool many = g.T >= 4096;
+    const std::integral_constant<int, 16> quarter;
+    if (many && g.groups <= 16 && g.E <= 32) {
+        run(std::integral_constant<int, 2>{}, quarter);
+    } else if (many && g.groups <= 16 && g.E <= 64) {
+        run(std::integral_constant<int, 4>{}, quarter);
+    } else if (many && g.groups <= 16 && g.E <= 128) {
+        run(std::integral_constant<int, 8>{}, quarter);
+    } else if (many && g.groups <= 32 && g.E <= 256) {
+        run(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{});
+    } else {
+        for_row(g.E, [&](auto n) { run(n, std::integral_constant<int, 64>{}); });
+    }
     return hipGetLastError();
 }
 template <typename T>

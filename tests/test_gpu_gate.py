@@ -150,6 +150,22 @@ def test_row_does_not_depend_on_the_batch():
             assert torch.equal(ids[lo:hi], i2) and torch.equal(w[lo:hi], w2)
 
 
+@pytest.mark.parametrize("score", [0, 1, 2])
+@pytest.mark.parametrize("kind", ["grid", "ties", "masked"])
+@pytest.mark.parametrize("E,k,groups,kept", [(20, 3, 1, 1), (32, 6, 8, 3), (45, 5, 15, 6), (64, 7, 16, 4), (72, 6, 8, 3),
+                                             (128, 16, 8, 4), (100, 2, 1, 1), (96, 6, 32, 9), (160, 5, 20, 7),
+                                             (256, 8, 8, 4), (255, 16, 1, 1), (300, 8, 4, 2)])
+def test_many_tokens(E, k, groups, kept, kind, score):
+    """Batches that put several tokens in a wave, the last wave not full: each row as in a small batch, in every bit."""
+    rng = np.random.default_rng([E, k, score])
+    z = logits_of(rng, 59, E, "f32", kind)
+    b = None if kind == "ties" else torch.randn(E, device=DEV) * 0.1
+    args = dict(score=score, bias=b, groups=groups, topk_groups=kept, renorm=bool(k % 2))
+    ids, w = v4moe.gate(z, k, **args)
+    many, mw = v4moe.gate(z.repeat(70, 1)[:4105], k, **args)
+    assert torch.equal(many, ids.repeat(70, 1)[:4105]) and torch.equal(mw, w.repeat(70, 1)[:4105])
+
+
 def weights64(z, ids, live, score, renorm, scale):
     _, s = scores64(z, score)
     p = np.where(live, np.take_along_axis(s, ids, 1), 0)
