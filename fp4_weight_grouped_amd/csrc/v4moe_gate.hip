@@ -79,18 +79,6 @@ __device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v)
 {
     return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
 }
-// Maximum over the wave, as a scalar: inside the rows of 16 lanes (quad xor 1,
-// xor 2, half-row mirror, mirror), then row 0 into 1 and 2 into 3, then 1 into 3.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
-{
-    v = max(v, dpp<0xB1>(0, v));
-    v = max(v, dpp<0x4E>(0, v));
-    v = max(v, dpp<0x141>(0, v));
-    v = max(v, dpp<0x140>(0, v));
-    v = max(v, dpp<0x142, 0xA>(0, v));
-    v = max(v, dpp<0x143, 0xC>(0, v));
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
 // Sum over the 16 lanes of a row, in every one of them.
 __device__ __forceinline__ float row_sum(float v)
 {
@@ -101,22 +89,6 @@ __device__ __forceinline__ float row_sum(float v)
     add(dpp<0x140>(0, __float_as_uint(v)));
     return v;
 }
-__device__ __forceinline__ float from_lane(float v, int lane)
-{
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
-}
-__device__ __forceinline__ float wave_sum(float v)
-{
-    v = row_sum(v);
-    return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
-}
-__device__ __forceinline__ double wave_sum(double v)
-{
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-    return v;
-}
-
 // Order-preserving map of floats (no NaN) to unsigned integers; -inf is kNone.
 constexpr uint32_t kNone = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_of(float f)
@@ -142,6 +114,21 @@ __device__ __forceinline__ uint32_t token_max(uint32_t v)
     if constexpr (LPT >= 64) {
         const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
         v = max(a[0], a[1]);
+    }
+    return v;
+}
+// ... their sum
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v)
+{
+    v = row_sum(v);
+    if constexpr (LPT >= 32) {
+        const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+    if constexpr (LPT >= 64) {
+        const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
     }
     return v;
 }
@@ -375,19 +362,22 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
 //   dz = ds s (1 - s) | ds sigmoid(z) / (2 s) | p_e (ds_e [picked] - sum_j ds_j p_j),
 // the softmax's last sum zero where the weights are renormalised, which leaves
 // only the picked logits and, as p_j / S = e_j / (sum of the picked e),
-// no need of the others.  One wave per token, lane j < topk its slot j; the
+// no need of the others.  LPT lanes per token, lane j < topk its slot j; the
 // picked logits' parts reach the lanes that write them through LDS.  Bound by HBM
-// where the softmax reaches every logit (read and written once), by the rows'
-// writes elsewhere.
-template <typename T, int EPL>
+// and a token's chain of loads (ids, their logits): where the softmax reaches
+// every logit, T = 19647, E = 256, fp32, 11.5 us for 42 MB, 3.6 TB/s (12.2 with one
+// token a wave); elsewhere only the rows' zeros and picks are written.
+template <typename T, int EPL, int LPT>
 __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
                                                        const int32_t* __restrict__ ids, const float* __restrict__ w,
                                                        const float* __restrict__ dw, T* __restrict__ dl, int64_t ldd)
 {
-    __shared__ __align__(16) float staged[4][EPL * 64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = blockIdx.x * 4 + wave;
-    if (t >= g.T) return;
+    constexpr int TOK = 64 / LPT;
+    __shared__ __align__(16) float staged[4][TOK][EPL * LPT];
+    const int lane = threadIdx.x & (LPT - 1), tok = (threadIdx.x & 63) / LPT;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), t0 = (blockIdx.x * 4 + wave) * TOK;
+    if (t0 >= g.T) return;
+    const int t = min(t0 + tok, g.T - 1);               // (past the last token: it again, not stored)
     const int e0 = lane * EPL;
     const T* row = logits + (int64_t)t * ld;
     const bool soft = g.score == V4MOE_SCORE_SOFTMAX, dense = soft && !g.renorm;
@@ -414,7 +404,7 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
                 best = max(best, order_of(p[q]));
             }
         }
-        best = wave_max(best);
+        best = token_max<LPT>(best);
         m = best == kNone ? 0.0f : float_of(best);
     }
     if (dense) {
@@ -424,7 +414,7 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
             p[q] = expf(p[q] - m);
             sum += p[q];
         }
-        total = wave_sum(sum);
+        total = token_sum<LPT>(sum);
         const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
         for (int q = 0; q < EPL; q++) p[q] *= inv;
@@ -435,7 +425,8 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
     if (g.renorm) {
         const float S = row_sum(s);                  // (lanes past topk <= 16 hold 0)
         float d = 0.0f;
-        for (int j = 0; j < g.topk; j++) d += from_lane(s, j) * (my_dw - from_lane(my_dw, j));
+#pragma unroll 4
+        for (int j = 0; j < g.topk; j++) d += __shfl(s, j, 16) * (my_dw - __shfl(my_dw, j, 16));
         ds = live && S > 0.0f ? g.scale * (d / S) / S : 0.0f;
     }
     float dz;
@@ -443,8 +434,8 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
     else if (g.score == V4MOE_SCORE_SIGMOID) dz = ds * s * (1.0f / (1.0f + expf(z)));
     else dz = ds * sigmoid(z) / (2.0f * s);
     if (!live || s == 0.0f) dz = 0.0f;
-    float* st = staged[wave];
-    const float dot = dense ? from_lane(row_sum(dz), 0) : 0.0f;
+    float* st = staged[wave][tok];
+    const float dot = dense ? token_sum<LPT>(dz) : 0.0f;
 #pragma unroll
     for (int q = 0; q < EPL; q++) st[e0 + q] = dense ? -p[q] * dot : 0.0f;
     __builtin_amdgcn_wave_barrier();
@@ -453,18 +444,38 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
     float out[EPL];
 #pragma unroll
     for (int q = 0; q < EPL; q++) out[q] = st[e0 + q];
-    store_logits<T, EPL>(dl + (int64_t)t * ldd, e0, g.E, out);
+    if (t0 + tok < g.T) store_logits<T, EPL>(dl + (int64_t)t * ldd, e0, g.E, out);
 }
 
-// calls f with the number of 64-expert steps of a row
+// Calls f with the experts per lane and the lanes per token, which hold at least
+// `lanes` groups and a row of E.  Several tokens to a wave share its reductions,
+// but each lane then has more experts to itself: one token a wave until that
+// fills the card (1024 SIMDs, four waves each).  Routing over E = 256, eight of
+// four groups' experts, one and two tokens a wave: T = 1 4.0 and 4.5 us, 2048 5.1
+// and 5.5, 4096 6.3 and 5.9, 8192 9.7 and 8.5, 20000 19.4 and 16.6; four of 16
+// lanes, sixteen experts each, 20000 17.5.  E = 128, one and four: 2048 4.6 and 5.5,
+// 4096 5.5 and 5.6, 8192 7.8 and 6.1.
 template <typename F>
-void for_row(int E, F f)
+void for_row(int T, int E, int lanes, F f)
 {
-    if (E <= 64) f(std::integral_constant<int, 1>{});
-    else if (E <= 128) f(std::integral_constant<int, 2>{});
-    else if (E <= 256) f(std::integral_constant<int, 4>{});
-    else if (E <= 512) f(std::integral_constant<int, 8>{});
-    else f(std::integral_constant<int, 16>{});
+    const std::integral_constant<int, 16> quarter;
+    const std::integral_constant<int, 32> half;
+    const std::integral_constant<int, 64> whole;
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
+    const std::integral_constant<int, 16> sixteen;
+    const bool many = T >= 4096;
+    if (many && lanes <= 16 && E <= 32) f(two, quarter);
+    else if (many && lanes <= 16 && E <= 64) f(four, quarter);
+    else if (many && lanes <= 16 && E <= 128) f(eight, quarter);
+    else if (many && lanes <= 32 && E <= 256) f(eight, half);
+    else if (E <= 64) f(one, whole);
+    else if (E <= 128) f(two, whole);
+    else if (E <= 256) f(four, whole);
+    else if (E <= 512) f(eight, whole);
+    else f(sixteen, whole);
 }
 
 int check_gate(const v4moe_gate* g, int32_t type, const void* logits, int64_t ld)
@@ -487,38 +498,22 @@ template <typename T>
 hipError_t launch_gate(const v4moe_gate& g, const void* logits, int64_t ld, const float* bias, int32_t* ids, float* w,
                        hipStream_t s)
 {
-    auto run = [&](auto epl, auto lpt) {
+    for_row(g.T, g.E, g.groups, [&](auto epl, auto lpt) {
         constexpr int PER = 4 * 64 / decltype(lpt)::value;        // tokens per block
         hipLaunchKernelGGL((k_gate<T, decltype(epl)::value, decltype(lpt)::value>), dim3((unsigned)((g.T + PER - 1) / PER)),
                            dim3(256), 0, s, g, static_cast<const T*>(logits), ld, bias, ids, w);
-    };
-    // Several tokens to a wave share its reductions, but each lane then has more experts to itself: one token a
-    // wave until that fills the card (1024 SIMDs, four waves each).  E = 256, eight of four groups' experts, one
-    // and two tokens a wave: T = 1 4.0 and 4.5 us, 2048 5.1 and 5.5, 4096 6.3 and 5.9, 8192 9.7 and 8.5, 20000 19.4
-    // and 16.6; four of 16 lanes, sixteen experts each, 20000 17.5.  E = 128, one and four: 2048 4.6 and 5.5, 4096
-    // 5.5 and 5.6, 8192 7.8 and 6.1.
-    const bool many = g.T >= 4096;
-    const std::integral_constant<int, 16> quarter;
-    if (many && g.groups <= 16 && g.E <= 32) {
-        run(std::integral_constant<int, 2>{}, quarter);
-    } else if (many && g.groups <= 16 && g.E <= 64) {
-        run(std::integral_constant<int, 4>{}, quarter);
-    } else if (many && g.groups <= 16 && g.E <= 128) {
-        run(std::integral_constant<int, 8>{}, quarter);
-    } else if (many && g.groups <= 32 && g.E <= 256) {
-        run(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{});
-    } else {
-        for_row(g.E, [&](auto n) { run(n, std::integral_constant<int, 64>{}); });
-    }
+    });
     return hipGetLastError();
 }
 template <typename T>
 hipError_t launch_gate_backward(const v4moe_gate& g, const void* logits, int64_t ld, const int32_t* ids, const float* w,
                                 const float* dw, void* dl, int64_t ldd, hipStream_t s)
 {
-    for_row(g.E, [&](auto n) {
-        hipLaunchKernelGGL((k_gate_backward<T, decltype(n)::value>), dim3((unsigned)((g.T + 3) / 4)), dim3(256), 0, s, g,
-                           static_cast<const T*>(logits), ld, ids, w, dw, static_cast<T*>(dl), ldd);
+    for_row(g.T, g.E, 1, [&](auto epl, auto lpt) {
+        constexpr int PER = 4 * 64 / decltype(lpt)::value;
+        hipLaunchKernelGGL((k_gate_backward<T, decltype(epl)::value, decltype(lpt)::value>),
+                           dim3((unsigned)((g.T + PER - 1) / PER)), dim3(256), 0, s, g, static_cast<const T*>(logits), ld,
+                           ids, w, dw, static_cast<T*>(dl), ldd);
     });
     return hipGetLastError();
 }

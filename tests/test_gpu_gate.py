@@ -240,6 +240,25 @@ def test_backward(case, kind, type, renorm, score):
             assert np.allclose(got[:, e], d, rtol=1e-4, atol=1e-6)
 
 
+@pytest.mark.parametrize("score", [0, 1, 2])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(20, 3), (32, 1), (45, 5), (64, 16), (72, 6), (128, 8), (160, 16), (256, 8), (255, 7), (300, 4)])
+def test_backward_many_tokens(E, k, renorm, score):
+    """Several tokens in a wave, the last wave not full: every row to the bar of the small batch."""
+    rng = np.random.default_rng([E, k, score, 9])
+    z = logits_of(rng, 61, E, "f32", "masked")
+    z[:20] = logits_of(rng, 20, E, "f32", "grid")
+    how = dict(score=score, renorm=renorm, scale=2.5)
+    ids, w = v4moe.gate(z, k, **how)
+    dw = torch.from_numpy(rng.standard_normal((61, k)).astype(np.float32)).to(DEV)
+    many = [t.repeat(68, 1)[:4109].contiguous() for t in (z, ids, w, dw)]
+    got = v4moe.gate_backward(*many, **how).cpu().numpy()
+    ref, size = backward64(z.cpu().numpy().astype(np.float64), ids.cpu().numpy().astype(np.int64), w.cpu().numpy() != 0,
+                           dw.cpu().numpy().astype(np.float64), score, renorm, 2.5)
+    ref, bar = (np.tile(a, (68, 1))[:4109] for a in (ref, 4e-6 * size + 1e-30))
+    assert (np.abs(got - ref) <= bar).all(), np.max(np.abs(got - ref) - bar)
+
+
 def test_empty():
     z = torch.zeros(0, 16, device=DEV)
     ids, w = v4moe.gate(z, 2)
