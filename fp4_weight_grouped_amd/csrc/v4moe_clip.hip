@@ -10,7 +10,9 @@
 // again in the same tree, so the norm is the same bits everywhere and on every
 // run.  Bound by HBM: every gradient is read for the norm, and read again and
 // written once the norm is known (the last of them still from the memory-side
-// cache, as the second pass goes backwards).
+// cache, as the second pass goes backwards).  Three fp32 tensors of 268 M elements:
+// the squares 540 us, 6.0 TB/s, the scaling 1197 us, 5.4 TB/s; 23 tensors of 3.0 M
+// together 5.5 and 7.4 us.
 #include "v4moe.h"
 #include "v4moe_device.h"
 #include "v4moe_internal.h"
@@ -22,7 +24,10 @@ namespace v4moe {
 namespace {
 
 constexpr int kTensors = 96;          // tensors per launch: their table travels in the kernel's arguments (< 4 KiB)
-constexpr int kMaxBlocks = 2048;      // partial sums per launch: eight blocks a CU
+// Blocks, and so partial sums, per launch: four a CU.  Twice as many have more
+// partial sums to add again in every block: 3 M fp32 elements 14.8 us (12.9), 300 M
+// 683 (676); half as many leave 10 M at 25.5 (24.5).
+constexpr int kMaxBlocks = 1024;
 constexpr int64_t kMaxElements = 1ll << 36;   // of a tensor: a launch's chunks then fit 31 bits
 constexpr int kThreads = 256;
 
@@ -188,7 +193,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(Table t, int n_partial,
 
 // Elements per chunk for a list of `total`: a power of two of 1024 (one access
 // per thread) to 65536, so that a small list still makes a block per CU and a
-// large one spends its time in the unrolled loop.
+// large one spends its time in the unrolled loop: 3.0 M elements take 15 us in chunks
+// of 1024 and 22 in chunks of 65536, 805 M fp32 ones 1915 and 1745.
 int chunk_of(int64_t total)
 {
     int chunk = 1024;
