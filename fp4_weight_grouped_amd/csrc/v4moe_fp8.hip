@@ -542,17 +542,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
         const uint4 y = *reinterpret_cast<const uint4*>(st + hi + tile * 2048);
         return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
     };
-    // Small wave tiles have all of a chunk's operands in registers, large ones two row tiles of A.
+    // Small wave tiles have all of a chunk's operands in registers, large ones two row tiles of A, or three where
+    // the products of one are too few to cover the read of the next (8192x4096x4096 125.5 -> 121.7 us; 64-row
+    // wave tiles and row scales lose by it: 2048x4096x8192 86 -> 111).
     constexpr bool SMALL = MI * NI <= 4;
-    v8i af[SMALL && MI > 2 ? MI : 2], bf[NI];
+    constexpr int D = MI >= 8 && !ROWS ? 3 : 2;
+    v8i af[SMALL && MI > 2 ? MI : D], bf[NI];
     float sa[MI], bs = 1.0f;
     float4 br[ROWS ? NI : 1];
     v4f p[NI];
-    // operands that every step of chunk c needs, and its first row tile
+    // operands that every step of chunk c needs, and its first row tiles
     auto open = [&](int c) {
         const uint8_t* st = smem + (c / KC % NS) * L::STAGE + (c % KC) * L::CHUNK;
 #pragma unroll
-        for (int i = 0; i < (SMALL ? MI : 1); i++) af[i] = frag(st, alo, ahi, i);
+        for (int i = 0; i < (SMALL ? MI : D - 1); i++) af[i] = frag(st, alo, ahi, i);
 #pragma unroll
         for (int j = 0; j < NI; j++) bf[j] = frag(st, blo, bhi, j);
 #pragma unroll
@@ -609,18 +612,18 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
         const uint8_t* st = smem + (c / KC % NS) * L::STAGE + (c % KC) * L::CHUNK;
 #pragma unroll
         for (int i = 0; i < MI - 1; i++) {
-            af[(i + 1) & 1] = frag(st, alo, ahi, i + 1);
+            if (i + D - 1 < MI) af[(i + D - 1) % D] = frag(st, alo, ahi, i + D - 1);
 #pragma unroll
             for (int j = 0; j < NI; j++) {
                 if (i > 0) add(i - 1, j, sa[i - 1] * bs, br[ROWS ? j : 0]);
-                p[j] = mfma_e4m3(bf[j], af[i & 1]);
+                p[j] = mfma_e4m3(bf[j], af[i % D]);
             }
         }
         mid();
 #pragma unroll
         for (int j = 0; j < NI; j++) {
             if (MI > 1) add(MI - 2, j, sa[MI > 1 ? MI - 2 : 0] * bs, br[ROWS ? j : 0]);
-            p[j] = mfma_e4m3(bf[j], af[(MI - 1) & 1]);
+            p[j] = mfma_e4m3(bf[j], af[(MI - 1) % D]);
         }
         // (with row scales the last tile is added first: both chunks' would not fit the registers)
         const float last = sa[MI - 1] * bs;
@@ -975,8 +978,9 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 // vector memory path (the 32x64 tiles of 128x4096x4096 move 0.4 MB a CU in about 7
 // of their 10 us; deeper rings, two to four chunks a stage and scales through
 // LDS left that as it was), the large ones the matrix pipe next to the copies.
-// At 8192x4096x4096 (128 us, 2.15 PFLOP/s, clock 2.1 GHz, matrix pipe 47% busy)
-// copies of the kernel that leave work out take: no stores of C 115 us, no
+// At 8192x4096x4096 (122 us, 2.25 PFLOP/s; clock 2.1 GHz, matrix pipe half busy)
+// copies of the kernel that leave work out take, of 128 us with two row tiles of A in
+// registers: no stores of C 115 us, no
 // copies into LDS 104, no scaling of the chunk sums 116, neither 87, and without
 // operand reads too 81 us, which is the products (65 us at the pipe's rate) and the
 // ends of the tiles.  64x64 takes two chunks a stage (one: 13.1 / 18.8 / 32.3 us).
