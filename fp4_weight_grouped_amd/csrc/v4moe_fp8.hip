@@ -964,7 +964,7 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 // K = 4096, N = 4096 and M = 16 .. 8192, in a graph of many calls.  Times are nearly
 // proportional to K, so the order holds for others; two blocks of the tiles up to
 // 128x128 share a CU, so that a second round costs less than the first.
-//                 tiles   round 1   2      3      4     each further
+//                 rounds:  1       2      3      4     each further
 //   k_fp8_split   16x16     6.6    10.2   14.0   17.8   3.7
 //   k_fp8_gemm    16x64     9.2    12.3   16.0   20.3   4.0
 //                 32x64    10.2    13.2   17.4   22.5   4.2
