@@ -443,12 +443,12 @@ struct GemmTile {
     static_assert(NI * 16 <= 128 && 128 % (NI * 16) == 0, "a wave's rows of B lie in one 128-row block");
 };
 
-// The tile of a block.  Blocks go to the eight XCDs in turn: XCD x takes the
+// The tile of a block of a product.  Blocks go to the eight XCDs in turn: an XCD x takes the
 // x-th eighth of the tiles, in columns of eight tiles of m, so that the blocks
 // that run together on one XCD share operand rows in its L2.
-__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& tn)
+__device__ __forceinline__ void tile_of(int block, int tiles_m, int tiles_n, int& tm, int& tn)
 {
-    const int n = tiles_m * tiles_n, x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const int n = tiles_m * tiles_n, x = block & 7, i = block >> 3;
     const int each = n >> 3, rest = n & 7;
     const int t = x * each + min(x, rest) + i;
     const int col = t / (8 * tiles_n), rows = min(8, tiles_m - col * 8), in = t - col * 8 * tiles_n;
@@ -461,13 +461,13 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& 
 // direct-to-LDS copies NS-1 stages ahead; 16-byte segments are XOR-swizzled by (row/2)%8, so
 // the 16 rows of an operand read hit distinct banks.
 template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
-__global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles_m, int tiles_n)
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, int block, int tiles_m, int tiles_n)
 {
     using L = GemmTile<WM, WN, MI, NI, NS, KC, ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int tm, tn;
-    tile_of(tiles_m, tiles_n, tm, tn);
+    tile_of(block, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * L::BM, n0 = tn * L::BN;
     const int nch = (g.K + 127) / 128;
     const uint8_t* abase = g.a + (int64_t)m0 * g.lda;
@@ -678,6 +678,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles
     constexpr bool STREAM = L::BM * L::BN >= 128 * 128;
     if (g.c_bf16) store_tile<STREAM, MI, NI>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
     else store_tile<STREAM, MI, NI>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
+}
+
+template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
+__global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm(GemmArgs g, int tiles_m, int tiles_n)
+{
+    gemm_tile<WM, WN, MI, NI, NS, KC, ROWS>(g, blockIdx.x, tiles_m, tiles_n);
+}
+// The two products of a backward in one launch, a's blocks first: block scales
+// for the data gradient, row scales for the weights'.
+template <int WM, int WN, int MI, int NI, int NS, int KC>
+__global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_pair(GemmArgs a, int am, int an, GemmArgs b, int bm, int bn)
+{
+    const int n = am * an;
+    if ((int)blockIdx.x < n) gemm_tile<WM, WN, MI, NI, NS, KC, false>(a, blockIdx.x, am, an);
+    else gemm_tile<WM, WN, MI, NI, NS, KC, true>(b, blockIdx.x - n, bm, bn);
 }
 
 // Few rows: the chunks of a tile of (16 MT) x (16 NT) are spread over the NW
@@ -992,14 +1007,18 @@ constexpr Variant kVariants[] = {
     {16, 16, {6.6f, 10.2f, 14.0f, 17.8f}, 3.7f},   {16, 64, {9.2f, 12.3f, 16.0f, 20.3f}, 4.0f},
     {32, 64, {10.2f, 13.2f, 17.4f, 22.5f}, 4.2f},  {64, 64, {12.5f, 15.7f, 24.6f, 29.1f}, 8.4f},
     {128, 128, {23.0f, 34.0f, 52.0f, 73.0f}, 19.0f}, {256, 256, {58.0f, 124.0f, 186.0f, 248.0f}, 62.0f}};
+int64_t tiles_of(const Variant& k, int64_t M, int64_t N) { return ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn); }
+float time_of(const Variant& k, int64_t tiles)
+{
+    const int64_t rounds = (tiles + 255) / 256;
+    return rounds <= 4 ? k.us[rounds - 1] : k.us[3] + k.further * (float)(rounds - 4);
+}
 int choose_variant(int64_t M, int64_t N)
 {
     int best = 0;
     float least = 0.0f;
     for (int v = 0; v < 6; v++) {
-        const Variant& k = kVariants[v];
-        const int64_t tiles = ((M + k.bm - 1) / k.bm) * ((N + k.bn - 1) / k.bn), rounds = (tiles + 255) / 256;
-        const float us = rounds <= 4 ? k.us[rounds - 1] : k.us[3] + k.further * (float)(rounds - 4);
+        const float us = time_of(kVariants[v], tiles_of(kVariants[v], M, N));
         if (v == 0 || us < least) best = v, least = us;
     }
     return best;
@@ -1021,6 +1040,46 @@ hipError_t run_gemm(const GemmArgs& g, hipStream_t s)
     }
 }
 
+template <int WM, int WN, int MI, int NI, int NS, int KC>
+hipError_t launch_gemm_pair(const GemmArgs& a, const GemmArgs& b, hipStream_t s)
+{
+    using L = GemmTile<WM, WN, MI, NI, NS, KC, true>;          // (the larger LDS of the two)
+    const auto kernel = k_fp8_gemm_pair<WM, WN, MI, NI, NS, KC>;
+    static bool allowed[kMaxDevices];
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
+    auto over = [](int n, int b) { return (n + b - 1) / b; };
+    const int am = over(a.M, L::BM), an = over(a.N, L::BN), bm = over(b.M, L::BM), bn = over(b.N, L::BN);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(am * an + bm * bn)), dim3(64 * L::NW), L::BYTES, s, a, am, an, b, bm, bn);
+    return hipGetLastError();
+}
+
+// A backward's products (block scales, row scales): in one launch of one of the
+// small tiles where the table has that shorter, the contractions weighing in: one
+// product's last round is then filled by the other's tiles, and a launch falls
+// away (1237x1999x1001, 320 and 512 tiles of 64x64: 13.4 + 10.6 us apart, 20.9
+// together, and 33.8 -> 29.9 of the whole call).
+hipError_t run_gemm_pair(const GemmArgs& a, const GemmArgs& b, hipStream_t s)
+{
+    auto alone = [](const GemmArgs& g) {
+        const Variant& k = kVariants[choose_variant(g.M, g.N)];
+        return time_of(k, tiles_of(k, g.M, g.N)) * (float)g.K;
+    };
+    float least = alone(a) + alone(b);
+    int best = 0;
+    for (int v = 1; v <= 3; v++) {
+        const int64_t na = tiles_of(kVariants[v], a.M, a.N), nb = tiles_of(kVariants[v], b.M, b.N);
+        const float us = time_of(kVariants[v], na + nb) * (float)((double)(na * a.K + nb * b.K) / (double)(na + nb));
+        if (us < least) best = v, least = us;
+    }
+    switch (best) {
+    case 1: return launch_gemm_pair<1, 4, 1, 1, 4, 1>(a, b, s);
+    case 2: return launch_gemm_pair<2, 2, 1, 2, 4, 1>(a, b, s);
+    case 3: return launch_gemm_pair<2, 2, 2, 2, 2, 2>(a, b, s);
+    }
+    if (const hipError_t e = run_gemm<false>(a, s); e != hipSuccess) return e;
+    return run_gemm<true>(b, s);
+}
+
 bool type_ok(int t) { return t == V4MOE_TYPE_F32 || t == V4MOE_TYPE_BF16; }
 size_t type_size(int t) { return t == V4MOE_TYPE_F32 ? 4 : 2; }
 constexpr int64_t kMaxSide = 1 << 22;     // rows times this many bytes of a tile stay below 2^31
@@ -1031,6 +1090,11 @@ int check_matrix(const void* x, int type, int64_t R, int64_t C, int64_t ld)
     if (!type_ok(type) || ld < C || ld > (1ll << 40)) return V4MOE_EDIMS;
     if (R > 0 && C > 0 && !x) return V4MOE_ENULL;
     return aligned_to(x, type_size(type)) ? V4MOE_OK : V4MOE_EALIGN;
+}
+GemmArgs gemm_args(const v4moe_gemm& p, const uint8_t* a, const float* as, const uint8_t* b, const float* bs, void* c)
+{
+    return GemmArgs{p.M, p.N, p.K, a, p.lda, as, b, p.ldb, bs, p.bs_n, p.bs_k, c, p.ldc,
+                    p.c_type == V4MOE_TYPE_BF16, p.accumulate != 0};
 }
 bool side_ok(int64_t n) { return n >= 0 && n <= kMaxSide; }
 
@@ -1115,10 +1179,9 @@ __attribute__((visibility("default"))) int moe_fp8_gemm(const v4moe_gemm* p, con
     if (p->K > 0 && (!a || !as || !b || !bs)) return V4MOE_ENULL;
     if (!aligned_to(a, 16) || !aligned_to(b, 16) || !aligned_to(as, 4) || !aligned_to(bs, 4)) return V4MOE_EALIGN;
     if (!device_ready()) return V4MOE_EDEVICE;
-    const bool bf16 = p->c_type == V4MOE_TYPE_BF16, rows = p->b_scale == V4MOE_SCALE_ROW;
-    const GemmArgs g{p->M, p->N, p->K, a, p->lda, as, b, p->ldb, bs, p->bs_n, p->bs_k, c, p->ldc, bf16, p->accumulate != 0};
+    const GemmArgs g = gemm_args(*p, a, as, b, bs, c);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return (rows ? run_gemm<true>(g, s) : run_gemm<false>(g, s)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+    return (p->b_scale == V4MOE_SCALE_ROW ? run_gemm<true>(g, s) : run_gemm<false>(g, s)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }
 
 __attribute__((visibility("default"))) size_t moe_fp8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K,
@@ -1203,16 +1266,17 @@ __attribute__((visibility("default"))) int moe_fp8_linear_backward(
     } else if (M > 0) {
         if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, ws + L.dq, f32(L.ds), nullptr, nullptr, stream)) return rc;
     }
-    if (dx && M > 0) {
-        // dx = dy W: contraction over N, block (i, c) of W^T is block (c, i) of W
-        const v4moe_gemm g{M, K, (int32_t)up16(N), V4MOE_SCALE_BLOCK, dx_type, 0, up16(N), up16(N), lddx, 1, chunks(K)};
-        if (const int rc = moe_fp8_gemm(&g, ws + L.dq, f32(L.ds), w->qt, w->blk, dx, stream)) return rc;
+    // dx = dy W: contraction over N, block (i, c) of W^T is block (c, i) of W
+    const v4moe_gemm gx{M, K, (int32_t)up16(N), V4MOE_SCALE_BLOCK, dx_type, 0, up16(N), up16(N), lddx, 1, chunks(K)};
+    // dW = dy^T x: contraction over the tokens, both scales per row
+    const v4moe_gemm gw{N, K, (int32_t)up16(M), V4MOE_SCALE_ROW, dw_type, accumulate, up16(M), up16(M), lddw, 0, 0};
+    if (dx && dw && M > 0) {
+        const GemmArgs a = gemm_args(gx, ws + L.dq, f32(L.ds), w->qt, w->blk, dx);
+        const GemmArgs b = gemm_args(gw, ws + L.dt, f32(L.dts), ws + L.xt, f32(L.xts), dw);
+        return run_gemm_pair(a, b, static_cast<hipStream_t>(stream)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
     }
-    if (dw) {
-        // dW = dy^T x: contraction over the tokens, both scales per row
-        const v4moe_gemm g{N, K, (int32_t)up16(M), V4MOE_SCALE_ROW, dw_type, accumulate, up16(M), up16(M), lddw, 0, 0};
-        if (const int rc = moe_fp8_gemm(&g, ws + L.dt, f32(L.dts), ws + L.xt, f32(L.xts), dw, stream)) return rc;
-    }
+    if (dx && M > 0) return moe_fp8_gemm(&gx, ws + L.dq, f32(L.ds), w->qt, w->blk, dx, stream);
+    if (dw) return moe_fp8_gemm(&gw, ws + L.dt, f32(L.dts), ws + L.xt, f32(L.xts), dw, stream);
     return V4MOE_OK;
 }
 

@@ -228,6 +228,23 @@ def test_linear(shape, type):
     assert bool(((dw32.double() - 1 - ref).abs() <= bar(ref, tol, torch.float32) + 2.0 ** -23 * (1 + ref.abs())).all())
 
 
+@pytest.mark.parametrize("shape", [(1, 128, 256), (40, 300, 520), (300, 1000, 900), (1237, 999, 1001), (700, 2100, 130),
+                                   (2100, 1500, 3000), (130, 4100, 4000)], ids=str)
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_backward_is_its_products(shape, accumulate):
+    """Both gradients in one launch or two, alone or together: the bits of the products of the quantised operands."""
+    M, N, K = shape
+    x, dy = source(5, M, K, torch.bfloat16), source(6, M, N, torch.bfloat16)
+    w = v4moe.fp8_weights(source(7, N, K, torch.float32))
+    q, s, qt, st = v4moe.fp8_quantize(dy, True, True)
+    _, _, xt, xts = v4moe.fp8_quantize(x, False, True)
+    old = torch.randn(N, K, device=DEV)
+    rdx = v4moe.fp8_gemm(q, s, w.qt, w.blk.t(), False, out=torch.empty(M, K, dtype=torch.bfloat16, device=DEV))
+    rdw = v4moe.fp8_gemm(qt, st, xt, xts, True, out=torch.empty(N, K, device=DEV))
+    dx, dw = v4moe.fp8_linear_backward(x, dy, w, dw=old.clone(), accumulate=accumulate)
+    assert torch.equal(dx, rdx) and torch.equal(dw, rdw + old if accumulate else rdw)
+
+
 @pytest.mark.parametrize("shape", [(1, 2048, 2048), (16, 256, 4096), (9, 64, 8), (40, 512, 1000), (5, 33, 1048)], ids=str)
 def test_linear_of_few_rows(shape):
     """bf16 rows at 16-byte addresses are quantised inside the product; others beforehand: the same bits."""
