@@ -174,17 +174,21 @@ __global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, int lg, co
 #pragma unroll
     for (int h = 0; h < 2; h++) f[h].load(x + (int64_t)r * ldx + min(at + 8 * h, C - 1), C - at - 8 * h);
     const Divisor d(group_scale(lanes_max<8>(max(largest(f[0]), largest(f[1])))));
-    if (at < C)
-        *reinterpret_cast<uint4*>(q + (int64_t)r * ldq + at) =
-            make_uint4(d.codes4(f[0][0], f[0][1], f[0][2], f[0][3]), d.codes4(f[0][4], f[0][5], f[0][6], f[0][7]),
-                       d.codes4(f[1][0], f[1][1], f[1][2], f[1][3]), d.codes4(f[1][4], f[1][5], f[1][6], f[1][7]));
+    uint4 codes;
+    if (d.y != 0.0f)
+        codes = make_uint4(d.quick4(f[0][0], f[0][1], f[0][2], f[0][3]), d.quick4(f[0][4], f[0][5], f[0][6], f[0][7]),
+                           d.quick4(f[1][0], f[1][1], f[1][2], f[1][3]), d.quick4(f[1][4], f[1][5], f[1][6], f[1][7]));
+    else
+        codes = make_uint4(d.codes4(f[0][0], f[0][1], f[0][2], f[0][3]), d.codes4(f[0][4], f[0][5], f[0][6], f[0][7]),
+                           d.codes4(f[1][0], f[1][1], f[1][2], f[1][3]), d.codes4(f[1][4], f[1][5], f[1][6], f[1][7]));
+    if (at < C) *reinterpret_cast<uint4*>(q + (int64_t)r * ldq + at) = codes;
     if ((threadIdx.x & 7) == 0) s[(int64_t)c * R + r] = d.s;
 }
 
 // One 128x128 tile of x [R][C] per block, read once for both orders: thread t
 // holds rows 4(t/16) .. +3, columns 8(t%16) .. +7 as they are in memory.  Bound by
 // HBM, next to the tile's own latency and instructions: 16384x4096 fp32 weights
-// 81 us (403 MB, 4.9 TB/s); 8192x2048 bf16 in both orders and 8192x4096 by columns
+// 77 us (403 MB, 5.2 TB/s; 83 with a branch per row); 8192x2048 bf16 in both orders and 8192x4096 by columns
 // in one launch 35 us (169 MB, 4.9 TB/s).  What helps is waves per CU (eight rows
 // per thread took 47 us for the latter where four took 40, with the elements kept
 // as floats or the next tile's loads out a tile ahead 60) and fewer instructions
@@ -233,17 +237,36 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
 #pragma unroll
     for (int i = 0; i < NR; i++)
         f[i].load(x + (int64_t)min(r0 + rt + i, R - 1) * ldx + min(c0 + ct, C - 1), r0 + rt + i < R ? C - c0 - ct : 0);
-    auto store_row = [&](int i, const Divisor& d) {
-        if (r0 + rt + i < R && c0 + ct < cpad)
-            *reinterpret_cast<uint2*>(q + (int64_t)(r0 + rt + i) * ldq + c0 + ct) =
-                make_uint2(d.codes4(f[i][0], f[i][1], f[i][2], f[i][3]), d.codes4(f[i][4], f[i][5], f[i][6], f[i][7]));
+    // rows' codes; together, so that no branch stands between one's divisions and the next's
+    auto store_rows = [&](const Divisor (&d)[NR]) {
+        uint2 codes[NR];
+        bool quick = true;
+#pragma unroll
+        for (int i = 0; i < NR; i++) quick = quick && d[i].y != 0.0f;
+        if (quick) {
+#pragma unroll
+            for (int i = 0; i < NR; i++)
+                codes[i] = make_uint2(d[i].quick4(f[i][0], f[i][1], f[i][2], f[i][3]), d[i].quick4(f[i][4], f[i][5], f[i][6], f[i][7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NR; i++)
+                codes[i] = make_uint2(d[i].codes4(f[i][0], f[i][1], f[i][2], f[i][3]), d[i].codes4(f[i][4], f[i][5], f[i][6], f[i][7]));
+        }
+#pragma unroll
+        for (int i = 0; i < NR; i++)
+            if (r0 + rt + i < R && c0 + ct < cpad) *reinterpret_cast<uint2*>(q + (int64_t)(r0 + rt + i) * ldq + c0 + ct) = codes[i];
     };
     if constexpr (MODE & kQuantRows) {
+        uint32_t big[NR];
 #pragma unroll
-        for (int i = 0; i < NR; i++) {
-            const Divisor d(group_scale(lanes_max<16>(largest(f[i]))));
-            store_row(i, d);
-            if ((t & 15) == 0 && r0 + rt + i < R) s[(int64_t)bx * R + r0 + rt + i] = d.s;
+        for (int i = 0; i < NR; i++) big[i] = lanes_max<16>(largest(f[i]));
+        const Divisor d[NR] = {Divisor(group_scale(big[0])), Divisor(group_scale(big[1])), Divisor(group_scale(big[2])),
+                               Divisor(group_scale(big[3]))};
+        store_rows(d);
+        if ((t & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < NR; i++)
+                if (r0 + rt + i < R) s[(int64_t)bx * R + r0 + rt + i] = d[i].s;
         }
     }
     // largest magnitude of each column in the wave's 16 rows, a word's columns together
@@ -285,8 +308,8 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
         for (int o = 1; o < 64; o <<= 1) all = max(all, (uint32_t)__shfl_xor((int)all, o));
         d8[0] = Divisor(group_scale(all));
         if (t == 0) s[tile] = d8[0].s;
-#pragma unroll
-        for (int i = 0; i < NR; i++) store_row(i, d8[0]);
+        const Divisor d[NR] = {d8[0], d8[0], d8[0], d8[0]};
+        store_rows(d);
 #pragma unroll
         for (int u = 1; u < 8; u++) d8[u] = d8[0];
     } else {
