@@ -245,6 +245,26 @@ def test_backward_is_its_products(shape, accumulate):
     assert torch.equal(dx, rdx) and torch.equal(dw, rdw + old if accumulate else rdw)
 
 
+@pytest.mark.parametrize("shape", [(5, 70, 200), (300, 520, 390), (1030, 1500, 2100)], ids=str)
+@pytest.mark.parametrize("types", [(torch.float32, torch.float32), (torch.float32, torch.bfloat16),
+                                   (torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16)], ids=str)
+def test_backward_of_one_operand(shape, types):
+    """dx or dW alone, x and dy of either type: the bits of both together."""
+    M, N, K = shape
+    x, dy = source(5, M, K, types[0], 3, 1), source(6, M, N, types[1], 8)
+    w = v4moe.fp8_weights(source(7, N, K, torch.float32))
+    dx, dw = v4moe.fp8_linear_backward(x, dy, w)
+    n = v4moe.moe_fp8_linear_workspace_bytes(M, N, K, 1)
+    ws, P, c = torch.empty(n, dtype=torch.uint8, device=DEV), v4moe._p, w.c()
+    code = {torch.float32: v4moe.TYPE_F32, torch.bfloat16: v4moe.TYPE_BF16}
+    args = (P(x), code[types[0]], x.stride(0), P(dy), code[types[1]], dy.stride(0), v4moe.ctypes.byref(c))
+    for one in (dx, dw):
+        got = torch.empty_like(one)
+        to = (P(got), v4moe.TYPE_BF16, K, None, v4moe.TYPE_BF16, K) if one is dx else (None, v4moe.TYPE_BF16, K, P(got), v4moe.TYPE_BF16, K)
+        assert v4moe.lib().moe_fp8_linear_backward(M, *args, *to, 0, P(ws), n, v4moe._stream()) == 0
+        assert torch.equal(got, one)
+
+
 @pytest.mark.parametrize("shape", [(1, 2048, 2048), (16, 256, 4096), (9, 64, 8), (40, 512, 1000), (5, 33, 1048)], ids=str)
 def test_linear_of_few_rows(shape):
     """bf16 rows at 16-byte addresses are quantised inside the product; others beforehand: the same bits."""
