@@ -349,6 +349,15 @@ def _on_device(t: torch.Tensor, what: str) -> int:
     return _raw_stream(i)
 
 
+def _empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """A new [rows][cols] tensor (strides spelled out: a call's time is the host's where the work is small)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _bytes(n: int, device) -> torch.Tensor:
+    return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device)
+
+
 def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dtype=None) -> int:
     """t's leading dimension, after checking that it is [rows][cols] with contiguous columns on a GPU."""
     if not t.is_cuda:
@@ -384,8 +393,8 @@ def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Opti
     b = None if bias is None else _dense(bias, (E,), torch.float32, "bias")
     g = GateC(T, E, topk, score, groups, topk_groups, 1 if renorm else 0, scale)
     dev = logits.device
-    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-    w = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    ids = _empty(T, topk, torch.int32, dev)
+    w = _empty(T, topk, torch.float32, dev)
     _check(lib().moe_gate(ctypes.byref(g), logits.data_ptr(), _type(logits), ld, b, ids.data_ptr(), w.data_ptr(), stream))
     return ids, w
 
@@ -401,7 +410,7 @@ def gate_backward(logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Te
     w = _dense(topk_w, (T, k), torch.float32, "topk_w")
     d = _dense(dw, (T, k), torch.float32, "dw")
     g = GateC(T, E, k, score, 1, 1, 1 if renorm else 0, scale)
-    dl = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    dl = _empty(T, E, logits.dtype, logits.device)
     _check(lib().moe_gate_backward(ctypes.byref(g), logits.data_ptr(), _type(logits), ld, ids, w, d, dl.data_ptr(), E,
                                    stream))
     return dl
@@ -426,9 +435,14 @@ class FP8Matrix:
 
     def c(self) -> FP8MatC:
         N, K = self.N, self.K
-        return FP8MatC(N, K, _dense(self.q, (N, _up16(K)), torch.uint8, "q"),
-                       _dense(self.qt, (K, _up16(N)), torch.uint8, "qt"),
-                       _dense(self.blk, (_chunks(N), _chunks(K)), torch.float32, "blk"))
+        q, qt, blk = _fp8_shapes(N, K)
+        return FP8MatC(N, K, _dense(self.q, q, torch.uint8, "q"), _dense(self.qt, qt, torch.uint8, "qt"),
+                       _dense(self.blk, blk, torch.float32, "blk"))
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_shapes(N: int, K: int):
+    return (N, _up16(K)), (K, _up16(N)), (_chunks(N), _chunks(K))
 
 
 def fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False):
@@ -437,10 +451,10 @@ def fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False):
     ld = _matrix(x, M, K, "x")
     stream = _on_device(x, "x")
     dev = x.device
-    q = torch.empty((M, _up16(K)), dtype=torch.uint8, device=dev) if rows else None
-    s = torch.empty((_chunks(K), M), dtype=torch.float32, device=dev) if rows else None
-    qt = torch.empty((K, _up16(M)), dtype=torch.uint8, device=dev) if cols else None
-    st = torch.empty((_chunks(M), K), dtype=torch.float32, device=dev) if cols else None
+    q = _empty(M, _up16(K), torch.uint8, dev) if rows else None
+    s = _empty(_chunks(K), M, torch.float32, dev) if rows else None
+    qt = _empty(K, _up16(M), torch.uint8, dev) if cols else None
+    st = _empty(_chunks(M), K, torch.float32, dev) if cols else None
     _check(lib().moe_fp8_quantize(M, K, x.data_ptr(), _type(x), ld, _p(q), _p(s), _p(qt), _p(st), stream))
     return q, s, qt, st
 
@@ -451,9 +465,9 @@ def fp8_weights(w: torch.Tensor) -> FP8Matrix:
     ld = _matrix(w, N, K, "w")
     stream = _on_device(w, "w")
     dev = w.device
-    m = FP8Matrix(N, K, torch.empty((N, _up16(K)), dtype=torch.uint8, device=dev),
-                  torch.empty((K, _up16(N)), dtype=torch.uint8, device=dev),
-                  torch.empty((_chunks(N), _chunks(K)), dtype=torch.float32, device=dev))
+    m = FP8Matrix(N, K, _empty(N, _up16(K), torch.uint8, dev),
+                  _empty(K, _up16(N), torch.uint8, dev),
+                  _empty(_chunks(N), _chunks(K), torch.float32, dev))
     _check(lib().moe_fp8_quantize_weights(N, K, w.data_ptr(), _type(w), ld, m.q.data_ptr(), m.qt.data_ptr(),
                                           m.blk.data_ptr(), stream))
     return m
@@ -476,7 +490,7 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
         sb, bs = b_scale.data_ptr(), b_scale.stride()
     if out is None:
         _require(not accumulate, "accumulate needs out")
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty(M, N, torch.bfloat16, a.device)
     ldc = _matrix(out, M, N, "out")
     g = GemmC(M, N, K, SCALE_ROW if rows else SCALE_BLOCK, _type(out), 1 if accumulate else 0, lda, ldb, ldc, bs[0], bs[1])
     _check(lib().moe_fp8_gemm(ctypes.byref(g), a.data_ptr(), sa, b.data_ptr(), sb, out.data_ptr(), stream))
@@ -495,12 +509,12 @@ def fp8_linear(x: torch.Tensor, w: FP8Matrix, out: Optional[torch.Tensor] = None
     stream = _on_device(x, "x")
     dev = x.device
     if out is None:
-        out, ldy, ty = torch.empty((M, N), dtype=torch.bfloat16, device=dev), N, TYPE_BF16
+        out, ldy, ty = _empty(M, N, torch.bfloat16, dev), N, TYPE_BF16
     else:
         ldy, ty = _matrix(out, M, N, "out"), _type(out)
     c = w.c()
     n = moe_fp8_linear_workspace_bytes(M, N, K, 0)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    ws = _bytes(n, dev)
     _check(lib().moe_fp8_linear(M, x.data_ptr(), _type(x), ldx, ctypes.byref(c), out.data_ptr(), ty, ldy, ws.data_ptr(), n,
                                 stream))
     return out
@@ -515,13 +529,13 @@ def fp8_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: FP8Matrix, dx: Opt
     dev = x.device
     _require(dw is not None or not accumulate, "accumulate needs dw")
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dx = _empty(M, K, torch.bfloat16, dev)
     if dw is None:
-        dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        dw = _empty(N, K, torch.bfloat16, dev)
     lddx, lddw = _matrix(dx, M, K, "dx"), _matrix(dw, N, K, "dw")
     c = w.c()
     n = moe_fp8_linear_workspace_bytes(M, N, K, 1)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    ws = _bytes(n, dev)
     _check(lib().moe_fp8_linear_backward(M, x.data_ptr(), _type(x), ldx, dy.data_ptr(), _type(dy), lddy, ctypes.byref(c),
                                          dx.data_ptr(), _type(dx), lddx, dw.data_ptr(), _type(dw), lddw,
                                          1 if accumulate else 0, ws.data_ptr(), n, stream))
@@ -557,7 +571,7 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
         raise TypeError(f"float32 or bfloat16 expected, got {e.args[0]}") from None
     norm = torch.empty((), dtype=torch.float32, device=dev)
     size = _clip_workspace_bytes(n)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    ws = _bytes(size, dev)
     _check(lib().moe_clip_grads(n, table.buffer_info()[0], max_norm, norm.data_ptr(), ws.data_ptr(), size, stream))
     return norm
 
