@@ -1233,8 +1233,15 @@ __attribute__((visibility("default"))) int moe_fp8_linear(int32_t M, const void*
         // few rows: the product quantises x itself
         if (!device_ready()) return V4MOE_EDEVICE;
         const GemmArgs g{M, N, K16, nullptr, 0, nullptr, w->q, K16, w->blk, chunks(K), 1, y, ldy, y_bf16, 0};
-        return launch_split<1, 1, 8, false, true>(g, static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(x), ldx,
-                                                  K) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+        const hipStream_t s = static_cast<hipStream_t>(stream);
+        const uint16_t* xb = static_cast<const uint16_t*>(x);
+        // Sixteen waves (and chunks) at a time where a CU has one tile and more than eight chunks to do: one row by
+        // 4096x2048 5.8 us (eight waves: 6.5), by 4096x4096 8.7 (10.5), by 4096x8192 14.4 (19.2).  Where several
+        // tiles share a CU two such blocks do not: by 16384x2048 17.8 (15.3).
+        const bool many = chunks(K) > 8 && tiles_of(kVariants[0], M, N) <= 256;
+        const hipError_t e = many ? launch_split<1, 1, 16, false, true>(g, s, xb, ldx, K)
+                                  : launch_split<1, 1, 8, false, true>(g, s, xb, ldx, K);
+        return e == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* xs = reinterpret_cast<float*>(ws + L.xs);

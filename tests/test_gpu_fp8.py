@@ -265,7 +265,8 @@ def test_backward_of_one_operand(shape, types):
         assert torch.equal(got, one)
 
 
-@pytest.mark.parametrize("shape", [(1, 2048, 2048), (16, 256, 4096), (9, 64, 8), (40, 512, 1000), (5, 33, 1048)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 2048, 2048), (16, 256, 4096), (9, 64, 8), (40, 512, 1000), (5, 33, 1048), (3, 100, 2056),
+                                   (16, 4000, 1096), (4300, 16, 1200)], ids=str)
 def test_linear_of_few_rows(shape):
     """bf16 rows at 16-byte addresses are quantised inside the product; others beforehand: the same bits."""
     M, N, K = shape
