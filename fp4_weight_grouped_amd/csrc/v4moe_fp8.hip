@@ -726,7 +726,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_pair(GemmArgs a, int 
 // so the same bits, as k_fp8_gemm.  X (MT = 1): A is x itself (bf16), each
 // chunk quantised by the wave that needs it, in every block: 16 rows cost less
 // than a launch of their own.
-// Bound by latency, then by the weights' bytes.
+// Bound by latency, then by the weights' bytes: one row by 4096x2048 5.8 us, the
+// 8.4 MB of weights at 1.4 TB/s; 16 rows of codes by 4096x4096 6.6 us, 2.5 TB/s.
 template <int MT, int NT, int NW, bool ROWS, bool X>
 struct SplitLds {
     static constexpr int P = 16 * MT * (16 * NT + 4);          // floats of a chunk's products (rows padded)
