@@ -63,7 +63,9 @@ __device__ __forceinline__ float group_scale(uint32_t mag)
 // the two are equal.  The others (y = 0) divide; a NaN scale gives codes 0.
 struct Divisor {
     float s, y;
-    __device__ __forceinline__ explicit Divisor(float scale) : s(scale), y(scale > 0x1p-80f && scale < 0x1p80f ? 1.0f / scale : 0.0f) {}
+    Divisor() = default;
+    __device__ __forceinline__ explicit Divisor(float scale)
+        : s(scale), y(scale > 0x1p-80f && scale < 0x1p80f ? 1.0f / scale : 0.0f) {}
     __device__ __forceinline__ Divisor(float scale, float inverse) : s(scale), y(inverse) {}
     __device__ __forceinline__ float corrected(float x) const
     {
@@ -122,7 +124,7 @@ struct Raw {
         } else {
 #pragma unroll
             for (int u = 0; u < 8; u++) {
-                const uint32_t b = u < n ? (sizeof(T) == 4 ? __float_as_uint(load_f32(p + u)) : __float_as_uint(load_f32(p + u)) >> 16) : 0u;
+                const uint32_t f = u < n ? __float_as_uint(load_f32(p + u)) : 0u, b = sizeof(T) == 4 ? f : f >> 16;
                 if constexpr (sizeof(T) == 4) w[u >> 2][u & 3] = b;
                 else w[0][u >> 1] = u & 1 ? w[0][u >> 1] | (b << 16) : b;
             }
@@ -139,7 +141,8 @@ template <typename T>
 __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b)
 {
     if constexpr (sizeof(T) == 4) return max(a, b);
-    else return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+    else return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                       __builtin_bit_cast(u16x2, b)));
 }
 // ... and of a word alone, as the bits of an fp32
 template <typename T>
@@ -167,7 +170,8 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, int lg, const T* __restrict__ x, int64_t ldx,
                                                         uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
 {
-    const int g = threadIdx.x >> 3, r = blockIdx.x * (32 >> lg) + (g >> lg), c = ((int)blockIdx.y << lg) + (g & ((1 << lg) - 1));
+    const int g = threadIdx.x >> 3;
+    const int r = blockIdx.x * (32 >> lg) + (g >> lg), c = ((int)blockIdx.y << lg) + (g & ((1 << lg) - 1));
     if (r >= R || c * 128 >= C) return;                   // whole groups of lanes
     const int at = c * 128 + 16 * (threadIdx.x & 7);
     Raw<T> f[2];
@@ -188,8 +192,8 @@ __global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, int lg, co
 // One 128x128 tile of x [R][C] per block, read once for both orders: thread t
 // holds rows 4(t/16) .. +3, columns 8(t%16) .. +7 as they are in memory.  Bound by
 // HBM, next to the tile's own latency and instructions: 16384x4096 fp32 weights
-// 77 us (403 MB, 5.2 TB/s; 83 with a branch per row); 8192x2048 bf16 in both orders and 8192x4096 by columns
-// in one launch 35 us (169 MB, 4.9 TB/s).  What helps is waves per CU (eight rows
+// 77 us (403 MB, 5.2 TB/s; 83 with a branch per row); 8192x2048 bf16 in both orders
+// and 8192x4096 by columns in one launch 35 us (169 MB, 4.9 TB/s).  What helps is waves per CU (eight rows
 // per thread took 47 us for the latter where four took 40, with the elements kept
 // as floats or the next tile's loads out a tile ahead 60) and fewer instructions
 // (40 -> 35: bf16 magnitudes two to an operation, their maxima over lanes by
@@ -246,15 +250,18 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
         if (quick) {
 #pragma unroll
             for (int i = 0; i < NR; i++)
-                codes[i] = make_uint2(d[i].quick4(f[i][0], f[i][1], f[i][2], f[i][3]), d[i].quick4(f[i][4], f[i][5], f[i][6], f[i][7]));
+                codes[i] = make_uint2(d[i].quick4(f[i][0], f[i][1], f[i][2], f[i][3]),
+                                      d[i].quick4(f[i][4], f[i][5], f[i][6], f[i][7]));
         } else {
 #pragma unroll
             for (int i = 0; i < NR; i++)
-                codes[i] = make_uint2(d[i].codes4(f[i][0], f[i][1], f[i][2], f[i][3]), d[i].codes4(f[i][4], f[i][5], f[i][6], f[i][7]));
+                codes[i] = make_uint2(d[i].codes4(f[i][0], f[i][1], f[i][2], f[i][3]),
+                                      d[i].codes4(f[i][4], f[i][5], f[i][6], f[i][7]));
         }
 #pragma unroll
         for (int i = 0; i < NR; i++)
-            if (r0 + rt + i < R && c0 + ct < cpad) *reinterpret_cast<uint2*>(q + (int64_t)(r0 + rt + i) * ldq + c0 + ct) = codes[i];
+            if (r0 + rt + i < R && c0 + ct < cpad)
+                *reinterpret_cast<uint2*>(q + (int64_t)(r0 + rt + i) * ldq + c0 + ct) = codes[i];
     };
     if constexpr (MODE & kQuantRows) {
         uint32_t big[NR];
@@ -289,7 +296,8 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
     if (lane < 16) {
 #pragma unroll
         for (int h = 0; h < Raw<T>::W; h++)
-            *reinterpret_cast<uint4*>(&mx[wave][(lane * Raw<T>::W + h) * 4]) = make_uint4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
+            *reinterpret_cast<uint4*>(&mx[wave][(lane * Raw<T>::W + h) * 4]) =
+                make_uint4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
     }
     __syncthreads();
     constexpr int WORDS = 128 * sizeof(T) / 4;           // of a tile's row
@@ -299,8 +307,7 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
         for (int i = 1; i < NW; i++) v = max_word<T>(v, mx[i][c]);
         return v;
     };
-    Divisor d8[8] = {Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f),
-                     Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f), Divisor(1.0f, 1.0f)};
+    Divisor d8[8];
     if constexpr (MODE & kQuantBlock) {
         uint32_t all = word_mag<T>(word(lane));
         if constexpr (WORDS == 128) all = max(all, word_mag<T>(word(64 + lane)));
@@ -326,7 +333,8 @@ __device__ __forceinline__ void quant_tile(const QuantJob<T>& job, int tile, Qua
         __syncthreads();
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const float4 sc = *reinterpret_cast<const float4*>(&mx[0][ct + 4 * h]), in = *reinterpret_cast<const float4*>(&mx[1][ct + 4 * h]);
+            const float4 sc = *reinterpret_cast<const float4*>(&mx[0][ct + 4 * h]);
+            const float4 in = *reinterpret_cast<const float4*>(&mx[1][ct + 4 * h]);
             d8[4 * h] = Divisor(sc.x, in.x);
             d8[4 * h + 1] = Divisor(sc.y, in.y);
             d8[4 * h + 2] = Divisor(sc.z, in.z);
@@ -872,7 +880,9 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_split(GemmArgs g, const uint16_
                     acc[3] = fmaf(s, v.w, acc[3]);
                 }
             };
-            auto product = [&](int w) { return *reinterpret_cast<const float4*>(p + w * (L::P + L::S) + em * (16 * NT + 4) + en); };
+            auto product = [&](int w) {
+                return *reinterpret_cast<const float4*>(p + w * (L::P + L::S) + em * (16 * NT + 4) + en);
+            };
             auto scale = [&](int w) { return p[w * (L::P + L::S) + L::P + em]; };
             auto rows = [&](int w) {
                 return ROWS ? *reinterpret_cast<const float4*>(p + w * (L::P + L::S) + L::P + 16 * MT + en) : float4{};
@@ -922,13 +932,14 @@ hipError_t launch_quant(int mode, int R, int C, const T* x, int64_t ldx, uint8_t
     if (mode == kQuantRows) {
         // groups of a row in a block: a power of two up to eight
         const int lg = chunks(C) >= 8 ? 3 : chunks(C) >= 4 ? 2 : chunks(C) >= 2 ? 1 : 0, per = 32 >> lg;
-        hipLaunchKernelGGL(k_fp8_quant_rows<T>, dim3((unsigned)((R + per - 1) / per), (unsigned)((chunks(C) + (1 << lg) - 1) >> lg)),
-                           dim3(256), 0, stream, R, C, lg, x, ldx, q, ldq, s);
+        const dim3 grid((unsigned)((R + per - 1) / per), (unsigned)((chunks(C) + (1 << lg) - 1) >> lg));
+        hipLaunchKernelGGL(k_fp8_quant_rows<T>, grid, dim3(256), 0, stream, R, C, lg, x, ldx, q, ldq, s);
         return hipGetLastError();
     }
     const QuantJob<T> job{R, C, x, ldx, q, ldq, s, qt, ldqt, st};
     auto run = [&](auto m) {
-        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), dim3((unsigned)job.tiles()), dim3(kQuantThreads), 0, stream, job);
+        hipLaunchKernelGGL((k_fp8_quant<T, decltype(m)::value>), dim3((unsigned)job.tiles()), dim3(kQuantThreads), 0, stream,
+                           job);
     };
     switch (mode) {
     case kQuantCols: run(std::integral_constant<int, kQuantCols>{}); break;
@@ -948,7 +959,8 @@ hipError_t launch_quant_pair(const QuantJob<T>& dy, const QuantJob<T>& x, bool r
         hipLaunchKernelGGL((k_fp8_quant_pair<T, kQuantRows | kQuantCols>), dim3((unsigned)(a + b)), dim3(kQuantThreads), 0,
                            stream, dy, a, x);
     else
-        hipLaunchKernelGGL((k_fp8_quant_pair<T, kQuantCols>), dim3((unsigned)(a + b)), dim3(kQuantThreads), 0, stream, dy, a, x);
+        hipLaunchKernelGGL((k_fp8_quant_pair<T, kQuantCols>), dim3((unsigned)(a + b)), dim3(kQuantThreads), 0, stream, dy, a,
+                           x);
     return hipGetLastError();
 }
 
@@ -1018,11 +1030,10 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 // of their 10 us; deeper rings, two to four chunks a stage and scales through
 // LDS left that as it was), the large ones the matrix pipe next to the copies.
 // At 8192x4096x4096 (122 us, 2.25 PFLOP/s; clock 2.1 GHz, matrix pipe half busy)
-// copies of the kernel that leave work out take, of 128 us with two row tiles of A in
-// registers: no stores of C 115 us, no
-// copies into LDS 104, no scaling of the chunk sums 116, neither 87, and without
-// operand reads too 81 us, which is the products (65 us at the pipe's rate) and the
-// ends of the tiles.  64x64 takes two chunks a stage (one: 13.1 / 18.8 / 32.3 us).
+// copies of the kernel that leave work out take, of 128 us with two row tiles of A
+// in registers: no stores of C 115 us, no copies into LDS 104, no scaling of the
+// chunk sums 116, neither 87, and without operand reads too 81 us, which is the
+// products (65 us at the pipe's rate) and the ends of the tiles.  64x64 takes two chunks a stage (one: 13.1 / 18.8 / 32.3 us).
 struct Variant {
     int bm, bn;
     float us[4], further;
@@ -1205,7 +1216,8 @@ __attribute__((visibility("default"))) int moe_fp8_gemm(const v4moe_gemm* p, con
     if (!device_ready()) return V4MOE_EDEVICE;
     const GemmArgs g = gemm_args(*p, a, as, b, bs, c);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return (p->b_scale == V4MOE_SCALE_ROW ? run_gemm<true>(g, s) : run_gemm<false>(g, s)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+    const hipError_t e = p->b_scale == V4MOE_SCALE_ROW ? run_gemm<true>(g, s) : run_gemm<false>(g, s);
+    return e == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }
 
 __attribute__((visibility("default"))) size_t moe_fp8_linear_workspace_bytes(int32_t M, int32_t N, int32_t K,
@@ -1280,12 +1292,14 @@ __attribute__((visibility("default"))) int moe_fp8_linear_backward(
         const hipStream_t s = static_cast<hipStream_t>(stream);
         auto both = [&](auto* as) {
             using T = std::remove_pointer_t<decltype(as)>;
-            const QuantJob<T> a{M, N, static_cast<const T*>(dy), lddy, ws + L.dq, up16(N), f32(L.ds), ws + L.dt, up16(M), f32(L.dts)};
+            const QuantJob<T> a{M, N, static_cast<const T*>(dy), lddy, ws + L.dq, up16(N), f32(L.ds),
+                                ws + L.dt, up16(M), f32(L.dts)};
             const QuantJob<T> b{M, K, static_cast<const T*>(x), ldx, nullptr, 0, nullptr, ws + L.xt, up16(M), f32(L.xts)};
             return launch_quant_pair(a, b, dx != nullptr, s);
         };
         if (one) {
-            const hipError_t e = x_type == V4MOE_TYPE_F32 ? both(static_cast<float*>(nullptr)) : both(static_cast<uint16_t*>(nullptr));
+            const hipError_t e =
+                x_type == V4MOE_TYPE_F32 ? both(static_cast<float*>(nullptr)) : both(static_cast<uint16_t*>(nullptr));
             if (e != hipSuccess) return V4MOE_ELAUNCH;
         } else {
             if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, dx ? ws + L.dq : nullptr, dx ? f32(L.ds) : nullptr,
@@ -1295,7 +1309,8 @@ __attribute__((visibility("default"))) int moe_fp8_linear_backward(
                 return rc;
         }
     } else if (M > 0) {
-        if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, ws + L.dq, f32(L.ds), nullptr, nullptr, stream)) return rc;
+        if (const int rc = moe_fp8_quantize(M, N, dy, dy_type, lddy, ws + L.dq, f32(L.ds), nullptr, nullptr, stream))
+            return rc;
     }
     // dx = dy W: contraction over N, block (i, c) of W^T is block (c, i) of W
     const v4moe_gemm gx{M, K, (int32_t)up16(N), V4MOE_SCALE_BLOCK, dx_type, 0, up16(N), up16(N), lddx, 1, chunks(K)};

@@ -281,7 +281,8 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
         __builtin_amdgcn_wave_barrier();
         int rank = 0;
 #pragma unroll 4
-        for (int o = 0; o < g.groups; o++) rank += values[o] >= v + (o < mine ? 0u : 1u) ? 1 : 0;    // larger, or as large with a lower number
+        for (int o = 0; o < g.groups; o++)
+            rank += values[o] >= v + (o < mine ? 0u : 1u) ? 1 : 0;      // larger, or as large with a lower number
         const bool keep = mine < g.groups && rank < g.topk_groups;
         if (own) {
             if (!keep) {
@@ -293,7 +294,8 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
             const float inv = 1.0f / (float)size;
 #pragma unroll
             for (int q = 0; q < EPL; q++) {
-                const int group = min((int)(((float)(e0 + q) + 0.5f) * inv), g.groups - 1);     // (e0 + q) / size: exact below 2^20
+                // (e0 + q) / size: exact below 2^20
+                const int group = min((int)(((float)(e0 + q) + 0.5f) * inv), g.groups - 1);
                 if (!((kept >> (group << shift)) & 1)) key[q] = kNone;
             }
         }
