@@ -295,18 +295,30 @@ def moe_layer_backward(d: Dims, x, w_router, bias, mode, token_ids, experts: Dev
                                     _p(dWu), _p(dWd), _p(workspace), workspace.numel(), _stream()))
 
 
+def _routing(d: Dims, x, topk_ids, topk_w):
+    """Addresses of the layer's input and of a routing the caller made, checked: the ids become indices."""
+    return (_given(x, (d.T, d.H), _BF16_BITS, "x"), _given(topk_ids, (d.T, d.topk), _INT32, "topk_ids"),
+            _given(topk_w, (d.T, d.topk), _FLOAT32, "topk_w"))
+
+
 def moe_routed_forward(d: Dims, x, topk_ids, topk_w, experts: DeviceExperts, expert_offsets, out, workspace):
     ex = experts.c()
-    _check(lib().moe_routed_forward(ctypes.byref(d), _p(x), _p(topk_ids), _p(topk_w), ctypes.byref(ex),
-                                    _p(expert_offsets), _p(out), _p(workspace), workspace.numel(), _stream()))
+    _check(lib().moe_routed_forward(ctypes.byref(d), *_routing(d, x, topk_ids, topk_w), ctypes.byref(ex),
+                                    _given(expert_offsets, (d.E + 1,), _INT32, "expert_offsets"),
+                                    _given(out, (d.T, d.H), _BF16_BITS, "out"), _p(workspace), workspace.numel(), _stream()))
 
 
 def moe_routed_backward(d: Dims, x, topk_ids, topk_w, experts: DeviceExperts, wt_gu, wt_d, dout, dx, dw, dWg, dWu, dWd,
                         workspace):
     ex = experts.c()
-    _check(lib().moe_routed_backward(ctypes.byref(d), _p(x), _p(topk_ids), _p(topk_w), ctypes.byref(ex), _p(wt_gu),
-                                     _p(wt_d), _p(dout), _p(dx), _p(dw), _p(dWg), _p(dWu), _p(dWd), _p(workspace),
-                                     workspace.numel(), _stream()))
+    T, H, I, E = d.T, d.H, d.I, d.E
+    _check(lib().moe_routed_backward(
+        ctypes.byref(d), *_routing(d, x, topk_ids, topk_w), ctypes.byref(ex),
+        _given(wt_gu, (E, H, 2 * I if d.act == ACT_SWIGLU else I), _UINT8, "wt_gu"), _given(wt_d, (E, I, H), _UINT8, "wt_d"),
+        _given(dout, (T, H), _BF16_BITS, "dout"), _given(dx, (T, H), _FLOAT32, "dx"),
+        _given(dw, (T, d.topk), _FLOAT32, "dw"), _given(dWg, (E, I, H), _FLOAT32, "dWg"),
+        _given(dWu, (E, I, H), _FLOAT32, "dWu"), _given(dWd, (E, H, I), _FLOAT32, "dWd"),
+        _p(workspace), workspace.numel(), _stream()))
 
 
 def moe_time_next_ffn(start_event, stop_event):
@@ -381,6 +393,19 @@ def _dense(t: torch.Tensor, shape: tuple, dtype, what: str) -> int:
     if not (t.is_cuda and t.shape == shape and t.dtype == dtype and t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous {dtype} {list(shape)} on a GPU, got {t.dtype} {list(t.shape)}")
     return t.data_ptr()
+
+
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+_INT32, _FLOAT32, _UINT8 = (torch.int32,), (torch.float32,), (torch.uint8,)
+
+
+def _given(t: Optional[torch.Tensor], shape: tuple, dtypes: tuple, what: str):
+    """t's address as _dense, of one of several types; None stays None (the library says where it may)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    return _dense(t, shape, t.dtype, what)
 
 
 def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Optional[torch.Tensor] = None,
