@@ -70,7 +70,8 @@ __device__ __forceinline__ void store_logits(T* row, int e0, int E, const float 
 __device__ __forceinline__ float clean(float z) { return z > -kMask ? fminf(z, kMask) : -kInf; }
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
-__device__ __forceinline__ float sqrt_softplus(float z) { return sqrtf(fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z)))); }
+__device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))); }
+__device__ __forceinline__ float sqrt_softplus(float z) { return sqrtf(softplus(z)); }
 
 // One step of a reduction over lanes: v as lane pattern CTRL brings it (DPP),
 // `none` where it brings nothing.
@@ -358,12 +359,15 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
 }
 
 // Gradient with respect to the logits.  A slot of weight zero (a filler, or a
-// score that underflowed) has none.  With a_j = dw_j over the live slots:
-//   renormalised: q_j = s_j / S, ds_j = scale / S * sum_i q_i (dw_j - dw_i)
-//   otherwise:    ds_j = scale * dw_j
-//   dz = ds s (1 - s) | ds sigmoid(z) / (2 s) | p_e (ds_e [picked] - sum_j ds_j p_j),
-// the softmax's last sum zero where the weights are renormalised, which leaves
-// only the picked logits and, as p_j / S = e_j / (sum of the picked e),
+// score that underflowed) has none.  With u_j = s_j / S renormalised (S the sum of
+// the live s), s_j otherwise, and f the score's logarithmic derivative,
+//   dz_j = scale d_j u_j f(z_j),  d_j = sum_i u_i (dw_j - dw_i) renormalised, dw_j otherwise,
+//   f = 1 / (1 + exp(z)) | sigmoid(z) / (2 softplus(z)) | 1, the softmax's other part
+//       -p_e sum_j scale d_j p_j at every logit.
+// Shares are formed first and the score itself is never divided by: S and s may lie
+// below fp32's normal numbers (a sigmoid's row of logits near -88) where the weights
+// and the gradient do not.  For a softmax the last sum is zero where the weights are
+// renormalised, which leaves only the picked logits and, as p_j / S = e_j / (sum of the picked e),
 // no need of the others.  LPT lanes per token, lane j < topk its slot j; the
 // picked logits' parts reach the lanes that write them through LDS.  Bound by HBM
 // and a token's chain of loads (ids, their logits): where the softmax reaches
@@ -423,18 +427,18 @@ __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __
     }
     float s = 0.0f;
     if (live) s = soft ? expf(z - m) / total : g.score == V4MOE_SCORE_SIGMOID ? sigmoid(z) : sqrt_softplus(z);
-    float ds = live ? g.scale * my_dw : 0.0f;
+    float u = s, d = my_dw;
     if (g.renorm) {
         const float S = row_sum(s);                  // (lanes past topk <= 16 hold 0)
-        float d = 0.0f;
+        u = S > 0.0f ? s / S : 0.0f;
+        d = 0.0f;
 #pragma unroll 4
-        for (int j = 0; j < g.topk; j++) d += __shfl(s, j, 16) * (my_dw - __shfl(my_dw, j, 16));
-        ds = live && S > 0.0f ? g.scale * (d / S) / S : 0.0f;
+        for (int j = 0; j < g.topk; j++) d += __shfl(u, j, 16) * (my_dw - __shfl(my_dw, j, 16));
     }
-    float dz;
-    if (soft) dz = ds * s;
-    else if (g.score == V4MOE_SCORE_SIGMOID) dz = ds * s * (1.0f / (1.0f + expf(z)));
-    else dz = ds * sigmoid(z) / (2.0f * s);
+    float dz = g.scale * d * u;
+    if (g.score == V4MOE_SCORE_SIGMOID) dz *= 1.0f / (1.0f + expf(z));
+    // (below -16 sigmoid / softplus = 1 - exp(z) / 2 + ... is 1 in fp32; neither needs to be a normal number)
+    else if (!soft) dz *= z < -16.0f ? 0.5f : sigmoid(z) / (2.0f * softplus(z));
     if (!live || s == 0.0f) dz = 0.0f;
     float* st = staged[wave][tok];
     const float dot = dense ? token_sum<LPT>(dz) : 0.0f;
