@@ -2,7 +2,11 @@
 // scaled down to a largest norm.
 //
 //   norm = sqrt(sum over every element of g^2), coef = norm > max ? max / norm : 1,
-//   out = g * coef (rounded once to the gradient's type)
+//   out = g * coef
+// coef comes from the 64-bit norm where that, or coef itself, is beyond fp32: finite
+// gradients are scaled whatever their norm.  It is an fp32 number where it can be (the
+// product rounded once to the gradient's type); below the normal ones it would have few
+// bits or none left, and the products are taken in fp64.
 // Squares are summed in fp64: nothing overflows or vanishes that fp32 holds,
 // and at the rate the gradients arrive from HBM the conversion and the fma
 // are hidden.  No atomics: a block sums the chunks b, b + grid, ... in order,
@@ -107,19 +111,21 @@ __device__ __forceinline__ void sum_squares(const T* p, int n, double (&s)[4])
         s[0] = fma(d, d, s[0]);
     }
 }
-template <typename T>
-__device__ __forceinline__ v4u scaled(const v4u& v, float coef)
+__device__ __forceinline__ float product(float g, float coef) { return g * coef; }
+__device__ __forceinline__ float product(float g, double coef) { return (float)((double)g * coef); }
+template <typename T, typename C>
+__device__ __forceinline__ v4u scaled(const v4u& v, C coef)
 {
     v4u r;
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        if constexpr (sizeof(T) == 4) r[k] = __float_as_uint(element<T>(v, k) * coef);
-        else r[k] = bf16x2(element<T>(v, 2 * k) * coef, element<T>(v, 2 * k + 1) * coef);
+        if constexpr (sizeof(T) == 4) r[k] = __float_as_uint(product(element<T>(v, k), coef));
+        else r[k] = bf16x2(product(element<T>(v, 2 * k), coef), product(element<T>(v, 2 * k + 1), coef));
     }
     return r;
 }
-template <typename T>
-__device__ __forceinline__ void scale_to(const T* p, T* o, int n, float coef)
+template <typename T, typename C>
+__device__ __forceinline__ void scale_to(const T* p, T* o, int n, C coef)
 {
     constexpr int V = 16 / sizeof(T), U = 4;
     const int nv = n / V;
@@ -135,7 +141,7 @@ __device__ __forceinline__ void scale_to(const T* p, T* o, int n, float coef)
         *reinterpret_cast<v4u_any*>(o + (int64_t)i * V) = scaled<T>(*reinterpret_cast<const v4u_any*>(p + (int64_t)i * V), coef);
     if ((int)threadIdx.x < n - nv * V) {
         const int at = nv * V + threadIdx.x;
-        const float f = to_f32(p[at]) * coef;
+        const float f = product(to_f32(p[at]), coef);
         if constexpr (sizeof(T) == 4) o[at] = f;
         else o[at] = (T)bf16x2(f, 0.0f);
     }
@@ -177,18 +183,26 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(Table t, int n_partial,
     double s = 0.0;
     for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
     stage_table(t, tab);
-    const float v = (float)sqrt(block_sum(s));
+    const double exact = sqrt(block_sum(s));
+    const float v = (float)exact;
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
-    // a norm that is not finite leaves the gradients as they are: the caller sees it and drops the step
-    const float coef = v > max_norm && v < __builtin_inff() ? max_norm / v : 1.0f;
-    for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-        const Entry& e = tab[find(tab, t.count, c)];
-        if (coef == 1.0f && e.out == e.g) continue;
-        const int64_t at = (int64_t)(c - e.first) * t.chunk;
-        const int n = (int)min((int64_t)t.chunk, e.n - at);
-        if (e.bf16) scale_to(static_cast<const uint16_t*>(e.g) + at, static_cast<uint16_t*>(e.out) + at, n, coef);
-        else scale_to(static_cast<const float*>(e.g) + at, static_cast<float*>(e.out) + at, n, coef);
-    }
+    // a norm that is not finite (in fp64: fp32 elements' squares do not overflow it) leaves the gradients as they
+    // are: the caller sees it and drops the step
+    const bool clip = v > max_norm && exact < __builtin_inf();
+    const double ratio = clip ? (double)max_norm / exact : 1.0;
+    const float coef = clip && v < __builtin_inff() ? max_norm / v : (float)ratio;
+    auto scale = [&](auto by) {
+        for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+            const Entry& e = tab[find(tab, t.count, c)];
+            if (by == 1 && e.out == e.g) continue;
+            const int64_t at = (int64_t)(c - e.first) * t.chunk;
+            const int n = (int)min((int64_t)t.chunk, e.n - at);
+            if (e.bf16) scale_to(static_cast<const uint16_t*>(e.g) + at, static_cast<uint16_t*>(e.out) + at, n, by);
+            else scale_to(static_cast<const float*>(e.g) + at, static_cast<float*>(e.out) + at, n, by);
+        }
+    };
+    if (ratio >= 0x1p-126) scale(coef);
+    else scale(ratio);
 }
 
 // Elements per chunk for a list of `total`: a power of two of 1024 (one access

@@ -450,8 +450,10 @@ size_t moe_clip_workspace_bytes(int32_t count);
 
 /* norm = sqrt(sum of the squares of all elements of all tensors) (squares and
  * sums in fp64, a fixed order), coef = norm > max_norm ? max_norm / norm : 1, and
- * out = g * coef in each tensor's type.  A norm that is not finite leaves the
- * gradients unscaled.  Nothing is read back to the host.
+ * out = g * coef in each tensor's type.  An infinity or NaN among the elements
+ * makes the norm that and leaves the gradients unscaled; a norm beyond fp32's
+ * range is returned as infinity, and the gradients are scaled by it all the same.
+ * Nothing is read back to the host.
  *   tensors: HOST array; norm: device fp32 [1] (out); max_norm >= 0 (infinity: the
  * norm only, and copies where out is not g). */
 int moe_clip_grads(int32_t count, const v4moe_tensor* tensors, float max_norm, float* norm,
