@@ -408,12 +408,13 @@ __device__ __forceinline__ v4f mfma_e4m3(v8i w, v8i x)
 // A wave's MI x NI tiles to C, 16 rows at a time through LDS (two buffers of
 // 16 rows): a lane's four columns become 16-byte stores along the rows, whole
 // lines where a row's part is one (straight from the registers the stores cost
-// 22 us of 139 at 8192 x 4096).  16-byte segments XOR-swizzled by the row.
-template <bool STREAM, int MI, int NI, typename T>
+// 22 us of 139 at 8192 x 4096).  16-byte segments XOR-swizzled by the row.  S: the
+// type staged, fp32 where C is added to, so that a bf16 C takes the sum rounded once.
+template <bool STREAM, int MI, int NI, typename S, typename T>
 __device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* stage, T* __restrict__ c, const GemmArgs& g,
                                            int m0, int n0)
 {
-    constexpr int ES = sizeof(T), RB = NI * 16 * ES, LR = RB / 16, PER = 16 / ES;    // bytes, lanes per row; elements per lane
+    constexpr int ES = sizeof(S), RB = NI * 16 * ES, LR = RB / 16, PER = 16 / ES;    // bytes, lanes per row; elements per lane
     constexpr int RP = 64 / LR;                                                    // rows per pass
     const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
 #pragma unroll
@@ -436,22 +437,21 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[MI][NI], uint8_t* st
             const int m = m0 + 16 * i + r, n = n0 + sg * PER;
             if (m >= g.M || n >= g.N) continue;
             T* o = c + (int64_t)m * g.ldc + n;
-            if (n + PER <= g.N && !g.accumulate) {
-                const v4u w4 = {v.x, v.y, v.z, v.w};
-                if (STREAM) __builtin_nontemporal_store(w4, reinterpret_cast<v4u_any*>(o));
-                else *reinterpret_cast<v4u_any*>(o) = w4;
-                continue;
+            if constexpr (sizeof(S) == sizeof(T)) {
+                if (n + PER <= g.N && !g.accumulate) {
+                    const v4u w4 = {v.x, v.y, v.z, v.w};
+                    if (STREAM) __builtin_nontemporal_store(w4, reinterpret_cast<v4u_any*>(o));
+                    else *reinterpret_cast<v4u_any*>(o) = w4;
+                    continue;
+                }
             }
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < PER; e++) {
                 if (n + e >= g.N) break;
-                if constexpr (ES == 2) {
-                    const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                    o[e] = g.accumulate ? (uint16_t)bf16x2(bf16_to_f32(o[e]) + bf16_to_f32(b), 0.0f) : (uint16_t)b;
-                } else {
-                    o[e] = g.accumulate ? o[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
-                }
+                if constexpr (ES == 2) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                else if constexpr (sizeof(T) == 2) o[e] = (uint16_t)bf16x2(bf16_to_f32(o[e]) + __uint_as_float(w[e]), 0.0f);
+                else o[e] = g.accumulate ? o[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -707,8 +707,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int block, int tile
     uint8_t* stage = smem + wave * (2 * 16 * NI * 16 * 4);
     const int mw = m0 + wm * MI * 16, nw = n0 + wn * NI * 16;
     constexpr bool STREAM = L::BM * L::BN >= 128 * 128;
-    if (g.c_bf16) store_tile<STREAM, MI, NI>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
-    else store_tile<STREAM, MI, NI>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
+    if (!g.c_bf16) store_tile<STREAM, MI, NI, float>(acc, stage, static_cast<float*>(g.c), g, mw, nw);
+    else if (g.accumulate) store_tile<STREAM, MI, NI, float>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
+    else store_tile<STREAM, MI, NI, uint16_t>(acc, stage, static_cast<uint16_t*>(g.c), g, mw, nw);
 }
 
 template <int WM, int WN, int MI, int NI, int NS, int KC, bool ROWS>
@@ -911,8 +912,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_split(GemmArgs g, const uint16_
         if (n + e >= g.N) break;
         if (g.c_bf16) {
             uint16_t* o = static_cast<uint16_t*>(g.c) + (int64_t)m * g.ldc + n + e;
-            const uint32_t b = bf16x2(acc[e], 0.0f);
-            *o = g.accumulate ? (uint16_t)bf16x2(bf16_to_f32(*o) + bf16_to_f32(b & 0xFFFFu), 0.0f) : (uint16_t)b;
+            *o = (uint16_t)bf16x2(g.accumulate ? bf16_to_f32(*o) + acc[e] : acc[e], 0.0f);
         } else {
             float* o = static_cast<float*>(g.c) + (int64_t)m * g.ldc + n + e;
             *o = g.accumulate ? *o + acc[e] : acc[e];

@@ -394,7 +394,7 @@ typedef struct {
     int32_t M, N, K;
     int32_t b_scale;      /* V4MOE_SCALE_*                          */
     int32_t c_type;       /* V4MOE_TYPE_*                           */
-    int32_t accumulate;   /* non-zero: added to what c holds        */
+    int32_t accumulate;   /* non-zero: c = what it holds + result, in fp32, rounded once */
     int64_t lda, ldb, ldc;
     int64_t bs_n, bs_k;   /* V4MOE_SCALE_BLOCK only                 */
 } v4moe_gemm;
