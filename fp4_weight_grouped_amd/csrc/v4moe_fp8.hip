@@ -1322,7 +1322,8 @@ __attribute__((visibility("default"))) int moe_fp8_linear_backward(
         return run_gemm_pair(a, b, static_cast<hipStream_t>(stream)) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
     }
     if (dx && M > 0) return moe_fp8_gemm(&gx, ws + L.dq, f32(L.ds), w->qt, w->blk, dx, stream);
-    if (dw) return moe_fp8_gemm(&gw, ws + L.dt, f32(L.dts), ws + L.xt, f32(L.xts), dw, stream);
+    if (dw && (M > 0 || !accumulate))      // (adding a sum of nothing would turn -0 into 0)
+        return moe_fp8_gemm(&gw, ws + L.dt, f32(L.dts), ws + L.xt, f32(L.xts), dw, stream);
     return V4MOE_OK;
 }
 

@@ -50,3 +50,19 @@ def test_weight_gradient(shape, type):
         v4moe.fp8_linear_backward(x, dy, w, dw=dw, accumulate=True)
         want = (want + new).to(type).float()
     assert torch.equal(dw.float(), want)
+
+
+@pytest.mark.parametrize("type", [torch.bfloat16, torch.float32])
+def test_weight_gradient_of_no_rows(type):
+    """Left alone, in every bit, where it accumulates; zero otherwise."""
+    w = v4moe.fp8_weights(torch.randn(33, 50, device=DEV))
+    x, dy = torch.zeros(0, 50, device=DEV), torch.zeros(0, 33, device=DEV)
+    old = torch.randn(33, 50, device=DEV).to(type)
+    old[::2] = -0.0
+    old[1] = float("nan")
+    bits = torch.int16 if type == torch.bfloat16 else torch.int32
+    dw = old.clone()
+    v4moe.fp8_linear_backward(x, dy, w, dw=dw, accumulate=True)
+    assert torch.equal(dw.view(bits), old.view(bits))
+    v4moe.fp8_linear_backward(x, dy, w, dw=dw)
+    assert not dw.view(bits).any()
