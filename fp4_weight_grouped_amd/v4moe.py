@@ -295,30 +295,33 @@ def moe_layer_backward(d: Dims, x, w_router, bias, mode, token_ids, experts: Dev
                                     _p(dWu), _p(dWd), _p(workspace), workspace.numel(), _stream()))
 
 
-def _routing(d: Dims, x, topk_ids, topk_w):
+def _routing(d: Dims, x, topk_ids, topk_w, dev: int):
     """Addresses of the layer's input and of a routing the caller made, checked: the ids become indices."""
-    return (_given(x, (d.T, d.H), _BF16_BITS, "x"), _given(topk_ids, (d.T, d.topk), _INT32, "topk_ids"),
-            _given(topk_w, (d.T, d.topk), _FLOAT32, "topk_w"))
+    return (_given(x, (d.T, d.H), _BF16_BITS, "x", dev), _given(topk_ids, (d.T, d.topk), _INT32, "topk_ids", dev),
+            _given(topk_w, (d.T, d.topk), _FLOAT32, "topk_w", dev))
 
 
 def moe_routed_forward(d: Dims, x, topk_ids, topk_w, experts: DeviceExperts, expert_offsets, out, workspace):
     ex = experts.c()
-    _check(lib().moe_routed_forward(ctypes.byref(d), *_routing(d, x, topk_ids, topk_w), ctypes.byref(ex),
-                                    _given(expert_offsets, (d.E + 1,), _INT32, "expert_offsets"),
-                                    _given(out, (d.T, d.H), _BF16_BITS, "out"), _p(workspace), workspace.numel(), _stream()))
+    dev = _device_of(workspace, "workspace")
+    _check(lib().moe_routed_forward(ctypes.byref(d), *_routing(d, x, topk_ids, topk_w, dev), ctypes.byref(ex),
+                                    _given(expert_offsets, (d.E + 1,), _INT32, "expert_offsets", dev),
+                                    _given(out, (d.T, d.H), _BF16_BITS, "out", dev), _p(workspace), workspace.numel(),
+                                    _stream()))
 
 
 def moe_routed_backward(d: Dims, x, topk_ids, topk_w, experts: DeviceExperts, wt_gu, wt_d, dout, dx, dw, dWg, dWu, dWd,
                         workspace):
     ex = experts.c()
+    dev = _device_of(workspace, "workspace")
     T, H, I, E = d.T, d.H, d.I, d.E
     _check(lib().moe_routed_backward(
-        ctypes.byref(d), *_routing(d, x, topk_ids, topk_w), ctypes.byref(ex),
-        _given(wt_gu, (E, H, 2 * I if d.act == ACT_SWIGLU else I), _UINT8, "wt_gu"), _given(wt_d, (E, I, H), _UINT8, "wt_d"),
-        _given(dout, (T, H), _BF16_BITS, "dout"), _given(dx, (T, H), _FLOAT32, "dx"),
-        _given(dw, (T, d.topk), _FLOAT32, "dw"), _given(dWg, (E, I, H), _FLOAT32, "dWg"),
-        _given(dWu, (E, I, H), _FLOAT32, "dWu"), _given(dWd, (E, H, I), _FLOAT32, "dWd"),
-        _p(workspace), workspace.numel(), _stream()))
+        ctypes.byref(d), *_routing(d, x, topk_ids, topk_w, dev), ctypes.byref(ex),
+        _given(wt_gu, (E, H, 2 * I if d.act == ACT_SWIGLU else I), _UINT8, "wt_gu", dev),
+        _given(wt_d, (E, I, H), _UINT8, "wt_d", dev), _given(dout, (T, H), _BF16_BITS, "dout", dev),
+        _given(dx, (T, H), _FLOAT32, "dx", dev), _given(dw, (T, d.topk), _FLOAT32, "dw", dev),
+        _given(dWg, (E, I, H), _FLOAT32, "dWg", dev), _given(dWu, (E, I, H), _FLOAT32, "dWu", dev),
+        _given(dWd, (E, H, I), _FLOAT32, "dWd", dev), _p(workspace), workspace.numel(), _stream()))
 
 
 def moe_time_next_ffn(start_event, stop_event):
@@ -351,14 +354,18 @@ def _type(t: torch.Tensor) -> int:
     return ty
 
 
-def _on_device(t: torch.Tensor, what: str) -> int:
-    """The current stream, after checking that t is on the current GPU."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on a GPU")
-    i = t.device.index
-    if i != _current_device():
-        raise ValueError(f"{what} is on GPU {i}, which is not the current device")
-    return _raw_stream(i)
+def _device_of(t: torch.Tensor, what: str) -> int:
+    """The current GPU, after checking that t is on it; the other tensors of a call are then compared with it, as
+    every address a kernel gets is that device's."""
+    i = t.get_device()
+    if i < 0 or i != _current_device():
+        _elsewhere(t, what)
+    return i
+
+
+def _elsewhere(t: torch.Tensor, what: str):
+    raise ValueError(f"{what} must be on a GPU" if t.get_device() < 0 else
+                     f"{what} is on GPU {t.get_device()}, which is not the current device")
 
 
 def _empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
@@ -370,10 +377,10 @@ def _bytes(n: int, device) -> torch.Tensor:
     return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device)
 
 
-def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dtype=None) -> int:
-    """t's leading dimension, after checking that it is [rows][cols] with contiguous columns on a GPU."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on a GPU")
+def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dev: int, dtype=None) -> int:
+    """t's leading dimension, after checking that it is [rows][cols] with contiguous columns on GPU dev."""
+    if t.get_device() != dev:
+        _elsewhere(t, what)
     if t.shape != (rows, cols):
         raise ValueError(f"{what} must be [{rows}][{cols}], got {list(t.shape)}")
     if dtype is not None and t.dtype != dtype:
@@ -388,10 +395,12 @@ def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, dtype=None) -> int
     return ld
 
 
-def _dense(t: torch.Tensor, shape: tuple, dtype, what: str) -> int:
-    """t's address, after checking that it is contiguous, of this shape and type, on a GPU."""
-    if not (t.is_cuda and t.shape == shape and t.dtype == dtype and t.is_contiguous()):
-        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)} on a GPU, got {t.dtype} {list(t.shape)}")
+def _dense(t: torch.Tensor, shape: tuple, dtype, what: str, dev: int) -> int:
+    """t's address, after checking that it is contiguous, of this shape and type, on GPU dev."""
+    if t.get_device() != dev:
+        _elsewhere(t, what)
+    if not (t.shape == shape and t.dtype == dtype and t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     return t.data_ptr()
 
 
@@ -399,13 +408,13 @@ _BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
 _INT32, _FLOAT32, _UINT8 = (torch.int32,), (torch.float32,), (torch.uint8,)
 
 
-def _given(t: Optional[torch.Tensor], shape: tuple, dtypes: tuple, what: str):
+def _given(t: Optional[torch.Tensor], shape: tuple, dtypes: tuple, what: str, dev: int):
     """t's address as _dense, of one of several types; None stays None (the library says where it may)."""
     if t is None:
         return None
     if t.dtype not in dtypes:
         raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    return _dense(t, shape, t.dtype, what)
+    return _dense(t, shape, t.dtype, what, dev)
 
 
 def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Optional[torch.Tensor] = None,
@@ -413,9 +422,10 @@ def gate(logits: torch.Tensor, topk: int, score: int = SCORE_SIGMOID, bias: Opti
     """Routing from logits [T][E] (fp32 or bf16, rows may be strided); bias: fp32 [E], selection only.
     Returns (topk_ids int32 [T][topk], topk_w fp32 [T][topk]).  See moe_gate in include/v4moe.h."""
     T, E = logits.shape
-    ld = _matrix(logits, T, E, "logits")
-    stream = _on_device(logits, "logits")
-    b = None if bias is None else _dense(bias, (E,), torch.float32, "bias")
+    gpu = _device_of(logits, "logits")
+    ld = _matrix(logits, T, E, "logits", gpu)
+    stream = _raw_stream(gpu)
+    b = None if bias is None else _dense(bias, (E,), torch.float32, "bias", gpu)
     g = GateC(T, E, topk, score, groups, topk_groups, 1 if renorm else 0, scale)
     dev = logits.device
     ids = _empty(T, topk, torch.int32, dev)
@@ -428,12 +438,13 @@ def gate_backward(logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Te
                   score: int = SCORE_SIGMOID, renorm: bool = True, scale: float = 1.0) -> torch.Tensor:
     """dL/dlogits [T][E] (the logits' type) from dw = dL/dtopk_w and gate()'s outputs."""
     T, E = logits.shape
-    ld = _matrix(logits, T, E, "logits")
-    stream = _on_device(logits, "logits")
+    gpu = _device_of(logits, "logits")
+    ld = _matrix(logits, T, E, "logits", gpu)
+    stream = _raw_stream(gpu)
     k = topk_ids.shape[1]
-    ids = _dense(topk_ids, (T, k), torch.int32, "topk_ids")
-    w = _dense(topk_w, (T, k), torch.float32, "topk_w")
-    d = _dense(dw, (T, k), torch.float32, "dw")
+    ids = _dense(topk_ids, (T, k), torch.int32, "topk_ids", gpu)
+    w = _dense(topk_w, (T, k), torch.float32, "topk_w", gpu)
+    d = _dense(dw, (T, k), torch.float32, "dw", gpu)
     g = GateC(T, E, k, score, 1, 1, 1 if renorm else 0, scale)
     dl = _empty(T, E, logits.dtype, logits.device)
     _check(lib().moe_gate_backward(ctypes.byref(g), logits.data_ptr(), _type(logits), ld, ids, w, d, dl.data_ptr(), E,
@@ -458,11 +469,14 @@ class FP8Matrix:
     qt: torch.Tensor    # uint8 [K][N rounded up to 16]
     blk: torch.Tensor   # float32 [ceil(N/128)][ceil(K/128)]
 
-    def c(self) -> FP8MatC:
+    def c(self, dev: Optional[int] = None) -> FP8MatC:
+        """For a call on GPU dev (by default the current one)."""
         N, K = self.N, self.K
         q, qt, blk = _fp8_shapes(N, K)
-        return FP8MatC(N, K, _dense(self.q, q, torch.uint8, "q"), _dense(self.qt, qt, torch.uint8, "qt"),
-                       _dense(self.blk, blk, torch.float32, "blk"))
+        if dev is None:
+            dev = _device_of(self.q, "q")
+        return FP8MatC(N, K, _dense(self.q, q, torch.uint8, "q", dev), _dense(self.qt, qt, torch.uint8, "qt", dev),
+                       _dense(self.blk, blk, torch.float32, "blk", dev))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -473,8 +487,9 @@ def _fp8_shapes(N: int, K: int):
 def fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False):
     """E4M3 codes of x [M][K] and their scales: (q, s) by rows and / or (qt, st) by columns, None where not asked."""
     M, K = x.shape
-    ld = _matrix(x, M, K, "x")
-    stream = _on_device(x, "x")
+    gpu = _device_of(x, "x")
+    ld = _matrix(x, M, K, "x", gpu)
+    stream = _raw_stream(gpu)
     dev = x.device
     q = _empty(M, _up16(K), torch.uint8, dev) if rows else None
     s = _empty(_chunks(K), M, torch.float32, dev) if rows else None
@@ -487,8 +502,9 @@ def fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False):
 def fp8_weights(w: torch.Tensor) -> FP8Matrix:
     """E4M3 codes of a weight [N][K] (fp32 or bf16) in both orders, a scale for each 128x128 block."""
     N, K = w.shape
-    ld = _matrix(w, N, K, "w")
-    stream = _on_device(w, "w")
+    gpu = _device_of(w, "w")
+    ld = _matrix(w, N, K, "w", gpu)
+    stream = _raw_stream(gpu)
     dev = w.device
     m = FP8Matrix(N, K, _empty(N, _up16(K), torch.uint8, dev),
                   _empty(K, _up16(N), torch.uint8, dev),
@@ -503,20 +519,22 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     """a [M][K] times b [N][K] transposed, E4M3 codes (K a multiple of 16) with scales a_scale [ceil(K/128)][M] and
     b_scale: [ceil(N/128)][ceil(K/128)] (any strides), or with ``rows`` [ceil(K/128)][N].  out: [M][N], bf16 by default."""
     (M, K), N = a.shape, b.shape[0]
-    stream = _on_device(a, "a")
-    lda, ldb = _matrix(a, M, K, "a", torch.uint8), _matrix(b, N, K, "b", torch.uint8)
+    gpu = _device_of(a, "a")
+    lda, ldb = _matrix(a, M, K, "a", gpu, torch.uint8), _matrix(b, N, K, "b", gpu, torch.uint8)
+    stream = _raw_stream(gpu)
     n = _chunks(K)
-    sa = _dense(a_scale, (n, M), torch.float32, "a_scale")
+    sa = _dense(a_scale, (n, M), torch.float32, "a_scale", gpu)
     if rows:
-        sb, bs = _dense(b_scale, (n, N), torch.float32, "b_scale"), (0, 0)
+        sb, bs = _dense(b_scale, (n, N), torch.float32, "b_scale", gpu), (0, 0)
     else:
-        _require(b_scale.is_cuda and b_scale.shape == (_chunks(N), n) and b_scale.dtype == torch.float32,
-                 f"b_scale must be float32 [{_chunks(N)}][{n}] on a GPU")
+        _device_of(b_scale, "b_scale")
+        _require(b_scale.shape == (_chunks(N), n) and b_scale.dtype == torch.float32,
+                 f"b_scale must be float32 [{_chunks(N)}][{n}]")
         sb, bs = b_scale.data_ptr(), b_scale.stride()
     if out is None:
         _require(not accumulate, "accumulate needs out")
         out = _empty(M, N, torch.bfloat16, a.device)
-    ldc = _matrix(out, M, N, "out")
+    ldc = _matrix(out, M, N, "out", gpu)
     g = GemmC(M, N, K, SCALE_ROW if rows else SCALE_BLOCK, _type(out), 1 if accumulate else 0, lda, ldb, ldc, bs[0], bs[1])
     _check(lib().moe_fp8_gemm(ctypes.byref(g), a.data_ptr(), sa, b.data_ptr(), sb, out.data_ptr(), stream))
     return out
@@ -530,14 +548,15 @@ def moe_fp8_linear_workspace_bytes(M: int, N: int, K: int, backward: int) -> int
 def fp8_linear(x: torch.Tensor, w: FP8Matrix, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = x W^T: x [M][K] bf16 or fp32, quantised by rows; y [M][N] (bf16 unless ``out`` says otherwise)."""
     M, N, K = x.shape[0], w.N, w.K
-    ldx = _matrix(x, M, K, "x")
-    stream = _on_device(x, "x")
+    gpu = _device_of(x, "x")
+    ldx = _matrix(x, M, K, "x", gpu)
+    stream = _raw_stream(gpu)
     dev = x.device
     if out is None:
         out, ldy, ty = _empty(M, N, torch.bfloat16, dev), N, TYPE_BF16
     else:
-        ldy, ty = _matrix(out, M, N, "out"), _type(out)
-    c = w.c()
+        ldy, ty = _matrix(out, M, N, "out", gpu), _type(out)
+    c = w.c(gpu)
     n = moe_fp8_linear_workspace_bytes(M, N, K, 0)
     ws = _bytes(n, dev)
     _check(lib().moe_fp8_linear(M, x.data_ptr(), _type(x), ldx, ctypes.byref(c), out.data_ptr(), ty, ldy, ws.data_ptr(), n,
@@ -549,16 +568,17 @@ def fp8_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: FP8Matrix, dx: Opt
                         dw: Optional[torch.Tensor] = None, accumulate: bool = False):
     """Gradients of fp8_linear: (dx [M][K], dw [N][K]), bf16 unless given; accumulate adds to the given dw."""
     M, N, K = x.shape[0], w.N, w.K
-    ldx, lddy = _matrix(x, M, K, "x"), _matrix(dy, M, N, "dy")
-    stream = _on_device(x, "x")
+    gpu = _device_of(x, "x")
+    ldx, lddy = _matrix(x, M, K, "x", gpu), _matrix(dy, M, N, "dy", gpu)
+    stream = _raw_stream(gpu)
     dev = x.device
     _require(dw is not None or not accumulate, "accumulate needs dw")
     if dx is None:
         dx = _empty(M, K, torch.bfloat16, dev)
     if dw is None:
         dw = _empty(N, K, torch.bfloat16, dev)
-    lddx, lddw = _matrix(dx, M, K, "dx"), _matrix(dw, N, K, "dw")
-    c = w.c()
+    lddx, lddw = _matrix(dx, M, K, "dx", gpu), _matrix(dw, N, K, "dw", gpu)
+    c = w.c(gpu)
     n = moe_fp8_linear_workspace_bytes(M, N, K, 1)
     ws = _bytes(n, dev)
     _check(lib().moe_fp8_linear_backward(M, x.data_ptr(), _type(x), ldx, dy.data_ptr(), _type(dy), lddy, ctypes.byref(c),
@@ -573,7 +593,7 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     grads = list(grads)
     n = len(grads)
     _require(n > 0, "no gradients")
-    stream = _on_device(grads[0], "gradients")
+    stream = _raw_stream(_device_of(grads[0], "gradients"))
     dev = grads[0].device
 
     def words(tensors):     # addresses, sizes and types, by maps over the list: a small step's time is the host's
