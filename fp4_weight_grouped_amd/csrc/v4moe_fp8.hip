@@ -20,6 +20,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 namespace v4moe {
@@ -972,16 +973,17 @@ hipError_t run_quant(int mode, int R, int C, const void* x, int type, int64_t ld
     return launch_quant(mode, R, C, static_cast<const uint16_t*>(x), ldx, q, ldq, s, qt, ldqt, st, stream);
 }
 
-// Lets a kernel have more than 64 KiB of LDS, once per device.
-hipError_t allow_lds(const void* kernel, int bytes, bool (&done)[kMaxDevices])
+// Lets a kernel have more than 64 KiB of LDS, once per device (or again by host threads that come to it at once).
+using LdsAllowed = std::atomic<bool>[kMaxDevices];
+hipError_t allow_lds(const void* kernel, int bytes, LdsAllowed& done)
 {
     if (bytes <= 65536) return hipSuccess;
     int dev = 0;
     if (const hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-    if (done[dev]) return hipSuccess;
+    if (done[dev].load(std::memory_order_acquire)) return hipSuccess;
     const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    done[dev] = e == hipSuccess;
+    if (e == hipSuccess) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
@@ -990,7 +992,7 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t s)
 {
     using L = GemmTile<WM, WN, MI, NI, NS, KC, ROWS>;
     const auto kernel = k_fp8_gemm<WM, WN, MI, NI, NS, KC, ROWS>;
-    static bool allowed[kMaxDevices];
+    static LdsAllowed allowed;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
     const int tm = (g.M + L::BM - 1) / L::BM, tn = (g.N + L::BN - 1) / L::BN;
     if ((int64_t)tm * tn > INT32_MAX / 8) return hipErrorInvalidValue;
@@ -1003,7 +1005,7 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 {
     using L = SplitLds<MT, NT, NW, ROWS, X>;
     const auto kernel = k_fp8_split<MT, NT, NW, ROWS, X>;
-    static bool allowed[kMaxDevices];
+    static LdsAllowed allowed;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
     const dim3 grid((unsigned)((g.N + 16 * NT - 1) / (16 * NT)), (unsigned)((g.M + 16 * MT - 1) / (16 * MT)));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), L::BYTES, s, g, x, ldx, kx);
@@ -1080,7 +1082,7 @@ hipError_t launch_gemm_pair(const GemmArgs& a, const GemmArgs& b, hipStream_t s)
 {
     using L = GemmTile<WM, WN, MI, NI, NS, KC, true>;          // (the larger LDS of the two)
     const auto kernel = k_fp8_gemm_pair<WM, WN, MI, NI, NS, KC>;
-    static bool allowed[kMaxDevices];
+    static LdsAllowed allowed;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
     auto over = [](int n, int b) { return (n + b - 1) / b; };
     const int am = over(a.M, L::BM), an = over(a.N, L::BN), bm = over(b.M, L::BM), bn = over(b.N, L::BN);
