@@ -23,6 +23,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 namespace v4moe {
 
 namespace {
@@ -256,6 +260,43 @@ int check_tensors(int32_t count, const v4moe_tensor* t)
     return V4MOE_OK;
 }
 
+// Whether memory that the call writes is also another entry's: blocks that scale them
+// would race, and a gradient listed twice would be scaled once or twice.  An infinite
+// max_norm writes nothing in place.  Ranges in order of address, each compared with
+// the furthest end of those before it.
+struct Range {
+    uintptr_t lo, hi;
+    bool written;
+};
+bool overlaps(int32_t count, const v4moe_tensor* t, float max_norm, Range* r)
+{
+    int n = 0;
+    for (int32_t i = 0; i < count; i++) {
+        const size_t bytes = (size_t)t[i].n * (t[i].type == V4MOE_TYPE_F32 ? 4 : 2);
+        if (bytes == 0) continue;
+        const uintptr_t g = (uintptr_t)t[i].g, out = (uintptr_t)t[i].out;
+        const bool in_place = !out || out == g;
+        r[n++] = Range{g, g + bytes, in_place && max_norm < __builtin_inff()};
+        if (!in_place) r[n++] = Range{out, out + bytes, true};
+    }
+    std::sort(r, r + n, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t any = 0, written = 0;
+    for (int i = 0; i < n; i++) {
+        if (r[i].lo < (r[i].written ? any : written)) return true;
+        any = std::max(any, r[i].hi);
+        if (r[i].written) written = std::max(written, r[i].hi);
+    }
+    return false;
+}
+int check_overlaps(int32_t count, const v4moe_tensor* t, float max_norm)
+{
+    constexpr int kFew = 128;
+    Range few[2 * kFew];
+    std::unique_ptr<Range[]> many(count > kFew ? new (std::nothrow) Range[2 * (size_t)count] : nullptr);
+    if (count > kFew && !many) return V4MOE_EWORKSPACE;
+    return overlaps(count, t, max_norm, many ? many.get() : few) ? V4MOE_EDIMS : V4MOE_OK;
+}
+
 size_t partials(int32_t count) { return (size_t)(count / kTensors + 1) * kMaxBlocks; }
 
 }  // namespace
@@ -276,6 +317,7 @@ __attribute__((visibility("default"))) int moe_clip_grads(int32_t count, const v
 {
     if (const int rc = check_tensors(count, tensors)) return rc;
     if (!(max_norm >= 0.0f)) return V4MOE_EDIMS;
+    if (const int rc = check_overlaps(count, tensors, max_norm)) return rc;
     if (!norm || !workspace) return V4MOE_ENULL;
     if (((uintptr_t)norm & 3) || ((uintptr_t)workspace & 15)) return V4MOE_EALIGN;
     if (ws_bytes < moe_clip_workspace_bytes(count)) return V4MOE_EWORKSPACE;

@@ -437,7 +437,8 @@ int moe_fp8_linear_backward(int32_t M, const void* x, int32_t x_type, int64_t ld
                             int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
 
 /* A gradient of n elements (0 <= n <= 2^36), contiguous, aligned to its
- * element; out NULL or equal to g: in place. */
+ * element; out NULL or equal to g: in place.  What a call writes must not overlap
+ * any other gradient or output of the list (V4MOE_EDIMS). */
 typedef struct {
     const void* g;
     void* out;
