@@ -43,6 +43,10 @@ sampled from the amdgpu sysfs files during about a second of back-to-back
 steps outside the timed region.  The weights of the large workloads (3.4 GB)
 are 13x the 256 MB last-level cache, so every step streams them from HBM.
 
+The line on standard output holds the headline record and, of the side records,
+what a reader compares (`line`): it stays short enough for a log's tail.
+`--record FILE` writes all of every record.
+
 `--copy-bytes N` runs only a plain device copy of N bytes (the calibration
 kernel for those counters) and prints what it did.
 """
@@ -501,6 +505,59 @@ def cpu_baseline(inp, gpu=None, max_tokens=128, min_seconds=10.0, max_reps=8):
     return rec
 
 
+def parity_text(p):
+    return (f"ids/offsets {'equal' if p['ids_bit_exact'] and p['offsets_bit_exact'] else 'DIFFER'}, weights "
+            f"{p['weights_max_rel']:.1e}, out rel-L2 {p['out_rel_l2']:.1e}, max {p['out_max_rel']:.1e}, "
+            f"{p['tokens_compared']} tokens, {'within' if p['within_bar'] else 'OUTSIDE'} the bar")
+
+
+def rounded(v):
+    """v with its floats to six digits."""
+    if isinstance(v, float):
+        return float(f"{v:.6g}")
+    if isinstance(v, dict):
+        return {k: rounded(x) for k, x in v.items()}
+    if isinstance(v, (list, tuple)):
+        return [rounded(x) for x in v]
+    return v
+
+
+def brief(r):
+    """A workload's side record in one line: its times, its roofline, how it compares with the oracle."""
+    b = {k: r[k] for k in ("T", "ms_per_step", "tokens_per_s", "ffn_ms", "deterministic")}
+    b["roofline"] = {k: r["roofline"][k] for k in ("bound", "achieved", "unit", "frac")}
+    if r.get("cold_cache"):
+        b["cold_step_ms"] = r["cold_cache"]["step_device_ms"]["median"]
+    p = (r.get("cpu_baseline") or {}).get("parity")
+    if p:
+        b["parity"] = {k: p[k] for k in ("ids_bit_exact", "offsets_bit_exact", "out_rel_l2", "within_bar")}
+    return rounded(b)
+
+
+SIDE = ("prefill", "zipf", "hash", "ragged", "tiny")
+
+
+def line(rec):
+    """The record as printed: the headline whole, the side records in brief."""
+    out = dict(rec)
+    head = out.pop("detail")
+    out["detail"] = rounded({k: head[k] for k in ("ffn_ms", "active_experts", "load_max_over_mean", "ffn_hbm_gbs", "ffn_tflops",
+                                                  "step_device_ms", "cold_cache", "attribution_ms", "power_clock")})
+    if out["cpu_baseline"]:
+        out["cpu_baseline"] = rounded({k: v for k, v in out["cpu_baseline"].items() if k != "parity"})
+    for k in SIDE:
+        if k in out:
+            out[k] = brief(out[k])
+    if "weight_quantizer" in out:
+        out["weight_quantizer"] = rounded({k: out["weight_quantizer"][k] for k in ("ms", "achieved", "unit", "frac")})
+    if "backward" in out:
+        out["backward"] = [rounded({k: b[k] for k in ("workload", "ms", "bound", "achieved", "unit", "frac")})
+                           for b in out["backward"]]
+    if "gateless" in out:
+        out["gateless"] = [dict(brief(g), workload=g["workload"]) for g in out["gateless"]]
+    return json.dumps(out)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -521,6 +578,7 @@ def main():
                     help="skip the tiny, zipf, hash and ragged side records")
     ap.add_argument("--no-cold", action="store_true",
                     help="skip the cold-cache protocol loop (scratch writes between steps)")
+    ap.add_argument("--record", default=None, metavar="FILE", help="write all of every record to FILE (JSON)")
     ap.add_argument("--only-quantizer", action="store_true",
                     help="only time the weight quantiser on the workload's layer shape and print its record")
     args = ap.parse_args()
@@ -600,11 +658,11 @@ def main():
     if not args.no_cpu_baseline:
         log("[bench] timing the CPU oracle")
         cpu = cpu_baseline(inp, head["_gpu"])
-        log(f"[bench] cpu baseline {cpu['value']:.1f} tokens/s on {cpu['cores']} threads; parity {cpu['parity']}")
+        log(f"[bench] cpu baseline {cpu['value']:.1f} tokens/s on {cpu['cores']} threads; {parity_text(cpu['parity'])}")
         # a bounded oracle leg per side record: its time, and the parity of that record
         for r, winp in ([(side, side_inp)] if side is not None else []) + others:
             r["cpu_baseline"] = cpu_baseline(winp, r["_gpu"], max_tokens=16, min_seconds=0.0, max_reps=1)
-            log(f"[bench] {r['workload']}: oracle parity {r['cpu_baseline']['parity']}")
+            log(f"[bench] {r['workload']}: oracle: {parity_text(r['cpu_baseline']['parity'])}")
     head.pop("_gpu")
 
     rec = {
@@ -642,7 +700,10 @@ def main():
         rec["backward"] = bwd
     if gateless is not None:
         rec["gateless"] = gateless
-    print(json.dumps(rec), flush=True)
+    if args.record:
+        with open(args.record, "w") as fh:
+            json.dump(rec, fh, indent=1)
+    print(line(rec), flush=True)
 
 
 if __name__ == "__main__":
