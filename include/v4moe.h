@@ -403,8 +403,9 @@ typedef struct {
  *   a uint8 [M][lda], as fp32 [ceil(K/128)][M], b uint8 [N][ldb], c [M][ldc]
  * Chunk sums come from the matrix cores, which align a chunk's products to the
  * largest and drop what lies far below it: a chunk is off by up to 4e-4 of its
- * largest product (measured; 1.3e-5 of the result in the 2-norm for codes of
- * normal numbers).  Chunks are added in fp32, in order, in every variant, so a row
+ * largest product (measured; 1.0e-5 to 1.4e-5 of the result in the 2-norm for codes
+ * of normal numbers, where fp32 products of the same values are off by 1e-7 to 1e-6:
+ * an fp32 c holds more digits than it has).  Chunks are added in fp32, in order, in every variant, so a row
  * does not depend on the other rows.  K = 0 writes zeros.  a, b: 16-byte
  * aligned. */
 int moe_fp8_gemm(const v4moe_gemm* g, const uint8_t* a, const float* as, const uint8_t* b,
