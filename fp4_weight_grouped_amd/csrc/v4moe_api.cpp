@@ -310,9 +310,9 @@ namespace {
 // routing in given_ids and given_w, moe_routed_backward).
 int layer_backward(
     const v4moe_dims* d, const uint16_t* x, const float* w_router, const float* bias, int32_t mode,
-    const int64_t* token_ids, const int32_t* given_ids, const float* given_w, const v4moe_experts* w, const uint8_t* wt_gu, const uint8_t* wt_d,
-    const uint16_t* dout, float* dx, float* dw, float* dWg, float* dWu, float* dWd, void* workspace,
-    size_t ws_bytes, void* stream)
+    const int64_t* token_ids, const int32_t* given_ids, const float* given_w, const v4moe_experts* w,
+    const uint8_t* wt_gu, const uint8_t* wt_d, const uint16_t* dout, float* dx, float* dw, float* dWg, float* dWu,
+    float* dWd, void* workspace, size_t ws_bytes, void* stream)
 {
     if (!dims_ok(d)) return V4MOE_EDIMS;
     if (mode != V4MOE_ROUTE_LEARNED && mode != V4MOE_ROUTE_HASH && mode != kRouteGiven) return V4MOE_EDIMS;

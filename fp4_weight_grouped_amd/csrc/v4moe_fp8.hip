@@ -164,9 +164,9 @@ __device__ __forceinline__ uint32_t largest(const Raw<T>& r)
 // Groups along rows: x [R][C] -> q [R][ldq] (up to C rounded up to 16, zeros
 // past C), s [ceil(C/128)][R].  Eight lanes per group, sixteen elements each; a
 // block takes 2^lg consecutive groups of a row (at most a wave's eight) and
-// 32 / 2^lg rows.  Bound by HBM: 8192x4096 bf16 19.8 us, 102 MB at 5.1 TB/s, the
-// rate of a copy (sixteen lanes per group, whose scales are then twice the work,
-// and a second correction of each quotient: 23 us, all of them issuing).
+// 32 / 2^lg rows.  Bound by HBM: 8192x4096 bf16 19.0 to 19.6 us, 102 MB at 5.3 TB/s
+// (an element-wise copy of 4 GiB: 6.2; sixteen lanes per group, whose scales are then
+// twice the work, and a second correction of each quotient: 23 us, all of them issuing).
 template <typename T>
 __global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, int lg, const T* __restrict__ x, int64_t ldx,
                                                         uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s)
@@ -193,8 +193,8 @@ __global__ __launch_bounds__(256) void k_fp8_quant_rows(int R, int C, int lg, co
 // One 128x128 tile of x [R][C] per block, read once for both orders: thread t
 // holds rows 4(t/16) .. +3, columns 8(t%16) .. +7 as they are in memory.  Bound by
 // HBM, next to the tile's own latency and instructions: 16384x4096 fp32 weights
-// 77 us (403 MB, 5.2 TB/s; 83 with a branch per row); 8192x2048 bf16 in both orders
-// and 8192x4096 by columns in one launch 35 us (169 MB, 4.9 TB/s).  What helps is waves per CU (eight rows
+// 78 us (403 MB, 5.2 TB/s; 83 with a branch per row); 8192x2048 bf16 in both orders
+// and 8192x4096 by columns in one launch 34 us (169 MB, 5.0 TB/s).  What helps is waves per CU (eight rows
 // per thread took 47 us for the latter where four took 40, with the elements kept
 // as floats or the next tile's loads out a tile ahead 60) and fewer instructions
 // (40 -> 35: bf16 magnitudes two to an operation, their maxima over lanes by
@@ -736,8 +736,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_pair(GemmArgs a, int 
 // so the same bits, as k_fp8_gemm.  X (MT = 1): A is x itself (bf16), each
 // chunk quantised by the wave that needs it, in every block: 16 rows cost less
 // than a launch of their own.
-// Bound by latency, then by the weights' bytes: one row by 4096x2048 5.8 us, the
-// 8.4 MB of weights at 1.4 TB/s; 16 rows of codes by 4096x4096 6.6 us, 2.5 TB/s.
+// Bound by latency: one row by 4096x2048 5.8 us, the 8.4 MB of weights at 1.4 TB/s;
+// 16 rows of codes by 4096x4096 6.6 us, 2.5 TB/s.  Longer contractions are held up by
+// the rounds, each wave with the operands of one chunk on their way and every round
+// with a barrier and the addition of its sums: one row by 4096x8192 14.4 to 15 us, 2.2 TB/s,
+// where 33.5 MB of weights would take 5.4 at a copy's rate.
 template <int MT, int NT, int NW, bool ROWS, bool X>
 struct SplitLds {
     static constexpr int P = 16 * MT * (16 * NT + 4);          // floats of a chunk's products (rows padded)
@@ -1016,7 +1019,10 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 // by the rounds its tiles make (a round is one tile per CU): microseconds at
 // K = 4096, N = 4096 and M = 16 .. 8192, in a graph of many calls.  Times are nearly
 // proportional to K, so the order holds for others; two blocks of the tiles up to
-// 128x128 share a CU, so that a second round costs less than the first.
+// 128x128 share a CU, so that a second round costs less than the first.  Rounds that
+// come from N instead read weights of their own, and from memory where no cache holds
+// them, which the table does not know: one row by 16384x4096, one round of 16x64 tiles,
+// takes 16.5 us (67 MB, 4.1 TB/s), 16 rows by 7168x4096 11.5.
 //                 rounds:  1       2      3      4     each further
 //   k_fp8_split   16x16     6.6    10.2   14.0   17.8   3.7
 //   k_fp8_gemm    16x64     9.2    12.3   16.0   20.3   4.0
@@ -1031,7 +1037,8 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s, const uint16_t* x = nu
 // vector memory path (the 32x64 tiles of 128x4096x4096 move 0.4 MB a CU in about 7
 // of their 10 us; deeper rings, two to four chunks a stage and scales through
 // LDS left that as it was), the large ones the matrix pipe next to the copies.
-// At 8192x4096x4096 (122 us, 2.25 PFLOP/s; clock 2.1 GHz, matrix pipe half busy)
+// At 8192x4096x4096 (122 us in a long run of launches, 2.25 PFLOP/s; 129 to 160 in the
+// first tens of milliseconds of load, at lower clocks; matrix pipe half busy)
 // copies of the kernel that leave work out take, of 128 us with two row tiles of A
 // in registers: no stores of C 115 us, no copies into LDS 104, no scaling of the
 // chunk sums 116, neither 87, and without operand reads too 81 us, which is the
@@ -1251,8 +1258,9 @@ __attribute__((visibility("default"))) int moe_fp8_linear(int32_t M, const void*
         const hipStream_t s = static_cast<hipStream_t>(stream);
         const uint16_t* xb = static_cast<const uint16_t*>(x);
         // Sixteen waves (and chunks) at a time where a CU has one tile and more than eight chunks to do: one row by
-        // 4096x2048 5.8 us (eight waves: 6.5), by 4096x4096 8.7 (10.5), by 4096x8192 14.4 (19.2).  Where several
-        // tiles share a CU two such blocks do not: by 16384x2048 17.8 (15.3).
+        // 4096x2048 5.8 us (eight waves: 6.5), by 4096x4096 8.7 (10.5), by 4096x8192 14.4 (19.2).  Two tiles a CU
+        // (which this variant is chosen for where N is at most 16 and the rows are 4112 to 8192) gain by eight:
+        // 8192 rows by 16x2048 11.5 us (sixteen waves: 13.4), by 16x4096 17.9 (21.4).
         const bool many = chunks(K) > 8 && tiles_of(kVariants[0], M, N) <= 256;
         const hipError_t e = many ? launch_split<1, 1, 16, false, true>(g, s, xb, ldx, K)
                                   : launch_split<1, 1, 8, false, true>(g, s, xb, ldx, K);

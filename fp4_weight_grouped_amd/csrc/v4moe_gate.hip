@@ -189,7 +189,7 @@ __device__ __forceinline__ void sort_down(uint64_t (&k)[N])
 // power of two, otherwise over keys staged in LDS, as groups need not end with a
 // lane.  Bound by the instructions a token takes, for a sigmoid half of them the
 // exponentials and divisions of its scores: T = 8192, E = 256, top-8 of four of
-// eight groups 8.5 us, where its 8.9 MB would take 2 (rescanning a lane's keys
+// eight groups 8.5 us in a run of calls, 9.2 alone, where its 8.9 MB would take 2 (rescanning a lane's keys
 // after each pick, and one token a wave, 10.7; lists in registers 9.3).
 template <typename T, int EPL, int LPT>
 __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
@@ -370,9 +370,11 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
 // renormalised, which leaves only the picked logits and, as p_j / S = e_j / (sum of the picked e),
 // no need of the others.  LPT lanes per token, lane j < topk its slot j; the
 // picked logits' parts reach the lanes that write them through LDS.  Bound by HBM
-// and a token's chain of loads (ids, their logits): where the softmax reaches
-// every logit, T = 19647, E = 256, fp32, 11.5 us for 42 MB, 3.6 TB/s (12.2 with one
-// token a wave); elsewhere only the rows' zeros and picks are written.
+// and the order of a token's loads (the row, then ids, then w, dw and the picked
+// logits, each waited for): where the softmax reaches every logit, T = 19647, E = 256,
+// fp32, 11.5 us for 42 MB in a run of calls, 3.6 TB/s, 12.8 alone (12.2 in a run with one
+// token a wave).  Elsewhere only the rows' zeros and picks are written: sigmoid,
+// renormalised, top-8 of the same, 10.5 us in a run, 11.0 alone, 22 MB.
 template <typename T, int EPL, int LPT>
 __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
                                                        const int32_t* __restrict__ ids, const float* __restrict__ w,
