@@ -372,9 +372,9 @@ __global__ __launch_bounds__(256) void k_gate(v4moe_gate g, const T* __restrict_
 // picked logits' parts reach the lanes that write them through LDS.  Bound by HBM
 // and the order of a token's loads (the row, then ids, then w, dw and the picked
 // logits, each waited for): where the softmax reaches every logit, T = 19647, E = 256,
-// fp32, 11.5 us for 42 MB in a run of calls, 3.6 TB/s, 12.8 alone (12.2 in a run with one
-// token a wave).  Elsewhere only the rows' zeros and picks are written: sigmoid,
-// renormalised, top-8 of the same, 10.5 us in a run, 11.0 alone, 22 MB.
+// fp32, 11 to 13 us for 42 MB, 11.5 in a run of calls, 3.6 TB/s (12.2 with one token
+// a wave).  Elsewhere only the rows' zeros and picks are written: sigmoid,
+// renormalised, top-8 of the same, 10.5 to 13 us, 22 MB.
 template <typename T, int EPL, int LPT>
 __global__ __launch_bounds__(256) void k_gate_backward(v4moe_gate g, const T* __restrict__ logits, int64_t ld,
                                                        const int32_t* __restrict__ ids, const float* __restrict__ w,
