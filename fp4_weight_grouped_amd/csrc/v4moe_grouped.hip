@@ -1,0 +1,368 @@
+// v4moe_grouped.hip -- products grouped by expert with ragged sizes, bf16 weights.
+//
+//   rows m of expert e: offsets[e] <= m < offsets[e + 1]
+//   forward           y[m]  = W[e] x[m]                      W [E][N][K]
+//   data gradient     dx[m] = W[e]^T dy[m]
+//   weight gradient   dW[e] = sum over e's rows of dy[m] x[m]^T
+//
+// Nothing but the offsets says how many tiles an expert has, and they stay on the
+// device: the grid is the most that any split of the rows needs, each block
+// derives its tile from the offsets, and blocks without one end.
+#include "v4moe.h"
+#include "v4moe_device.h"
+#include "v4moe_internal.h"
+#include "v4moe_mm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+
+namespace v4moe {
+
+namespace {
+
+struct GroupedArgs {
+    int M, N, K, E;                  // rows, and a group's product: C columns N, contraction K (data gradients: the weight's K and N)
+    const int32_t* offsets;
+    const uint16_t* a; int64_t lda;  // rows x or dy
+    const uint16_t* b; int64_t ldb;  // weights, `group` elements apart; weight gradients: rows x
+    int64_t group;
+    MmOut c;
+};
+
+// Rows [first, first + count) of expert e, within [0, M] whatever the offsets hold.
+__device__ __forceinline__ int rows_of(const int32_t* offsets, int e, int M, int& first)
+{
+    first = min(max(offsets[e], 0), M);
+    return max(min(max(offsets[e + 1], 0), M) - first, 0);     // (both ends clamped first: their difference cannot overflow)
+}
+
+// Finds the expert of a block's tile, per row tile tn column tiles: experts in order, an
+// expert's tiles column by column in bands of eight row tiles.  `found` is LDS.
+struct Found { int e, first, count, tile, total, wave[16]; };
+template <int BM, int THREADS>
+__device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, Found* found, int& e, int& first, int& count, int& im,
+                                          int& in)
+{
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int each = (g.E + THREADS - 1) / THREADS, e0 = t * each, e1 = min(e0 + each, g.E);
+    int mine = 0;
+    for (int i = e0; i < e1; i++) {
+        int f;
+        mine += (rows_of(g.offsets, i, g.M, f) + BM - 1) / BM;
+    }
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 63) found->wave[wave] = scan;
+    __syncthreads();
+    int before = scan - mine, total = 0;
+    for (int w = 0; w < THREADS / 64; w++) {
+        if (w < wave) before += found->wave[w];
+        total += found->wave[w];
+    }
+    if ((int64_t)total * tn > (int64_t)gridDim.x) return false;        // (offsets that do not ascend: nothing is done)
+    const int turn = mm_turn(blockIdx.x, total * tn);
+    if (turn < 0) return false;
+    if (turn >= before * tn && turn < (before + mine) * tn) {
+        for (int i = e0; i < e1; i++) {
+            int f;
+            const int n = rows_of(g.offsets, i, g.M, f), tiles = (n + BM - 1) / BM;
+            if (turn < (before + tiles) * tn) {
+                found->e = i;
+                found->first = f;
+                found->count = n;
+                found->tile = turn - before * tn;
+                break;
+            }
+            before += tiles;
+        }
+    }
+    __syncthreads();
+    e = __builtin_amdgcn_readfirstlane(found->e);
+    first = __builtin_amdgcn_readfirstlane(found->first);
+    count = __builtin_amdgcn_readfirstlane(found->count);
+    const int tile = __builtin_amdgcn_readfirstlane(found->tile), tm = (count + BM - 1) / BM;
+    const int band = tile / (8 * tn), rows = min(8, tm - band * 8), inside = tile - band * 8 * tn;
+    im = band * 8 + inside % rows;
+    in = inside / rows;
+    __syncthreads();
+    return true;
+}
+
+// Forward and data gradient: row tiles of each expert by column tiles of C.
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_grouped_rows(GroupedArgs g, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int e, first, count, im, in;
+    if (!find_tile<L::BM, L::THREADS>(g, tn, reinterpret_cast<Found*>(smem), e, first, count, im, in)) return;
+    const MmOperand a{g.a + first * g.lda, g.lda, count}, b{g.b + e * g.group, g.ldb, L::BCOL ? (g.N + 7) / 8 * 8 : g.N};
+    v4f acc[L::MI][L::NI];
+    mm_tile<L>(a, b, im * L::BM, in * L::BN, g.K, smem, acc);
+    MmOut c = g.c;
+    c.M = count;
+    c.c = static_cast<uint8_t*>(c.c) + first * c.ldc * (c.bf16 ? 2 : 4);
+    mm_store_tile<L>(acc, smem, c, im * L::BM, in * L::BN);
+}
+
+// Weight gradient: the tiles of each expert's dW, its rows the contraction.
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_grouped_weights(GroupedArgs g, int tm, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int turn = mm_turn(blockIdx.x, g.E * tm * tn), e = turn / (tm * tn), tile = turn % (tm * tn);
+    int first;
+    const int count = rows_of(g.offsets, e, g.M, first);
+    MmOut c = g.c;
+    if (count == 0 && c.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
+    const int band = tile / (8 * tn), rows = min(8, tm - band * 8), inside = tile - band * 8 * tn;
+    const int m0 = (band * 8 + inside % rows) * L::BM, n0 = inside / rows * L::BN;
+    const MmOperand a{g.a + first * g.lda, g.lda, (c.M + 7) / 8 * 8}, b{g.b + first * g.ldb, g.ldb, (g.N + 7) / 8 * 8};
+    v4f acc[L::MI][L::NI];
+    mm_tile<L>(a, b, m0, n0, count, smem, acc);
+    c.c = static_cast<uint8_t*>(c.c) + (int64_t)e * c.M * c.ldc * (c.bf16 ? 2 : 4);
+    mm_store_tile<L>(acc, smem, c, m0, n0);
+}
+
+inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+inline int64_t over(int64_t n, int64_t b) { return (n + b - 1) / b; }
+constexpr int64_t kMaxSide = 1 << 22;     // rows of a tile times this many elements stay below 2^31 bytes
+
+// Rows of 2-byte elements, src [R][C] -> dst [R][C8] (C8 = C rounded up to 8), zeros past C: what the
+// copies of mm_tile need of operands whose rows do not begin or end at 16 bytes.
+__global__ __launch_bounds__(256) void k_pad_rows(int64_t R, int C, const uint16_t* __restrict__ src, int64_t lds_,
+                                                  uint16_t* __restrict__ dst, int C8)
+{
+    const int segs = C8 / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < R * segs; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / segs;
+        const int c = (int)(i - r * segs) * 8;
+        const uint16_t* s = src + r * lds_ + c;
+        v4u32 v;
+        if (c + 8 <= C) {
+            v = *reinterpret_cast<const v4u32_any*>(s);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                v[u] = (c + 2 * u < C ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < C ? (uint32_t)s[2 * u + 1] << 16 : 0u);
+        }
+        *reinterpret_cast<v4u32*>(dst + r * C8 + c) = v;
+    }
+}
+
+using LdsAllowed = std::atomic<bool>[kMaxDevices];
+hipError_t allow_lds(const void* kernel, int bytes, LdsAllowed& done)
+{
+    if (bytes <= 65536) return hipSuccess;
+    int dev = 0;
+    if (const hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+template <class L>
+hipError_t launch_rows(const GroupedArgs& g, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_grouped_rows<L>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
+    // the most row tiles: every expert's last one may hold a single row
+    const int64_t tn = over(g.N, L::BN), tm = g.M / L::BM + (g.M < g.E ? g.M : g.E);
+    if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(L::THREADS), L::BYTES, s, g, (int)tn);
+    return hipGetLastError();
+}
+template <class L>
+hipError_t launch_weights(const GroupedArgs& g, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_grouped_weights<L>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
+    const int64_t tn = over(g.N, L::BN), tm = over(g.c.M, L::BM);
+    if (g.E * tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(g.E * tm * tn)), dim3(L::THREADS), L::BYTES, s, g, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+
+// Rows of an expert on average choose the tile.
+template <bool BCOL>
+hipError_t run_rows(const GroupedArgs& g, hipStream_t s)
+{
+    const int64_t mean = over(g.M, g.E);
+    if (mean <= 16) return launch_rows<MmTile<1, 4, 1, 1, 4, false, BCOL>>(g, s);
+    if (mean <= 32) return launch_rows<MmTile<2, 2, 1, 2, 4, false, BCOL>>(g, s);
+    if (mean <= 64) return launch_rows<MmTile<2, 2, 2, 2, 3, false, BCOL>>(g, s);
+    if (mean <= 128) return launch_rows<MmTile<2, 2, 4, 4, 2, false, BCOL>>(g, s);
+    return launch_rows<MmTile<2, 4, 8, 4, 2, false, BCOL>>(g, s);
+}
+hipError_t run_weights(const GroupedArgs& g, hipStream_t s)
+{
+    if (g.E * over(g.c.M, 256) * over(g.N, 256) >= 256) return launch_weights<MmTile<2, 4, 8, 4, 2, true, true>>(g, s);
+    return launch_weights<MmTile<2, 2, 4, 4, 2, true, true>>(g, s);
+}
+
+// An operand that mm_tile reads in place: rows that begin at 16 bytes and are whole segments.
+bool in_place(const void* p, int64_t cols, int64_t ld) { return aligned_to(p, 16) && cols % 8 == 0 && ld % 8 == 0; }
+
+struct GroupedLayout {
+    size_t x, dy, w, total;
+    bool pad_x, pad_dy, pad_w;
+};
+// Room for padded copies of the operands that cannot be read in place.
+GroupedLayout grouped_layout(int64_t M, int64_t E, int64_t N, int64_t K, const void* x, int64_t ldx, const void* dy,
+                             int64_t lddy, const void* w, bool backward)
+{
+    GroupedLayout L{};
+    L.pad_x = !in_place(x, K, ldx);
+    L.pad_dy = backward && !in_place(dy, N, lddy);
+    L.pad_w = !in_place(w, K, K);
+    size_t o = 0;
+    auto take = [&](int64_t rows, int64_t cols, bool need) {
+        const size_t at = o;
+        if (need) o += up256((size_t)(rows * up8(cols) * 2));
+        return at;
+    };
+    L.x = take(M, K, L.pad_x);
+    L.dy = take(M, N, L.pad_dy);
+    L.w = take(E * N, K, L.pad_w);
+    L.total = o;
+    return L;
+}
+
+bool side_ok(int64_t n) { return n >= 0 && n <= kMaxSide; }
+int check_grouped(int32_t M, int32_t E, int32_t N, int32_t K)
+{
+    return side_ok(M) && side_ok(N) && side_ok(K) && N >= 1 && K >= 1 && E >= 1 && E <= 1024 ? V4MOE_OK : V4MOE_EDIMS;
+}
+// bf16 rows [R][ld], C used
+int check_rows(const void* p, int64_t R, int64_t C, int64_t ld)
+{
+    if (ld < C || ld > kMaxSide) return V4MOE_EDIMS;
+    if (R > 0 && !p) return V4MOE_ENULL;
+    return aligned_to(p, 2) ? V4MOE_OK : V4MOE_EALIGN;
+}
+// an output [R][ld] of a type
+int check_out(const void* p, int32_t type, int64_t R, int64_t C, int64_t ld)
+{
+    if ((type != V4MOE_TYPE_F32 && type != V4MOE_TYPE_BF16) || ld < C || ld > (1ll << 40)) return V4MOE_EDIMS;
+    if (R > 0 && !p) return V4MOE_ENULL;
+    return aligned_to(p, type == V4MOE_TYPE_F32 ? 4 : 2) ? V4MOE_OK : V4MOE_EALIGN;
+}
+
+hipError_t pad_rows(int64_t R, int C, const void* src, int64_t ld, void* dst, hipStream_t s)
+{
+    if (R == 0) return hipSuccess;
+    const int64_t blocks = over(R * (up8(C) / 8), 256);
+    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, s, R, C,
+                       static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), (int)up8(C));
+    return hipGetLastError();
+}
+
+struct GroupedCall {
+    const uint16_t *x, *dy, *w;
+    int64_t ldx, lddy, ldw;
+};
+// The operands as the products read them: in place, or copied into the workspace.
+int grouped_operands(GroupedCall& o, int32_t M, int32_t E, int32_t N, int32_t K, bool backward, bool need_x, bool need_w,
+                     void* workspace, size_t ws_bytes, hipStream_t s)
+{
+    const GroupedLayout L = grouped_layout(M, E, N, K, o.x, o.ldx, o.dy, o.lddy, o.w, backward);
+    if (L.total > 0 && !workspace) return V4MOE_ENULL;
+    if (!aligned_to(workspace, 16)) return V4MOE_EALIGN;
+    if (ws_bytes < L.total) return V4MOE_EWORKSPACE;
+    if (!device_ready()) return V4MOE_EDEVICE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    auto pad = [&](const uint16_t*& p, int64_t& ld, int64_t rows, int cols, size_t at) {
+        if (pad_rows(rows, cols, p, ld, ws + at, s) != hipSuccess) return false;
+        p = reinterpret_cast<const uint16_t*>(ws + at);
+        ld = up8(cols);
+        return true;
+    };
+    if (L.pad_x && need_x && !pad(o.x, o.ldx, M, K, L.x)) return V4MOE_ELAUNCH;
+    if (L.pad_dy && !pad(o.dy, o.lddy, M, N, L.dy)) return V4MOE_ELAUNCH;
+    if (L.pad_w && need_w && !pad(o.w, o.ldw, (int64_t)E * N, K, L.w)) return V4MOE_ELAUNCH;
+    return V4MOE_OK;
+}
+
+}  // namespace
+
+}  // namespace v4moe
+
+using namespace v4moe;
+
+extern "C" {
+
+__attribute__((visibility("default"))) size_t moe_grouped_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K,
+                                                                          const uint16_t* x, int64_t ldx,
+                                                                          const uint16_t* dy, int64_t lddy,
+                                                                          const uint16_t* w, int32_t backward)
+{
+    if (check_grouped(M, E, N, K)) return 0;
+    return grouped_layout(M, E, N, K, x, ldx, dy, lddy, w, backward != 0).total;
+}
+
+__attribute__((visibility("default"))) int moe_grouped_linear(int32_t M, int32_t E, int32_t N, int32_t K,
+                                                              const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                                              const int32_t* offsets, void* y, int32_t y_type,
+                                                              int64_t ldy, void* workspace, size_t ws_bytes,
+                                                              void* stream)
+{
+    if (const int rc = check_grouped(M, E, N, K)) return rc;
+    if (const int rc = check_rows(x, M, K, ldx)) return rc;
+    if (const int rc = check_out(y, y_type, M, N, ldy)) return rc;
+    if (M == 0) return V4MOE_OK;
+    if (!w || !offsets) return V4MOE_ENULL;
+    if (!aligned_to(w, 2) || !aligned_to(offsets, 4)) return V4MOE_EALIGN;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    GroupedCall o{x, nullptr, w, ldx, 0, K};
+    if (const int rc = grouped_operands(o, M, E, N, K, false, true, true, workspace, ws_bytes, s)) return rc;
+    const GroupedArgs g{M, N, K, E, offsets, o.x, o.ldx, o.w, o.ldw, (int64_t)N * o.ldw,
+                        MmOut{y, ldy, 0, N, y_type == V4MOE_TYPE_BF16, 0}};
+    return run_rows<false>(g, s) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+}
+
+__attribute__((visibility("default"))) int moe_grouped_linear_backward(
+    int32_t M, int32_t E, int32_t N, int32_t K, const uint16_t* x, int64_t ldx, const uint16_t* dy, int64_t lddy,
+    const uint16_t* w, const int32_t* offsets, void* dx, int32_t dx_type, int64_t lddx, void* dw, int32_t dw_type,
+    int32_t accumulate, void* workspace, size_t ws_bytes, void* stream)
+{
+    if (const int rc = check_grouped(M, E, N, K)) return rc;
+    if (!dx && !dw) return V4MOE_ENULL;
+    if (dw)
+        if (const int rc = check_rows(x, M, K, ldx)) return rc;
+    if (const int rc = check_rows(dy, M, N, lddy)) return rc;
+    if (dx)
+        if (const int rc = check_out(dx, dx_type, M, K, lddx)) return rc;
+    if (dw)
+        if (const int rc = check_out(dw, dw_type, 1, K, K)) return rc;
+    if (!offsets || (dx && M > 0 && !w)) return V4MOE_ENULL;
+    if (!aligned_to(offsets, 4) || !aligned_to(w, 2)) return V4MOE_EALIGN;
+    if (M == 0 && (!dw || accumulate)) return V4MOE_OK;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    GroupedCall o{x, dy, w, ldx, lddy, K};
+    if (const int rc = grouped_operands(o, M, E, N, K, true, dw != nullptr, dx != nullptr && M > 0, workspace, ws_bytes, s))
+        return rc;
+    if (dx && M > 0) {
+        // contraction over N, which the weights have across their rows
+        const GroupedArgs g{M, K, N, E, offsets, o.dy, o.lddy, o.w, o.ldw, (int64_t)N * o.ldw,
+                            MmOut{dx, lddx, 0, K, dx_type == V4MOE_TYPE_BF16, 0}};
+        if (run_rows<true>(g, s) != hipSuccess) return V4MOE_ELAUNCH;
+    }
+    if (dw) {
+        const GroupedArgs g{M, K, 0, E, offsets, o.dy, o.lddy, o.x, o.ldx, 0,
+                            MmOut{dw, K, N, K, dw_type == V4MOE_TYPE_BF16, accumulate != 0}};
+        if (run_weights(g, s) != hipSuccess) return V4MOE_ELAUNCH;
+    }
+    return V4MOE_OK;
+}
+
+}  // extern "C"

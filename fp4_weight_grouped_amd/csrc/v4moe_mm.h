@@ -1,0 +1,321 @@
+// v4moe_mm.h -- a block's tile of a bf16 matrix product on gfx950, for the kernels
+// that differ in where a tile's operands lie and in what becomes of its sums.
+//
+//   C[m][n] = sum_k A(m, k) B(n, k),  fp32 sums
+//
+// Either operand may be contiguous along k ("rows": [m][k]) or along its own
+// index ("columns": [k][m]), which the gradients need: dx = dy W reads W along
+// the contraction, dW = dy^T x both operands.  Nothing is transposed in memory:
+// columns are staged as they lie and gfx950's transposing LDS read turns them
+// into the matrix instruction's operand.
+//
+// Every element of C is one chain of matrix instructions over k in steps of 32,
+// ascending, whatever the tile: a result does not depend on the variant, nor on
+// the other rows of a call, in any bit.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "v4moe_device.h"
+
+namespace v4moe {
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef uint32_t v4u32 __attribute__((ext_vector_type(4)));
+typedef v4u32 v4u32_any __attribute__((aligned(2)));
+
+// What a 16-byte segment past the end of the contraction is copied from.
+static __device__ const uint4 g_mm_zeros[64] = {};
+
+// An operand: element (i, k) at p[i * ld + k], or with columns at p[k * ld + i];
+// i < n, n >= 1.  p 16-byte aligned, ld a multiple of 8, the contiguous length too.
+struct MmOperand {
+    const uint16_t* p;
+    int64_t ld;
+    int n;
+};
+
+// WM x WN waves, each MI x NI tiles of 16x16; NS stages of 64 k in LDS.
+template <int WM_, int WN_, int MI_, int NI_, int NS_, bool ACOL_, bool BCOL_>
+struct MmTile {
+    static constexpr int WM = WM_, WN = WN_, MI = MI_, NI = NI_, NS = NS_;
+    static constexpr bool ACOL = ACOL_, BCOL = BCOL_;
+    static constexpr int NW = WM * WN, THREADS = 64 * NW, BM = WM * MI * 16, BN = WN * NI * 16;
+    static constexpr int AP = BM / 8, BP = BN / 8;                          // 1 KiB pieces of a stage
+    static constexpr int AJ = (AP + NW - 1) / NW, BJ = (BP + NW - 1) / NW;  // per wave
+    static constexpr int OPS = AJ + BJ;
+    static constexpr int B_OFF = BM * 128, STAGE = (BM + BN) * 128, RING = NS * STAGE;
+    static constexpr int C_BYTES = 2 * 16 * NI * 16 * 4;                    // of staging per wave (mm_store)
+    static constexpr int BYTES = RING > NW * C_BYTES ? RING : NW * C_BYTES;
+    static_assert(NW > 1 && NS >= 2 && OPS * (NS - 1) < 64, "the barrier frees a slot; vmcnt range");
+    static_assert(!ACOL || BM >= 64, "columns are staged in rows of 128 bytes or more");
+    static_assert(!BCOL || BN >= 64, "columns are staged in rows of 128 bytes or more");
+};
+
+// Where the 16-byte segments of a stage go.  Rows [i][64 k]: segment s of row i at
+// s ^ (i / 2 % 8), so that the 16 rows of an operand read hit distinct banks.
+// Columns [k][W]: pairs of segments (the 32 bytes a transposing read takes of a row)
+// XORed by column_swizzle(k), so that the eight rows read together do.
+template <int W>
+__device__ __forceinline__ int column_swizzle(int k)
+{
+    if constexpr (W >= 128) return (k & 3) | ((k >> 1) & 4);
+    else return ((k >> 1) & 1) | ((k >> 2) & 2);
+}
+
+// One operand of a tile, its first index i0: copies into LDS and reads of fragments.
+// W: indices of the tile, COL: columns, PJ: pieces per wave, NW: waves.
+template <int W, bool COL, int PJ, int NW>
+struct MmSide {
+    static constexpr int SEGS = W / 8;              // 16-byte segments of a row of k, columns
+    const uint8_t* base;                            // of chunk 0
+    int64_t step;                                   // bytes to the next chunk
+    uint32_t off[PJ];                               // this lane's segments
+    int wave, lane;
+
+    __device__ __forceinline__ void begin(const MmOperand& o, int i0, int wave_, int lane_)
+    {
+        wave = wave_;
+        lane = lane_;
+        base = reinterpret_cast<const uint8_t*>(o.p + (COL ? (int64_t)i0 : (int64_t)i0 * o.ld));
+        step = COL ? o.ld * 128 : 128;
+#pragma unroll
+        for (int j = 0; j < PJ; j++) {
+            const int p = piece(j);
+            if constexpr (COL) {
+                const int k = row_of(p);
+                off[j] = (uint32_t)(k * (int)o.ld * 2 + min(seg_of(p), (o.n - i0) / 8 - 1) * 16);
+            } else {
+                const int r = row_of(p);
+                off[j] = (uint32_t)(min(r, o.n - 1 - i0) * (int)o.ld * 2 + seg_of(p) * 16);
+            }
+        }
+    }
+    __device__ __forceinline__ int piece(int j) const { return min(wave + j * NW, W / 8 - 1); }
+    // the row (i, or k with columns) and the segment in it that this lane copies of a piece
+    __device__ __forceinline__ int row_of(int p) const { return COL ? (p * 64 + lane) / SEGS : p * 8 + (lane >> 3); }
+    __device__ __forceinline__ int seg_of(int p) const
+    {
+        if constexpr (COL) return ((p * 64 + lane) % SEGS) ^ (2 * column_swizzle<W>(row_of(p)));
+        else return (lane & 7) ^ ((row_of(p) >> 1) & 7);
+    }
+    // this wave's copies of a chunk into a stage; left: of the contraction, from the chunk's first k
+    __device__ __forceinline__ void issue(int c, uint32_t to, int left) const
+    {
+        const uint8_t* at = base + (int64_t)c * step;
+        if (left >= 64) {
+#pragma unroll
+            for (int j = 0; j < PJ; j++) dma16s(at, off[j], __builtin_amdgcn_readfirstlane(to + piece(j) * 1024));
+        } else {
+#pragma unroll
+            for (int j = 0; j < PJ; j++) {
+                const int p = piece(j);
+                const bool in = COL ? row_of(p) < left : seg_of(p) * 8 < left;
+                dma16(in ? (const void*)(at + off[j]) : (const void*)&g_mm_zeros[lane],
+                      __builtin_amdgcn_readfirstlane(to + p * 1024));
+            }
+        }
+    }
+};
+
+// A lane's reads of the fragments of T tiles from `first` on: fragment s (0, 1) of tile t
+// holds index 16 (first + t) + lane % 16 and k = 32 s + 8 (lane / 16) .. + 7.
+template <int W, bool COL, int T>
+struct MmReader {
+    int at[COL ? T : 2];
+    __device__ __forceinline__ void begin(int first, int lane)
+    {
+        const int i = lane & 15, kq = lane >> 4;
+        if constexpr (COL) {
+            const int k = 8 * kq + (i >> 2), f = column_swizzle<W>(k);
+#pragma unroll
+            for (int t = 0; t < T; t++) at[t] = k * W * 2 + ((first + t) ^ f) * 32 + (i & 3) * 8;
+        } else {
+            const int sw = (lane >> 1) & 7, row = (16 * first + i) * 128;
+            at[0] = row + ((kq ^ sw) * 16);
+            at[1] = row + (((4 + kq) ^ sw) * 16);
+        }
+    }
+    __device__ __forceinline__ v8bf read(const uint8_t* stage, int t, int s) const
+    {
+        if constexpr (COL) {
+            typedef __attribute__((address_space(3))) v4s* lds4;
+            // (four rows of k further on the swizzle is the same)
+            const lds4 p = (lds4)(stage + at[t] + s * 32 * W * 2), q = (lds4)(stage + at[t] + (s * 32 + 4) * W * 2);
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p), hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(q);
+            typedef short v8s __attribute__((ext_vector_type(8)));
+            return __builtin_bit_cast(v8bf, v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        } else {
+            return *reinterpret_cast<const v8bf*>(stage + at[s] + t * 2048);
+        }
+    }
+};
+
+// The sums of a block's tile from (m0, n0): acc[i][j] of a wave (wm, wn) holds, in lane l,
+// row m0 + 16 (wm MI + i) + l % 16 and columns n0 + 16 (wn NI + j) + 4 (l / 16) .. + 3.
+// B is the instruction's first operand, so that a lane has consecutive columns.  The
+// block's LDS (L::BYTES) is free when it returns.
+template <class L>
+__device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, int m0, int n0, int K, uint8_t* smem,
+                                        v4f (&acc)[L::MI][L::NI])
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = wave / L::WN, wn = wave % L::WN;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+    MmSide<L::BM, L::ACOL, L::AJ, L::NW> sa;
+    MmSide<L::BN, L::BCOL, L::BJ, L::NW> sb;
+    sa.begin(a, m0, wave, lane);
+    sb.begin(b, n0, wave, lane);
+    const int nch = (K + 63) / 64;
+    auto issue = [&](int c) {
+        const uint32_t slot = lds0 + (uint32_t)(c % L::NS) * L::STAGE;
+        sa.issue(c, slot, K - c * 64);
+        sb.issue(c, slot + L::B_OFF, K - c * 64);
+    };
+    MmReader<L::BM, L::ACOL, L::MI> ra;
+    MmReader<L::BN, L::BCOL, L::NI> rb;
+    ra.begin(wm * L::MI, lane);
+    rb.begin(wn * L::NI, lane);
+#pragma unroll
+    for (int i = 0; i < L::MI; i++)
+#pragma unroll
+        for (int j = 0; j < L::NI; j++) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    // Row tiles of A in registers: all of a small wave tile's, three of a large one's.
+    constexpr int MI = L::MI, NI = L::NI, D = MI < 3 ? MI : 3;
+    v8bf af[D][2], bf[NI][2];
+    auto read_a = [&](const uint8_t* st, int i) {
+#pragma unroll
+        for (int s = 0; s < 2; s++) af[i % D][s] = ra.read(st, i, s);
+    };
+    auto open = [&](int c) {
+        const uint8_t* st = smem + (c % L::NS) * L::STAGE;
+#pragma unroll
+        for (int j = 0; j < NI; j++)
+#pragma unroll
+            for (int s = 0; s < 2; s++) bf[j][s] = rb.read(st + L::B_OFF, j, s);
+#pragma unroll
+        for (int i = 0; i < (D < MI ? D - 1 : D); i++) read_a(st, i);
+    };
+    auto row = [&](int i) {
+#pragma unroll
+        for (int s = 0; s < 2; s++)
+#pragma unroll
+            for (int j = 0; j < NI; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[i % D][s], acc[i][j], 0, 0, 0);
+    };
+    if (nch > 0) {
+#pragma unroll
+        for (int c = 0; c < L::NS; c++)
+            if (c < nch) issue(c);
+        if (nch >= L::NS) wait_vm<L::OPS * (L::NS - 1)>();
+        else wait_vm<0>();
+        __syncthreads();
+        open(0);
+    }
+    for (int c = 0; c < nch; c++) {
+        const uint8_t* st = smem + (c % L::NS) * L::STAGE;
+#pragma unroll
+        for (int i = 0; i < MI - 1; i++) {
+            if (D < MI && i + D - 1 < MI) read_a(st, i + D - 1);
+            row(i);
+        }
+        // Every operand of the chunk is in registers: the barrier frees its slot and makes the
+        // next chunk whole (only later ones' copies are then out).
+        if (c + 1 < nch) {
+            if (c + L::NS <= nch) wait_vm<L::OPS * (L::NS - 2)>();
+            else wait_vm<0>();
+            __syncthreads();
+            if (c + L::NS < nch) issue(c + L::NS);
+        }
+        row(MI - 1);
+        if (c + 1 < nch) open(c + 1);
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// A matrix that takes a tile's sums
+// ---------------------------------------------------------------------------
+struct MmOut {
+    void* c;                 // element (m, n) at c[m * ldc + n], m < M, n < N
+    int64_t ldc;
+    int M, N;
+    int bf16, accumulate;    // accumulate: what c holds + the sum, in fp32, rounded once
+};
+
+// A wave's sums to C from (m0, n0), 16 rows at a time through LDS (two buffers of 16
+// rows): a lane's four columns become 16-byte stores along the rows.  Segments are
+// XOR-swizzled by the row.  S: the type staged, fp32 where C is added to.
+template <bool STREAM, int MI, int NI, typename S, typename T>
+__device__ __forceinline__ void mm_store(const v4f (&acc)[MI][NI], uint8_t* stage, const MmOut& o, int m0, int n0)
+{
+    constexpr int ES = sizeof(S), RB = NI * 16 * ES, LR = RB / 16, PER = 16 / ES;
+    constexpr int RP = 64 / LR;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < MI; i++) {
+        uint8_t* buf = stage + (i & 1) * (16 * NI * 16 * 4);
+#pragma unroll
+        for (int j = 0; j < NI; j++) {
+            const int at = (16 * j + 4 * kq) * ES;
+            uint8_t* d = buf + r16 * RB + (((at >> 4) ^ (r16 & (LR - 1))) << 4) + (at & 15);
+            if constexpr (ES == 2)
+                *reinterpret_cast<uint2*>(d) =
+                    make_uint2(bf16x2(acc[i][j][0], acc[i][j][1]), bf16x2(acc[i][j][2], acc[i][j][3]));
+            else
+                *reinterpret_cast<float4*>(d) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 16; q += RP) {
+            const int r = q + lane / LR, sg = lane % LR;
+            if (r >= 16) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + r * RB + ((sg ^ (r & (LR - 1))) << 4));
+            const int m = m0 + 16 * i + r, n = n0 + sg * PER;
+            if (m >= o.M || n >= o.N) continue;
+            T* c = static_cast<T*>(o.c) + (int64_t)m * o.ldc + n;
+            if constexpr (sizeof(S) == sizeof(T)) {
+                if (n + PER <= o.N && !o.accumulate) {
+                    const v4u32 w4 = {v.x, v.y, v.z, v.w};
+                    if (STREAM) __builtin_nontemporal_store(w4, reinterpret_cast<v4u32_any*>(c));
+                    else *reinterpret_cast<v4u32_any*>(c) = w4;
+                    continue;
+                }
+            }
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < PER; e++) {
+                if (n + e >= o.N) break;
+                if constexpr (ES == 2) c[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                else if constexpr (sizeof(T) == 2) c[e] = (uint16_t)bf16x2(bf16_to_f32(c[e]) + __uint_as_float(w[e]), 0.0f);
+                else c[e] = o.accumulate ? c[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ... of a block's tile.
+template <class L>
+__device__ __forceinline__ void mm_store_tile(const v4f (&acc)[L::MI][L::NI], uint8_t* smem, const MmOut& o, int m0, int n0)
+{
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    uint8_t* stage = smem + wave * L::C_BYTES;
+    const int mw = m0 + wave / L::WN * L::MI * 16, nw = n0 + wave % L::WN * L::NI * 16;
+    constexpr bool STREAM = L::BM * L::BN >= 128 * 128;
+    if (!o.bf16) mm_store<STREAM, L::MI, L::NI, float, float>(acc, stage, o, mw, nw);
+    else if (o.accumulate) mm_store<STREAM, L::MI, L::NI, float, uint16_t>(acc, stage, o, mw, nw);
+    else mm_store<STREAM, L::MI, L::NI, uint16_t, uint16_t>(acc, stage, o, mw, nw);
+}
+
+// The tile of a block's turn.  Blocks go to the eight XCDs in turn: XCD x takes the x-th
+// eighth of n tiles, so that tiles that follow each other share operands in its L2.
+__device__ __forceinline__ int mm_turn(int block, int n)
+{
+    const int x = block & 7, i = block >> 3, each = n >> 3, rest = n & 7;
+    return i < each + (x < rest) ? x * each + min(x, rest) + i : -1;
+}
+
+}  // namespace v4moe

@@ -138,6 +138,11 @@ def lib():
         EP = ctypes.POINTER(ExpertsC)
         L.moe_routed_forward.argtypes = [_DP, _vp, _vp, _vp, EP, _vp, _vp, _vp, _sz, _vp]
         L.moe_routed_backward.argtypes = [_DP, _vp, _vp, _vp, EP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.moe_grouped_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i32]
+        L.moe_grouped_workspace_bytes.restype = _sz
+        L.moe_grouped_linear.argtypes = [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
+        L.moe_grouped_linear_backward.argtypes = [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i64,
+                                                  _vp, _i32, _i32, _vp, _sz, _vp]
         L.moe_time_next_ffn.argtypes = [_vp, _vp]
         L.moe_time_next_ffn.restype = None
         for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
@@ -145,7 +150,7 @@ def lib():
                   "moe_prepack_weights", "moe_dequant_fp8", "moe_quantize_weights", "moe_transpose_weights",
                   "moe_layer_backward", "moe_routed_forward", "moe_routed_backward", "moe_gate", "moe_gate_backward", "moe_fp8_quantize",
                   "moe_fp8_quantize_weights", "moe_fp8_gemm", "moe_fp8_linear", "moe_fp8_linear_backward",
-                  "moe_clip_grads"):
+                  "moe_clip_grads", "moe_grouped_linear", "moe_grouped_linear_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -624,6 +629,53 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
 @functools.lru_cache(maxsize=1024)
 def _clip_workspace_bytes(count: int) -> int:
     return int(lib().moe_clip_workspace_bytes(count))
+
+
+def _grouped(x, w, offsets):
+    """(M, E, N, K, GPU, x's leading dimension, addresses of w and of the offsets) of a grouped product, checked."""
+    M, (E, N, K) = x.shape[0], w.shape
+    gpu = _device_of(x, "x")
+    ldx = _matrix(x, M, K, "x", gpu, torch.bfloat16)
+    return (M, E, N, K, gpu, ldx, _dense(w, (E, N, K), torch.bfloat16, "w", gpu),
+            _dense(offsets, (E + 1,), torch.int32, "offsets", gpu))
+
+
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[m] = W[e] x[m] for the rows offsets[e] <= m < offsets[e + 1] of each expert e: x bf16 [M][K] (rows may be
+    strided), w bf16 [E][N][K], offsets int32 [E + 1] (forward_routed's expert_offsets), y [M][N] (bf16 unless ``out``
+    says otherwise).  Rows of no expert are not written.  See moe_grouped_linear in include/v4moe.h."""
+    M, E, N, K, gpu, ldx, wp, op = _grouped(x, w, offsets)
+    stream = _raw_stream(gpu)
+    dev = x.device
+    if out is None:
+        out = _empty(M, N, torch.bfloat16, dev)
+    ldy, xp = _matrix(out, M, N, "out", gpu), x.data_ptr()
+    n = lib().moe_grouped_workspace_bytes(M, E, N, K, xp, ldx, None, 0, wp, 0)
+    ws = _bytes(n, dev) if n else None
+    _check(lib().moe_grouped_linear(M, E, N, K, xp, ldx, wp, op, out.data_ptr(), _type(out), ldy,
+                                    ws.data_ptr() if n else None, n, stream))
+    return out
+
+
+def grouped_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                            dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False):
+    """Gradients of grouped_linear: (dx [M][K], dw [E][N][K]), bf16 unless given; accumulate adds to the given dw."""
+    M, E, N, K, gpu, ldx, wp, op = _grouped(x, w, offsets)
+    lddy = _matrix(dy, M, N, "dy", gpu, torch.bfloat16)
+    stream = _raw_stream(gpu)
+    dev = x.device
+    _require(dw is not None or not accumulate, "accumulate needs dw")
+    if dx is None:
+        dx = _empty(M, K, torch.bfloat16, dev)
+    if dw is None:
+        dw = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev)
+    lddx, dwp = _matrix(dx, M, K, "dx", gpu), _dense(dw, (E, N, K), dw.dtype, "dw", gpu)
+    xp, dyp = x.data_ptr(), dy.data_ptr()
+    n = lib().moe_grouped_workspace_bytes(M, E, N, K, xp, ldx, dyp, lddy, wp, 1)
+    ws = _bytes(n, dev) if n else None
+    _check(lib().moe_grouped_linear_backward(M, E, N, K, xp, ldx, dyp, lddy, wp, op, dx.data_ptr(), _type(dx), lddx, dwp,
+                                             _type(dw), 1 if accumulate else 0, ws.data_ptr() if n else None, n, stream))
+    return dx, dw
 
 
 # ---- conveniences for callers holding host (numpy) weights ----------------------------------

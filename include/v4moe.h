@@ -461,6 +461,38 @@ size_t moe_clip_workspace_bytes(int32_t count);
 int moe_clip_grads(int32_t count, const v4moe_tensor* tensors, float max_norm, float* norm,
                    void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Products grouped by expert, bf16 weights ----
+ * Rows are sorted by expert: expert e has the rows offsets[e] <= m < offsets[e + 1]
+ * (offsets int32 [E+1] on the device, as moe_permute writes them: ascending, within
+ * [0, M]; 1 <= E <= 1024).  w bf16 [E][N][K], contiguous; x, dy, y, dx have leading
+ * dimensions.  0 <= M, 1 <= N, K, and leading dimensions of bf16 operands, up to 2^22.
+ * Sums are fp32, in an order that depends on the contraction alone: a row's result
+ * does not depend on the other rows.  Rows before the first expert's and behind the
+ * last one's take no part, and those of outputs are left as they are.  Pointers:
+ * aligned to their element. */
+
+/* Workspace bytes of the calls below (host-only, pure; 0 for invalid sizes): operands
+ * whose rows do not begin at 16 bytes, or are not a multiple of 8 elements long, are
+ * copied there first; the pointers are only looked at for that.  16-byte aligned. */
+size_t moe_grouped_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K, const uint16_t* x,
+                                   int64_t ldx, const uint16_t* dy, int64_t lddy, const uint16_t* w,
+                                   int32_t backward);
+
+/* y[m] = W[e] x[m] for each row m of each expert e: y [M][ldy] of a type. */
+int moe_grouped_linear(int32_t M, int32_t E, int32_t N, int32_t K, const uint16_t* x, int64_t ldx,
+                       const uint16_t* w, const int32_t* offsets, void* y, int32_t y_type,
+                       int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+
+/* Its gradients: dx[m] = W[e]^T dy[m], dW[e] (+)= sum over e's rows of dy[m] x[m]^T
+ * (dw [E][N][K], contiguous; with accumulate added to in fp32 and rounded once).
+ * dx or dw may be NULL.  Experts without rows get a dW of zeros (with accumulate:
+ * theirs is left alone). */
+int moe_grouped_linear_backward(int32_t M, int32_t E, int32_t N, int32_t K, const uint16_t* x,
+                                int64_t ldx, const uint16_t* dy, int64_t lddy, const uint16_t* w,
+                                const int32_t* offsets, void* dx, int32_t dx_type, int64_t lddx,
+                                void* dw, int32_t dw_type, int32_t accumulate, void* workspace,
+                                size_t ws_bytes, void* stream);
+
 /* Profiling hook (no effect on results).  start/stop are hipEvent_t handles
  * created by the caller (or NULL to clear).  The next moe_expert_ffn or
  * moe_layer_forward call made by this host thread records `start` on its
