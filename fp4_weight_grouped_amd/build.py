@@ -9,7 +9,8 @@ ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libv4moe.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("v4moe_kernels.hip", "v4moe_bwd.hip", "v4moe_api.cpp",
                                                                "v4moe_noalloc.hip", "v4moe_gate.hip",
-                                                               "v4moe_fp8.hip", "v4moe_clip.hip", "v4moe_grouped.hip")]
+                                                               "v4moe_fp8.hip", "v4moe_clip.hip", "v4moe_grouped.hip",
+                                                               "v4moe_xent.hip")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("v4moe_device.h", "v4moe_internal.h", "v4moe_mm.h")] + \
     [os.path.join(ROOT, "include", "v4moe.h")]
 

@@ -15,8 +15,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <atomic>
-
 namespace v4moe {
 
 namespace {
@@ -85,10 +83,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, Found* f
     e = __builtin_amdgcn_readfirstlane(found->e);
     first = __builtin_amdgcn_readfirstlane(found->first);
     count = __builtin_amdgcn_readfirstlane(found->count);
-    const int tile = __builtin_amdgcn_readfirstlane(found->tile), tm = (count + BM - 1) / BM;
-    const int band = tile / (8 * tn), rows = min(8, tm - band * 8), inside = tile - band * 8 * tn;
-    im = band * 8 + inside % rows;
-    in = inside / rows;
+    mm_band(__builtin_amdgcn_readfirstlane(found->tile), (count + BM - 1) / BM, tn, im, in);
     __syncthreads();
     return true;
 }
@@ -119,20 +114,15 @@ __global__ __launch_bounds__(L::THREADS) void k_grouped_weights(GroupedArgs g, i
     const int count = rows_of(g.offsets, e, g.M, first);
     MmOut c = g.c;
     if (count == 0 && c.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
-    const int band = tile / (8 * tn), rows = min(8, tm - band * 8), inside = tile - band * 8 * tn;
-    const int m0 = (band * 8 + inside % rows) * L::BM, n0 = inside / rows * L::BN;
+    int im, in;
+    mm_band(tile, tm, tn, im, in);
+    const int m0 = im * L::BM, n0 = in * L::BN;
     const MmOperand a{g.a + first * g.lda, g.lda, (c.M + 7) / 8 * 8}, b{g.b + first * g.ldb, g.ldb, (g.N + 7) / 8 * 8};
     v4f acc[L::MI][L::NI];
     mm_tile<L>(a, b, m0, n0, count, smem, acc);
     c.c = static_cast<uint8_t*>(c.c) + (int64_t)e * c.M * c.ldc * (c.bf16 ? 2 : 4);
     mm_store_tile<L>(acc, smem, c, m0, n0);
 }
-
-inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
-inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
-inline int64_t over(int64_t n, int64_t b) { return (n + b - 1) / b; }
-constexpr int64_t kMaxSide = 1 << 22;     // rows of a tile times this many elements stay below 2^31 bytes
 
 // Rows of 2-byte elements, src [R][C] -> dst [R][C8] (C8 = C rounded up to 8), zeros past C: what the
 // copies of mm_tile need of operands whose rows do not begin or end at 16 bytes.
@@ -154,19 +144,6 @@ __global__ __launch_bounds__(256) void k_pad_rows(int64_t R, int C, const uint16
         }
         *reinterpret_cast<v4u32*>(dst + r * C8 + c) = v;
     }
-}
-
-using LdsAllowed = std::atomic<bool>[kMaxDevices];
-hipError_t allow_lds(const void* kernel, int bytes, LdsAllowed& done)
-{
-    if (bytes <= 65536) return hipSuccess;
-    int dev = 0;
-    if (const hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire)) return hipSuccess;
-    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == hipSuccess) done[dev].store(true, std::memory_order_release);
-    return e;
 }
 
 template <class L>
@@ -210,9 +187,6 @@ hipError_t run_weights(const GroupedArgs& g, hipStream_t s)
     return launch_weights<MmTile<2, 2, 4, 4, 2, true, true>>(g, s);
 }
 
-// An operand that mm_tile reads in place: rows that begin at 16 bytes and are whole segments.
-bool in_place(const void* p, int64_t cols, int64_t ld) { return aligned_to(p, 16) && cols % 8 == 0 && ld % 8 == 0; }
-
 struct GroupedLayout {
     size_t x, dy, w, total;
     bool pad_x, pad_dy, pad_w;
@@ -238,35 +212,10 @@ GroupedLayout grouped_layout(int64_t M, int64_t E, int64_t N, int64_t K, const v
     return L;
 }
 
-bool side_ok(int64_t n) { return n >= 0 && n <= kMaxSide; }
 int check_grouped(int32_t M, int32_t E, int32_t N, int32_t K)
 {
     return side_ok(M) && side_ok(N) && side_ok(K) && N >= 1 && K >= 1 && E >= 1 && E <= 1024 ? V4MOE_OK : V4MOE_EDIMS;
 }
-// bf16 rows [R][ld], C used
-int check_rows(const void* p, int64_t R, int64_t C, int64_t ld)
-{
-    if (ld < C || ld > kMaxSide) return V4MOE_EDIMS;
-    if (R > 0 && !p) return V4MOE_ENULL;
-    return aligned_to(p, 2) ? V4MOE_OK : V4MOE_EALIGN;
-}
-// an output [R][ld] of a type
-int check_out(const void* p, int32_t type, int64_t R, int64_t C, int64_t ld)
-{
-    if ((type != V4MOE_TYPE_F32 && type != V4MOE_TYPE_BF16) || ld < C || ld > (1ll << 40)) return V4MOE_EDIMS;
-    if (R > 0 && !p) return V4MOE_ENULL;
-    return aligned_to(p, type == V4MOE_TYPE_F32 ? 4 : 2) ? V4MOE_OK : V4MOE_EALIGN;
-}
-
-hipError_t pad_rows(int64_t R, int C, const void* src, int64_t ld, void* dst, hipStream_t s)
-{
-    if (R == 0) return hipSuccess;
-    const int64_t blocks = over(R * (up8(C) / 8), 256);
-    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, s, R, C,
-                       static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), (int)up8(C));
-    return hipGetLastError();
-}
-
 struct GroupedCall {
     const uint16_t *x, *dy, *w;
     int64_t ldx, lddy, ldw;
@@ -282,7 +231,7 @@ int grouped_operands(GroupedCall& o, int32_t M, int32_t E, int32_t N, int32_t K,
     if (!device_ready()) return V4MOE_EDEVICE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto pad = [&](const uint16_t*& p, int64_t& ld, int64_t rows, int cols, size_t at) {
-        if (pad_rows(rows, cols, p, ld, ws + at, s) != hipSuccess) return false;
+        if (launch_pad_rows(rows, cols, p, ld, ws + at, s) != hipSuccess) return false;
         p = reinterpret_cast<const uint16_t*>(ws + at);
         ld = up8(cols);
         return true;
@@ -294,6 +243,15 @@ int grouped_operands(GroupedCall& o, int32_t M, int32_t E, int32_t N, int32_t K,
 }
 
 }  // namespace
+
+hipError_t launch_pad_rows(int64_t R, int C, const void* src, int64_t ld, void* dst, hipStream_t s)
+{
+    if (R == 0) return hipSuccess;
+    const int64_t blocks = over(R * (up8(C) / 8), 256);
+    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, s, R, C,
+                       static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), (int)up8(C));
+    return hipGetLastError();
+}
 
 }  // namespace v4moe
 

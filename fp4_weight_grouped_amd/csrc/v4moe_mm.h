@@ -17,7 +17,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "v4moe.h"
 #include "v4moe_device.h"
+#include "v4moe_internal.h"
 
 namespace v4moe {
 
@@ -25,6 +29,8 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u32 __attribute__((ext_vector_type(4)));
 typedef v4u32 v4u32_any __attribute__((aligned(2)));
+typedef uint32_t v2u32 __attribute__((ext_vector_type(2)));
+typedef v2u32 v2u32_any __attribute__((aligned(2)));
 
 // What a 16-byte segment past the end of the contraction is copied from.
 static __device__ const uint4 g_mm_zeros[64] = {};
@@ -285,6 +291,23 @@ __device__ __forceinline__ void mm_store(const v4f (&acc)[MI][NI], uint8_t* stag
                 }
             }
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (ES == 4) {
+                if (n + PER <= o.N) {                  // added to, four at a time
+                    const float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+                    if constexpr (sizeof(T) == 4) {
+                        v4u32 b = *reinterpret_cast<const v4u32_any*>(c);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) b[e] = __float_as_uint(__uint_as_float(b[e]) + f[e]);
+                        *reinterpret_cast<v4u32_any*>(c) = b;
+                    } else {
+                        const v2u32 b = *reinterpret_cast<const v2u32_any*>(c);
+                        *reinterpret_cast<v2u32_any*>(c) =
+                            v2u32{bf16x2(bf16_to_f32(b[0] & 0xFFFFu) + f[0], bf16_to_f32(b[0] >> 16) + f[1]),
+                                  bf16x2(bf16_to_f32(b[1] & 0xFFFFu) + f[2], bf16_to_f32(b[1] >> 16) + f[3])};
+                    }
+                    continue;
+                }
+            }
 #pragma unroll
             for (int e = 0; e < PER; e++) {
                 if (n + e >= o.N) break;
@@ -297,14 +320,13 @@ __device__ __forceinline__ void mm_store(const v4f (&acc)[MI][NI], uint8_t* stag
     }
 }
 
-// ... of a block's tile.
-template <class L>
+// ... of a block's tile.  STREAM: past the caches, for what nothing reads soon.
+template <class L, bool STREAM = (L::BM * L::BN >= 128 * 128)>
 __device__ __forceinline__ void mm_store_tile(const v4f (&acc)[L::MI][L::NI], uint8_t* smem, const MmOut& o, int m0, int n0)
 {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     uint8_t* stage = smem + wave * L::C_BYTES;
     const int mw = m0 + wave / L::WN * L::MI * 16, nw = n0 + wave % L::WN * L::NI * 16;
-    constexpr bool STREAM = L::BM * L::BN >= 128 * 128;
     if (!o.bf16) mm_store<STREAM, L::MI, L::NI, float, float>(acc, stage, o, mw, nw);
     else if (o.accumulate) mm_store<STREAM, L::MI, L::NI, float, uint16_t>(acc, stage, o, mw, nw);
     else mm_store<STREAM, L::MI, L::NI, uint16_t, uint16_t>(acc, stage, o, mw, nw);
@@ -316,6 +338,63 @@ __device__ __forceinline__ int mm_turn(int block, int n)
 {
     const int x = block & 7, i = block >> 3, each = n >> 3, rest = n & 7;
     return i < each + (x < rest) ? x * each + min(x, rest) + i : -1;
+}
+
+// Tile `tile` of tm x tn, column by column in bands of eight row tiles: those that run
+// together share rows of both operands.
+__device__ __forceinline__ void mm_band(int tile, int tm, int tn, int& im, int& in)
+{
+    const int band = tile / (8 * tn), rows = min(8, tm - band * 8), inside = tile - band * 8 * tn;
+    im = band * 8 + inside % rows;
+    in = inside / rows;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+inline int64_t over(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+// Sizes and leading dimensions of operands: a tile's 256 rows of this many elements stay below 2^31 bytes.
+constexpr int64_t kMaxSide = 1 << 22;
+inline bool side_ok(int64_t n) { return n >= 0 && n <= kMaxSide; }
+
+// An operand that mm_tile reads in place: rows that begin at 16 bytes and are whole segments.
+inline bool in_place(const void* p, int64_t cols, int64_t ld) { return aligned_to(p, 16) && cols % 8 == 0 && ld % 8 == 0; }
+
+// bf16 rows [R][ld] of an operand, C used
+inline int check_rows(const void* p, int64_t R, int64_t C, int64_t ld)
+{
+    if (ld < C || ld > kMaxSide) return V4MOE_EDIMS;
+    if (R > 0 && !p) return V4MOE_ENULL;
+    return aligned_to(p, 2) ? V4MOE_OK : V4MOE_EALIGN;
+}
+// an output [R][ld] of a type, C used
+inline int check_out(const void* p, int32_t type, int64_t R, int64_t C, int64_t ld)
+{
+    if ((type != V4MOE_TYPE_F32 && type != V4MOE_TYPE_BF16) || ld < C || ld > (1ll << 40)) return V4MOE_EDIMS;
+    if (R > 0 && !p) return V4MOE_ENULL;
+    return aligned_to(p, type == V4MOE_TYPE_F32 ? 4 : 2) ? V4MOE_OK : V4MOE_EALIGN;
+}
+
+// Rows of bf16, src [R][ld] -> dst [R][C8] (C8 = C rounded up to 8), zeros past C: for operands that cannot be read
+// in place.
+hipError_t launch_pad_rows(int64_t R, int C, const void* src, int64_t ld, void* dst, hipStream_t s);
+
+// Lets a kernel have more than 64 KiB of LDS, once per device (or again by host threads that come to it at once).
+using LdsAllowed = std::atomic<bool>[kMaxDevices];
+inline hipError_t allow_lds(const void* kernel, int bytes, LdsAllowed& done)
+{
+    if (bytes <= 65536) return hipSuccess;
+    int dev = 0;
+    if (const hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 }  // namespace v4moe

@@ -1,0 +1,587 @@
+// v4moe_xent.hip -- softmax cross entropy over a large vocabulary from the hidden
+// states and the head's weight: loss, and the gradients of both, without the logits
+// [T][V] in memory.
+//
+//   z[t][v] = sum_h x[t][h] W[v][h]
+//   lse[t]  = log sum_v exp(z[t][v]),   loss[t] = lse[t] - z[t][y_t]
+//   d[t][v] = g_t (exp(z[t][v] - lse[t]) - [v = y_t]),   dx = d W,   dW = d^T x
+//
+// Tokens without a target (y_t not in [0, V)) have loss 0 and no gradient, and what
+// their rows hold reaches nothing: the others' rows are packed first, so that they cost
+// nothing either.
+//
+// Forward: the logits of a tile end in registers, where each row's maximum and sum of
+// exponentials over 64 columns are taken; the parts are joined in a fixed order.
+// Backward: pieces of the vocabulary, of which d is held in bf16 (at most about 256 MiB);
+// the logits are computed again from the same operands, in the same order.
+#include "v4moe.h"
+#include "v4moe_device.h"
+#include "v4moe_internal.h"
+#include "v4moe_mm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace v4moe {
+
+namespace {
+
+// What k_xent_rows leaves for the later kernels: how many rows were packed, and the
+// largest finite |g| among them (1 where that is 0).
+struct XentCtrl { int n; float largest; };
+
+__device__ __forceinline__ float exp_(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
+// Numbers the tokens with a target: pos[t] their place among them (-1 for the others),
+// idx the tokens in order.  One block: 4096 tokens a step.
+// loss, lse (or null): zeros for the tokens without one.  g (or null): the incoming gradients.
+__global__ __launch_bounds__(1024) void k_xent_rows(int T, int V, const int64_t* __restrict__ targets,
+                                                    const float* __restrict__ g, int64_t gs, int* __restrict__ pos,
+                                                    int* __restrict__ idx, XentCtrl* __restrict__ ctrl,
+                                                    float* __restrict__ loss, float* __restrict__ lse)
+{
+    __shared__ int totals[16];
+    __shared__ float largest[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int done = 0;
+    float big = 0.0f;
+    for (int base = 0; base < T; base += 4096) {
+        const int t0 = base + 4 * tid;
+        bool has[4];
+        int mine = 0;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            has[u] = false;
+            if (t0 + u < T) {
+                const int64_t y = targets[t0 + u];
+                has[u] = y >= 0 && y < V;
+                if (has[u] && g) {
+                    const float f = fabsf(g[(t0 + u) * gs]);
+                    if (f < INFINITY) big = fmaxf(big, f);
+                }
+                if (!has[u] && loss) loss[t0 + u] = lse[t0 + u] = 0.0f;
+            }
+            mine += has[u];
+        }
+        int scan = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(scan, o);
+            if (lane >= o) scan += v;
+        }
+        if (lane == 63) totals[wave] = scan;
+        __syncthreads();
+        int at = done + scan - mine;
+        for (int w = 0; w < 16; w++) {
+            if (w < wave) at += totals[w];
+            done += totals[w];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (t0 + u < T) {
+                pos[t0 + u] = has[u] ? at : -1;
+                if (has[u]) idx[at++] = t0 + u;
+            }
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) big = fmaxf(big, __shfl_xor(big, o));
+    if (lane == 0) largest[wave] = big;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < 16; w++) big = fmaxf(big, largest[w]);
+        *ctrl = XentCtrl{done, big > 0.0f ? big : 1.0f};
+    }
+}
+
+// The packed rows: x [n][H8] (zeros past H), targets, and in the backward lse and g / largest
+// (a mean's gradients are equal: theirs is exactly 1, and d is not rounded twice).
+__global__ __launch_bounds__(256) void k_xent_pack(int H, int H8, const uint16_t* __restrict__ x, int64_t ldx,
+                                                   const int64_t* __restrict__ targets, const float* __restrict__ lse,
+                                                   const float* __restrict__ g, int64_t gs, const int* __restrict__ idx,
+                                                   const XentCtrl* __restrict__ ctrl, uint16_t* __restrict__ xp,
+                                                   int* __restrict__ yp, float* __restrict__ lsep, float* __restrict__ gp)
+{
+    const int segs = H8 / 8;
+    const int64_t all = (int64_t)ctrl->n * segs;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int r = (int)(i / segs), c = (int)(i - (int64_t)r * segs) * 8, t = idx[r];
+        const uint16_t* s = x + t * ldx + c;
+        v4u32 v;
+        if (c + 8 <= H) {
+            v = *reinterpret_cast<const v4u32_any*>(s);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                v[u] = (c + 2 * u < H ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < H ? (uint32_t)s[2 * u + 1] << 16 : 0u);
+        }
+        *reinterpret_cast<v4u32*>(xp + (int64_t)r * H8 + c) = v;
+        if (c == 0) {
+            yp[r] = (int)targets[t];
+            if (g) {
+                lsep[r] = lse[t];
+                gp[r] = g[t * gs] / ctrl->largest;
+            }
+        }
+    }
+}
+
+struct LogitsArgs {
+    int T, H, V;                       // V: columns of this piece
+    int v0;                            // its first
+    const XentCtrl* ctrl;
+    const uint16_t* x; int64_t ldx;    // packed rows
+    const uint16_t* w; int64_t ldw;    // the piece's rows of the weight
+    const int* y;
+    // forward: (maximum, sum of exponentials) of 64 columns each, [V/64][T], and the target's logit
+    float2* parts; float* zy;
+    // backward
+    const float* lse; const float* g;
+    uint16_t* d; int64_t ldd;
+};
+
+// Logits of a piece, a tile per block, and what becomes of them.
+template <class L, bool GRAD>
+__global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
+{
+    static_assert(L::NI == 4, "parts are of 64 columns in every variant, so that a row's result is the same in all");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int n = p.ctrl->n, tm = (n + L::BM - 1) / L::BM, tn = (p.V + L::BN - 1) / L::BN;
+    const int turn = mm_turn(blockIdx.x, tm * tn);
+    if (turn < 0) return;
+    int im, in;
+    mm_band(turn, tm, tn, im, in);
+    const MmOperand a{p.x, p.ldx, n}, b{p.w, p.ldw, p.V};
+    v4f acc[L::MI][4];
+    mm_tile<L>(a, b, im * L::BM, in * L::BN, p.H, smem, acc);
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int mw = im * L::BM + wave / L::WN * L::MI * 16, nw = in * L::BN + wave % L::WN * 64;
+    if constexpr (!GRAD) {
+        if (nw >= p.V) return;
+#pragma unroll
+        for (int i = 0; i < L::MI; i++) {
+            const int m = mw + 16 * i + r16;
+            const int y = m < n ? p.y[m] - p.v0 - nw : -1;
+            float big = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    if (nw + 16 * j + 4 * kq + e >= p.V) acc[i][j][e] = -INFINITY;
+                    big = fmaxf(big, acc[i][j][e]);
+                    if (y == 16 * j + 4 * kq + e) p.zy[m] = acc[i][j][e];
+                }
+            big = fmaxf(big, __shfl_xor(big, 16));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            const float off = big == -INFINITY ? 0.0f : big;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sum += exp_(acc[i][j][e] - off);
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (kq == 0 && m < n) p.parts[(int64_t)((p.v0 + nw) >> 6) * p.T + m] = make_float2(big, sum);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < L::MI; i++) {
+            const int m = min(mw + 16 * i + r16, n - 1);
+            const int y = p.y[m] - p.v0 - nw;
+            const float lse = p.lse[m], g = p.g[m];
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int c = 16 * j + 4 * kq + e;
+                    const float d = g * (exp_(acc[i][j][e] - lse) - (y == c ? 1.0f : 0.0f));
+                    acc[i][j][e] = nw + c < p.V ? d : 0.0f;
+                }
+        }
+        // (columns up to a multiple of 8: the products read whole segments)
+        const MmOut o{p.d, p.ldd, n, (p.V + 7) / 8 * 8, 1, 0};
+        mm_store_tile<L, false>(acc, smem, o, im * L::BM, in * L::BN);
+    }
+}
+
+// lse and loss of the packed rows from P parts each: 16 rows by 64 groups of parts per
+// block; a group takes every 64th part in order, then the groups are joined in a tree.
+__global__ __launch_bounds__(1024) void k_xent_join(int T, int P, const XentCtrl* __restrict__ ctrl,
+                                                    const int* __restrict__ idx, const float2* __restrict__ parts,
+                                                    const float* __restrict__ zy, float* __restrict__ loss,
+                                                    float* __restrict__ lse)
+{
+    __shared__ float2 joined[64][17];
+    const int n = ctrl->n, r = threadIdx.x & 15, grp = threadIdx.x >> 4, m = blockIdx.x * 16 + r;
+    if (blockIdx.x * 16 >= n) return;
+    auto join = [](float2 a, float2 b) {
+        const float big = fmaxf(a.x, b.x);
+        if (big == -INFINITY) return make_float2(big, a.y + b.y);
+        return make_float2(big, a.y * exp_(a.x - big) + b.y * exp_(b.x - big));
+    };
+    float2 acc = make_float2(-INFINITY, 0.0f);
+    for (int p0 = grp; p0 < P; p0 += 64 * 8) {
+        float2 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++)
+            v[u] = p0 + 64 * u < P && m < n ? parts[(int64_t)(p0 + 64 * u) * T + m] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int u = 0; u < 8; u++) acc = join(acc, v[u]);
+    }
+    joined[grp][r] = acc;
+    __syncthreads();
+    for (int o = 32; o > 0; o >>= 1) {
+        if (grp < o) joined[grp][r] = join(joined[grp][r], joined[grp + o][r]);
+        __syncthreads();
+    }
+    if (grp == 0 && m < n) {
+        const float2 v = joined[0][r];
+        const float l = v.x + logf(v.y);
+        const int t = idx[m];
+        lse[t] = l;
+        loss[t] = l - zy[m];
+    }
+}
+
+struct XentGradArgs {
+    int T, H, H8, V;                    // V: columns of this piece
+    int slices, per;                    // of its contraction: `per` columns each
+    const XentCtrl* ctrl;
+    const uint16_t* x; const uint16_t* w; int64_t ldw;
+    const uint16_t* d; int64_t ldd;
+    float* dx;                          // [slices][T][H8]
+    int first;                          // the first piece writes dx, the others add to it
+    MmOut dw;                           // the piece's rows
+};
+
+// dx of the packed rows over a slice of a piece's columns.
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_xent_dx(XentGradArgs p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int n = p.ctrl->n, tm = (n + L::BM - 1) / L::BM, tn = (p.H8 + L::BN - 1) / L::BN;
+    const int turn = mm_turn(blockIdx.x, tm * tn * p.slices);
+    if (turn < 0) return;
+    const int slice = turn / (tm * tn), k0 = slice * p.per;
+    int im, in;
+    mm_band(turn % (tm * tn), tm, tn, im, in);
+    const MmOperand a{p.d + k0, p.ldd, n}, b{p.w + k0 * p.ldw, p.ldw, p.H8};
+    v4f acc[L::MI][L::NI];
+    mm_tile<L>(a, b, im * L::BM, in * L::BN, max(min(p.V - k0, p.per), 0), smem, acc);
+    const MmOut o{p.dx + (int64_t)slice * p.T * p.H8, p.H8, n, p.H8, 0, !p.first};
+    mm_store_tile<L>(acc, smem, o, im * L::BM, in * L::BN);
+}
+
+// The piece's rows of dW: the packed tokens are the contraction.
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_xent_dw(XentGradArgs p, int tm, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int n = p.ctrl->n;
+    if (n == 0 && p.dw.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
+    int im, in;
+    mm_band(mm_turn(blockIdx.x, tm * tn), tm, tn, im, in);
+    const MmOperand a{p.d, p.ldd, (p.V + 7) / 8 * 8}, b{p.x, p.H8, p.H8};
+    v4f acc[L::MI][L::NI];
+    mm_tile<L>(a, b, im * L::BM, in * L::BN, n, smem, acc);
+    const float s = p.ctrl->largest;
+#pragma unroll
+    for (int i = 0; i < L::MI; i++)
+#pragma unroll
+        for (int j = 0; j < L::NI; j++) acc[i][j] *= s;
+    mm_store_tile<L>(acc, smem, p.dw, im * L::BM, in * L::BN);
+}
+
+// dx of every token: the slices' sums in order, times the largest |g|; zeros without a target.
+template <typename T_>
+__global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int slices, const XentCtrl* __restrict__ ctrl,
+                                                     const int* __restrict__ pos, const float* __restrict__ acc,
+                                                     T_* __restrict__ dx, int64_t ld)
+{
+    const int quads = H8 / 4;
+    const int64_t all = (int64_t)T * quads;
+    const float s = ctrl->largest;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int t = (int)(i / quads), c = (int)(i - (int64_t)t * quads) * 4, m = pos[t];
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (m >= 0)
+            for (int k = 0; k < slices; k++) {
+                const float4 f = *reinterpret_cast<const float4*>(acc + ((int64_t)k * T + m) * H8 + c);
+                v[0] += f.x;
+                v[1] += f.y;
+                v[2] += f.z;
+                v[3] += f.w;
+            }
+        T_* o = dx + t * ld + c;
+        if constexpr (sizeof(T_) == 2) {
+            const uint32_t lo = bf16x2(v[0] * s, v[1] * s), hi = bf16x2(v[2] * s, v[3] * s);
+            if (c + 4 <= H) {
+                *reinterpret_cast<v2u32_any*>(o) = v2u32{lo, hi};
+            } else {
+                for (int e = 0; e < 4 && c + e < H; e++) o[e] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e & 1)));
+            }
+        } else {
+            for (int e = 0; e < 4 && c + e < H; e++) o[e] = v[e] * s;
+        }
+    }
+}
+
+// ---- host ----
+template <class L, bool GRAD>
+hipError_t launch_logits(const LogitsArgs& p, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_xent_logits<L, GRAD>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
+    const int64_t tiles = over(p.T, L::BM) * over(p.V, L::BN);
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(L::THREADS), L::BYTES, s, p);
+    return hipGetLastError();
+}
+template <bool GRAD>
+hipError_t run_logits(const LogitsArgs& p, hipStream_t s)
+{
+    if (p.T <= 16) return launch_logits<MmTile<1, 4, 1, 4, 4, false, false>, GRAD>(p, s);
+    if (p.T <= 32) return launch_logits<MmTile<1, 4, 2, 4, 3, false, false>, GRAD>(p, s);
+    if (p.T <= 64) return launch_logits<MmTile<1, 4, 4, 4, 2, false, false>, GRAD>(p, s);
+    if (over(p.T, 256) * over(p.V, 256) < 200) return launch_logits<MmTile<2, 2, 4, 4, 2, false, false>, GRAD>(p, s);
+    return launch_logits<MmTile<2, 4, 8, 4, 2, false, false>, GRAD>(p, s);
+}
+
+template <class L>
+hipError_t launch_dx(const XentGradArgs& p, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_xent_dx<L>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
+    const int64_t tiles = over(p.T, L::BM) * over(p.H8, L::BN) * p.slices;
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(L::THREADS), L::BYTES, s, p);
+    return hipGetLastError();
+}
+struct DxTile { int bm, bn; };
+DxTile dx_tile(int64_t T, int64_t H8)
+{
+    if (T <= 32) return {32, 64};
+    if (T <= 128 || over(T, 256) * over(H8, 256) < 128) return {128, 128};
+    return {256, 256};
+}
+hipError_t run_dx(const XentGradArgs& p, hipStream_t s)
+{
+    switch (dx_tile(p.T, p.H8).bm) {
+    case 32: return launch_dx<MmTile<2, 2, 1, 2, 4, false, true>>(p, s);
+    case 128: return launch_dx<MmTile<2, 2, 4, 4, 2, false, true>>(p, s);
+    default: return launch_dx<MmTile<2, 4, 8, 4, 2, false, true>>(p, s);
+    }
+}
+template <class L>
+hipError_t launch_dw(const XentGradArgs& p, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_xent_dw<L>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
+    const int64_t tm = over(p.V, L::BM), tn = over(p.H, L::BN);
+    if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(L::THREADS), L::BYTES, s, p, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+hipError_t run_dw(const XentGradArgs& p, hipStream_t s)
+{
+    if (over(p.V, 256) * over(p.H, 256) < 200) return launch_dw<MmTile<2, 2, 4, 4, 2, true, true>>(p, s);
+    return launch_dw<MmTile<2, 4, 8, 4, 2, true, true>>(p, s);
+}
+
+struct XentLayout {
+    size_t ctrl, idx, pos, y, zy, x, parts, lse, g, d, dx, w, total;
+    bool pad_w;
+    int piece, slices, per;         // columns of a piece; slices of its contraction for dx
+};
+XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t ldw, bool backward)
+{
+    XentLayout L{};
+    if (T == 0) T = 1;
+    L.pad_w = !in_place(w, H, ldw);
+    size_t o = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t at = o;
+        o += up256((size_t)bytes);
+        return at;
+    };
+    const int64_t H8 = up8(H);
+    L.ctrl = take(sizeof(XentCtrl));
+    L.idx = take(T * 4);
+    L.pos = take(T * 4);
+    L.y = take(T * 4);
+    L.x = take(T * H8 * 2);
+    if (L.pad_w) L.w = take(V * H8 * 2);
+    if (!backward) {
+        L.zy = take(T * 4);
+        L.parts = take(over(V, 64) * T * 8);
+    } else {
+        // d of a piece in at most 256 MiB, but for 256 columns at least
+        const int64_t most = std::max<int64_t>((int64_t(128) << 20) / T / 256 * 256, 256);
+        L.piece = (int)std::min(most, (V + 255) / 256 * 256);
+        // few tiles of dx: the contraction is split until there are some two blocks for each CU
+        const DxTile t = dx_tile(T, H8);
+        const int64_t tiles = over(T, t.bm) * over(H8, t.bn);
+        L.slices = (int)std::max<int64_t>(1, std::min<int64_t>(512 / tiles, over(L.piece, 256)));
+        L.per = (int)(over(over(L.piece, 64), L.slices) * 64);
+        L.lse = take(T * 4);
+        L.g = take(T * 4);
+        L.d = take(T * (int64_t)L.piece * 2);
+        L.dx = take((int64_t)L.slices * T * H8 * 4);
+    }
+    L.total = o;
+    return L;
+}
+
+int check_xent(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+               const int64_t* targets)
+{
+    if (!side_ok(T) || !side_ok(H) || !side_ok(V) || H < 1 || V < 1) return V4MOE_EDIMS;
+    if (const int rc = check_rows(x, T, H, ldx)) return rc;
+    if (const int rc = check_rows(w, V, H, ldw)) return rc;
+    if (T > 0 && !targets) return V4MOE_ENULL;
+    return aligned_to(targets, 8) ? V4MOE_OK : V4MOE_EALIGN;
+}
+
+// The weight as the products read it, and the packed rows.
+struct XentCall {
+    XentLayout L;
+    uint8_t* ws;
+    const uint16_t* w;
+    int64_t ldw;
+    int H8;
+    template <typename T> T* at(size_t o) const { return reinterpret_cast<T*>(ws + o); }
+};
+int xent_begin(XentCall& c, int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+               const int64_t* targets, const float* lse_in, const float* g, int64_t gs, float* loss, float* lse, void* workspace,
+               size_t ws_bytes, bool backward, hipStream_t s)
+{
+    if (!workspace) return V4MOE_ENULL;
+    if (!aligned_to(workspace, 16)) return V4MOE_EALIGN;
+    c.L = xent_layout(T, H, V, w, ldw, backward);
+    if (ws_bytes < c.L.total) return V4MOE_EWORKSPACE;
+    if (!device_ready()) return V4MOE_EDEVICE;
+    c.ws = static_cast<uint8_t*>(workspace);
+    c.w = w;
+    c.ldw = ldw;
+    c.H8 = (int)up8(H);
+    if (c.L.pad_w) {
+        if (launch_pad_rows(V, H, w, ldw, c.ws + c.L.w, s) != hipSuccess) return V4MOE_ELAUNCH;
+        c.w = c.at<uint16_t>(c.L.w);
+        c.ldw = c.H8;
+    }
+    hipLaunchKernelGGL(k_xent_rows, dim3(1), dim3(1024), 0, s, T, V, targets, g, gs, c.at<int>(c.L.pos), c.at<int>(c.L.idx),
+                       c.at<XentCtrl>(c.L.ctrl), loss, lse);
+    const int64_t blocks = over((int64_t)T * (c.H8 / 8), 256);
+    if (blocks > 0)
+        hipLaunchKernelGGL(k_xent_pack, dim3((unsigned)std::min<int64_t>(blocks, 8192)), dim3(256), 0, s, H, c.H8, x, ldx, targets,
+                           lse_in, g, gs, c.at<int>(c.L.idx), c.at<XentCtrl>(c.L.ctrl), c.at<uint16_t>(c.L.x),
+                           c.at<int>(c.L.y), c.at<float>(c.L.lse), c.at<float>(c.L.g));
+    return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+}
+
+}  // namespace
+
+}  // namespace v4moe
+
+using namespace v4moe;
+
+extern "C" {
+
+__attribute__((visibility("default"))) size_t moe_linear_xent_workspace_bytes(int32_t T, int32_t H, int32_t V,
+                                                                              const uint16_t* w, int64_t ldw,
+                                                                              int32_t backward)
+{
+    if (!side_ok(T) || !side_ok(H) || !side_ok(V) || H < 1 || V < 1) return 0;
+    return xent_layout(T, H, V, w, ldw, backward != 0).total;
+}
+
+__attribute__((visibility("default"))) int moe_linear_xent(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx,
+                                                           const uint16_t* w, int64_t ldw, const int64_t* targets,
+                                                           float* loss, float* lse, void* workspace, size_t ws_bytes,
+                                                           void* stream)
+{
+    if (const int rc = check_xent(T, H, V, x, ldx, w, ldw, targets)) return rc;
+    if (T == 0) return V4MOE_OK;
+    if (!loss || !lse) return V4MOE_ENULL;
+    if (!aligned_to(loss, 4) || !aligned_to(lse, 4)) return V4MOE_EALIGN;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    XentCall c;
+    if (const int rc = xent_begin(c, T, H, V, x, ldx, w, ldw, targets, nullptr, nullptr, 0, loss, lse, workspace, ws_bytes,
+                                  false, s))
+        return rc;
+    LogitsArgs p{};
+    p.T = T, p.H = H, p.V = V;
+    p.ctrl = c.at<XentCtrl>(c.L.ctrl);
+    p.x = c.at<uint16_t>(c.L.x), p.ldx = c.H8;
+    p.w = c.w, p.ldw = c.ldw;
+    p.y = c.at<int>(c.L.y);
+    p.parts = c.at<float2>(c.L.parts), p.zy = c.at<float>(c.L.zy);
+    if (run_logits<false>(p, s) != hipSuccess) return V4MOE_ELAUNCH;
+    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)over(T, 16)), dim3(1024), 0, s, T, (int)over(V, 64), p.ctrl,
+                       c.at<int>(c.L.idx), p.parts, p.zy, loss, lse);
+    return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+}
+
+__attribute__((visibility("default"))) int moe_linear_xent_backward(
+    int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, const int64_t* targets,
+    const float* lse, const float* dloss, int64_t dloss_stride, void* dx, int32_t dx_type, int64_t lddx, void* dw,
+    int32_t dw_type, int64_t lddw, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream)
+{
+    if (const int rc = check_xent(T, H, V, x, ldx, w, ldw, targets)) return rc;
+    if (!dx && !dw) return V4MOE_ENULL;
+    if (dx)
+        if (const int rc = check_out(dx, dx_type, T, H, lddx)) return rc;
+    if (dw)
+        if (const int rc = check_out(dw, dw_type, V, H, lddw)) return rc;
+    if (dloss_stride < 0 || dloss_stride > (1ll << 40)) return V4MOE_EDIMS;
+    if (T > 0 && (!lse || !dloss)) return V4MOE_ENULL;
+    if (!aligned_to(lse, 4) || !aligned_to(dloss, 4)) return V4MOE_EALIGN;
+    if (T == 0 && (!dw || accumulate)) return V4MOE_OK;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    XentCall c;
+    if (const int rc = xent_begin(c, T, H, V, x, ldx, w, ldw, targets, lse, dloss, dloss_stride, nullptr, nullptr, workspace,
+                                  ws_bytes, true, s))
+        return rc;
+    const auto* ctrl = c.at<XentCtrl>(c.L.ctrl);
+    for (int v0 = 0; v0 < V; v0 += c.L.piece) {
+        const int n = std::min(c.L.piece, V - v0);
+        LogitsArgs p{};
+        p.T = T, p.H = H, p.V = n, p.v0 = v0;
+        p.ctrl = ctrl;
+        p.x = c.at<uint16_t>(c.L.x), p.ldx = c.H8;
+        p.w = c.w + v0 * c.ldw, p.ldw = c.ldw;
+        p.y = c.at<int>(c.L.y);
+        p.lse = c.at<float>(c.L.lse), p.g = c.at<float>(c.L.g);
+        p.d = c.at<uint16_t>(c.L.d), p.ldd = c.L.piece;
+        if (T > 0 && run_logits<true>(p, s) != hipSuccess) return V4MOE_ELAUNCH;
+        XentGradArgs q{};
+        q.T = T, q.H = H, q.H8 = c.H8, q.V = n;
+        q.slices = c.L.slices, q.per = c.L.per;
+        q.ctrl = ctrl;
+        q.x = p.x, q.w = p.w, q.ldw = p.ldw, q.d = p.d, q.ldd = p.ldd;
+        q.dx = c.at<float>(c.L.dx), q.first = v0 == 0;
+        if (dx && T > 0 && run_dx(q, s) != hipSuccess) return V4MOE_ELAUNCH;
+        if (dw) {
+            const bool bf16 = dw_type == V4MOE_TYPE_BF16;
+            q.dw = MmOut{static_cast<uint8_t*>(dw) + (int64_t)v0 * lddw * (bf16 ? 2 : 4), lddw, n, H, bf16, accumulate != 0};
+            if (run_dw(q, s) != hipSuccess) return V4MOE_ELAUNCH;
+        }
+    }
+    if (dx && T > 0) {
+        const dim3 grid((unsigned)std::min<int64_t>(over((int64_t)T * (c.H8 / 4), 256), 8192));
+        if (dx_type == V4MOE_TYPE_BF16)
+            hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, c.L.slices, ctrl,
+                               c.at<int>(c.L.pos), c.at<float>(c.L.dx), static_cast<uint16_t*>(dx), lddx);
+        else
+            hipLaunchKernelGGL(k_xent_finish<float>, grid, dim3(256), 0, s, T, H, c.H8, c.L.slices, ctrl, c.at<int>(c.L.pos),
+                               c.at<float>(c.L.dx), static_cast<float*>(dx), lddx);
+    }
+    return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
+}
+
+}  // extern "C"

@@ -143,6 +143,11 @@ def lib():
         L.moe_grouped_linear.argtypes = [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
         L.moe_grouped_linear_backward.argtypes = [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i64,
                                                   _vp, _i32, _i32, _vp, _sz, _vp]
+        L.moe_linear_xent_workspace_bytes.argtypes = [_i32, _i32, _i32, _vp, _i64, _i32]
+        L.moe_linear_xent_workspace_bytes.restype = _sz
+        L.moe_linear_xent.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.moe_linear_xent_backward.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i64,
+                                               _vp, _i32, _i64, _i32, _vp, _sz, _vp]
         L.moe_time_next_ffn.argtypes = [_vp, _vp]
         L.moe_time_next_ffn.restype = None
         for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
@@ -150,7 +155,8 @@ def lib():
                   "moe_prepack_weights", "moe_dequant_fp8", "moe_quantize_weights", "moe_transpose_weights",
                   "moe_layer_backward", "moe_routed_forward", "moe_routed_backward", "moe_gate", "moe_gate_backward", "moe_fp8_quantize",
                   "moe_fp8_quantize_weights", "moe_fp8_gemm", "moe_fp8_linear", "moe_fp8_linear_backward",
-                  "moe_clip_grads", "moe_grouped_linear", "moe_grouped_linear_backward"):
+                  "moe_clip_grads", "moe_grouped_linear", "moe_grouped_linear_backward", "moe_linear_xent",
+                  "moe_linear_xent_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -675,6 +681,54 @@ def grouped_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: torch.Tensor, 
     ws = _bytes(n, dev) if n else None
     _check(lib().moe_grouped_linear_backward(M, E, N, K, xp, ldx, dyp, lddy, wp, op, dx.data_ptr(), _type(dx), lddx, dwp,
                                              _type(dw), 1 if accumulate else 0, ws.data_ptr() if n else None, n, stream))
+    return dx, dw
+
+
+def _xent(x, w, targets):
+    """(T, H, V, GPU, leading dimensions of x and w, address of the targets) of a cross entropy, checked."""
+    T, (V, H) = x.shape[0], w.shape
+    gpu = _device_of(x, "x")
+    return (T, H, V, gpu, _matrix(x, T, H, "x", gpu, torch.bfloat16), _matrix(w, V, H, "w", gpu, torch.bfloat16),
+            _dense(targets, (T,), torch.int64, "targets", gpu))
+
+
+def linear_xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
+    """Softmax cross entropy of the logits x W^T without keeping them: x bf16 [T][H], w bf16 [V][H] (rows of both may be
+    strided), targets int64 [T] (outside [0, V): no target).  Returns (loss, lse), fp32 [T], 0 without a target.  See
+    moe_linear_xent in include/v4moe.h."""
+    T, H, V, gpu, ldx, ldw, tp = _xent(x, w, targets)
+    stream = _raw_stream(gpu)
+    dev, wp = x.device, w.data_ptr()
+    loss, lse = (torch.empty_strided((T,), (1,), dtype=torch.float32, device=dev) for _ in range(2))
+    n = lib().moe_linear_xent_workspace_bytes(T, H, V, wp, ldw, 0)
+    ws = _bytes(n, dev)
+    _check(lib().moe_linear_xent(T, H, V, x.data_ptr(), ldx, wp, ldw, tp, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n,
+                                 stream))
+    return loss, lse
+
+
+def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
+                         dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False):
+    """Gradients of sum(dloss * loss) for linear_xent's loss: (dx [T][H], dw [V][H]), bf16 unless given; lse from
+    linear_xent; dloss fp32 [T], of any stride (an expanded scalar, say); accumulate adds to the given dw."""
+    T, H, V, gpu, ldx, ldw, tp = _xent(x, w, targets)
+    lp = _dense(lse, (T,), torch.float32, "lse", gpu)
+    if dloss.get_device() != gpu:
+        _elsewhere(dloss, "dloss")
+    _require(dloss.shape == (T,) and dloss.dtype == torch.float32, f"dloss must be float32 [{T}]")
+    stream = _raw_stream(gpu)
+    dev, wp = x.device, w.data_ptr()
+    _require(dw is not None or not accumulate, "accumulate needs dw")
+    if dx is None:
+        dx = _empty(T, H, torch.bfloat16, dev)
+    if dw is None:
+        dw = _empty(V, H, torch.bfloat16, dev)
+    lddx, lddw = _matrix(dx, T, H, "dx", gpu), _matrix(dw, V, H, "dw", gpu)
+    n = lib().moe_linear_xent_workspace_bytes(T, H, V, wp, ldw, 1)
+    ws = _bytes(n, dev)
+    _check(lib().moe_linear_xent_backward(T, H, V, x.data_ptr(), ldx, wp, ldw, tp, lp, dloss.data_ptr(), dloss.stride(0),
+                                          dx.data_ptr(), _type(dx), lddx, dw.data_ptr(), _type(dw), lddw,
+                                          1 if accumulate else 0, ws.data_ptr(), n, stream))
     return dx, dw
 
 

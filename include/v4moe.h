@@ -493,6 +493,39 @@ int moe_grouped_linear_backward(int32_t M, int32_t E, int32_t N, int32_t K, cons
                                 void* dw, int32_t dw_type, int32_t accumulate, void* workspace,
                                 size_t ws_bytes, void* stream);
 
+/* ---- Softmax cross entropy over a large vocabulary, from the hidden states ----
+ *   z = x W^T (x bf16 [T][ldx], W bf16 [V][ldw], H used of both), never in memory as a whole
+ *   lse[t] = log sum_v exp(z[t][v]); loss[t] = lse[t] - z[t][targets[t]]
+ * targets int64 [T]: a token whose target is not in [0, V) (-100, say) has loss and lse 0
+ * and no gradient, costs no products, and what its row of x holds reaches nothing.
+ * 0 <= T, 1 <= H, V, all up to 2^22, leading dimensions of x and W too.  fp32 sums; a
+ * token's loss and lse do not depend on the other tokens, in any bit.  Pointers: aligned
+ * to their element. */
+
+/* Workspace bytes (host-only, pure; 0 for invalid sizes; W's pointer is looked at for its
+ * alignment only: where its rows do not begin at 16 bytes, or H is no multiple of 8, there
+ * is room for a copy).  16-byte aligned, no initialisation.  The backward holds the logits'
+ * gradient of a piece of the vocabulary in it, at most 256 MiB or 256 columns. */
+size_t moe_linear_xent_workspace_bytes(int32_t T, int32_t H, int32_t V, const uint16_t* w,
+                                       int64_t ldw, int32_t backward);
+
+/* loss, lse: fp32 [T] (out). */
+int moe_linear_xent(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx,
+                    const uint16_t* w, int64_t ldw, const int64_t* targets, float* loss, float* lse,
+                    void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of sum_t dloss[t] loss[t], given lse from moe_linear_xent:
+ *   d[t][v] = dloss[t] (exp(z[t][v] - lse[t]) - [v = targets[t]])
+ *   dx [T][lddx] = d W;  dW [V][lddw] (+)= d^T x (accumulate: added to in fp32, rounded once)
+ * dx or dw may be NULL.  dloss fp32, element t at dloss[t * dloss_stride] (0: one for all).
+ * d enters the products in bf16 (divided by the largest |dloss| first): fp32 results are
+ * good to about 2e-3 of their 2-norm. */
+int moe_linear_xent_backward(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx,
+                             const uint16_t* w, int64_t ldw, const int64_t* targets, const float* lse,
+                             const float* dloss, int64_t dloss_stride, void* dx, int32_t dx_type,
+                             int64_t lddx, void* dw, int32_t dw_type, int64_t lddw,
+                             int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
 /* Profiling hook (no effect on results).  start/stop are hipEvent_t handles
  * created by the caller (or NULL to clear).  The next moe_expert_ffn or
  * moe_layer_forward call made by this host thread records `start` on its
