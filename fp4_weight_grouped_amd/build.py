@@ -10,7 +10,7 @@ SO = os.path.join(HERE, "libv4moe.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("v4moe_kernels.hip", "v4moe_bwd.hip", "v4moe_api.cpp",
                                                                "v4moe_noalloc.hip", "v4moe_gate.hip",
                                                                "v4moe_fp8.hip", "v4moe_clip.hip", "v4moe_grouped.hip",
-                                                               "v4moe_xent.hip")]
+                                                               "v4moe_xent.hip", "v4moe_lora.hip")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("v4moe_device.h", "v4moe_internal.h", "v4moe_mm.h")] + \
     [os.path.join(ROOT, "include", "v4moe.h")]
 

@@ -68,7 +68,8 @@ template <int W>
 __device__ __forceinline__ int column_swizzle(int k)
 {
     if constexpr (W >= 128) return (k & 3) | ((k >> 1) & 4);
-    else return ((k >> 1) & 1) | ((k >> 2) & 2);
+    else if constexpr (W == 64) return ((k >> 1) & 1) | ((k >> 2) & 2);
+    else return (k >> 3) & 1;
 }
 
 // One operand of a tile, its first index i0: copies into LDS and reads of fragments.
@@ -131,13 +132,18 @@ struct MmSide {
 template <int W, bool COL, int T>
 struct MmReader {
     int at[COL ? T : 2];
+    // columns, from k0 of the lane's own on (rows of k that its swizzle depends on: k0 + 0 .. 3, and 4 further)
+    __device__ __forceinline__ void begin_at(int first, int lane, int k0)
+    {
+        const int i = lane & 15, k = k0 + (i >> 2), f = column_swizzle<W>(k);
+#pragma unroll
+        for (int t = 0; t < T; t++) at[t] = k * W * 2 + ((first + t) ^ f) * 32 + (i & 3) * 8;
+    }
     __device__ __forceinline__ void begin(int first, int lane)
     {
         const int i = lane & 15, kq = lane >> 4;
         if constexpr (COL) {
-            const int k = 8 * kq + (i >> 2), f = column_swizzle<W>(k);
-#pragma unroll
-            for (int t = 0; t < T; t++) at[t] = k * W * 2 + ((first + t) ^ f) * 32 + (i & 3) * 8;
+            begin_at(first, lane, 8 * kq);
         } else {
             const int sw = (lane >> 1) & 7, row = (16 * first + i) * 128;
             at[0] = row + ((kq ^ sw) * 16);
@@ -146,16 +152,17 @@ struct MmReader {
     }
     __device__ __forceinline__ v8bf read(const uint8_t* stage, int t, int s) const
     {
-        if constexpr (COL) {
-            typedef __attribute__((address_space(3))) v4s* lds4;
-            // (four rows of k further on the swizzle is the same)
-            const lds4 p = (lds4)(stage + at[t] + s * 32 * W * 2), q = (lds4)(stage + at[t] + (s * 32 + 4) * W * 2);
-            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p), hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(q);
-            typedef short v8s __attribute__((ext_vector_type(8)));
-            return __builtin_bit_cast(v8bf, v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
-        } else {
-            return *reinterpret_cast<const v8bf*>(stage + at[s] + t * 2048);
-        }
+        if constexpr (COL) return read_at(stage, t, 32 * s);
+        else return *reinterpret_cast<const v8bf*>(stage + at[s] + t * 2048);
+    }
+    // columns: of eight k from k1 further on, a multiple of 16 (where the swizzle is the same, as it is 4 further on)
+    __device__ __forceinline__ v8bf read_at(const uint8_t* stage, int t, int k1) const
+    {
+        typedef __attribute__((address_space(3))) v4s* lds4;
+        const lds4 p = (lds4)(stage + at[t] + k1 * W * 2), q = (lds4)(stage + at[t] + (k1 + 4) * W * 2);
+        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p), hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(q);
+        typedef short v8s __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(v8bf, v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     }
 };
 

@@ -78,6 +78,11 @@ class FP8MatC(ctypes.Structure):
                 ("blk", ctypes.c_void_p)]
 
 
+class LoraC(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("r", ctypes.c_int32),
+                ("L", ctypes.c_int32)]
+
+
 class TensorC(ctypes.Structure):
     _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32)]
 
@@ -148,6 +153,12 @@ def lib():
         L.moe_linear_xent.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
         L.moe_linear_xent_backward.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i64,
                                                _vp, _i32, _i64, _i32, _vp, _sz, _vp]
+        LP = ctypes.POINTER(LoraC)
+        L.moe_lora_workspace_bytes.argtypes = [LP, _i32]
+        L.moe_lora_workspace_bytes.restype = _sz
+        L.moe_lora_add.argtypes = [LP, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]
+        L.moe_lora_backward.argtypes = [LP, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _vp, _i32,
+                                        _vp, _i32, _i32, _vp, _sz, _vp]
         L.moe_time_next_ffn.argtypes = [_vp, _vp]
         L.moe_time_next_ffn.restype = None
         for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward",
@@ -156,7 +167,7 @@ def lib():
                   "moe_layer_backward", "moe_routed_forward", "moe_routed_backward", "moe_gate", "moe_gate_backward", "moe_fp8_quantize",
                   "moe_fp8_quantize_weights", "moe_fp8_gemm", "moe_fp8_linear", "moe_fp8_linear_backward",
                   "moe_clip_grads", "moe_grouped_linear", "moe_grouped_linear_backward", "moe_linear_xent",
-                  "moe_linear_xent_backward"):
+                  "moe_linear_xent_backward", "moe_lora_add", "moe_lora_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -730,6 +741,63 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
                                           dx.data_ptr(), _type(dx), lddx, dw.data_ptr(), _type(dw), lddw,
                                           1 if accumulate else 0, ws.data_ptr(), n, stream))
     return dx, dw
+
+
+def _lora(x, a, b, ids, scale):
+    """(sizes, GPU, x's leading dimension, addresses of a, b, ids and scale) of an adapters' call, checked."""
+    M, (L, r, K), N = x.shape[0], a.shape, b.shape[2]
+    gpu = _device_of(x, "x")
+    return (LoraC(M, N, K, r, L), gpu, _matrix(x, M, K, "x", gpu, torch.bfloat16),
+            (_dense(a, (L, r, K), torch.bfloat16, "a", gpu), _dense(b, (L, r, N), torch.bfloat16, "b", gpu),
+             _dense(ids, (M,), torch.int32, "ids", gpu), _dense(scale, (L,), torch.float32, "scale", gpu)))
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Adapters of many requests beside a projection's result y [M][N] (bf16 or fp32): y[m] + scale[i] B[i]^T (A[i] x[m]) for
+    i = ids[m] (int32 [M], outside [0, L): none); x bf16 [M][K], a bf16 [L][r][K], b bf16 [L][r][N], scale fp32 [L].  A new
+    tensor, or into ``out`` of y's type (which may be y).  See moe_lora_add in include/v4moe.h."""
+    p, gpu, ldx, (ap, bp, ip, sp) = _lora(x, a, b, ids, scale)
+    ldy, ty = _matrix(y, p.M, p.N, "y", gpu), _type(y)
+    stream = _raw_stream(gpu)
+    if out is None:
+        out = _empty(p.M, p.N, y.dtype, y.device)
+    ldo = _matrix(out, p.M, p.N, "out", gpu, y.dtype)
+    ref = ctypes.byref(p)
+    n = lib().moe_lora_workspace_bytes(ref, 0)
+    ws = _bytes(n, x.device)
+    _check(lib().moe_lora_add(ref, y.data_ptr(), ty, ldy, x.data_ptr(), ldx, ap, bp, ip, sp, out.data_ptr(), ldo,
+                              ws.data_ptr(), n, stream))
+    return out
+
+
+def lora_backward(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
+                  scale: torch.Tensor, base: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                  da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None, accumulate: bool = False):
+    """Gradients of lora_add from dy (bf16): (dx [M][K], da [L][r][K], db [L][r][N]), bf16 unless given.  base: the shared
+    projection's dx, added to (of dx's type; dx may be it); accumulate adds to the given da and db."""
+    p, gpu, ldx, (ap, bp, ip, sp) = _lora(x, a, b, ids, scale)
+    M, N, K, r, L = p.M, p.N, p.K, p.r, p.L
+    lddy = _matrix(dy, M, N, "dy", gpu, torch.bfloat16)
+    stream = _raw_stream(gpu)
+    dev = x.device
+    _require((da is not None and db is not None) or not accumulate, "accumulate needs da and db")
+    if dx is None:
+        dx = _empty(M, K, torch.bfloat16 if base is None else base.dtype, dev)
+    if da is None:
+        da = torch.empty((L, r, K), dtype=torch.bfloat16, device=dev)
+    if db is None:
+        db = torch.empty((L, r, N), dtype=torch.bfloat16, device=dev)
+    lddx = _matrix(dx, M, K, "dx", gpu)
+    ldbase = 0 if base is None else _matrix(base, M, K, "base", gpu, dx.dtype)
+    dap, dbp = _dense(da, (L, r, K), da.dtype, "da", gpu), _dense(db, (L, r, N), db.dtype, "db", gpu)
+    ref = ctypes.byref(p)
+    n = lib().moe_lora_workspace_bytes(ref, 1)
+    ws = _bytes(n, dev)
+    _check(lib().moe_lora_backward(ref, x.data_ptr(), ldx, dy.data_ptr(), lddy, ap, bp, ip, sp,
+                                   None if base is None else base.data_ptr(), ldbase, dx.data_ptr(), _type(dx), lddx, dap,
+                                   _type(da), dbp, _type(db), 1 if accumulate else 0, ws.data_ptr(), n, stream))
+    return dx, da, db
 
 
 # ---- conveniences for callers holding host (numpy) weights ----------------------------------

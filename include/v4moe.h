@@ -526,6 +526,47 @@ int moe_linear_xent_backward(int32_t T, int32_t H, int32_t V, const uint16_t* x,
                              int64_t lddx, void* dw, int32_t dw_type, int64_t lddw,
                              int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Low-rank adapters of many requests beside a shared projection ----
+ * Row m uses adapter ids[m] (int32 [M] on the device, in any order; outside [0, L): none)
+ *   a bf16 [L][r][K], b bf16 [L][r][N], contiguous; scale fp32 [L]
+ *   x, dy bf16 rows [M][ldx], [M][lddy]
+ * 0 <= M, 1 <= N, K, leading dimensions of bf16 operands, all up to 2^22; 1 <= r <= 512;
+ * 1 <= L <= 65535.  Sums are fp32 in a fixed order, the rank-sized intermediates kept to
+ * 16 bits of significand; a row's result does not depend on the other rows.  Pointers: aligned
+ * to their element. */
+typedef struct {
+    int32_t M;      /* rows                       */
+    int32_t N;      /* columns of the projection  */
+    int32_t K;      /* its inputs                 */
+    int32_t r;      /* rank                       */
+    int32_t L;      /* adapters                   */
+} v4moe_lora;
+
+/* Workspace bytes of moe_lora_add (backward = 0) and moe_lora_backward (host-only, pure; 0
+ * for invalid sizes).  16-byte aligned, no initialisation. */
+size_t moe_lora_workspace_bytes(const v4moe_lora* p, int32_t backward);
+
+/* out[m] = y[m] + scale[i] B[i]^T (A[i] x[m]), i = ids[m]; rows without an adapter: out[m] =
+ * y[m].  y [M][ldy], out [M][ldo] of one type (V4MOE_TYPE_*); out may be y. */
+int moe_lora_add(const v4moe_lora* p, const void* y, int32_t type, int64_t ldy, const uint16_t* x,
+                 int64_t ldx, const uint16_t* a, const uint16_t* b, const int32_t* ids,
+                 const float* scale, void* out, int64_t ldo, void* workspace, size_t ws_bytes,
+                 void* stream);
+
+/* Its gradients, from dy = dL/dout:
+ *   dx[m] = base[m] + scale[i] A[i]^T (B[i] dy[m])  (base: what the shared projection's
+ *           backward gave, of dx's type; NULL: zeros; may be dx)
+ *   da[i] (+)= scale[i] sum over i's rows of (B[i] dy[m]) x[m]^T
+ *   db[i] (+)= scale[i] sum over i's rows of (A[i] x[m]) dy[m]^T
+ * Any of dx, da, db may be NULL.  Adapters without rows get zeros (with accumulate: theirs are
+ * left alone).  accumulate: da and db are added to, in fp32, rounded once. */
+int moe_lora_backward(const v4moe_lora* p, const uint16_t* x, int64_t ldx, const uint16_t* dy,
+                      int64_t lddy, const uint16_t* a, const uint16_t* b, const int32_t* ids,
+                      const float* scale, const void* base, int64_t ldbase, void* dx,
+                      int32_t dx_type, int64_t lddx, void* da, int32_t da_type, void* db,
+                      int32_t db_type, int32_t accumulate, void* workspace, size_t ws_bytes,
+                      void* stream);
+
 /* Profiling hook (no effect on results).  start/stop are hipEvent_t handles
  * created by the caller (or NULL to clear).  The next moe_expert_ffn or
  * moe_layer_forward call made by this host thread records `start` on its
