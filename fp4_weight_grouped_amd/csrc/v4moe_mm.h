@@ -56,6 +56,7 @@ struct MmTile {
     static constexpr int C_BYTES = 2 * 16 * NI * 16 * 4;                    // of staging per wave (mm_store)
     static constexpr int BYTES = RING > NW * C_BYTES ? RING : NW * C_BYTES;
     static_assert(NW > 1 && NS >= 2 && OPS * (NS - 1) < 64, "the barrier frees a slot; vmcnt range");
+    static_assert(BYTES <= 163840, "LDS of a CU");
     static_assert(!ACOL || BM >= 64, "columns are staged in rows of 128 bytes or more");
     static_assert(!BCOL || BN >= 64, "columns are staged in rows of 128 bytes or more");
 };
@@ -108,22 +109,18 @@ struct MmSide {
         if constexpr (COL) return ((p * 64 + lane) % SEGS) ^ (2 * column_swizzle<W>(row_of(p)));
         else return (lane & 7) ^ ((row_of(p) >> 1) & 7);
     }
-    // this wave's copies of a chunk into a stage; left: of the contraction, from the chunk's first k
-    __device__ __forceinline__ void issue(int c, uint32_t to, int left) const
+    // this wave's copy j of a chunk into a stage
+    __device__ __forceinline__ void copy(int j, int c, uint32_t to) const
     {
-        const uint8_t* at = base + (int64_t)c * step;
-        if (left >= 64) {
-#pragma unroll
-            for (int j = 0; j < PJ; j++) dma16s(at, off[j], __builtin_amdgcn_readfirstlane(to + piece(j) * 1024));
-        } else {
-#pragma unroll
-            for (int j = 0; j < PJ; j++) {
-                const int p = piece(j);
-                const bool in = COL ? row_of(p) < left : seg_of(p) * 8 < left;
-                dma16(in ? (const void*)(at + off[j]) : (const void*)&g_mm_zeros[lane],
-                      __builtin_amdgcn_readfirstlane(to + p * 1024));
-            }
-        }
+        dma16s(base + (int64_t)c * step, off[j], __builtin_amdgcn_readfirstlane(to + piece(j) * 1024));
+    }
+    // ... of the last chunk, of which `left` k are the contraction's: zeros past them
+    __device__ __forceinline__ void copy_tail(int j, int c, uint32_t to, int left) const
+    {
+        const int p = piece(j);
+        const bool in = COL ? row_of(p) < left : seg_of(p) * 8 < left;
+        dma16(in ? (const void*)(base + (int64_t)c * step + off[j]) : (const void*)&g_mm_zeros[lane],
+              __builtin_amdgcn_readfirstlane(to + p * 1024));
     }
 };
 
@@ -182,10 +179,25 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
     sa.begin(a, m0, wave, lane);
     sb.begin(b, n0, wave, lane);
     const int nch = (K + 63) / 64;
-    auto issue = [&](int c) {
+    const int full = K / 64;
+    // copies q0 .. of this wave's of chunk c, which is whole
+    auto copy = [&](int c, int q0, int n) {
         const uint32_t slot = lds0 + (uint32_t)(c % L::NS) * L::STAGE;
-        sa.issue(c, slot, K - c * 64);
-        sb.issue(c, slot + L::B_OFF, K - c * 64);
+#pragma unroll
+        for (int q = q0; q < min(q0 + n, L::OPS); q++) {
+            if (q < L::AJ) sa.copy(q, c, slot);
+            else sb.copy(q - L::AJ, c, slot + L::B_OFF);
+        }
+    };
+    // all of them of any chunk
+    auto copy_all = [&](int c) {
+        if (c < full) return copy(c, 0, L::OPS);
+        const uint32_t slot = lds0 + (uint32_t)(c % L::NS) * L::STAGE;
+#pragma unroll
+        for (int q = 0; q < L::OPS; q++) {
+            if (q < L::AJ) sa.copy_tail(q, c, slot, K - c * 64);
+            else sb.copy_tail(q - L::AJ, c, slot + L::B_OFF, K - c * 64);
+        }
     };
     MmReader<L::BM, L::ACOL, L::MI> ra;
     MmReader<L::BN, L::BCOL, L::NI> rb;
@@ -195,6 +207,14 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
     for (int i = 0; i < L::MI; i++)
 #pragma unroll
         for (int j = 0; j < L::NI; j++) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (nch > 0) {
+#pragma unroll
+        for (int c = 0; c < L::NS; c++)
+            if (c < nch) copy_all(c);
+        if (nch >= L::NS) wait_vm<L::OPS * (L::NS - 1)>();
+        else wait_vm<0>();
+        __syncthreads();
+    }
     // Row tiles of A in registers: all of a small wave tile's, three of a large one's.
     constexpr int MI = L::MI, NI = L::NI, D = MI < 3 ? MI : 3;
     v8bf af[D][2], bf[NI][2];
@@ -218,19 +238,16 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
             for (int j = 0; j < NI; j++)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[i % D][s], acc[i][j], 0, 0, 0);
     };
-    if (nch > 0) {
-#pragma unroll
-        for (int c = 0; c < L::NS; c++)
-            if (c < nch) issue(c);
-        if (nch >= L::NS) wait_vm<L::OPS * (L::NS - 1)>();
-        else wait_vm<0>();
-        __syncthreads();
-        open(0);
-    }
+    // The copies of a large tile's next stage go out in groups, a row tile's products after each: all at once they
+    // would hold up every wave's products until the memory path has taken them (8192x8192x8192 792 -> 752 us).
+    constexpr int GROUPS = MI >= 4 ? MI / 2 : 1, PER = (L::OPS + GROUPS - 1) / GROUPS;
+    if (nch > 0) open(0);
     for (int c = 0; c < nch; c++) {
         const uint8_t* st = smem + (c % L::NS) * L::STAGE;
+        const bool rest = c > 0 && c - 1 + L::NS < full;          // of the stage that the last barrier freed
 #pragma unroll
         for (int i = 0; i < MI - 1; i++) {
+            if (i + 1 < GROUPS && rest) copy(c - 1 + L::NS, PER * (i + 1), PER);
             if (D < MI && i + D - 1 < MI) read_a(st, i + D - 1);
             row(i);
         }
@@ -240,7 +257,8 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
             if (c + L::NS <= nch) wait_vm<L::OPS * (L::NS - 2)>();
             else wait_vm<0>();
             __syncthreads();
-            if (c + L::NS < nch) issue(c + L::NS);
+            if (c + L::NS < full) copy(c + L::NS, 0, PER);
+            else if (c + L::NS < nch) copy_all(c + L::NS);
         }
         row(MI - 1);
         if (c + 1 < nch) open(c + 1);

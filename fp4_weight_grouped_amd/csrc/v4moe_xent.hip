@@ -145,7 +145,7 @@ struct LogitsArgs {
 template <class L, bool GRAD>
 __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
 {
-    static_assert(L::NI == 4, "parts are of 64 columns in every variant, so that a row's result is the same in all");
+    static_assert(L::NI % 4 == 0, "parts are of 64 columns in every variant, so that a row's result is the same in all");
     extern __shared__ __align__(1024) uint8_t smem[];
     const int n = p.ctrl->n, tm = (n + L::BM - 1) / L::BM, tn = (p.V + L::BN - 1) / L::BN;
     const int turn = mm_turn(blockIdx.x, tm * tn);
@@ -153,37 +153,42 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
     int im, in;
     mm_band(turn, tm, tn, im, in);
     const MmOperand a{p.x, p.ldx, n}, b{p.w, p.ldw, p.V};
-    v4f acc[L::MI][4];
+    v4f acc[L::MI][L::NI];
     mm_tile<L>(a, b, im * L::BM, in * L::BN, p.H, smem, acc);
     const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int mw = im * L::BM + wave / L::WN * L::MI * 16, nw = in * L::BN + wave % L::WN * 64;
+    const int mw = im * L::BM + wave / L::WN * L::MI * 16, nw = in * L::BN + wave % L::WN * L::NI * 16;
     if constexpr (!GRAD) {
-        if (nw >= p.V) return;
 #pragma unroll
         for (int i = 0; i < L::MI; i++) {
             const int m = mw + 16 * i + r16;
-            const int y = m < n ? p.y[m] - p.v0 - nw : -1;
-            float big = -INFINITY;
+            const int target = m < n ? p.y[m] - p.v0 - nw : -1;
 #pragma unroll
-            for (int j = 0; j < 4; j++)
+            for (int j0 = 0; j0 < L::NI; j0 += 4) {
+                const int n0 = nw + 16 * j0, y = target - 16 * j0;
+                if (n0 >= p.V) continue;
+                float big = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    if (nw + 16 * j + 4 * kq + e >= p.V) acc[i][j][e] = -INFINITY;
-                    big = fmaxf(big, acc[i][j][e]);
-                    if (y == 16 * j + 4 * kq + e) p.zy[m] = acc[i][j][e];
-                }
-            big = fmaxf(big, __shfl_xor(big, 16));
-            big = fmaxf(big, __shfl_xor(big, 32));
-            const float off = big == -INFINITY ? 0.0f : big;
-            float sum = 0.0f;
+                for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int j = 0; j < 4; j++)
+                    for (int e = 0; e < 4; e++) {
+                        const float z = n0 + 16 * j + 4 * kq + e < p.V ? acc[i][j0 + j][e] : -INFINITY;
+                        acc[i][j0 + j][e] = z;
+                        big = fmaxf(big, z);
+                        if (y == 16 * j + 4 * kq + e) p.zy[m] = z;
+                    }
+                big = fmaxf(big, __shfl_xor(big, 16));
+                big = fmaxf(big, __shfl_xor(big, 32));
+                const float off = big == -INFINITY ? 0.0f : big;
+                float sum = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; e++) sum += exp_(acc[i][j][e] - off);
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (kq == 0 && m < n) p.parts[(int64_t)((p.v0 + nw) >> 6) * p.T + m] = make_float2(big, sum);
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) sum += exp_(acc[i][j0 + j][e] - off);
+                sum += __shfl_xor(sum, 16);
+                sum += __shfl_xor(sum, 32);
+                if (kq == 0 && m < n) p.parts[(int64_t)((p.v0 + n0) >> 6) * p.T + m] = make_float2(big, sum);
+            }
         }
     } else {
 #pragma unroll
@@ -192,7 +197,7 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
             const int y = p.y[m] - p.v0 - nw;
             const float lse = p.lse[m], g = p.g[m];
 #pragma unroll
-            for (int j = 0; j < 4; j++)
+            for (int j = 0; j < L::NI; j++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int c = 16 * j + 4 * kq + e;
