@@ -6,8 +6,10 @@
 //
 // Both factors have the rank first, so that forward and backward are made of the same
 // three products: rows by a factor (shrink), the result by a factor (expand), and sums
-// over an adapter's rows (outer).  Rows of one adapter need not follow each other: a
-// tile of rows is computed once for each adapter among its rows, and a row takes its own.
+// over an adapter's rows (outer).  Rows of one adapter need not follow each other.  Many
+// rows are listed by adapter first, and tiles are made of the list.  Where there are few
+// (a launch would cost more than it saves), tiles are of rows as they come, computed once
+// for each adapter among them, and a row takes its own.
 //
 // u and dU pass between the products as two bf16 numbers, u rounded and what that leaves:
 // 16 bits of significand, so that the results are as good as with fp32 (one bf16 number
@@ -20,12 +22,15 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace v4moe {
 
 namespace {
 
-constexpr int kSlice = 256;      // of a shrink's contraction: one chain of matrix instructions; slices are added in order
+// A shrink's contraction in slices, each one chain of matrix instructions; every fourth slice is added to the same of
+// four sums, in order, and these are added in order.
+constexpr int kSlice = 256, kSums = 4;
 
 // Sixteen bytes of a row from element k on; zeros past K.
 __device__ __forceinline__ v4u32 load8(const uint16_t* row, int k, int K)
@@ -58,139 +63,439 @@ __device__ __forceinline__ int adapter_of(const int32_t* ids, int m, int M, int 
     return id >= 0 && id < L ? id : -1;
 }
 
+// Rows listed by adapter, those of one in ascending order, those without one last (as
+// adapter L): order[p] is the row at place p, begin[a] .. begin[a + 1] adapter a's places,
+// tiles the list in pieces of 64 places of one adapter.
+constexpr int kTile = 64;
+struct Tile { int a, first, count, unused; };
+struct Listing {
+    int* order;
+    int* begin;                      // [L + 2]
+    int* tiles_n;
+    Tile* tiles;
+};
+constexpr int kListAdapters = 1024;  // counters of sixteen waves fit LDS up to here
+// One block.  Each wave counts its share of the rows, the counts become places (adapter by
+// adapter, wave by wave), and the waves go through their rows again; rows of one adapter
+// among a wave's 64 find each other by a ballot for each bit of the id.
+// 8192 rows 11 us, 512 rows 7.
+__global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t* __restrict__ ids, Listing out, int most)
+{
+    extern __shared__ int counts[];               // [16][L + 1], then totals
+    __shared__ int wave_rows[16], wave_tiles[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = L + 1;
+    int* begin = counts + 16 * n;                 // [n] first place, [n] first tile
+    int* first_tile = begin + n;
+    for (int i = tid; i < 16 * n; i += 1024) counts[i] = 0;
+    __syncthreads();
+    const int share = (M + 1023) / 1024 * 64, m0 = wave * share, m1 = min(m0 + share, M);
+    int* mine = counts + wave * n;
+    // 512 rows of the wave's share at a time, eight loads on their way together; -1 past the share
+    int id[8];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            const int m = base + 64 * q + lane;
+            id[q] = m < m1 ? ids[m] : -1;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; q++) id[q] = base + 64 * q + lane >= m1 ? -1 : id[q] >= 0 && id[q] < L ? id[q] : L;
+    };
+    int bits = 0;
+    while ((n - 1) >> bits) bits++;
+    // id[q]'s place among those of its adapter that the wave has counted, which it then joins
+    auto join = [&](int q) {
+        const int a = max(id[q], 0);
+        const bool in = id[q] >= 0;
+        uint64_t same = __ballot(in);
+        for (int b = 0; b < bits; b++) {
+            const uint64_t ones = __ballot(a >> b & 1);
+            same &= a >> b & 1 ? ones : ~ones;
+        }
+        const int at = in ? mine[a] + __popcll(same & ((1ull << lane) - 1)) : 0;
+        __builtin_amdgcn_wave_barrier();
+        if (in && (same >> lane >> 1) == 0) mine[a] += __popcll(same);       // (the last of them)
+        __builtin_amdgcn_wave_barrier();
+        return at;
+    };
+    const bool once = share <= 512;                                 // then the places below the wave's first stay here
+    int at[8];
+    for (int base = m0; base < m1; base += 512) {
+        load(base);
+#pragma unroll
+        for (int q = 0; q < 8; q++) at[q] = join(q);
+    }
+    __syncthreads();
+    // thread a: adapter a's rows and tiles (n <= 1025: the last by thread 0 too)
+    int rows = 0;
+    if (tid < n)
+        for (int w = 0; w < 16; w++) rows += counts[w * n + tid];
+    int tiles = (rows + kTile - 1) / kTile, r = rows, t = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(r, o), v = __shfl_up(t, o);
+        if (lane >= o) r += u, t += v;
+    }
+    if (lane == 63) wave_rows[wave] = r, wave_tiles[wave] = t;
+    __syncthreads();
+    int rows_before = r - rows, tiles_before = t - tiles, all_rows = 0, all_tiles = 0;
+    for (int w = 0; w < 16; w++) {
+        if (w < wave) rows_before += wave_rows[w], tiles_before += wave_tiles[w];
+        all_rows += wave_rows[w], all_tiles += wave_tiles[w];
+    }
+    if (tid < n) {
+        begin[tid] = rows_before;
+        first_tile[tid] = tiles_before;
+        out.begin[tid] = rows_before;
+        int at = rows_before;
+        for (int w = 0; w < 16; w++) {
+            const int c = counts[w * n + tid];
+            counts[w * n + tid] = at;
+            at += c;
+        }
+    }
+    if (n > 1024) all_tiles += (M - all_rows + kTile - 1) / kTile;
+    if (n > 1024 && tid == 0) {                    // adapter 1024: none
+        begin[1024] = all_rows;
+        first_tile[1024] = all_tiles - (M - all_rows + kTile - 1) / kTile;
+        out.begin[1024] = all_rows;
+        int at = all_rows;
+        for (int w = 0; w < 16; w++) {
+            const int c = counts[w * n + 1024];
+            counts[w * n + 1024] = at;
+            at += c;
+        }
+    }
+    if (tid == 0) {
+        out.begin[n] = M;
+        *out.tiles_n = all_tiles;
+    }
+    __syncthreads();
+    for (int base = m0; base < m1; base += 512) {
+        if (!once) load(base);
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            const int a = max(id[q], 0), place = once ? mine[a] + at[q] : join(q), off = place - begin[a];
+            if (id[q] < 0) continue;
+            out.order[place] = base + 64 * q + lane;
+            if (off % kTile == 0) {
+                const int end = a + 1 < n ? begin[a + 1] : M;
+                out.tiles[first_tile[a] + off / kTile] = Tile{a, place, min(kTile, end - place), 0};
+            }
+        }
+    }
+    // no tiles behind the last
+    for (int i = all_tiles + tid; i < most; i += 1024) out.tiles[i] = Tile{-1, 0, 0, 0};
+}
+
 struct ShrinkJob {
     const uint16_t* x; int64_t ldx; int K;     // rows
     const uint16_t* f;                         // factor [L][r][K]
-    uint16_t* u;                               // [M][2][rp]
+    uint16_t* u;                               // [M][2][rp], by row, or by place
 };
 struct ShrinkArgs {
     int M, L, r, rp;
     const int32_t* ids; const float* scale;
     ShrinkJob job[2];
+    Listing list;
 };
 
-// u of 16 MI rows and 16 NJ ranks per block: the waves take the slices of the contraction
-// in turn, operands straight from memory into registers (each is used once per wave), and
-// the slices meet in LDS.  grid: row tiles, slots of the tile's adapters, rank chunks x jobs.
-template <int MI, int NJ, int NW>
-__global__ __launch_bounds__(64 * NW) void k_lora_shrink(ShrinkArgs p, int chunks)
+// Two numbers for each of four sums: rounded to bf16, and what that leaves.
+__device__ __forceinline__ void store_u(uint16_t* u, int rp, const float (&v)[4])
 {
-    constexpr int LD = 16 * NJ + 4, QUADS = 16 * MI * 4 * NJ, PER = (QUADS + 64 * NW - 1) / (64 * NW);
-    extern __shared__ __align__(16) float part[];            // [NW][16 MI][LD]
+    float hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        hi[e] = bf16_to_f32(bf16x2(v[e], 0.0f) & 0xFFFFu);
+        lo[e] = fabsf(hi[e]) < INFINITY ? v[e] - hi[e] : 0.0f;     // (infinities and NaN stand alone)
+    }
+    *reinterpret_cast<uint2*>(u) = make_uint2(bf16x2(hi[0], hi[1]), bf16x2(hi[2], hi[3]));
+    *reinterpret_cast<uint2*>(u + rp) = make_uint2(bf16x2(lo[0], lo[1]), bf16x2(lo[2], lo[3]));
+}
+
+// u of 16 rows and 16 NJ ranks per block, of any alignment.  The sixteen waves take the slices
+// of the contraction in turn, rows straight from memory into registers, the factor through a
+// wave's own LDS (as the instruction wants its lanes, neighbours would read rows far apart, and
+// the L1 takes a lane at a time: 64 rows with adapters of their own 12.0 us); the slices meet in LDS.
+// grid: 16-row tiles, slots of the tile's adapters (LISTED: quarters of a tile), rank chunks x jobs.
+constexpr int kShrinkWaves = 16, kShrinkRow = kSlice * 2 + 16;       // bytes of a staged row: 16 rows hit distinct banks
+template <int NJ>
+constexpr int shrink_room()          // the waves' staged rows, then the slices' products
+{
+    const int staged = kShrinkWaves * 16 * kShrinkRow, part = kShrinkWaves * 16 * (16 * NJ + 4) * 4;
+    return staged > part ? staged : part;
+}
+template <int NJ>
+constexpr int shrink_bytes() { return shrink_room<NJ>() + 16 * 16 * NJ * kSums * 4; }
+template <int NJ, bool LISTED>
+__global__ __launch_bounds__(64 * kShrinkWaves) void k_lora_shrink(ShrinkArgs p, int chunks)
+{
+    constexpr int NW = kShrinkWaves, LD = 16 * NJ + 4, QUADS = 16 * 4 * NJ;
+    static_assert(QUADS <= 64 * NW, "a thread per four sums");
+    static_assert(shrink_bytes<NJ>() <= 163840, "LDS of a CU");
+    extern __shared__ __align__(16) uint8_t lds[];           // [NW][16][kShrinkRow], then [NW][16][LD] fp32; the sums
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, kq = lane >> 4;
     const ShrinkJob& job = p.job[blockIdx.z / chunks];
-    const int m0 = blockIdx.x * 16 * MI, j0 = (int)(blockIdx.z % chunks) * 16 * NJ, K = job.K;
-    const uint16_t* xrow[MI];
+    const int j0 = (int)(blockIdx.z % chunks) * 16 * NJ, K = job.K;
+    const uint16_t* xrow;
+    int first;                                               // row or place of the tile's first
+    uint8_t* mine = lds + wave * 16 * kShrinkRow;
+    float* part = reinterpret_cast<float*>(lds);
+    auto work = [&](int a, uint64_t rows) {
+        const float scale = p.scale[a];
+        const bool has = rows >> r16 & 1;
+        const uint16_t* factor = job.f + (int64_t)a * p.r * K;
+        float4* sums = reinterpret_cast<float4*>(lds + shrink_room<NJ>()) + (tid < QUADS ? tid : 0) * kSums;   // this thread's
+        if (tid < QUADS) {
 #pragma unroll
-    for (int i = 0; i < MI; i++) xrow[i] = job.x + (int64_t)min(m0 + 16 * i + r16, p.M - 1) * job.ldx + 8 * kq;
-    const int id = lane < 16 * MI ? adapter_of(p.ids, m0 + lane, p.M, p.L) : -1;
-    each_adapter(id, blockIdx.y, gridDim.y, [&](int a, uint64_t rows) {
-        const uint16_t* frow[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; j++) frow[j] = job.f + ((int64_t)a * p.r + min(j0 + 16 * j + r16, p.r - 1)) * K + 8 * kq;
-        float4 sum[PER];
-#pragma unroll
-        for (int q = 0; q < PER; q++) sum[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int w = 0; w < kSums; w++) sums[w] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
         for (int k0 = 0; k0 < K; k0 += NW * kSlice) {
             const int k1 = k0 + wave * kSlice;
+            v4f acc[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; j++) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
             if (k1 < K) {
-                v4f acc[MI][NJ];
+                constexpr int STEPS = kSlice / 32;
+                v4u32 x[STEPS], f[STEPS];
+                auto load = [&](int j) {                     // 16 ranks, two of them an instruction
+                    int half = lane >> 5;
+                    asm volatile("" : "+v"(half));           // (addresses are made here: kept over the loop they would not fit the registers)
 #pragma unroll
-                for (int i = 0; i < MI; i++)
-#pragma unroll
-                    for (int j = 0; j < NJ; j++) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-                auto products = [&](const v4u32 (&x)[MI], const v4u32 (&f)[NJ]) {
-#pragma unroll
-                    for (int i = 0; i < MI; i++)
-#pragma unroll
-                        for (int j = 0; j < NJ; j++)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(v8bf, f[j]), __builtin_bit_cast(v8bf, x[i]), acc[i][j], 0, 0, 0);
-                };
-                if (k1 + kSlice <= K) {
-                    constexpr int AHEAD = NJ * MI <= 2 ? 8 : 4;      // steps whose operands are loaded together
-#pragma unroll
-                    for (int s0 = 0; s0 < kSlice / 32; s0 += AHEAD) {
-                        v4u32 x[AHEAD][MI], f[AHEAD][NJ];
-#pragma unroll
-                        for (int s = 0; s < AHEAD; s++) {
-#pragma unroll
-                            for (int i = 0; i < MI; i++)
-                                x[s][i] = *reinterpret_cast<const v4u32_any*>(xrow[i] + k1 + 32 * (s0 + s));
-#pragma unroll
-                            for (int j = 0; j < NJ; j++)
-                                f[s][j] = *reinterpret_cast<const v4u32_any*>(frow[j] + k1 + 32 * (s0 + s));
-                        }
-#pragma unroll
-                        for (int s = 0; s < AHEAD; s++) products(x[s], f[s]);
+                    for (int s = 0; s < STEPS; s++) {
+                        const int rank = j0 + 16 * j + 2 * s + half, k = k1 + 8 * (lane & 31);
+                        f[s] = v4u32{0u, 0u, 0u, 0u};
+                        if (rank < p.r && k < K) f[s] = load8(factor + (int64_t)rank * K, k, K);
                     }
-                } else {
-                    for (int k = k1; k < K; k += 32) {
-                        v4u32 x[MI], f[NJ];
+                };
 #pragma unroll
-                        for (int i = 0; i < MI; i++) x[i] = load8(xrow[i], k, K - 8 * kq);
+                for (int s = 0; s < STEPS; s++) {
+                    x[s] = v4u32{0u, 0u, 0u, 0u};
+                    if (has && k1 + 32 * s + 8 * kq < K) x[s] = load8(xrow, k1 + 32 * s + 8 * kq, K);
+                }
+                if (NJ == 1) load(0);
 #pragma unroll
-                        for (int j = 0; j < NJ; j++) f[j] = load8(frow[j], k, K - 8 * kq);
-                        products(x, f);
+                for (int j = 0; j < NJ; j++) {
+                    asm volatile("" ::: "memory");           // (loads of later ranks stay behind: registers)
+                    if (NJ > 1) load(j);
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int s = 0; s < STEPS; s++)
+                        *reinterpret_cast<v4u32*>(mine + (2 * s + (lane >> 5)) * kShrinkRow + (lane & 31) * 16) = f[s];
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int s = 0; s < STEPS; s++) {
+                        const v8bf fv = *reinterpret_cast<const v8bf*>(mine + r16 * kShrinkRow + s * 64 + kq * 16);
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, __builtin_bit_cast(v8bf, x[s]), acc[j], 0, 0, 0);
                     }
                 }
-                float* to = part + wave * 16 * MI * LD;
+            }
+            __syncthreads();                                 // (the staged rows are read)
+            if (k1 < K) {
 #pragma unroll
-                for (int i = 0; i < MI; i++)
-#pragma unroll
-                    for (int j = 0; j < NJ; j++)
-                        *reinterpret_cast<float4*>(to + (16 * i + r16) * LD + 16 * j + 4 * kq) =
-                            make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+                for (int j = 0; j < NJ; j++)
+                    *reinterpret_cast<float4*>(part + (wave * 16 + r16) * LD + 16 * j + 4 * kq) =
+                        make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
             }
             __syncthreads();
             const int slices = min(NW, (K - k0 + kSlice - 1) / kSlice);
+            if (tid < QUADS) {
+                const float* from = part + tid / (4 * NJ) * LD + tid % (4 * NJ) * 4;
+                static_assert(NW % kSums == 0, "a round's slices go on where the last one's ended");
+                float4 sum[kSums];
 #pragma unroll
-            for (int q = 0; q < PER; q++) {
-                const int at = tid + q * 64 * NW;
-                if (at < QUADS) {
-                    const float* from = part + at / (4 * NJ) * LD + at % (4 * NJ) * 4;
-                    for (int w = 0; w < slices; w++) {
-                        const float4 v = *reinterpret_cast<const float4*>(from + w * 16 * MI * LD);
-                        sum[q].x += v.x;
-                        sum[q].y += v.y;
-                        sum[q].z += v.z;
-                        sum[q].w += v.w;
+                for (int w = 0; w < kSums; w++) sum[w] = sums[w];
+#pragma unroll
+                for (int w0 = 0; w0 < NW; w0 += kSums) {
+                    float4 v[kSums];
+#pragma unroll
+                    for (int w = 0; w < kSums; w++)
+                        v[w] = w0 + w < slices ? *reinterpret_cast<const float4*>(from + (w0 + w) * 16 * LD)
+                                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int w = 0; w < kSums; w++) {
+                        sum[w].x += v[w].x;
+                        sum[w].y += v[w].y;
+                        sum[w].z += v[w].z;
+                        sum[w].w += v[w].w;
                     }
                 }
+#pragma unroll
+                for (int w = 0; w < kSums; w++) sums[w] = sum[w];
             }
             __syncthreads();
         }
-        const float scale = p.scale[a];
+        const int row = tid / (4 * NJ), j = j0 + tid % (4 * NJ) * 4;
+        if (tid < QUADS && (rows >> row & 1) && j < p.rp) {
+            float4 s = sums[0];
 #pragma unroll
-        for (int q = 0; q < PER; q++) {
-            const int at = tid + q * 64 * NW, row = at / (4 * NJ), j = j0 + at % (4 * NJ) * 4;
-            if (at < QUADS && (rows >> row & 1) && j < p.rp) {
-                const float s[4] = {sum[q].x, sum[q].y, sum[q].z, sum[q].w};
-                float hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float v = j + e < p.r ? s[e] * scale : 0.0f;
-                    hi[e] = bf16_to_f32(bf16x2(v, 0.0f) & 0xFFFFu);
-                    lo[e] = fabsf(hi[e]) < INFINITY ? v - hi[e] : 0.0f;     // (infinities and NaN stand alone)
-                }
-                uint16_t* u = job.u + (int64_t)(m0 + row) * 2 * p.rp + j;
-                *reinterpret_cast<uint2*>(u) = make_uint2(bf16x2(hi[0], hi[1]), bf16x2(hi[2], hi[3]));
-                *reinterpret_cast<uint2*>(u + p.rp) = make_uint2(bf16x2(lo[0], lo[1]), bf16x2(lo[2], lo[3]));
+            for (int w = 1; w < kSums; w++) {
+                s.x += sums[w].x;
+                s.y += sums[w].y;
+                s.z += sums[w].z;
+                s.w += sums[w].w;
             }
+            const float v[4] = {s.x * scale, j + 1 < p.r ? s.y * scale : 0.0f, j + 2 < p.r ? s.z * scale : 0.0f,
+                                j + 3 < p.r ? s.w * scale : 0.0f};
+            const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            store_u(job.u + (int64_t)(first + row) * 2 * p.rp + j, p.rp, j < p.r ? v : zero);
         }
-    });
+    };
+    if constexpr (LISTED) {
+        const Tile t = p.list.tiles[blockIdx.x];
+        const int at = 16 * blockIdx.y, count = min(16, t.count - at);
+        if (t.a >= p.L || count <= 0) return;
+        first = t.first + at;
+        xrow = job.x + (int64_t)p.list.order[first + min(r16, count - 1)] * job.ldx;
+        work(t.a, (1ull << count) - 1);
+    } else {
+        first = blockIdx.x * 16;
+        xrow = job.x + (int64_t)min(first + r16, p.M - 1) * job.ldx;
+        each_adapter(lane < 16 ? adapter_of(p.ids, first + lane, p.M, p.L) : -1, blockIdx.y, gridDim.y, work);
+    }
+}
+
+// u of a tile of the list and 16 NI ranks per block, rows that begin at 16 bytes.  Each of the four
+// waves has every fourth slice: rows and factor pass through a ring of its own in LDS, 64 k a stage
+// (whole lines of 128 bytes: halves are requests of their own, and as many of those fit the L1), so
+// that nothing waits for another wave until the four sums meet.
+template <int NI, int NS>
+struct ShrinkRing {
+    static constexpr int MI = kTile / 16, AP = 2 * MI, BP = 2 * NI, OPS = AP + BP;     // 1 KiB pieces of a stage: 8 rows each
+    static constexpr int B_OFF = AP * 1024, STAGE = OPS * 1024, RING = NS * STAGE, LD = 16 * NI + 4;
+    static constexpr int SUMS = kSums * kTile * LD * 4, BYTES = kSums * RING > SUMS ? kSums * RING : SUMS;
+    static_assert(OPS * (NS - 1) < 64 && NS >= 2 && BYTES <= 163840, "vmcnt range; LDS of a CU");
+};
+template <int NI, int NS>
+__global__ __launch_bounds__(64 * kSums) void k_lora_shrink_ring(ShrinkArgs p, int chunks)
+{
+    using R = ShrinkRing<NI, NS>;
+    constexpr int MI = R::MI;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int turn = mm_turn(blockIdx.x, *p.list.tiles_n);
+    if (turn < 0) return;
+    const Tile t = p.list.tiles[turn];
+    if (t.a >= p.L) return;
+    const ShrinkJob& job = p.job[blockIdx.z / chunks];
+    const int j0 = (int)(blockIdx.z % chunks) * 16 * NI, K = job.K;
+    const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem + wave * R::RING;
+    // this lane's segments: row lane / 8 of each piece, segments as MmSide has them
+    const int r8 = lane >> 3;
+    auto segment = [&](int piece) { return (lane & 7) ^ (((piece * 8 + r8) >> 1) & 7); };
+    const uint16_t *px[R::AP], *pf[R::BP];
+#pragma unroll
+    for (int i = 0; i < R::AP; i++)
+        px[i] = job.x + (int64_t)p.list.order[t.first + min(8 * i + r8, t.count - 1)] * job.ldx + segment(i) * 8;
+#pragma unroll
+    for (int j = 0; j < R::BP; j++)
+        pf[j] = job.f + ((int64_t)t.a * p.r + min(j0 + 8 * j + r8, p.r - 1)) * K + segment(j) * 8;
+    // the wave's step q: 64 k of its slice q / PER
+    constexpr int PER = kSlice / 64;
+    auto begin_of = [&](int q) { return ((q / PER) * kSums + wave) * kSlice + q % PER * 64; };
+    int steps = 0;
+    for (int k = wave * kSlice; k < K; k += kSums * kSlice) steps += (min(K - k, kSlice) + 63) / 64;
+    auto copy = [&](int q) {
+        const int k = begin_of(q);
+        const uint32_t to = ring0 + (uint32_t)(q % NS) * R::STAGE;
+        auto one = [&](const uint16_t* from, int piece, uint32_t at) {
+            const bool in = k + segment(piece) * 8 < K;           // (K a multiple of 8: whole segments)
+            dma16(in ? (const void*)(from + k) : (const void*)&g_mm_zeros[lane], __builtin_amdgcn_readfirstlane(at));
+        };
+#pragma unroll
+        for (int i = 0; i < R::AP; i++) one(px[i], i, to + i * 1024);
+#pragma unroll
+        for (int j = 0; j < R::BP; j++) one(pf[j], j, to + R::B_OFF + j * 1024);
+    };
+    const int r16 = lane & 15, kq = lane >> 4;
+    MmReader<kTile, false, MI> ra;
+    MmReader<16 * NI, false, NI> rb;
+    ra.begin(0, lane);
+    rb.begin(0, lane);
+    v4f acc[MI][NI], sum[MI][NI];
+#pragma unroll
+    for (int i = 0; i < MI; i++)
+#pragma unroll
+        for (int j = 0; j < NI; j++) acc[i][j] = sum[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int q = 0; q < NS; q++)
+        if (q < steps) copy(q);
+    for (int q = 0; q < steps; q++) {
+        // step q is whole once only later ones' copies are out
+        if (q + NS <= steps) wait_vm<R::OPS * (NS - 1)>();
+        else wait_vm<0>();
+        asm volatile("" ::: "memory");
+        const uint8_t* st = smem + wave * R::RING + (q % NS) * R::STAGE;
+        v8bf a[2][MI], b[2][NI];
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+#pragma unroll
+            for (int i = 0; i < MI; i++) a[s][i] = ra.read(st, i, s);
+#pragma unroll
+            for (int j = 0; j < NI; j++) b[s][j] = rb.read(st + R::B_OFF, j, s);
+        }
+        // the slot is free once its operands are in registers
+        if (q + NS < steps) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0)
+            asm volatile("" ::: "memory");
+            copy(q + NS);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; s++)
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+#pragma unroll
+                for (int j = 0; j < NI; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s][j], a[s][i], acc[i][j], 0, 0, 0);
+        if ((q + 1) % PER == 0 || q + 1 == steps) {
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+#pragma unroll
+                for (int j = 0; j < NI; j++) {
+                    sum[i][j] += acc[i][j];
+                    acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+        }
+    }
+    __syncthreads();                                    // (every ring is read)
+    float* sums = reinterpret_cast<float*>(smem);       // [kSums][kTile][LD]
+#pragma unroll
+    for (int i = 0; i < MI; i++)
+#pragma unroll
+        for (int j = 0; j < NI; j++)
+            *reinterpret_cast<float4*>(sums + (wave * kTile + 16 * i + r16) * R::LD + 16 * j + 4 * kq) =
+                make_float4(sum[i][j][0], sum[i][j][1], sum[i][j][2], sum[i][j][3]);
+    __syncthreads();
+    const float scale = p.scale[t.a];
+#pragma unroll
+    for (int q = 0; q < NI; q++) {
+        const int at = q * 256 + tid, row = at / (4 * NI), k = at % (4 * NI) * 4;
+        if (row >= t.count || j0 + k >= p.rp) continue;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kSums; w++) {
+            const float4 f = *reinterpret_cast<const float4*>(sums + (w * kTile + row) * R::LD + k);
+            v[0] = w ? v[0] + f.x : f.x;
+            v[1] = w ? v[1] + f.y : f.y;
+            v[2] = w ? v[2] + f.z : f.z;
+            v[3] = w ? v[3] + f.w : f.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = j0 + k + e < p.r ? v[e] * scale : 0.0f;
+        store_u(job.u + (int64_t)(t.first + row) * 2 * p.rp + j0 + k, p.rp, v);
+    }
 }
 
 struct ExpandArgs {
     int M, N, L, r, rp;
     const int32_t* ids;
-    const uint16_t* u;                          // [M][2][rp]
+    const uint16_t* u;                          // [M][2][rp], by row, or by place
     const uint16_t* f;                          // factor [L][r][N]
     const void* y; int64_t ldy;                 // added to (null: zeros)
     void* out; int64_t ldo;
-    int tiles;                                  // 16-row tiles per wave
     int in_place;                               // out is y: rows without an adapter are there already
+    Listing list;
 };
 
 // Sixteen values of a row from column n on, as fp32; past N zeros.
@@ -251,93 +556,259 @@ __device__ __forceinline__ void store16f(T* row, int n, int N, const float (&v)[
     }
 }
 
-// A wave: 64 columns of `tiles` 16-row tiles.  The factor's 16 RC ranks by 64 columns pass
-// through LDS, where transposing reads make operands of them that stay in registers while
-// the adapter lasts.  A step of the contraction is 16 ranks twice, by u and by what its
-// rounding left.  Columns are dealt so that a lane ends with 16 consecutive ones: of the
-// instruction's column i of tile t it is 16 (i / 4) + 4 t + i % 4.
+// The factor's 16 RC ranks from j0 on by 64 columns from c0 on, adapter a, into registers, and from there
+// into a wave's LDS, where transposing reads make operands of them.  Columns are dealt so that a lane ends with
+// 16 consecutive ones: of the instruction's column i of tile t it is 16 (i / 4) + 4 t + i % 4.
+template <int RC>
+__device__ __forceinline__ void load_factor(const uint16_t* f, int a, int r, int j0, int c0, int N, v4u32 (&v)[2 * RC])
+{
+    const int lane = threadIdx.x & 63, s = lane & 7;
+#pragma unroll
+    for (int q = 0; q < 2 * RC; q++) {
+        const int j = j0 + 8 * q + (lane >> 3);
+        v[q] = v4u32{0u, 0u, 0u, 0u};
+        if (j < r && c0 + 8 * s < N) v[q] = load8(f + ((int64_t)a * r + j) * N, c0 + 8 * s, N);
+    }
+}
+template <int RC>
+__device__ __forceinline__ void stage_factor(const v4u32 (&v)[2 * RC], uint8_t* to)
+{
+    const int lane = threadIdx.x & 63, s = lane & 7;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 2 * RC; q++) {
+        const int j = 8 * q + (lane >> 3), swizzle = column_swizzle<64>(j);
+        // the segment's halves: columns 16 (s / 2) + 4 t + 0 .. 3 for t = 2 (s % 2), + 1
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+            *reinterpret_cast<uint2*>(to + j * 128 + ((2 * (s & 1) + h) ^ swizzle) * 32 + (s >> 1) * 8) =
+                make_uint2(v[q][2 * h], v[q][2 * h + 1]);
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Few rows: a wave has 64 columns of a 16-row tile, once for each adapter among its rows.  A step of
+// the contraction is 16 ranks twice, by u and by what its rounding left.
 template <int RC, typename T>
 __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs p)
 {
     __shared__ __align__(128) uint8_t lds[4][16 * RC * 128];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r16 = lane & 15, kq = lane >> 4;
-    const int c0 = ((int)blockIdx.x * 4 + wave) * 64;
+    const int columns = (p.N + 255) / 256;                    // blocks along a row first
+    const int c0 = ((int)(blockIdx.x % columns) * 4 + wave) * 64, n = c0 + 16 * kq;
     if (c0 >= p.N) return;                                    // (no barrier below: waves are on their own)
     uint8_t* mine = lds[wave];
-    v8bf bf[RC][4];
-    int staged = -1, staged_j = -1;
-    // ranks j0 .. of adapter a into the operands
-    auto stage = [&](int a, int j0) {
-        if (a == staged && j0 == staged_j) return;
-        staged = a;
-        staged_j = j0;
-        __builtin_amdgcn_wave_barrier();
+    MmReader<64, true, 4> reader;
+    reader.begin_at(0, lane, 8 * (kq & 1));
+    const int m = (int)(blockIdx.x / columns) * 16 + r16, row = min(m, p.M - 1);
+    const int id = adapter_of(p.ids, m, p.M, p.L);
+    const bool real = m < p.M && n < p.N;
+    const uint16_t* urow = p.u + ((int64_t)row * 2 + (kq >> 1)) * p.rp + 8 * (kq & 1);
+    T* orow = static_cast<T*>(p.out) + (int64_t)row * p.ldo;
+    float y[16];
 #pragma unroll
-        for (int q = 0; q < 2 * RC; q++) {
-            const int j = 8 * q + (lane >> 3), s = lane & 7;
+    for (int e = 0; e < 16; e++) y[e] = 0.0f;
+    if (p.y && real) load16f(static_cast<const T*>(p.y) + (int64_t)row * p.ldy, n, p.N, y);
+    if (blockIdx.y == 0 && real && id < 0 && !p.in_place) store16f(orow, n, p.N, y);
+    each_adapter(lane < 16 ? id : -1, blockIdx.y, gridDim.y, [&](int a, uint64_t) {
+        v4f acc[4];
+#pragma unroll
+        for (int t = 0; t < 4; t++) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j0 = 0; j0 < p.r; j0 += 16 * RC) {
+            v4u32 u[RC];
+#pragma unroll
+            for (int c = 0; c < RC; c++) {
+                u[c] = v4u32{0u, 0u, 0u, 0u};
+                // (rows of other adapters give results that nobody takes; a lane has its part of the contraction
+                // where its columns are past the end, too)
+                if (id == a && j0 + 16 * c < p.rp) u[c] = *reinterpret_cast<const v4u32*>(urow + j0 + 16 * c);
+            }
+            v4u32 f[2 * RC];
+            load_factor<RC>(p.f, a, p.r, j0, c0, p.N, f);
+            stage_factor<RC>(f, mine);
+#pragma unroll
+            for (int c = 0; c < RC; c++)
+#pragma unroll
+                for (int t = 0; t < 4; t++)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(reader.read_at(mine, t, 16 * c),
+                                                                     __builtin_bit_cast(v8bf, u[c]), acc[t], 0, 0, 0);
+        }
+        if (id == a && real) {
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; e++) v[e] = y[e] + acc[e >> 2][e & 3];
+            store16f(orow, n, p.N, v);
+        }
+    });
+}
+
+// Eight values of a row from column n on, as fp32; past N zeros.
+template <typename T>
+struct Eight {
+    v4u32 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* row, int n, int N)
+    {
+        if constexpr (sizeof(T) == 2) {
+            w[0] = load8(row, n, N);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if (n + 4 * h + 4 <= N) {
+                    w[h] = *reinterpret_cast<const v4u32_any*>(row + n + 4 * h);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) w[h][e] = n + 4 * h + e < N ? __float_as_uint(row[n + 4 * h + e]) : 0u;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float operator[](int e) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e >> 2][e & 3]);
+        else return __uint_as_float(e & 1 ? w[0][e >> 1] & 0xFFFF0000u : w[0][e >> 1] << 16);
+    }
+};
+template <typename T>
+__device__ __forceinline__ void store8f(T* row, int n, int N, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        const v4u32 w = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
+        if (n + 8 <= N) {
+            *reinterpret_cast<v4u32_any*>(row + n) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                if (n + e < N) row[n + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (n + 4 * h + 4 <= N) {
+                *reinterpret_cast<v4u32_any*>(row + n + 4 * h) =
+                    v4u32{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                          __float_as_uint(v[4 * h + 3])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (n + 4 * h + e < N) row[n + 4 * h + e] = v[4 * h + e];
+            }
+        }
+    }
+}
+
+// A tile of the list by 256 columns per block, a wave 64 of them.  y is on its way while the tile's u, for
+// all waves, and the factor, for each, are staged in LDS; the sums pass through LDS to where neighbouring lanes
+// have neighbouring columns, as y came (as the instruction leaves them, a lane's row is far from its
+// neighbour's, and the L1 takes a lane at a time).
+// ONE: all ranks at once (RC chosen so); else 16 RC of them in turn, staged anew for each row tile.
+template <int RC, typename T, bool ONE>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_lora_expand_tile(ExpandArgs p)
+{
+    constexpr int UROW = 16 * RC * 4;                          // bytes of a row of u: 16 RC ranks twice
+    constexpr int FACTOR = 16 * RC * 128, SUMS = 16 * 256;     // a wave's part of the factor, then of the sums: 16 rows
+    __shared__ __align__(128) uint8_t us[kTile * UROW];
+    __shared__ __align__(128) uint8_t lds[4][FACTOR > SUMS ? FACTOR : SUMS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, kq = lane >> 4;
+    const int blocks = (p.N + 255) / 256;                      // along a row, which go first
+    const Tile t = p.list.tiles[blockIdx.x / blocks];
+    const bool none = t.a >= p.L;
+    if (t.count == 0 || (none && p.in_place)) return;
+    const int c = (int)(blockIdx.x % blocks) * 256 + 64 * wave, s8 = lane & 7, n = c + 8 * s8;
+    // this lane's rows 8 q + lane / 8, and its columns n .. + 7
+    int m[8];
+#pragma unroll
+    for (int q = 0; q < 8; q++) m[q] = 8 * q + (lane >> 3) < t.count ? p.list.order[t.first + 8 * q + (lane >> 3)] : -1;
+    v4u32 f[2 * RC];
+    if (ONE && !none) load_factor<RC>(p.f, t.a, p.r, 0, c, p.N, f);
+    Eight<T> y[8];
+#pragma unroll
+    for (int q = 0; q < 8; q++) {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; h++) y[q].w[h] = v4u32{0u, 0u, 0u, 0u};
+        if (p.y && m[q] >= 0 && n < p.N) y[q].load(static_cast<const T*>(p.y) + (int64_t)m[q] * p.ldy, n, p.N);
+    }
+    // Where 16-byte segments go, so that the lanes that are served together (0-3, 12-15 and 20-27 of each 32, and
+    // the others; of a write eight in a row) hit distinct banks.
+    auto u_at = [](int i, int sg) {
+        if constexpr (RC == 1) return i * 64 + (sg ^ ((i >> 3 & 1) * 3)) * 16;
+        else if constexpr (RC == 2) return i * 128 + (sg ^ (i >> 1 & 7)) * 16;
+        else return i * 256 + (sg ^ (i & 15)) * 16;
+    };
+    auto sum_at = [](int i, int sg) { return i * 64 + (sg ^ ((i >> 1 & 1) | (i & 1) << 1 | (i & 12))) * 4; };
+    MmReader<64, true, 4> reader;
+    reader.begin_at(0, lane, 8 * (kq & 1));
+    auto stage_u = [&](int j0) {
+        constexpr int SEGS = 4 * RC, EACH = kTile * SEGS / 256;       // 16-byte segments of a row: half u, half what it left
+#pragma unroll
+        for (int q = 0; q < EACH; q++) {
+            const int i = (q * 256 + tid) / SEGS, sg = (q * 256 + tid) % SEGS, j = j0 + sg % (SEGS / 2) * 8;
             v4u32 v = {0u, 0u, 0u, 0u};
-            if (j0 + j < p.r && c0 + 8 * s < p.N) v = load8(p.f + ((int64_t)a * p.r + j0 + j) * p.N, c0 + 8 * s, p.N);
-            // the segment's halves: columns 16 (s / 2) + 4 t + 0 .. 3 for t = 2 (s % 2), + 1
-            const int f = column_swizzle<64>(j);
+            if (i < t.count && j < p.rp)
+                v = *reinterpret_cast<const v4u32*>(p.u + ((int64_t)(t.first + i) * 2 + sg / (SEGS / 2)) * p.rp + j);
+            *reinterpret_cast<v4u32*>(us + u_at(i, sg)) = v;
+        }
+    };
+    v8bf b[RC][4];
+    auto operands = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; h++)
-                *reinterpret_cast<uint2*>(mine + j * 128 + ((2 * (s & 1) + h) ^ f) * 32 + (s >> 1) * 8) =
-                    make_uint2(v[2 * h], v[2 * h + 1]);
+        for (int k = 0; k < RC; k++)
+#pragma unroll
+            for (int w = 0; w < 4; w++) b[k][w] = reader.read_at(lds[wave], w, 16 * k);
+    };
+    if (ONE && !none) {
+        stage_u(0);
+        stage_factor<RC>(f, lds[wave]);
+        __syncthreads();
+        operands();
+    }
+    float* sums = reinterpret_cast<float*>(lds[wave]);
+#pragma unroll
+    for (int i = 0; i < kTile / 16; i++) {
+        if (16 * i >= t.count) break;
+        v4f acc[4];
+#pragma unroll
+        for (int w = 0; w < 4; w++) acc[w] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j0 = 0; j0 < (none ? 0 : ONE ? 1 : p.r); j0 += 16 * RC) {
+            if constexpr (!ONE) {
+                __syncthreads();                               // (the ranks, or the sums, before are read)
+                stage_u(j0);
+                load_factor<RC>(p.f, t.a, p.r, j0, c, p.N, f);
+                stage_factor<RC>(f, lds[wave]);
+                __syncthreads();
+                operands();
+            }
+#pragma unroll
+            for (int k = 0; k < RC; k++) {
+                const v8bf u = *reinterpret_cast<const v8bf*>(us + u_at(16 * i + r16, (kq >> 1) * 2 * RC + 2 * k + (kq & 1)));
+#pragma unroll
+                for (int w = 0; w < 4; w++) acc[w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[k][w], u, acc[w], 0, 0, 0);
+            }
         }
         __builtin_amdgcn_wave_barrier();
-        MmReader<64, true, 4> reader;
-        reader.begin_at(0, lane, 8 * (kq & 1));
 #pragma unroll
-        for (int c = 0; c < RC; c++)
+        for (int k = 0; k < 4; k++)
+            *reinterpret_cast<float4*>(sums + sum_at(r16, 4 * kq + k)) = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int t = 0; t < 4; t++) bf[c][t] = reader.read_at(mine, t, 16 * c);
-    };
-    for (int i = 0; i < p.tiles; i++) {
-        const int m0 = ((int)blockIdx.y * p.tiles + i) * 16, m = m0 + r16;
-        if (m0 >= p.M) return;
-        const int id = adapter_of(p.ids, m, p.M, p.L);
-        const int n = c0 + 16 * kq;
-        const bool real = m < p.M && n < p.N;
-        const T* yrow = static_cast<const T*>(p.y) + (int64_t)min(m, p.M - 1) * p.ldy;
-        T* orow = static_cast<T*>(p.out) + (int64_t)min(m, p.M - 1) * p.ldo;
-        float y[16];
+        for (int h = 0; h < 2; h++) {
+            const int q = 2 * i + h, r = 8 * h + (lane >> 3);
+            const float4 lo = *reinterpret_cast<const float4*>(sums + sum_at(r, 2 * s8));
+            const float4 hi = *reinterpret_cast<const float4*>(sums + sum_at(r, 2 * s8 + 1));
+            if (m[q] < 0 || n >= p.N) continue;
+            const float add[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            float v[8];
+            // (a row without an adapter stays what it is, a negative zero too)
 #pragma unroll
-        for (int e = 0; e < 16; e++) y[e] = 0.0f;
-        if (p.y && real) load16f(yrow, n, p.N, y);
-        if (blockIdx.z == 0 && real && id < 0 && !p.in_place) store16f(orow, n, p.N, y);
-        const uint16_t* urow = p.u + (int64_t)min(m, p.M - 1) * 2 * p.rp + (kq >> 1) * p.rp + 8 * (kq & 1);
-        each_adapter(lane < 16 ? id : -1, blockIdx.z, gridDim.z, [&](int a, uint64_t) {
-            v4f acc[4];
-#pragma unroll
-            for (int t = 0; t < 4; t++) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            for (int j0 = 0; j0 < p.r; j0 += 16 * RC) {
-                v4u32 u[RC];
-#pragma unroll
-                for (int c = 0; c < RC; c++) {
-                    u[c] = v4u32{0u, 0u, 0u, 0u};
-                    // (rows of other adapters, or none, give results that nobody takes)
-                    if (id == a && j0 + 16 * c < p.rp) u[c] = *reinterpret_cast<const v4u32*>(urow + j0 + 16 * c);
-                }
-                stage(a, j0);
-#pragma unroll
-                for (int c = 0; c < RC; c++)
-#pragma unroll
-                    for (int t = 0; t < 4; t++)
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[c][t], __builtin_bit_cast(v8bf, u[c]), acc[t], 0, 0, 0);
-            }
-            if (id == a && real) {
-                float v[16];
-#pragma unroll
-                for (int e = 0; e < 16; e++) v[e] = y[e] + acc[e >> 2][e & 3];
-                store16f(orow, n, p.N, v);
-            }
-        });
+            for (int e = 0; e < 8; e++) v[e] = none ? y[q][e] : y[q][e] + add[e];
+            store8f(static_cast<T*>(p.out) + (int64_t)m[q] * p.ldo, n, p.N, v);
+        }
     }
 }
 
 struct OuterJob {
-    const uint16_t* u;                          // [M][2][rp]
+    const uint16_t* u;                          // [M][2][rp], by row, or by place
     const uint16_t* x; int64_t ldx; int N;      // rows, columns
     void* d;                                    // [L][r][N]
     int bf16, blocks;                           // column blocks of 64
@@ -346,18 +817,20 @@ struct OuterArgs {
     int M, L, r, rp, accumulate;
     const int32_t* ids;
     OuterJob job[2];
+    Listing list;
 };
 
-// Sums over the rows of one adapter: 16 RC ranks by 64 columns per block.  The block lists
-// the adapter's rows, 2048 rows at a time, in order; its waves take 32 of the list in turn,
-// the next ones on their way while these are multiplied, and add up in the order of the waves.
+// Sums over the rows of one adapter: 16 RC ranks by 64 columns per block.  The adapter's rows
+// are its part of the list, or listed here, 2048 rows at a time, in order; the waves take 32 of
+// them in turn, the next ones on their way while these are multiplied, and add up in the order
+// of the waves.
 constexpr int kOuterRows = 2048;
-template <int RC>
+template <int RC, bool LISTED>
 __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
 {
     constexpr int UW = 32 * RC, XB = 32 * 128, UB = 32 * UW * 2;          // ranks of a row (twice 16 RC), bytes of a step
     __shared__ __align__(128) uint8_t lds[4][XB + UB];
-    __shared__ uint16_t list[kOuterRows];
+    __shared__ uint16_t listed[LISTED ? 1 : kOuterRows];
     __shared__ int counts[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, kq = lane >> 4;
@@ -374,71 +847,47 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
     MmReader<UW, true, 2 * RC> ru;
     rx.begin(0, lane);
     ru.begin(0, lane);
-    int any = 0;
-    for (int seg = 0; seg < p.M; seg += kOuterRows) {
-        // this segment's rows of the adapter: eight ids per thread
-        uint32_t has = 0;
+    // n rows: row(i) of x, place(i) of u
+    auto sums = [&](int n, auto row, auto place) {
+        // 32 of them: where they are, a step ahead of them; columns and ranks in registers, zeros past the end
+        constexpr int DEEP = RC <= 2 ? 2 : 1;                  // steps of the wave on their way
+        constexpr int SEGS = UW / 8;                           // of a row of u: half for u, half for what it left
+        int at_row[4];
+        v4u32 xv[DEEP][4], uv[DEEP][2 * RC];
+        auto find = [&](int s) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int m = seg + 8 * tid + e;
-            if (m < p.M && p.ids[m] == a) has |= 1u << e;
-        }
-        int scan = __popc(has);
-        const int mine = scan;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(scan, o);
-            if (lane >= o) scan += v;
-        }
-        __syncthreads();                     // (the list and the counts of the segment before are read)
-        if (lane == 63) counts[wave] = scan;
-        __syncthreads();
-        int at = scan - mine, n = 0;
-        for (int w = 0; w < 4; w++) {
-            if (w < wave) at += counts[w];
-            n += counts[w];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (has >> e & 1) list[at++] = (uint16_t)(8 * tid + e);
-        __syncthreads();
-        any |= n;
-        // 32 rows of the list: columns and ranks into registers, zeros past its end
-        v4u32 xv[4], uv[2 * RC];
-        auto load = [&](int s) {
+            for (int q = 0; q < 4; q++) at_row[q] = 32 * s + 8 * q + (lane >> 3) < n ? row(32 * s + 8 * q + (lane >> 3)) : -1;
+        };
+        auto load = [&](int s, v4u32 (&x)[4], v4u32 (&u)[2 * RC]) {
 #pragma unroll
             for (int q = 0; q < 4; q++) {
-                const int i = 32 * s + 8 * q + (lane >> 3), c = c0 + 8 * (lane & 7);
-                xv[q] = v4u32{0u, 0u, 0u, 0u};
-                if (i < n && c < job.N) xv[q] = load8(job.x + (int64_t)(seg + list[i]) * job.ldx, c, job.N);
+                const int c = c0 + 8 * (lane & 7);
+                x[q] = v4u32{0u, 0u, 0u, 0u};
+                if (at_row[q] >= 0 && c < job.N) x[q] = load8(job.x + (int64_t)at_row[q] * job.ldx, c, job.N);
             }
 #pragma unroll
             for (int q = 0; q < 2 * RC; q++) {
-                constexpr int SEGS = UW / 8;                       // of a row: half for u, half for what it left
                 const int at = q * 64 + lane, i = 32 * s + at / SEGS, sg = at % SEGS;
                 const int j = j0 + (sg % (SEGS / 2)) * 8;
-                uv[q] = v4u32{0u, 0u, 0u, 0u};
+                u[q] = v4u32{0u, 0u, 0u, 0u};
                 if (i < n && j < p.rp)
-                    uv[q] = *reinterpret_cast<const v4u32*>(job.u + (int64_t)(seg + list[i]) * 2 * p.rp +
-                                                            (sg / (SEGS / 2)) * p.rp + j);
+                    u[q] = *reinterpret_cast<const v4u32*>(job.u + ((int64_t)place(i) * 2 + sg / (SEGS / 2)) * p.rp + j);
             }
         };
-        const int steps = (n + 31) / 32;
-        if (wave < steps) load(wave);
-        for (int s = wave; s < steps; s += 4) {
+        auto step = [&](int s, v4u32 (&x)[4], v4u32 (&u)[2 * RC]) {
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int q = 0; q < 4; q++) {
                 const int i = 8 * q + (lane >> 3);
-                *reinterpret_cast<v4u32*>(xs + i * 128 + ((lane & 7) ^ (2 * column_swizzle<64>(i))) * 16) = xv[q];
+                *reinterpret_cast<v4u32*>(xs + i * 128 + ((lane & 7) ^ (2 * column_swizzle<64>(i))) * 16) = x[q];
             }
 #pragma unroll
             for (int q = 0; q < 2 * RC; q++) {
-                constexpr int SEGS = UW / 8;
                 const int at = q * 64 + lane, i = at / SEGS;
-                *reinterpret_cast<v4u32*>(us + i * UW * 2 + ((at % SEGS) ^ (2 * column_swizzle<UW>(i))) * 16) = uv[q];
+                *reinterpret_cast<v4u32*>(us + i * UW * 2 + ((at % SEGS) ^ (2 * column_swizzle<UW>(i))) * 16) = u[q];
             }
-            if (s + 4 < steps) load(s + 4);
+            load(s + 4 * DEEP, x, u);
+            find(s + 4 * DEEP + 4);
             __builtin_amdgcn_wave_barrier();
             v8bf xf[4];
 #pragma unroll
@@ -450,11 +899,62 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
                 for (int t = 0; t < 4; t++)
                     acc[c % RC][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[t], uf, acc[c % RC][t], 0, 0, 0);
             }
+        };
+        // (steps past the end load zeros)
+        const int steps = (n + 31) / 32;
+        if (wave >= steps) return;
+#pragma unroll
+        for (int d = 0; d < DEEP; d++) {
+            find(wave + 4 * d);
+            load(wave + 4 * d, xv[d], uv[d]);
+        }
+        find(wave + 4 * DEEP);
+        for (int s = wave; s < steps; s += 4 * DEEP)
+#pragma unroll
+            for (int d = 0; d < DEEP; d++) step(s + 4 * d, xv[d], uv[d]);
+    };
+    int any = 0;
+    if constexpr (LISTED) {
+        const int begin = p.list.begin[a];
+        any = p.list.begin[a + 1] - begin;
+        const int* order = p.list.order + begin;
+        sums(any, [&](int i) { return order[i]; }, [&](int i) { return begin + i; });
+    } else {
+        for (int seg = 0; seg < p.M; seg += kOuterRows) {
+            // this segment's rows of the adapter: eight ids per thread
+            uint32_t has = 0;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int m = seg + 8 * tid + e;
+                if (m < p.M && p.ids[m] == a) has |= 1u << e;
+            }
+            int scan = __popc(has);
+            const int mine = scan;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(scan, o);
+                if (lane >= o) scan += v;
+            }
+            __syncthreads();                     // (the list and the counts of the segment before are read)
+            if (lane == 63) counts[wave] = scan;
+            __syncthreads();
+            int at = scan - mine, n = 0;
+            for (int w = 0; w < 4; w++) {
+                if (w < wave) at += counts[w];
+                n += counts[w];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                if (has >> e & 1) listed[at++] = (uint16_t)(8 * tid + e);
+            __syncthreads();
+            any |= n;
+            auto row = [&](int i) { return seg + listed[i]; };
+            sums(n, row, row);
         }
     }
     if (any == 0 && p.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
     // lane: rank 16 c + r16, columns 16 t + 4 kq .. + 3
-    float* sums = reinterpret_cast<float*>(lds);
+    float* total = reinterpret_cast<float*>(lds);
     static_assert(sizeof(lds) >= 16 * RC * 64 * 4, "the sums fit");
     for (int w = 0; w < 4; w++) {
         __syncthreads();
@@ -463,7 +963,7 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
             for (int c = 0; c < RC; c++)
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    float4* to = reinterpret_cast<float4*>(sums + (16 * c + r16) * 64 + 16 * t + 4 * kq);
+                    float4* to = reinterpret_cast<float4*>(total + (16 * c + r16) * 64 + 16 * t + 4 * kq);
                     float4 v = make_float4(acc[c][t][0], acc[c][t][1], acc[c][t][2], acc[c][t][3]);
                     if (w > 0) {
                         const float4 b = *to;
@@ -480,52 +980,92 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
         const int64_t to = ((int64_t)a * p.r + j) * job.N + c;
         if (job.bf16) {
             uint16_t* d = static_cast<uint16_t*>(job.d) + to;
-            *d = (uint16_t)bf16x2(p.accumulate ? bf16_to_f32(*d) + sums[i] : sums[i], 0.0f);
+            *d = (uint16_t)bf16x2(p.accumulate ? bf16_to_f32(*d) + total[i] : total[i], 0.0f);
         } else {
             float* d = static_cast<float*>(job.d) + to;
-            *d = p.accumulate ? *d + sums[i] : sums[i];
+            *d = p.accumulate ? *d + total[i] : total[i];
         }
     }
 }
 
 // ---- host ----
-template <int MI, int NJ, int NW>
-hipError_t launch_shrink(const ShrinkArgs& p, int jobs, int slots, hipStream_t s)
+// Whether the rows are listed first: from a few hundred on the tiles' gain outweighs the launch (see k_lora_list).
+bool listed_first(int M, int L) { return M > 256 && L <= kListAdapters; }
+int64_t most_tiles(int64_t M, int64_t L) { return M / kTile + std::min<int64_t>(M, L + 1); }
+
+hipError_t run_list(int M, int L, const int32_t* ids, const Listing& list, hipStream_t s)
 {
     static LdsAllowed allowed;
-    const auto kernel = k_lora_shrink<MI, NJ, NW>;
-    constexpr int BYTES = NW * 16 * MI * (16 * NJ + 4) * 4;
-    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), BYTES, allowed); e != hipSuccess) return e;
-    const int chunks = (int)over(p.r, 16 * NJ);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)over(p.M, 16 * MI), (unsigned)slots, (unsigned)(chunks * jobs)), dim3(64 * NW),
-                       BYTES, s, p, chunks);
+    const auto kernel = k_lora_list;
+    const int bytes = (16 + 2) * (kListAdapters + 1) * 4;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), bytes, allowed); e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), (16 + 2) * (L + 1) * 4, s, M, L, ids, list, (int)most_tiles(M, L));
     return hipGetLastError();
 }
-// Blocks for a tile's adapters: one where there are tiles enough, up to one each where there are few.
-int slots_of(int64_t blocks, int rows) { return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 1024 / blocks)); }
+
+template <int NJ, bool LISTED>
+hipError_t launch_shrink(const ShrinkArgs& p, int jobs, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_lora_shrink<NJ, LISTED>;
+    constexpr int BYTES = shrink_bytes<NJ>();
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), BYTES, allowed); e != hipSuccess) return e;
+    const int chunks = (int)over(p.r, 16 * NJ);
+    const int64_t tiles = LISTED ? most_tiles(p.M, p.L) : over(p.M, 16);
+    // a block for each adapter that a tile's rows may have, where there are few tiles
+    const int slots = LISTED ? kTile / 16 : (int)std::max<int64_t>(1, std::min<int64_t>(16, 1024 / tiles));
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles, (unsigned)slots, (unsigned)(chunks * jobs)), dim3(64 * kShrinkWaves), BYTES,
+                       s, p, chunks);
+    return hipGetLastError();
+}
+template <bool LISTED>
+hipError_t shrink_by_rank(const ShrinkArgs& p, int jobs, hipStream_t s)
+{
+    if (p.r <= 16) return launch_shrink<1, LISTED>(p, jobs, s);
+    if (p.r <= 32) return launch_shrink<2, LISTED>(p, jobs, s);
+    return launch_shrink<4, LISTED>(p, jobs, s);
+}
+template <int NI, int NS>
+hipError_t launch_ring(const ShrinkArgs& p, int jobs, hipStream_t s)
+{
+    static LdsAllowed allowed;
+    const auto kernel = k_lora_shrink_ring<NI, NS>;
+    using R = ShrinkRing<NI, NS>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), R::BYTES, allowed); e != hipSuccess) return e;
+    const int chunks = (int)over(p.r, 16 * NI);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)most_tiles(p.M, p.L), 1, (unsigned)(chunks * jobs)), dim3(64 * kSums), R::BYTES, s,
+                       p, chunks);
+    return hipGetLastError();
+}
 hipError_t run_shrink(const ShrinkArgs& p, int jobs, hipStream_t s)
 {
-    if (p.M <= 2048) {
-        const int slots = slots_of(over(p.M, 16), 16);
-        if (p.r <= 16) return launch_shrink<1, 1, 16>(p, jobs, slots, s);
-        if (p.r <= 32) return launch_shrink<1, 2, 16>(p, jobs, slots, s);
-        return launch_shrink<1, 4, 16>(p, jobs, slots, s);
-    }
-    const int slots = slots_of(over(p.M, 32), 32);
-    if (p.r <= 16) return launch_shrink<2, 1, 8>(p, jobs, slots, s);
-    if (p.r <= 32) return launch_shrink<2, 2, 8>(p, jobs, slots, s);
-    return launch_shrink<2, 4, 8>(p, jobs, slots, s);
+    if (!listed_first(p.M, p.L)) return shrink_by_rank<false>(p, jobs, s);
+    for (int j = 0; j < jobs; j++)
+        if (!in_place(p.job[j].x, p.job[j].K, p.job[j].ldx) || !aligned_to(p.job[j].f, 16)) return shrink_by_rank<true>(p, jobs, s);
+    if (p.r <= 16) return launch_ring<1, 4>(p, jobs, s);
+    if (p.r <= 32) return launch_ring<2, 3>(p, jobs, s);
+    return launch_ring<4, 2>(p, jobs, s);
 }
 
 template <int RC>
-hipError_t launch_expand(ExpandArgs p, int bf16, hipStream_t s)
+hipError_t launch_expand(const ExpandArgs& p, int bf16, hipStream_t s)
 {
-    const int64_t columns = over(p.N, 256), rows = over(p.M, 16);
-    const int64_t waves = columns * 4 * rows;
-    // some 8192 waves at least: a few tiles each where there are more, several for a tile's adapters where there are fewer
-    p.tiles = (int)std::max<int64_t>(over(rows, 65535), std::min<int64_t>(4, std::max<int64_t>(1, waves / 8192)));
-    const int slots = (int)std::max<int64_t>(1, std::min<int64_t>(16, 8192 / waves));
-    const dim3 grid((unsigned)columns, (unsigned)over(rows, p.tiles), (unsigned)slots);
+    if (listed_first(p.M, p.L)) {
+        const int64_t blocks = over(p.N, 256) * most_tiles(p.M, p.L);
+        if (blocks > INT32_MAX) return hipErrorInvalidValue;
+        auto run = [&](auto one) {
+            constexpr bool ONE = decltype(one)::value;
+            if (bf16) hipLaunchKernelGGL((k_lora_expand_tile<RC, uint16_t, ONE>), dim3((unsigned)blocks), dim3(256), 0, s, p);
+            else hipLaunchKernelGGL((k_lora_expand_tile<RC, float, ONE>), dim3((unsigned)blocks), dim3(256), 0, s, p);
+        };
+        if (RC < 4 || p.r <= 64) run(std::true_type{});
+        else if constexpr (RC == 4) run(std::false_type{});
+        return hipGetLastError();
+    }
+    const int64_t blocks = over(p.N, 256) * over(p.M, 16);
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    // (a wave for each adapter that a tile's rows may have, where there are few tiles)
+    const dim3 grid((unsigned)blocks, (unsigned)std::max<int64_t>(1, std::min<int64_t>(16, 2048 / blocks)));
     if (bf16) hipLaunchKernelGGL((k_lora_expand<RC, uint16_t>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((k_lora_expand<RC, float>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
@@ -537,22 +1077,42 @@ hipError_t run_expand(const ExpandArgs& p, int bf16, hipStream_t s)
     return launch_expand<4>(p, bf16, s);
 }
 
-template <int RC>
+template <int RC, bool LISTED>
 hipError_t launch_outer(const OuterArgs& p, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_lora_outer<RC>, dim3((unsigned)(p.job[0].blocks + p.job[1].blocks), (unsigned)p.L,
-                                              (unsigned)over(p.r, 16 * RC)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_lora_outer<RC, LISTED>), dim3((unsigned)(p.job[0].blocks + p.job[1].blocks), (unsigned)p.L,
+                                                        (unsigned)over(p.r, 16 * RC)), dim3(256), 0, s, p);
     return hipGetLastError();
+}
+template <bool LISTED>
+hipError_t outer_by_rank(const OuterArgs& p, hipStream_t s)
+{
+    if (p.r <= 16) return launch_outer<1, LISTED>(p, s);
+    if (p.r <= 32) return launch_outer<2, LISTED>(p, s);
+    return launch_outer<4, LISTED>(p, s);
 }
 hipError_t run_outer(const OuterArgs& p, hipStream_t s)
 {
-    if (p.r <= 16) return launch_outer<1>(p, s);
-    if (p.r <= 32) return launch_outer<2>(p, s);
-    return launch_outer<4>(p, s);
+    return listed_first(p.M, p.L) ? outer_by_rank<true>(p, s) : outer_by_rank<false>(p, s);
 }
 
 int ranks(int r) { return (r + 15) / 16 * 16; }
 size_t lora_u(int64_t M, int r) { return up256((size_t)(M * 2 * ranks(r) * 2)); }
+size_t lora_list(int M, int L)
+{
+    if (!listed_first(M, L)) return 0;
+    return up256((size_t)M * 4) + up256((size_t)(L + 2) * 4) + 256 + up256((size_t)most_tiles(M, L) * sizeof(Tile));
+}
+Listing listing(uint8_t* ws, int M, int L)
+{
+    if (!listed_first(M, L)) return Listing{};
+    Listing l;
+    l.order = reinterpret_cast<int*>(ws);
+    l.begin = reinterpret_cast<int*>(ws += up256((size_t)M * 4));
+    l.tiles_n = reinterpret_cast<int*>(ws += up256((size_t)(L + 2) * 4));
+    l.tiles = reinterpret_cast<Tile*>(ws += 256);
+    return l;
+}
 
 int check_lora(const v4moe_lora* p)
 {
@@ -579,7 +1139,7 @@ extern "C" {
 __attribute__((visibility("default"))) size_t moe_lora_workspace_bytes(const v4moe_lora* p, int32_t backward)
 {
     if (check_lora(p)) return 0;
-    return lora_u(p->M, p->r) * (backward ? 2 : 1);
+    return lora_list(p->M, p->L) + lora_u(p->M, p->r) * (backward ? 2 : 1);
 }
 
 __attribute__((visibility("default"))) int moe_lora_add(const v4moe_lora* p, const void* y, int32_t type, int64_t ldy,
@@ -597,14 +1157,17 @@ __attribute__((visibility("default"))) int moe_lora_add(const v4moe_lora* p, con
     if (p->M == 0) return V4MOE_OK;
     if (!workspace) return V4MOE_ENULL;
     if (!aligned_to(workspace, 16)) return V4MOE_EALIGN;
-    if (ws_bytes < lora_u(p->M, p->r)) return V4MOE_EWORKSPACE;
+    if (ws_bytes < moe_lora_workspace_bytes(p, 0)) return V4MOE_EWORKSPACE;
     if (!device_ready()) return V4MOE_EDEVICE;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    uint16_t* u = static_cast<uint16_t*>(workspace);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Listing list = listing(ws, p->M, p->L);
+    if (list.order && run_list(p->M, p->L, ids, list, s) != hipSuccess) return V4MOE_ELAUNCH;
+    uint16_t* u = reinterpret_cast<uint16_t*>(ws + lora_list(p->M, p->L));
     const int rp = ranks(p->r);
-    const ShrinkArgs sh{p->M, p->L, p->r, rp, ids, scale, {{x, ldx, p->K, a, u}, {}}};
+    const ShrinkArgs sh{p->M, p->L, p->r, rp, ids, scale, {{x, ldx, p->K, a, u}, {}}, list};
     if (run_shrink(sh, 1, s) != hipSuccess) return V4MOE_ELAUNCH;
-    const ExpandArgs ex{p->M, p->N, p->L, p->r, rp, ids, u, b, y, ldy, out, ldo, 1, out == y};
+    const ExpandArgs ex{p->M, p->N, p->L, p->r, rp, ids, u, b, y, ldy, out, ldo, out == y, list};
     return run_expand(ex, type == V4MOE_TYPE_BF16, s) == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }
 
@@ -633,26 +1196,29 @@ __attribute__((visibility("default"))) int moe_lora_backward(
     if (p->M == 0 && ((!da && !db) || accumulate)) return V4MOE_OK;
     if (p->M > 0 && !workspace) return V4MOE_ENULL;
     if (!aligned_to(workspace, 16)) return V4MOE_EALIGN;
-    const size_t each = lora_u(p->M, p->r);
-    if (ws_bytes < 2 * each) return V4MOE_EWORKSPACE;
+    if (ws_bytes < moe_lora_workspace_bytes(p, 1)) return V4MOE_EWORKSPACE;
     if (!device_ready()) return V4MOE_EDEVICE;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    uint16_t* du = static_cast<uint16_t*>(workspace);
-    uint16_t* u = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + each);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Listing list = listing(ws, p->M, p->L);
+    if (list.order && run_list(p->M, p->L, ids, list, s) != hipSuccess) return V4MOE_ELAUNCH;
+    ws += lora_list(p->M, p->L);
+    uint16_t* du = reinterpret_cast<uint16_t*>(ws);
+    uint16_t* u = reinterpret_cast<uint16_t*>(ws + lora_u(p->M, p->r));
     const int rp = ranks(p->r);
     if (p->M > 0) {
-        ShrinkArgs sh{p->M, p->L, p->r, rp, ids, scale, {}};
+        ShrinkArgs sh{p->M, p->L, p->r, rp, ids, scale, {}, list};
         int jobs = 0;
         if (dx || da) sh.job[jobs++] = ShrinkJob{dy, lddy, p->N, b, du};
         if (db) sh.job[jobs++] = ShrinkJob{x, ldx, p->K, a, u};
         if (run_shrink(sh, jobs, s) != hipSuccess) return V4MOE_ELAUNCH;
     }
     if (dx && p->M > 0) {
-        const ExpandArgs ex{p->M, p->K, p->L, p->r, rp, ids, du, a, base, ldbase, dx, lddx, 1, base == dx};
+        const ExpandArgs ex{p->M, p->K, p->L, p->r, rp, ids, du, a, base, ldbase, dx, lddx, base == dx, list};
         if (run_expand(ex, dx_type == V4MOE_TYPE_BF16, s) != hipSuccess) return V4MOE_ELAUNCH;
     }
     if (da || db) {
-        OuterArgs o{p->M, p->L, p->r, rp, accumulate != 0, ids, {}};
+        OuterArgs o{p->M, p->L, p->r, rp, accumulate != 0, ids, {}, list};
         int jobs = 0;
         if (da) o.job[jobs++] = OuterJob{du, x, ldx, p->K, da, da_type == V4MOE_TYPE_BF16, (int)over(p->K, 64)};
         if (db) o.job[jobs++] = OuterJob{u, dy, lddy, p->N, db, db_type == V4MOE_TYPE_BF16, (int)over(p->N, 64)};
