@@ -126,23 +126,30 @@ __global__ __launch_bounds__(L::THREADS) void k_grouped_weights(GroupedArgs g, i
 
 // Rows of 2-byte elements, src [R][C] -> dst [R][C8] (C8 = C rounded up to 8), zeros past C: what the
 // copies of mm_tile need of operands whose rows do not begin or end at 16 bytes.
-__global__ __launch_bounds__(256) void k_pad_rows(int64_t R, int C, const uint16_t* __restrict__ src, int64_t lds_,
-                                                  uint16_t* __restrict__ dst, int C8)
+// Up to three matrices in a launch, their blocks one after the other.
+struct PadJobs {
+    PadRows job[3];
+    int blocks[3];
+};
+__global__ __launch_bounds__(256) void k_pad_rows(PadJobs p)
 {
-    const int segs = C8 / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < R * segs; i += (int64_t)gridDim.x * 256) {
+    int block = blockIdx.x, j = 0;
+    while (j < 2 && block >= p.blocks[j]) block -= p.blocks[j++];
+    const PadRows& g = p.job[j];
+    const int C8 = (g.C + 7) / 8 * 8, segs = C8 / 8;
+    for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < g.R * segs; i += (int64_t)p.blocks[j] * 256) {
         const int64_t r = i / segs;
         const int c = (int)(i - r * segs) * 8;
-        const uint16_t* s = src + r * lds_ + c;
+        const uint16_t* s = g.src + r * g.ld + c;
         v4u32 v;
-        if (c + 8 <= C) {
+        if (c + 8 <= g.C) {
             v = *reinterpret_cast<const v4u32_any*>(s);
         } else {
 #pragma unroll
             for (int u = 0; u < 4; u++)
-                v[u] = (c + 2 * u < C ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < C ? (uint32_t)s[2 * u + 1] << 16 : 0u);
+                v[u] = (c + 2 * u < g.C ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < g.C ? (uint32_t)s[2 * u + 1] << 16 : 0u);
         }
-        *reinterpret_cast<v4u32*>(dst + r * C8 + c) = v;
+        *reinterpret_cast<v4u32*>(g.dst + r * C8 + c) = v;
     }
 }
 
@@ -170,21 +177,32 @@ hipError_t launch_weights(const GroupedArgs& g, hipStream_t s)
     return hipGetLastError();
 }
 
-// Rows of an expert on average choose the tile.
+// Row tiles are estimated: the offsets are the device's.  Every expert's last one is half empty on average, and an
+// expert with rows has one at least.
 template <bool BCOL>
 hipError_t run_rows(const GroupedArgs& g, hipStream_t s)
 {
-    const int64_t mean = over(g.M, g.E);
-    if (mean <= 16) return launch_rows<MmTile<1, 4, 1, 1, 4, false, BCOL>>(g, s);
-    if (mean <= 32) return launch_rows<MmTile<2, 2, 1, 2, 4, false, BCOL>>(g, s);
-    if (mean <= 64) return launch_rows<MmTile<2, 2, 2, 2, 3, false, BCOL>>(g, s);
-    if (mean <= 128) return launch_rows<MmTile<2, 2, 4, 4, 2, false, BCOL>>(g, s);
-    return launch_rows<MmTile<2, 4, 8, 4, 2, false, BCOL>>(g, s);
+    const int64_t groups = g.M < g.E ? g.M : g.E;
+    const int v = mm_choose(0, g.K, [&](int64_t bm, int64_t bn) {
+        const int64_t tm = g.M / bm + (groups + 1) / 2;
+        return (tm > groups ? tm : groups) * over(g.N, bn);
+    });
+    switch (v) {
+    case 0: return launch_rows<MmTile<1, 4, 1, 1, 4, false, BCOL>>(g, s);
+    case 1: return launch_rows<MmTile<2, 2, 1, 2, 4, false, BCOL>>(g, s);
+    case 2: return launch_rows<MmTile<2, 2, 2, 2, 3, false, BCOL>>(g, s);
+    case 3: return launch_rows<MmTile<2, 2, 4, 4, 2, false, BCOL, true>>(g, s);
+    default: return launch_rows<MmTile<2, 4, 8, 4, 2, false, BCOL, true>>(g, s);
+    }
 }
 hipError_t run_weights(const GroupedArgs& g, hipStream_t s)
 {
-    if (g.E * over(g.c.M, 256) * over(g.N, 256) >= 256) return launch_weights<MmTile<2, 4, 8, 4, 2, true, true>>(g, s);
-    return launch_weights<MmTile<2, 2, 4, 4, 2, true, true>>(g, s);
+    const int v = mm_choose(2, g.M / g.E, [&](int64_t bm, int64_t bn) { return g.E * over(g.c.M, bm) * over(g.N, bn); });
+    switch (v) {
+    case 2: return launch_weights<MmTile<2, 2, 2, 2, 3, true, true>>(g, s);
+    case 3: return launch_weights<MmTile<2, 2, 4, 4, 2, true, true>>(g, s);
+    default: return launch_weights<MmTile<2, 4, 8, 4, 2, true, true>>(g, s);
+    }
 }
 
 struct GroupedLayout {
@@ -230,26 +248,35 @@ int grouped_operands(GroupedCall& o, int32_t M, int32_t E, int32_t N, int32_t K,
     if (ws_bytes < L.total) return V4MOE_EWORKSPACE;
     if (!device_ready()) return V4MOE_EDEVICE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PadRows jobs[3];
+    int n = 0;
     auto pad = [&](const uint16_t*& p, int64_t& ld, int64_t rows, int cols, size_t at) {
-        if (launch_pad_rows(rows, cols, p, ld, ws + at, s) != hipSuccess) return false;
-        p = reinterpret_cast<const uint16_t*>(ws + at);
+        uint16_t* to = reinterpret_cast<uint16_t*>(ws + at);
+        jobs[n++] = PadRows{rows, cols, p, ld, to};
+        p = to;
         ld = up8(cols);
-        return true;
     };
-    if (L.pad_x && need_x && !pad(o.x, o.ldx, M, K, L.x)) return V4MOE_ELAUNCH;
-    if (L.pad_dy && !pad(o.dy, o.lddy, M, N, L.dy)) return V4MOE_ELAUNCH;
-    if (L.pad_w && need_w && !pad(o.w, o.ldw, (int64_t)E * N, K, L.w)) return V4MOE_ELAUNCH;
+    if (L.pad_x && need_x) pad(o.x, o.ldx, M, K, L.x);
+    if (L.pad_dy) pad(o.dy, o.lddy, M, N, L.dy);
+    if (L.pad_w && need_w) pad(o.w, o.ldw, (int64_t)E * N, K, L.w);
+    if (launch_pad_rows(jobs, n, s) != hipSuccess) return V4MOE_ELAUNCH;
     return V4MOE_OK;
 }
 
 }  // namespace
 
-hipError_t launch_pad_rows(int64_t R, int C, const void* src, int64_t ld, void* dst, hipStream_t s)
+hipError_t launch_pad_rows(const PadRows* jobs, int n, hipStream_t s)
 {
-    if (R == 0) return hipSuccess;
-    const int64_t blocks = over(R * (up8(C) / 8), 256);
-    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, s, R, C,
-                       static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), (int)up8(C));
+    PadJobs p{};
+    int all = 0;
+    for (int j = 0; j < n; j++) {
+        p.job[j] = jobs[j];
+        const int64_t blocks = over(jobs[j].R * (up8(jobs[j].C) / 8), 256);
+        p.blocks[j] = (int)(blocks < 16384 ? blocks : 16384);
+        all += p.blocks[j];
+    }
+    if (all == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)all), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

@@ -43,9 +43,15 @@ struct MmOperand {
     int n;
 };
 
-// WM x WN waves, each MI x NI tiles of 16x16; NS stages of 64 k in LDS.
-template <int WM_, int WN_, int MI_, int NI_, int NS_, bool ACOL_, bool BCOL_>
+// WM x WN waves, each MI x NI tiles of 16x16; NS stages of 64 k in LDS.  RAGGED: many tiles end before BM rows (the
+// last one of each group).  The row tiles are then dealt to the wave rows in turn, and those past A's end cost no
+// products, so that such a tile's waves end together and early (32768 rows of 128 experts, uneven: 1457 -> 1345 us);
+// whole tiles pay 2.5% for it.
+template <int WM_, int WN_, int MI_, int NI_, int NS_, bool ACOL_, bool BCOL_, bool RAGGED_ = false>
 struct MmTile {
+    static constexpr bool RAGGED = RAGGED_;
+    static constexpr int STEP = RAGGED_ ? WM_ : 1;                          // of a wave's row tiles
+    static __host__ __device__ constexpr int first_row(int wm) { return wm * (RAGGED_ ? 1 : MI_) * 16; }
     static constexpr int WM = WM_, WN = WN_, MI = MI_, NI = NI_, NS = NS_;
     static constexpr bool ACOL = ACOL_, BCOL = BCOL_;
     static constexpr int NW = WM * WN, THREADS = 64 * NW, BM = WM * MI * 16, BN = WN * NI * 16;
@@ -71,6 +77,14 @@ __device__ __forceinline__ int column_swizzle(int k)
     if constexpr (W >= 128) return (k & 3) | ((k >> 1) & 4);
     else if constexpr (W == 64) return ((k >> 1) & 1) | ((k >> 2) & 2);
     else return (k >> 3) & 1;
+}
+
+// The same pointer, in scalar registers.
+__device__ __forceinline__ const uint8_t* mm_uniform(const uint8_t* p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
 }
 
 // One operand of a tile, its first index i0: copies into LDS and reads of fragments.
@@ -109,10 +123,13 @@ struct MmSide {
         if constexpr (COL) return ((p * 64 + lane) % SEGS) ^ (2 * column_swizzle<W>(row_of(p)));
         else return (lane & 7) ^ ((row_of(p) >> 1) & 7);
     }
-    // this wave's copy j of a chunk into a stage
+    // this wave's copy j of a chunk into a stage (UNIFORM: c is in vector registers)
+    template <bool UNIFORM>
     __device__ __forceinline__ void copy(int j, int c, uint32_t to) const
     {
-        dma16s(base + (int64_t)c * step, off[j], __builtin_amdgcn_readfirstlane(to + piece(j) * 1024));
+        const uint8_t* from = base + (int64_t)c * step;
+        if constexpr (UNIFORM) from = mm_uniform(from);
+        dma16s(from, off[j], __builtin_amdgcn_readfirstlane(to + piece(j) * 1024));
     }
     // ... of the last chunk, of which `left` k are the contraction's: zeros past them
     __device__ __forceinline__ void copy_tail(int j, int c, uint32_t to, int left) const
@@ -124,9 +141,9 @@ struct MmSide {
     }
 };
 
-// A lane's reads of the fragments of T tiles from `first` on: fragment s (0, 1) of tile t
-// holds index 16 (first + t) + lane % 16 and k = 32 s + 8 (lane / 16) .. + 7.
-template <int W, bool COL, int T>
+// A lane's reads of the fragments of T tiles, `first` and every STEP-th further: fragment s (0, 1) of tile t
+// holds index 16 (first + STEP t) + lane % 16 and k = 32 s + 8 (lane / 16) .. + 7.
+template <int W, bool COL, int T, int STEP = 1>
 struct MmReader {
     int at[COL ? T : 2];
     // columns, from k0 of the lane's own on (rows of k that its swizzle depends on: k0 + 0 .. 3, and 4 further)
@@ -134,7 +151,7 @@ struct MmReader {
     {
         const int i = lane & 15, k = k0 + (i >> 2), f = column_swizzle<W>(k);
 #pragma unroll
-        for (int t = 0; t < T; t++) at[t] = k * W * 2 + ((first + t) ^ f) * 32 + (i & 3) * 8;
+        for (int t = 0; t < T; t++) at[t] = k * W * 2 + ((first + STEP * t) ^ f) * 32 + (i & 3) * 8;
     }
     __device__ __forceinline__ void begin(int first, int lane)
     {
@@ -150,7 +167,7 @@ struct MmReader {
     __device__ __forceinline__ v8bf read(const uint8_t* stage, int t, int s) const
     {
         if constexpr (COL) return read_at(stage, t, 32 * s);
-        else return *reinterpret_cast<const v8bf*>(stage + at[s] + t * 2048);
+        else return *reinterpret_cast<const v8bf*>(stage + at[s] + t * STEP * 2048);
     }
     // columns: of eight k from k1 further on, a multiple of 16 (where the swizzle is the same, as it is 4 further on)
     __device__ __forceinline__ v8bf read_at(const uint8_t* stage, int t, int k1) const
@@ -164,7 +181,7 @@ struct MmReader {
 };
 
 // The sums of a block's tile from (m0, n0): acc[i][j] of a wave (wm, wn) holds, in lane l,
-// row m0 + 16 (wm MI + i) + l % 16 and columns n0 + 16 (wn NI + j) + 4 (l / 16) .. + 3.
+// row m0 + first_row(wm) + 16 STEP i + l % 16 and columns n0 + 16 (wn NI + j) + 4 (l / 16) .. + 3.
 // B is the instruction's first operand, so that a lane has consecutive columns.  The
 // block's LDS (L::BYTES) is free when it returns.
 template <class L>
@@ -185,8 +202,8 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
         const uint32_t slot = lds0 + (uint32_t)(c % L::NS) * L::STAGE;
 #pragma unroll
         for (int q = q0; q < min(q0 + n, L::OPS); q++) {
-            if (q < L::AJ) sa.copy(q, c, slot);
-            else sb.copy(q - L::AJ, c, slot + L::B_OFF);
+            if (q < L::AJ) sa.template copy<L::RAGGED>(q, c, slot);
+            else sb.template copy<L::RAGGED>(q - L::AJ, c, slot + L::B_OFF);
         }
     };
     // all of them of any chunk
@@ -199,9 +216,9 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
             else sb.copy_tail(q - L::AJ, c, slot + L::B_OFF, K - c * 64);
         }
     };
-    MmReader<L::BM, L::ACOL, L::MI> ra;
+    MmReader<L::BM, L::ACOL, L::MI, L::STEP> ra;
     MmReader<L::BN, L::BCOL, L::NI> rb;
-    ra.begin(wm * L::MI, lane);
+    ra.begin(L::first_row(wm) / 16, lane);
     rb.begin(wn * L::NI, lane);
 #pragma unroll
     for (int i = 0; i < L::MI; i++)
@@ -241,6 +258,8 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
     // The copies of a large tile's next stage go out in groups, a row tile's products after each: all at once they
     // would hold up every wave's products until the memory path has taken them (8192x8192x8192 792 -> 752 us).
     constexpr int GROUPS = MI >= 4 ? MI / 2 : 1, PER = (L::OPS + GROUPS - 1) / GROUPS;
+    // row tiles of this wave with rows in them
+    const int live = __builtin_amdgcn_readfirstlane((min(a.n - m0, L::BM) - 16 * wm + 16 * L::WM - 1) / (16 * L::WM));
     if (nch > 0) open(0);
     for (int c = 0; c < nch; c++) {
         const uint8_t* st = smem + (c % L::NS) * L::STAGE;
@@ -248,8 +267,8 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
 #pragma unroll
         for (int i = 0; i < MI - 1; i++) {
             if (i + 1 < GROUPS && rest) copy(c - 1 + L::NS, PER * (i + 1), PER);
-            if (D < MI && i + D - 1 < MI) read_a(st, i + D - 1);
-            row(i);
+            if (D < MI && i + D - 1 < MI && (!L::RAGGED || i + D - 1 < live)) read_a(st, i + D - 1);
+            if (!L::RAGGED || i < live) row(i);
         }
         // Every operand of the chunk is in registers: the barrier frees its slot and makes the
         // next chunk whole (only later ones' copies are then out).
@@ -260,7 +279,7 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
             if (c + L::NS < full) copy(c + L::NS, 0, PER);
             else if (c + L::NS < nch) copy_all(c + L::NS);
         }
-        row(MI - 1);
+        if (!L::RAGGED || MI - 1 < live) row(MI - 1);
         if (c + 1 < nch) open(c + 1);
     }
     __syncthreads();
@@ -276,10 +295,10 @@ struct MmOut {
     int bf16, accumulate;    // accumulate: what c holds + the sum, in fp32, rounded once
 };
 
-// A wave's sums to C from (m0, n0), 16 rows at a time through LDS (two buffers of 16
-// rows): a lane's four columns become 16-byte stores along the rows.  Segments are
-// XOR-swizzled by the row.  S: the type staged, fp32 where C is added to.
-template <bool STREAM, int MI, int NI, typename S, typename T>
+// A wave's sums to C from (m0, n0), its row tiles STEP apart, 16 rows at a time through LDS
+// (two buffers of 16 rows): a lane's four columns become 16-byte stores along the rows.
+// Segments are XOR-swizzled by the row.  S: the type staged, fp32 where C is added to.
+template <bool STREAM, int STEP, int MI, int NI, typename S, typename T>
 __device__ __forceinline__ void mm_store(const v4f (&acc)[MI][NI], uint8_t* stage, const MmOut& o, int m0, int n0)
 {
     constexpr int ES = sizeof(S), RB = NI * 16 * ES, LR = RB / 16, PER = 16 / ES;
@@ -287,6 +306,7 @@ __device__ __forceinline__ void mm_store(const v4f (&acc)[MI][NI], uint8_t* stag
     const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
 #pragma unroll
     for (int i = 0; i < MI; i++) {
+        if (m0 + 16 * STEP * i >= o.M) break;
         uint8_t* buf = stage + (i & 1) * (16 * NI * 16 * 4);
 #pragma unroll
         for (int j = 0; j < NI; j++) {
@@ -304,7 +324,7 @@ __device__ __forceinline__ void mm_store(const v4f (&acc)[MI][NI], uint8_t* stag
             const int r = q + lane / LR, sg = lane % LR;
             if (r >= 16) continue;
             const uint4 v = *reinterpret_cast<const uint4*>(buf + r * RB + ((sg ^ (r & (LR - 1))) << 4));
-            const int m = m0 + 16 * i + r, n = n0 + sg * PER;
+            const int m = m0 + 16 * STEP * i + r, n = n0 + sg * PER;
             if (m >= o.M || n >= o.N) continue;
             T* c = static_cast<T*>(o.c) + (int64_t)m * o.ldc + n;
             if constexpr (sizeof(S) == sizeof(T)) {
@@ -351,10 +371,10 @@ __device__ __forceinline__ void mm_store_tile(const v4f (&acc)[L::MI][L::NI], ui
 {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     uint8_t* stage = smem + wave * L::C_BYTES;
-    const int mw = m0 + wave / L::WN * L::MI * 16, nw = n0 + wave % L::WN * L::NI * 16;
-    if (!o.bf16) mm_store<STREAM, L::MI, L::NI, float, float>(acc, stage, o, mw, nw);
-    else if (o.accumulate) mm_store<STREAM, L::MI, L::NI, float, uint16_t>(acc, stage, o, mw, nw);
-    else mm_store<STREAM, L::MI, L::NI, uint16_t, uint16_t>(acc, stage, o, mw, nw);
+    const int mw = m0 + L::first_row(wave / L::WN), nw = n0 + wave % L::WN * L::NI * 16;
+    if (!o.bf16) mm_store<STREAM, L::STEP, L::MI, L::NI, float, float>(acc, stage, o, mw, nw);
+    else if (o.accumulate) mm_store<STREAM, L::STEP, L::MI, L::NI, float, uint16_t>(acc, stage, o, mw, nw);
+    else mm_store<STREAM, L::STEP, L::MI, L::NI, uint16_t, uint16_t>(acc, stage, o, mw, nw);
 }
 
 // The tile of a block's turn.  Blocks go to the eight XCDs in turn: XCD x takes the x-th
@@ -405,8 +425,54 @@ inline int check_out(const void* p, int32_t type, int64_t R, int64_t C, int64_t 
 }
 
 // Rows of bf16, src [R][ld] -> dst [R][C8] (C8 = C rounded up to 8), zeros past C: for operands that cannot be read
-// in place.
-hipError_t launch_pad_rows(int64_t R, int C, const void* src, int64_t ld, void* dst, hipStream_t s);
+// in place.  Up to three of them in one launch.
+struct PadRows {
+    int64_t R;
+    int C;
+    const uint16_t* src; int64_t ld;
+    uint16_t* dst;
+};
+hipError_t launch_pad_rows(const PadRows* jobs, int n, hipStream_t s);
+
+// The tiles of a product.  A call takes the one of the least time in this table, by the rounds its tiles make (a
+// round is one tile per CU): microseconds for 1 to 4 rounds at contractions of 256 and of 4096, between and beyond
+// which times are nearly linear, in a graph of many calls (rows by rows; columns are within a few percent).
+//                        K = 256                       K = 4096
+//   16x64      4.2    4.7    5.4    5.9      15.1   18.8   26.9   33.5
+//   32x64      4.3    5.0    5.7    7.8      18.4   23.5   31.7   41.7
+//   64x64      4.9    5.9    6.9    9.6      23.6   32.0   43.9   55.2
+//   128x128    7.2    8.9   13.7   16.2      47.5   65.6  106.7  121.9
+//   256x256   15.3   32.6   41.0   59.9     107.7  206.0  300.5  394.1
+// (128x256 and 256x128 of eight waves, 9.8 to 32 and 66 to 237, lie between the last two and are never the least by more
+// than a few percent; 64x256 of four waves takes 51 / 73 / 115 / 136.)
+struct MmVariant {
+    int bm, bn;
+    float us256[4], us4096[4];
+};
+constexpr MmVariant kMmVariants[] = {{16, 64, {4.2f, 4.7f, 5.4f, 5.9f}, {15.1f, 18.8f, 26.9f, 33.5f}},
+                                     {32, 64, {4.3f, 5.0f, 5.7f, 7.8f}, {18.4f, 23.5f, 31.7f, 41.7f}},
+                                     {64, 64, {4.9f, 5.9f, 6.9f, 9.6f}, {23.6f, 32.0f, 43.9f, 55.2f}},
+                                     {128, 128, {7.2f, 8.9f, 13.7f, 16.2f}, {47.5f, 65.6f, 106.7f, 121.9f}},
+                                     {256, 256, {15.3f, 32.6f, 41.0f, 59.9f}, {107.7f, 206.0f, 300.5f, 394.1f}}};
+inline float mm_time(const MmVariant& v, int64_t tiles, int64_t K)
+{
+    const int64_t rounds = tiles < 1 ? 1 : (tiles + 255) / 256;
+    const int r = rounds < 4 ? (int)rounds - 1 : 3;
+    const float us = v.us256[r] + (v.us4096[r] - v.us256[r]) * (float)(K - 256) / 3840.0f;
+    return rounds <= 4 ? us : us * (float)rounds / 4.0f;
+}
+// first: the smallest variant that may be taken; tiles(bm, bn): of the product
+template <typename F>
+int mm_choose(int first, int64_t K, F&& tiles)
+{
+    int best = first;
+    float least = 0.0f;
+    for (int v = first; v < 5; v++) {
+        const float us = mm_time(kMmVariants[v], tiles(kMmVariants[v].bm, kMmVariants[v].bn), K);
+        if (v == first || us < least) best = v, least = us;
+    }
+    return best;
+}
 
 // Lets a kernel have more than 64 KiB of LDS, once per device (or again by host threads that come to it at once).
 using LdsAllowed = std::atomic<bool>[kMaxDevices];

@@ -157,26 +157,36 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
     mm_tile<L>(a, b, im * L::BM, in * L::BN, p.H, smem, acc);
     const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int mw = im * L::BM + wave / L::WN * L::MI * 16, nw = in * L::BN + wave % L::WN * L::NI * 16;
+    const int mw = im * L::BM + L::first_row(wave / L::WN), nw = in * L::BN + wave % L::WN * L::NI * 16;
     if constexpr (!GRAD) {
 #pragma unroll
         for (int i = 0; i < L::MI; i++) {
-            const int m = mw + 16 * i + r16;
+            const int m = mw + 16 * L::STEP * i + r16;
+            if (mw + 16 * L::STEP * i >= n) break;
             const int target = m < n ? p.y[m] - p.v0 - nw : -1;
 #pragma unroll
             for (int j0 = 0; j0 < L::NI; j0 += 4) {
                 const int n0 = nw + 16 * j0, y = target - 16 * j0;
                 if (n0 >= p.V) continue;
+                if (n0 + 64 > p.V) {                                   // the last group's end
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (n0 + 16 * j + 4 * kq + e >= p.V) acc[i][j0 + j][e] = -INFINITY;
+                }
+                if (__ballot((uint32_t)y < 64u)) {                     // a target of the 16 rows lies here
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (y == 16 * j + 4 * kq + e) p.zy[m] = acc[i][j0 + j][e];
+                }
                 float big = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const float z = n0 + 16 * j + 4 * kq + e < p.V ? acc[i][j0 + j][e] : -INFINITY;
-                        acc[i][j0 + j][e] = z;
-                        big = fmaxf(big, z);
-                        if (y == 16 * j + 4 * kq + e) p.zy[m] = z;
-                    }
+                    for (int e = 0; e < 4; e++) big = fmaxf(big, acc[i][j0 + j][e]);
                 big = fmaxf(big, __shfl_xor(big, 16));
                 big = fmaxf(big, __shfl_xor(big, 32));
                 const float off = big == -INFINITY ? 0.0f : big;
@@ -193,17 +203,32 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
     } else {
 #pragma unroll
         for (int i = 0; i < L::MI; i++) {
-            const int m = min(mw + 16 * i + r16, n - 1);
+            if (mw + 16 * L::STEP * i >= n) break;
+            const int m = min(mw + 16 * L::STEP * i + r16, n - 1);
             const int y = p.y[m] - p.v0 - nw;
             const float lse = p.lse[m], g = p.g[m];
+            // d without the target's 1, which is taken off where a target of the 16 rows lies here
+            const bool end = nw + 16 * L::NI > p.V, target = __ballot((uint32_t)y < 16u * L::NI) != 0;
 #pragma unroll
             for (int j = 0; j < L::NI; j++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int c = 16 * j + 4 * kq + e;
-                    const float d = g * (exp_(acc[i][j][e] - lse) - (y == c ? 1.0f : 0.0f));
-                    acc[i][j][e] = nw + c < p.V ? d : 0.0f;
-                }
+                for (int e = 0; e < 4; e++) acc[i][j][e] = exp_(acc[i][j][e] - lse);
+            if (target) {
+#pragma unroll
+                for (int j = 0; j < L::NI; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (y == 16 * j + 4 * kq + e) acc[i][j][e] -= 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < L::NI; j++) acc[i][j] *= g;
+            if (end) {
+#pragma unroll
+                for (int j = 0; j < L::NI; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (nw + 16 * j + 4 * kq + e >= p.V) acc[i][j][e] = 0.0f;
+            }
         }
         // (columns up to a multiple of 8: the products read whole segments)
         const MmOut o{p.d, p.ldd, n, (p.V + 7) / 8 * 8, 1, 0};
@@ -252,14 +277,26 @@ __global__ __launch_bounds__(1024) void k_xent_join(int T, int P, const XentCtrl
 
 struct XentGradArgs {
     int T, H, H8, V;                    // V: columns of this piece
-    int slices, per;                    // of its contraction: `per` columns each
+    int piece;                          // columns of a whole piece
     const XentCtrl* ctrl;
     const uint16_t* x; const uint16_t* w; int64_t ldw;
     const uint16_t* d; int64_t ldd;
-    float* dx;                          // [slices][T][H8]
+    float* dx;                          // [slices][n][H8] of the n packed rows
     int first;                          // the first piece writes dx, the others add to it
     MmOut dw;                           // the piece's rows
 };
+
+// Slices of a piece's contraction for dx: where the packed rows make few tiles, until there is a block for each CU
+// at 256 rows a tile and two at fewer.  A slice's columns are a multiple of 64.
+__host__ __device__ inline int dx_blocks(int bm) { return bm >= 256 ? 256 : 512; }
+struct DxSlices { int count, columns; };
+__host__ __device__ inline DxSlices dx_slices(int64_t tiles, int bm, int piece)
+{
+    int64_t n = tiles > 0 ? dx_blocks(bm) / tiles : 1;
+    const int64_t most = (piece + 255) / 256;
+    n = n < 1 ? 1 : n > most ? most : n;
+    return DxSlices{(int)n, (int)(((piece + 63) / 64 + n - 1) / n * 64)};
+}
 
 // dx of the packed rows over a slice of a piece's columns.
 template <class L>
@@ -267,15 +304,16 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_dx(XentGradArgs p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int n = p.ctrl->n, tm = (n + L::BM - 1) / L::BM, tn = (p.H8 + L::BN - 1) / L::BN;
-    const int turn = mm_turn(blockIdx.x, tm * tn * p.slices);
+    const DxSlices sl = dx_slices((int64_t)tm * tn, L::BM, p.piece);
+    const int turn = mm_turn(blockIdx.x, tm * tn * sl.count);
     if (turn < 0) return;
-    const int slice = turn / (tm * tn), k0 = slice * p.per;
+    const int slice = turn / (tm * tn), k0 = slice * sl.columns;
     int im, in;
     mm_band(turn % (tm * tn), tm, tn, im, in);
     const MmOperand a{p.d + k0, p.ldd, n}, b{p.w + k0 * p.ldw, p.ldw, p.H8};
     v4f acc[L::MI][L::NI];
-    mm_tile<L>(a, b, im * L::BM, in * L::BN, max(min(p.V - k0, p.per), 0), smem, acc);
-    const MmOut o{p.dx + (int64_t)slice * p.T * p.H8, p.H8, n, p.H8, 0, !p.first};
+    mm_tile<L>(a, b, im * L::BM, in * L::BN, max(min(p.V - k0, sl.columns), 0), smem, acc);
+    const MmOut o{p.dx + (int64_t)slice * n * p.H8, p.H8, n, p.H8, 0, !p.first};
     mm_store_tile<L>(acc, smem, o, im * L::BM, in * L::BN);
 }
 
@@ -301,23 +339,32 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_dw(XentGradArgs p, int tm, 
 
 // dx of every token: the slices' sums in order, times the largest |g|; zeros without a target.
 template <typename T_>
-__global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int slices, const XentCtrl* __restrict__ ctrl,
+__global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int bm, int bn, int piece,
+                                                     const XentCtrl* __restrict__ ctrl,
                                                      const int* __restrict__ pos, const float* __restrict__ acc,
                                                      T_* __restrict__ dx, int64_t ld)
 {
     const int quads = H8 / 4;
     const int64_t all = (int64_t)T * quads;
     const float s = ctrl->largest;
+    const int n = ctrl->n, slices = dx_slices((int64_t)((n + bm - 1) / bm) * ((H8 + bn - 1) / bn), bm, piece).count;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
         const int t = (int)(i / quads), c = (int)(i - (int64_t)t * quads) * 4, m = pos[t];
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (m >= 0)
-            for (int k = 0; k < slices; k++) {
-                const float4 f = *reinterpret_cast<const float4*>(acc + ((int64_t)k * T + m) * H8 + c);
-                v[0] += f.x;
-                v[1] += f.y;
-                v[2] += f.z;
-                v[3] += f.w;
+            for (int k = 0; k < slices; k += 4) {
+                float4 f[4];
+#pragma unroll
+                for (int u = 0; u < 4; u++)
+                    f[u] = k + u < slices ? *reinterpret_cast<const float4*>(acc + ((int64_t)(k + u) * n + m) * H8 + c)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    v[0] += f[u].x;
+                    v[1] += f[u].y;
+                    v[2] += f[u].z;
+                    v[3] += f[u].w;
+                }
             }
         T_* o = dx + t * ld + c;
         if constexpr (sizeof(T_) == 2) {
@@ -351,7 +398,8 @@ hipError_t run_logits(const LogitsArgs& p, hipStream_t s)
     if (p.T <= 16) return launch_logits<MmTile<1, 4, 1, 4, 4, false, false>, GRAD>(p, s);
     if (p.T <= 32) return launch_logits<MmTile<1, 4, 2, 4, 3, false, false>, GRAD>(p, s);
     if (p.T <= 64) return launch_logits<MmTile<1, 4, 4, 4, 2, false, false>, GRAD>(p, s);
-    if (over(p.T, 256) * over(p.V, 256) < 200) return launch_logits<MmTile<2, 2, 4, 4, 2, false, false>, GRAD>(p, s);
+    const int v = mm_choose(3, p.H, [&](int64_t bm, int64_t bn) { return over(p.T, bm) * over(p.V, bn); });
+    if (v == 3) return launch_logits<MmTile<2, 2, 4, 4, 2, false, false>, GRAD>(p, s);
     return launch_logits<MmTile<2, 4, 8, 4, 2, false, false>, GRAD>(p, s);
 }
 
@@ -361,22 +409,30 @@ hipError_t launch_dx(const XentGradArgs& p, hipStream_t s)
     static LdsAllowed allowed;
     const auto kernel = k_xent_dx<L>;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
-    const int64_t tiles = over(p.T, L::BM) * over(p.H8, L::BN) * p.slices;
+    const int64_t tiles = std::max<int64_t>(over(p.T, L::BM) * over(p.H8, L::BN), dx_blocks(L::BM));    // whatever n is
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(L::THREADS), L::BYTES, s, p);
     return hipGetLastError();
 }
-struct DxTile { int bm, bn; };
-DxTile dx_tile(int64_t T, int64_t H8)
+// The tile of the least time with its slices, whose sums are written and read again at some 5 TB/s.  (The tokens
+// with a target are the device's to know: all of them are counted.)
+const MmVariant& dx_tile(int64_t T, int64_t H8, int64_t piece)
 {
-    if (T <= 32) return {32, 64};
-    if (T <= 128 || over(T, 256) * over(H8, 256) < 128) return {128, 128};
-    return {256, 256};
+    int best = 1;
+    float least = 0.0f;
+    for (int v = 1; v < 5; v++) {
+        const int64_t tiles = over(T, kMmVariants[v].bm) * over(H8, kMmVariants[v].bn);
+        const DxSlices sl = dx_slices(tiles, kMmVariants[v].bm, (int)piece);
+        const float us = mm_time(kMmVariants[v], tiles * sl.count, sl.columns) + (float)(T * H8) * sl.count * 8.0f / 5.0e6f;
+        if (v == 1 || us < least) best = v, least = us;
+    }
+    return kMmVariants[best];
 }
 hipError_t run_dx(const XentGradArgs& p, hipStream_t s)
 {
-    switch (dx_tile(p.T, p.H8).bm) {
+    switch (dx_tile(p.T, p.H8, p.piece).bm) {
     case 32: return launch_dx<MmTile<2, 2, 1, 2, 4, false, true>>(p, s);
+    case 64: return launch_dx<MmTile<2, 2, 2, 2, 3, false, true>>(p, s);
     case 128: return launch_dx<MmTile<2, 2, 4, 4, 2, false, true>>(p, s);
     default: return launch_dx<MmTile<2, 4, 8, 4, 2, false, true>>(p, s);
     }
@@ -394,14 +450,15 @@ hipError_t launch_dw(const XentGradArgs& p, hipStream_t s)
 }
 hipError_t run_dw(const XentGradArgs& p, hipStream_t s)
 {
-    if (over(p.V, 256) * over(p.H, 256) < 200) return launch_dw<MmTile<2, 2, 4, 4, 2, true, true>>(p, s);
+    const int v = mm_choose(3, p.T, [&](int64_t bm, int64_t bn) { return over(p.V, bm) * over(p.H, bn); });
+    if (v == 3) return launch_dw<MmTile<2, 2, 4, 4, 2, true, true>>(p, s);
     return launch_dw<MmTile<2, 4, 8, 4, 2, true, true>>(p, s);
 }
 
 struct XentLayout {
     size_t ctrl, idx, pos, y, zy, x, parts, lse, g, d, dx, w, total;
     bool pad_w;
-    int piece, slices, per;         // columns of a piece; slices of its contraction for dx
+    int piece;                      // columns of a piece
 };
 XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t ldw, bool backward)
 {
@@ -428,15 +485,12 @@ XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t l
         // d of a piece in at most 256 MiB, but for 256 columns at least
         const int64_t most = std::max<int64_t>((int64_t(128) << 20) / T / 256 * 256, 256);
         L.piece = (int)std::min(most, (V + 255) / 256 * 256);
-        // few tiles of dx: the contraction is split until there are some two blocks for each CU
-        const DxTile t = dx_tile(T, H8);
-        const int64_t tiles = over(T, t.bm) * over(H8, t.bn);
-        L.slices = (int)std::max<int64_t>(1, std::min<int64_t>(512 / tiles, over(L.piece, 256)));
-        L.per = (int)(over(over(L.piece, 64), L.slices) * 64);
         L.lse = take(T * 4);
         L.g = take(T * 4);
         L.d = take(T * (int64_t)L.piece * 2);
-        L.dx = take((int64_t)L.slices * T * H8 * 4);
+        // dx of every row, or of fewer rows in slices: dx_blocks tiles then
+        const MmVariant& t = dx_tile(T, H8, L.piece);
+        L.dx = take(std::max<int64_t>(T * H8, std::min<int64_t>((int64_t)dx_blocks(t.bm) * t.bm * t.bn, T * H8 * over(L.piece, 256))) * 4);
     }
     L.total = o;
     return L;
@@ -475,8 +529,9 @@ int xent_begin(XentCall& c, int32_t T, int32_t H, int32_t V, const uint16_t* x, 
     c.ldw = ldw;
     c.H8 = (int)up8(H);
     if (c.L.pad_w) {
-        if (launch_pad_rows(V, H, w, ldw, c.ws + c.L.w, s) != hipSuccess) return V4MOE_ELAUNCH;
-        c.w = c.at<uint16_t>(c.L.w);
+        const PadRows job{V, H, w, ldw, c.at<uint16_t>(c.L.w)};
+        if (launch_pad_rows(&job, 1, s) != hipSuccess) return V4MOE_ELAUNCH;
+        c.w = job.dst;
         c.ldw = c.H8;
     }
     hipLaunchKernelGGL(k_xent_rows, dim3(1), dim3(1024), 0, s, T, V, targets, g, gs, c.at<int>(c.L.pos), c.at<int>(c.L.idx),
@@ -566,7 +621,7 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         if (T > 0 && run_logits<true>(p, s) != hipSuccess) return V4MOE_ELAUNCH;
         XentGradArgs q{};
         q.T = T, q.H = H, q.H8 = c.H8, q.V = n;
-        q.slices = c.L.slices, q.per = c.L.per;
+        q.piece = c.L.piece;
         q.ctrl = ctrl;
         q.x = p.x, q.w = p.w, q.ldw = p.ldw, q.d = p.d, q.ldd = p.ldd;
         q.dx = c.at<float>(c.L.dx), q.first = v0 == 0;
@@ -579,11 +634,12 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
     }
     if (dx && T > 0) {
         const dim3 grid((unsigned)std::min<int64_t>(over((int64_t)T * (c.H8 / 4), 256), 8192));
+        const MmVariant& t = dx_tile(T, c.H8, c.L.piece);
         if (dx_type == V4MOE_TYPE_BF16)
-            hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, c.L.slices, ctrl,
+            hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl,
                                c.at<int>(c.L.pos), c.at<float>(c.L.dx), static_cast<uint16_t*>(dx), lddx);
         else
-            hipLaunchKernelGGL(k_xent_finish<float>, grid, dim3(256), 0, s, T, H, c.H8, c.L.slices, ctrl, c.at<int>(c.L.pos),
+            hipLaunchKernelGGL(k_xent_finish<float>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl, c.at<int>(c.L.pos),
                                c.at<float>(c.L.dx), static_cast<float*>(dx), lddx);
     }
     return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
