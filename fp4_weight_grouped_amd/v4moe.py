@@ -745,7 +745,7 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
 
 def _lora(x, a, b, ids, scale):
     """(sizes, GPU, x's leading dimension, addresses of a, b, ids and scale) of an adapters' call, checked."""
-    M, (L, r, K), N = x.shape[0], a.shape, b.shape[2]
+    M, (L, r, K), (_, _, N) = x.shape[0], a.shape, b.shape
     gpu = _device_of(x, "x")
     return (LoraC(M, N, K, r, L), gpu, _matrix(x, M, K, "x", gpu, torch.bfloat16),
             (_dense(a, (L, r, K), torch.bfloat16, "a", gpu), _dense(b, (L, r, N), torch.bfloat16, "b", gpu),
