@@ -39,8 +39,8 @@ __device__ __forceinline__ int rows_of(const int32_t* offsets, int e, int M, int
 // expert's tiles column by column in bands of eight row tiles.  `found` is LDS.
 struct Found { int e, first, count, tile, total, wave[16]; };
 template <int BM, int THREADS>
-__device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, Found* found, int& e, int& first, int& count, int& im,
-                                          int& in)
+__device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, int block, int blocks, Found* found, int& e, int& first,
+                                          int& count, int& im, int& in)
 {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int each = (g.E + THREADS - 1) / THREADS, e0 = t * each, e1 = min(e0 + each, g.E);
@@ -62,8 +62,8 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, Found* f
         if (w < wave) before += found->wave[w];
         total += found->wave[w];
     }
-    if ((int64_t)total * tn > (int64_t)gridDim.x) return false;        // (offsets that do not ascend: nothing is done)
-    const int turn = mm_turn(blockIdx.x, total * tn);
+    if ((int64_t)total * tn > blocks) return false;        // (offsets that do not ascend: nothing is done)
+    const int turn = mm_turn(block, total * tn);
     if (turn < 0) return false;
     if (turn >= before * tn && turn < (before + mine) * tn) {
         for (int i = e0; i < e1; i++) {
@@ -90,11 +90,10 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, Found* f
 
 // Forward and data gradient: row tiles of each expert by column tiles of C.
 template <class L>
-__global__ __launch_bounds__(L::THREADS) void k_grouped_rows(GroupedArgs g, int tn)
+__device__ __forceinline__ void rows_tile(const GroupedArgs& g, int tn, int block, int blocks, uint8_t* smem)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
     int e, first, count, im, in;
-    if (!find_tile<L::BM, L::THREADS>(g, tn, reinterpret_cast<Found*>(smem), e, first, count, im, in)) return;
+    if (!find_tile<L::BM, L::THREADS>(g, tn, block, blocks, reinterpret_cast<Found*>(smem), e, first, count, im, in)) return;
     const MmOperand a{g.a + first * g.lda, g.lda, count}, b{g.b + e * g.group, g.ldb, L::BCOL ? (g.N + 7) / 8 * 8 : g.N};
     v4f acc[L::MI][L::NI];
     mm_tile<L>(a, b, im * L::BM, in * L::BN, g.K, smem, acc);
@@ -103,13 +102,18 @@ __global__ __launch_bounds__(L::THREADS) void k_grouped_rows(GroupedArgs g, int 
     c.c = static_cast<uint8_t*>(c.c) + first * c.ldc * (c.bf16 ? 2 : 4);
     mm_store_tile<L>(acc, smem, c, im * L::BM, in * L::BN);
 }
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_grouped_rows(GroupedArgs g, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    rows_tile<L>(g, tn, blockIdx.x, gridDim.x, smem);
+}
 
 // Weight gradient: the tiles of each expert's dW, its rows the contraction.
 template <class L>
-__global__ __launch_bounds__(L::THREADS) void k_grouped_weights(GroupedArgs g, int tm, int tn)
+__device__ __forceinline__ void weights_tile(const GroupedArgs& g, int tm, int tn, int block, uint8_t* smem)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const int turn = mm_turn(blockIdx.x, g.E * tm * tn), e = turn / (tm * tn), tile = turn % (tm * tn);
+    const int turn = mm_turn(block, g.E * tm * tn), e = turn / (tm * tn), tile = turn % (tm * tn);
     int first;
     const int count = rows_of(g.offsets, e, g.M, first);
     MmOut c = g.c;
@@ -122,6 +126,21 @@ __global__ __launch_bounds__(L::THREADS) void k_grouped_weights(GroupedArgs g, i
     mm_tile<L>(a, b, m0, n0, count, smem, acc);
     c.c = static_cast<uint8_t*>(c.c) + (int64_t)e * c.M * c.ldc * (c.bf16 ? 2 : 4);
     mm_store_tile<L>(acc, smem, c, m0, n0);
+}
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_grouped_weights(GroupedArgs g, int tm, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    weights_tile<L>(g, tm, tn, blockIdx.x, smem);
+}
+
+// Both gradients in a launch, the data gradient's blocks first.
+template <class R, class W>
+__global__ __launch_bounds__(R::THREADS) void k_grouped_both(GroupedArgs r, int rtn, int rblocks, GroupedArgs w, int wtm, int wtn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((int)blockIdx.x < rblocks) rows_tile<R>(r, rtn, blockIdx.x, rblocks, smem);
+    else weights_tile<W>(w, wtm, wtn, (int)blockIdx.x - rblocks, smem);
 }
 
 // Rows of 2-byte elements, src [R][C] -> dst [R][C8] (C8 = C rounded up to 8), zeros past C: what the
@@ -153,14 +172,15 @@ __global__ __launch_bounds__(256) void k_pad_rows(PadJobs p)
     }
 }
 
+// the most row tiles: every expert's last one may hold a single row
+int64_t most_row_tiles(const GroupedArgs& g, int64_t bm) { return g.M / bm + (g.M < g.E ? g.M : g.E); }
 template <class L>
 hipError_t launch_rows(const GroupedArgs& g, hipStream_t s)
 {
     static LdsAllowed allowed;
     const auto kernel = k_grouped_rows<L>;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
-    // the most row tiles: every expert's last one may hold a single row
-    const int64_t tn = over(g.N, L::BN), tm = g.M / L::BM + (g.M < g.E ? g.M : g.E);
+    const int64_t tn = over(g.N, L::BN), tm = most_row_tiles(g, L::BM);
     if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(L::THREADS), L::BYTES, s, g, (int)tn);
     return hipGetLastError();
@@ -176,33 +196,77 @@ hipError_t launch_weights(const GroupedArgs& g, hipStream_t s)
     hipLaunchKernelGGL(kernel, dim3((unsigned)(g.E * tm * tn)), dim3(L::THREADS), L::BYTES, s, g, (int)tm, (int)tn);
     return hipGetLastError();
 }
+template <class R, class W>
+hipError_t launch_both(const GroupedArgs& r, const GroupedArgs& w, hipStream_t s)
+{
+    static_assert(R::THREADS == W::THREADS, "one launch");
+    static LdsAllowed allowed;
+    const auto kernel = k_grouped_both<R, W>;
+    constexpr int BYTES = R::BYTES > W::BYTES ? R::BYTES : W::BYTES;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), BYTES, allowed); e != hipSuccess) return e;
+    const int64_t rtn = over(r.N, R::BN), rblocks = most_row_tiles(r, R::BM) * rtn;
+    const int64_t wtn = over(w.N, W::BN), wtm = over(w.c.M, W::BM), all = rblocks + w.E * wtm * wtn;
+    if (all > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)all), dim3(R::THREADS), BYTES, s, r, (int)rtn, (int)rblocks, w, (int)wtm, (int)wtn);
+    return hipGetLastError();
+}
+
+template <int V, bool BCOL>
+struct RowTile;
+template <bool BCOL> struct RowTile<0, BCOL> { using L = MmTile<1, 4, 1, 1, 4, false, BCOL>; };
+template <bool BCOL> struct RowTile<1, BCOL> { using L = MmTile<2, 2, 1, 2, 4, false, BCOL>; };
+template <bool BCOL> struct RowTile<2, BCOL> { using L = MmTile<2, 2, 2, 2, 3, false, BCOL>; };
+template <bool BCOL> struct RowTile<3, BCOL> { using L = MmTile<2, 2, 4, 4, 2, false, BCOL, true>; };
+template <bool BCOL> struct RowTile<4, BCOL> { using L = MmTile<2, 4, 8, 4, 2, false, BCOL, true>; };
+using Weights64 = MmTile<2, 2, 2, 2, 3, true, true>;
+using Weights128 = MmTile<2, 2, 4, 4, 2, true, true>;
+using Weights256 = MmTile<2, 4, 8, 4, 2, true, true>;
 
 // Row tiles are estimated: the offsets are the device's.  Every expert's last one is half empty on average, and an
 // expert with rows has one at least.
+int64_t row_tiles(const GroupedArgs& g, int64_t bm, int64_t bn)
+{
+    const int64_t groups = g.M < g.E ? g.M : g.E, tm = g.M / bm + (groups + 1) / 2;
+    return (tm > groups ? tm : groups) * over(g.N, bn);
+}
+int64_t weight_tiles(const GroupedArgs& g, int64_t bm, int64_t bn) { return g.E * over(g.c.M, bm) * over(g.N, bn); }
+int row_variant(const GroupedArgs& g)
+{
+    return mm_choose(0, g.K, [&](int64_t bm, int64_t bn) { return row_tiles(g, bm, bn); });
+}
+int weight_variant(const GroupedArgs& g)
+{
+    return mm_choose(2, g.M / g.E, [&](int64_t bm, int64_t bn) { return weight_tiles(g, bm, bn); });
+}
 template <bool BCOL>
 hipError_t run_rows(const GroupedArgs& g, hipStream_t s)
 {
-    const int64_t groups = g.M < g.E ? g.M : g.E;
-    const int v = mm_choose(0, g.K, [&](int64_t bm, int64_t bn) {
-        const int64_t tm = g.M / bm + (groups + 1) / 2;
-        return (tm > groups ? tm : groups) * over(g.N, bn);
-    });
-    switch (v) {
-    case 0: return launch_rows<MmTile<1, 4, 1, 1, 4, false, BCOL>>(g, s);
-    case 1: return launch_rows<MmTile<2, 2, 1, 2, 4, false, BCOL>>(g, s);
-    case 2: return launch_rows<MmTile<2, 2, 2, 2, 3, false, BCOL>>(g, s);
-    case 3: return launch_rows<MmTile<2, 2, 4, 4, 2, false, BCOL, true>>(g, s);
-    default: return launch_rows<MmTile<2, 4, 8, 4, 2, false, BCOL, true>>(g, s);
+    switch (row_variant(g)) {
+    case 0: return launch_rows<typename RowTile<0, BCOL>::L>(g, s);
+    case 1: return launch_rows<typename RowTile<1, BCOL>::L>(g, s);
+    case 2: return launch_rows<typename RowTile<2, BCOL>::L>(g, s);
+    case 3: return launch_rows<typename RowTile<3, BCOL>::L>(g, s);
+    default: return launch_rows<typename RowTile<4, BCOL>::L>(g, s);
     }
 }
 hipError_t run_weights(const GroupedArgs& g, hipStream_t s)
 {
-    const int v = mm_choose(2, g.M / g.E, [&](int64_t bm, int64_t bn) { return g.E * over(g.c.M, bm) * over(g.N, bn); });
-    switch (v) {
-    case 2: return launch_weights<MmTile<2, 2, 2, 2, 3, true, true>>(g, s);
-    case 3: return launch_weights<MmTile<2, 2, 4, 4, 2, true, true>>(g, s);
-    default: return launch_weights<MmTile<2, 4, 8, 4, 2, true, true>>(g, s);
+    switch (weight_variant(g)) {
+    case 2: return launch_weights<Weights64>(g, s);
+    case 3: return launch_weights<Weights128>(g, s);
+    default: return launch_weights<Weights256>(g, s);
     }
+}
+// Both gradients.  Where neither fills the GPU for long they go out in one launch, the end of the one beside the begin of
+// the other, with 128x128 tiles both (3001 rows of 12 experts, 1001 x 499: 30 us with the copies of its odd operands, 36
+// in two launches with the tiles that are best alone, 33 with those in one).
+hipError_t run_both(const GroupedArgs& r, const GroupedArgs& w, hipStream_t s)
+{
+    const int rv = row_variant(r), wv = weight_variant(w);
+    if ((rv == 2 || rv == 3) && wv < 4 && row_tiles(r, 128, 128) <= 1024 && weight_tiles(w, 128, 128) <= 1024)
+        return launch_both<RowTile<3, true>::L, Weights128>(r, w, s);
+    if (const hipError_t e = run_rows<true>(r, s); e != hipSuccess) return e;
+    return run_weights(w, s);
 }
 
 struct GroupedLayout {
@@ -336,17 +400,14 @@ __attribute__((visibility("default"))) int moe_grouped_linear_backward(
     GroupedCall o{x, dy, w, ldx, lddy, K};
     if (const int rc = grouped_operands(o, M, E, N, K, true, dw != nullptr, dx != nullptr && M > 0, workspace, ws_bytes, s))
         return rc;
-    if (dx && M > 0) {
-        // contraction over N, which the weights have across their rows
-        const GroupedArgs g{M, K, N, E, offsets, o.dy, o.lddy, o.w, o.ldw, (int64_t)N * o.ldw,
-                            MmOut{dx, lddx, 0, K, dx_type == V4MOE_TYPE_BF16, 0}};
-        if (run_rows<true>(g, s) != hipSuccess) return V4MOE_ELAUNCH;
-    }
-    if (dw) {
-        const GroupedArgs g{M, K, 0, E, offsets, o.dy, o.lddy, o.x, o.ldx, 0,
-                            MmOut{dw, K, N, K, dw_type == V4MOE_TYPE_BF16, accumulate != 0}};
-        if (run_weights(g, s) != hipSuccess) return V4MOE_ELAUNCH;
-    }
+    // data gradient: the contraction is over N, which the weights have across their rows
+    const GroupedArgs r{M, K, N, E, offsets, o.dy, o.lddy, o.w, o.ldw, (int64_t)N * o.ldw,
+                        MmOut{dx, lddx, 0, K, dx_type == V4MOE_TYPE_BF16, 0}};
+    const GroupedArgs g{M, K, 0, E, offsets, o.dy, o.lddy, o.x, o.ldx, 0,
+                        MmOut{dw, K, N, K, dw_type == V4MOE_TYPE_BF16, accumulate != 0}};
+    const bool rows = dx && M > 0;
+    if ((rows && dw ? run_both(r, g, s) : rows ? run_rows<true>(r, s) : dw ? run_weights(g, s) : hipSuccess) != hipSuccess)
+        return V4MOE_ELAUNCH;
     return V4MOE_OK;
 }
 
