@@ -702,20 +702,24 @@ __device__ __forceinline__ void store8f(T* row, int n, int N, const float (&v)[8
 // have neighbouring columns, as y came (as the instruction leaves them, a lane's row is far from its
 // neighbour's, and the L1 takes a lane at a time).
 // ONE: all ranks at once (RC chosen so); else 16 RC of them in turn, staged anew for each row tile.
+template <int RC>
+struct ExpandLds {
+    static constexpr int FACTOR = 16 * RC * 128, SUMS = 16 * 256;     // a wave's part of the factor, then of the sums: 16 rows
+    uint8_t us[kTile * 16 * RC * 4];                                  // (16 RC ranks of a row, twice)
+    uint8_t wave[4][FACTOR > SUMS ? FACTOR : SUMS];
+};
 template <int RC, typename T, bool ONE>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_lora_expand_tile(ExpandArgs p)
+__device__ __forceinline__ void expand_tile(const ExpandArgs& p, int block, ExpandLds<RC>& shared)
 {
-    constexpr int UROW = 16 * RC * 4;                          // bytes of a row of u: 16 RC ranks twice
-    constexpr int FACTOR = 16 * RC * 128, SUMS = 16 * 256;     // a wave's part of the factor, then of the sums: 16 rows
-    __shared__ __align__(128) uint8_t us[kTile * UROW];
-    __shared__ __align__(128) uint8_t lds[4][FACTOR > SUMS ? FACTOR : SUMS];
+    uint8_t* us = shared.us;
+    auto& lds = shared.wave;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, kq = lane >> 4;
     const int blocks = (p.N + 255) / 256;                      // along a row, which go first
-    const Tile t = p.list.tiles[blockIdx.x / blocks];
+    const Tile t = p.list.tiles[block / blocks];
     const bool none = t.a >= p.L;
     if (t.count == 0 || (none && p.in_place)) return;
-    const int c = (int)(blockIdx.x % blocks) * 256 + 64 * wave, s8 = lane & 7, n = c + 8 * s8;
+    const int c = block % blocks * 256 + 64 * wave, s8 = lane & 7, n = c + 8 * s8;
     // this lane's rows 8 q + lane / 8, and its columns n .. + 7
     int m[8];
 #pragma unroll
@@ -807,6 +811,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_lora_expand_til
     }
 }
 
+template <int RC, typename T, bool ONE>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void k_lora_expand_tile(ExpandArgs p)
+{
+    __shared__ __align__(128) ExpandLds<RC> shared;
+    expand_tile<RC, T, ONE>(p, blockIdx.x, shared);
+}
+
 struct OuterJob {
     const uint16_t* u;                          // [M][2][rp], by row, or by place
     const uint16_t* x; int64_t ldx; int N;      // rows, columns
@@ -826,17 +837,24 @@ struct OuterArgs {
 // of the waves.
 constexpr int kOuterRows = 2048;
 template <int RC, bool LISTED>
-__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
+struct OuterLds {
+    static constexpr int UW = 32 * RC, XB = 32 * 128, UB = 32 * UW * 2;   // ranks of a row (twice 16 RC), bytes of a step
+    uint8_t wave[4][XB + UB];
+    uint16_t listed[LISTED ? 8 : kOuterRows];
+    int counts[4];
+};
+template <int RC, bool LISTED>
+__device__ __forceinline__ void outer_block(const OuterArgs& p, int block, int a, int chunk, OuterLds<RC, LISTED>& shared)
 {
-    constexpr int UW = 32 * RC, XB = 32 * 128, UB = 32 * UW * 2;          // ranks of a row (twice 16 RC), bytes of a step
-    __shared__ __align__(128) uint8_t lds[4][XB + UB];
-    __shared__ uint16_t listed[LISTED ? 1 : kOuterRows];
-    __shared__ int counts[4];
+    constexpr int UW = 32 * RC, XB = 32 * 128;
+    auto& lds = shared.wave;
+    uint16_t* listed = shared.listed;
+    int* counts = shared.counts;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, kq = lane >> 4;
-    const bool second = (int)blockIdx.x >= p.job[0].blocks;
+    const bool second = block >= p.job[0].blocks;
     const OuterJob& job = p.job[second];
-    const int c0 = ((int)blockIdx.x - (second ? p.job[0].blocks : 0)) * 64, j0 = blockIdx.z * 16 * RC, a = blockIdx.y;
+    const int c0 = (block - (second ? p.job[0].blocks : 0)) * 64, j0 = chunk * 16 * RC;
     uint8_t *xs = lds[wave], *us = lds[wave] + XB;
     v4f acc[RC][4];
 #pragma unroll
@@ -988,6 +1006,26 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
     }
 }
 
+template <int RC, bool LISTED>
+__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs p)
+{
+    __shared__ __align__(128) OuterLds<RC, LISTED> shared;
+    outer_block<RC, LISTED>(p, blockIdx.x, blockIdx.y, blockIdx.z, shared);
+}
+
+// dx, and the gradients of the factors: the longer blocks of these first, all ranks at once.
+template <int RC, typename T>
+__global__ __launch_bounds__(256, RC < 4 ? 3 : 2) void k_lora_gradients(OuterArgs o, int columns, int outer, ExpandArgs e)
+{
+    __shared__ __align__(128) union {
+        ExpandLds<RC> expand;
+        OuterLds<RC, true> outer;
+    } shared;
+    const int block = blockIdx.x;
+    if (block < outer) outer_block<RC, true>(o, block % columns, block / columns, 0, shared.outer);
+    else expand_tile<RC, T, true>(e, block - outer, shared.expand);
+}
+
 // ---- host ----
 // Whether the rows are listed first: from a few hundred on the tiles' gain outweighs the launch (see k_lora_list).
 bool listed_first(int M, int L) { return M > 256 && L <= kListAdapters; }
@@ -1094,6 +1132,27 @@ hipError_t outer_by_rank(const OuterArgs& p, hipStream_t s)
 hipError_t run_outer(const OuterArgs& p, hipStream_t s)
 {
     return listed_first(p.M, p.L) ? outer_by_rank<true>(p, s) : outer_by_rank<false>(p, s);
+}
+
+// Both gradients, in one launch where the rows are listed and all ranks fit a block.
+template <int RC>
+hipError_t launch_gradients(const OuterArgs& o, const ExpandArgs& e, int bf16, hipStream_t s)
+{
+    const int64_t columns = o.job[0].blocks + o.job[1].blocks, outer = columns * o.L, all = outer + over(e.N, 256) * most_tiles(e.M, e.L);
+    if (all > INT32_MAX) return hipErrorInvalidValue;
+    if (bf16) hipLaunchKernelGGL((k_lora_gradients<RC, uint16_t>), dim3((unsigned)all), dim3(256), 0, s, o, (int)columns, (int)outer, e);
+    else hipLaunchKernelGGL((k_lora_gradients<RC, float>), dim3((unsigned)all), dim3(256), 0, s, o, (int)columns, (int)outer, e);
+    return hipGetLastError();
+}
+hipError_t run_gradients(const OuterArgs& o, const ExpandArgs& e, int bf16, hipStream_t s)
+{
+    if (listed_first(o.M, o.L) && o.r <= 64) {
+        if (o.r <= 16) return launch_gradients<1>(o, e, bf16, s);
+        if (o.r <= 32) return launch_gradients<2>(o, e, bf16, s);
+        return launch_gradients<4>(o, e, bf16, s);
+    }
+    if (const hipError_t x = run_expand(e, bf16, s); x != hipSuccess) return x;
+    return run_outer(o, s);
 }
 
 int ranks(int r) { return (r + 15) / 16 * 16; }
@@ -1213,17 +1272,16 @@ __attribute__((visibility("default"))) int moe_lora_backward(
         if (db) sh.job[jobs++] = ShrinkJob{x, ldx, p->K, a, u};
         if (run_shrink(sh, jobs, s) != hipSuccess) return V4MOE_ELAUNCH;
     }
-    if (dx && p->M > 0) {
-        const ExpandArgs ex{p->M, p->K, p->L, p->r, rp, ids, du, a, base, ldbase, dx, lddx, base == dx, list};
-        if (run_expand(ex, dx_type == V4MOE_TYPE_BF16, s) != hipSuccess) return V4MOE_ELAUNCH;
-    }
-    if (da || db) {
-        OuterArgs o{p->M, p->L, p->r, rp, accumulate != 0, ids, {}, list};
-        int jobs = 0;
-        if (da) o.job[jobs++] = OuterJob{du, x, ldx, p->K, da, da_type == V4MOE_TYPE_BF16, (int)over(p->K, 64)};
-        if (db) o.job[jobs++] = OuterJob{u, dy, lddy, p->N, db, db_type == V4MOE_TYPE_BF16, (int)over(p->N, 64)};
-        if (run_outer(o, s) != hipSuccess) return V4MOE_ELAUNCH;
-    }
+    const ExpandArgs ex{p->M, p->K, p->L, p->r, rp, ids, du, a, base, ldbase, dx, lddx, base == dx, list};
+    OuterArgs o{p->M, p->L, p->r, rp, accumulate != 0, ids, {}, list};
+    int jobs = 0;
+    if (da) o.job[jobs++] = OuterJob{du, x, ldx, p->K, da, da_type == V4MOE_TYPE_BF16, (int)over(p->K, 64)};
+    if (db) o.job[jobs++] = OuterJob{u, dy, lddy, p->N, db, db_type == V4MOE_TYPE_BF16, (int)over(p->N, 64)};
+    const int bf16 = dx_type == V4MOE_TYPE_BF16;
+    const bool rows = dx && p->M > 0;
+    if ((rows && jobs > 0 ? run_gradients(o, ex, bf16, s) : rows ? run_expand(ex, bf16, s) : jobs > 0 ? run_outer(o, s) : hipSuccess) !=
+        hipSuccess)
+        return V4MOE_ELAUNCH;
     return V4MOE_OK;
 }
 
