@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 namespace v4moe {
 
@@ -1270,6 +1271,7 @@ __attribute__((visibility("default"))) int moe_lora_backward(
         int jobs = 0;
         if (dx || da) sh.job[jobs++] = ShrinkJob{dy, lddy, p->N, b, du};
         if (db) sh.job[jobs++] = ShrinkJob{x, ldx, p->K, a, u};
+        if (jobs == 2 && p->K > p->N) std::swap(sh.job[0], sh.job[1]);       // (the longer one's blocks begin first)
         if (run_shrink(sh, jobs, s) != hipSuccess) return V4MOE_ELAUNCH;
     }
     const ExpandArgs ex{p->M, p->K, p->L, p->r, rp, ids, du, a, base, ldbase, dx, lddx, base == dx, list};
