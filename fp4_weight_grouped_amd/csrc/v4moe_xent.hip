@@ -300,12 +300,11 @@ __host__ __device__ inline DxSlices dx_slices(int64_t tiles, int bm, int piece)
 
 // dx of the packed rows over a slice of a piece's columns.
 template <class L>
-__global__ __launch_bounds__(L::THREADS) void k_xent_dx(XentGradArgs p)
+__device__ __forceinline__ void dx_block(const XentGradArgs& p, int block, uint8_t* smem)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
     const int n = p.ctrl->n, tm = (n + L::BM - 1) / L::BM, tn = (p.H8 + L::BN - 1) / L::BN;
     const DxSlices sl = dx_slices((int64_t)tm * tn, L::BM, p.piece);
-    const int turn = mm_turn(blockIdx.x, tm * tn * sl.count);
+    const int turn = mm_turn(block, tm * tn * sl.count);
     if (turn < 0) return;
     const int slice = turn / (tm * tn), k0 = slice * sl.columns;
     int im, in;
@@ -319,13 +318,12 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_dx(XentGradArgs p)
 
 // The piece's rows of dW: the packed tokens are the contraction.
 template <class L>
-__global__ __launch_bounds__(L::THREADS) void k_xent_dw(XentGradArgs p, int tm, int tn)
+__device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, int block, uint8_t* smem)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
     const int n = p.ctrl->n;
     if (n == 0 && p.dw.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
     int im, in;
-    mm_band(mm_turn(blockIdx.x, tm * tn), tm, tn, im, in);
+    mm_band(mm_turn(block, tm * tn), tm, tn, im, in);
     const MmOperand a{p.d, p.ldd, (p.V + 7) / 8 * 8}, b{p.x, p.H8, p.H8};
     v4f acc[L::MI][L::NI];
     mm_tile<L>(a, b, im * L::BM, in * L::BN, n, smem, acc);
@@ -335,6 +333,27 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_dw(XentGradArgs p, int tm, 
 #pragma unroll
         for (int j = 0; j < L::NI; j++) acc[i][j] *= s;
     mm_store_tile<L>(acc, smem, p.dw, im * L::BM, in * L::BN);
+}
+
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_xent_dx(XentGradArgs p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    dx_block<L>(p, blockIdx.x, smem);
+}
+template <class L>
+__global__ __launch_bounds__(L::THREADS) void k_xent_dw(XentGradArgs p, int tm, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    dw_block<L>(p, tm, tn, blockIdx.x, smem);
+}
+// Both, dx's blocks, whose contraction is the longer one, first.
+template <class X, class W>
+__global__ __launch_bounds__(X::THREADS) void k_xent_gradients(XentGradArgs p, int xblocks, int tm, int tn)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((int)blockIdx.x < xblocks) dx_block<X>(p, blockIdx.x, smem);
+    else dw_block<W>(p, tm, tn, (int)blockIdx.x - xblocks, smem);
 }
 
 // dx of every token: the slices' sums in order, times the largest |g|; zeros without a target.
@@ -403,21 +422,36 @@ hipError_t run_logits(const LogitsArgs& p, hipStream_t s)
     return launch_logits<MmTile<2, 4, 8, 4, 2, false, false>, GRAD>(p, s);
 }
 
+// blocks of dx, whatever n is
+template <class L>
+int64_t dx_tiles(const XentGradArgs& p) { return std::max<int64_t>(over(p.T, L::BM) * over(p.H8, L::BN), dx_blocks(L::BM)); }
 template <class L>
 hipError_t launch_dx(const XentGradArgs& p, hipStream_t s)
 {
     static LdsAllowed allowed;
     const auto kernel = k_xent_dx<L>;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::BYTES, allowed); e != hipSuccess) return e;
-    const int64_t tiles = std::max<int64_t>(over(p.T, L::BM) * over(p.H8, L::BN), dx_blocks(L::BM));    // whatever n is
+    const int64_t tiles = dx_tiles<L>(p);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(L::THREADS), L::BYTES, s, p);
     return hipGetLastError();
 }
+using XentW128 = MmTile<2, 2, 4, 4, 2, true, true>;
+using XentX128 = MmTile<2, 2, 4, 4, 2, false, true>;
+constexpr int kX128 = 3;                // of kMmVariants
+int dw_variant(int64_t T, int64_t H, int64_t V)
+{
+    return mm_choose(3, T, [&](int64_t bm, int64_t bn) { return over(V, bm) * over(H, bn); });
+}
+// Both gradients in one launch where dW has few tiles, with 128x128 ones both: the end of the one runs beside the
+// begin of the other.
+bool both_at_once(int64_t T, int64_t H, int64_t piece) { return dw_variant(T, H, piece) == kX128; }
+
 // The tile of the least time with its slices, whose sums are written and read again at some 5 TB/s.  (The tokens
 // with a target are the device's to know: all of them are counted.)
-const MmVariant& dx_tile(int64_t T, int64_t H8, int64_t piece)
+const MmVariant& dx_tile(int64_t T, int64_t H8, int64_t piece, bool both)
 {
+    if (both) return kMmVariants[kX128];
     int best = 1;
     float least = 0.0f;
     for (int v = 1; v < 5; v++) {
@@ -430,10 +464,10 @@ const MmVariant& dx_tile(int64_t T, int64_t H8, int64_t piece)
 }
 hipError_t run_dx(const XentGradArgs& p, hipStream_t s)
 {
-    switch (dx_tile(p.T, p.H8, p.piece).bm) {
+    switch (dx_tile(p.T, p.H8, p.piece, false).bm) {
     case 32: return launch_dx<MmTile<2, 2, 1, 2, 4, false, true>>(p, s);
     case 64: return launch_dx<MmTile<2, 2, 2, 2, 3, false, true>>(p, s);
-    case 128: return launch_dx<MmTile<2, 2, 4, 4, 2, false, true>>(p, s);
+    case 128: return launch_dx<XentX128>(p, s);
     default: return launch_dx<MmTile<2, 4, 8, 4, 2, false, true>>(p, s);
     }
 }
@@ -450,9 +484,25 @@ hipError_t launch_dw(const XentGradArgs& p, hipStream_t s)
 }
 hipError_t run_dw(const XentGradArgs& p, hipStream_t s)
 {
-    const int v = mm_choose(3, p.T, [&](int64_t bm, int64_t bn) { return over(p.V, bm) * over(p.H, bn); });
-    if (v == 3) return launch_dw<MmTile<2, 2, 4, 4, 2, true, true>>(p, s);
+    if (dw_variant(p.T, p.H, p.piece) == kX128) return launch_dw<XentW128>(p, s);
     return launch_dw<MmTile<2, 4, 8, 4, 2, true, true>>(p, s);
+}
+hipError_t run_gradients(const XentGradArgs& p, hipStream_t s)
+{
+    if (!both_at_once(p.T, p.H, p.piece)) {
+        if (const hipError_t e = run_dx(p, s); e != hipSuccess) return e;
+        return run_dw(p, s);
+    }
+    using X = XentX128;
+    using W = XentW128;
+    static_assert(X::BYTES == W::BYTES && X::THREADS == W::THREADS, "one launch");
+    static LdsAllowed allowed;
+    const auto kernel = k_xent_gradients<X, W>;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), X::BYTES, allowed); e != hipSuccess) return e;
+    const int64_t blocks = dx_tiles<X>(p), tm = over(p.V, W::BM), tn = over(p.H, W::BN);
+    if (blocks + tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks + tm * tn)), dim3(X::THREADS), X::BYTES, s, p, (int)blocks, (int)tm, (int)tn);
+    return hipGetLastError();
 }
 
 struct XentLayout {
@@ -488,9 +538,13 @@ XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t l
         L.lse = take(T * 4);
         L.g = take(T * 4);
         L.d = take(T * (int64_t)L.piece * 2);
-        // dx of every row, or of fewer rows in slices: dx_blocks tiles then
-        const MmVariant& t = dx_tile(T, H8, L.piece);
-        L.dx = take(std::max<int64_t>(T * H8, std::min<int64_t>((int64_t)dx_blocks(t.bm) * t.bm * t.bn, T * H8 * over(L.piece, 256))) * 4);
+        // dx of every row, or of fewer rows in slices: dx_blocks tiles then (of either tile, with dW or alone)
+        int64_t most_dx = T * H8;
+        for (int both = 0; both < 2; both++) {
+            const MmVariant& t = dx_tile(T, H8, L.piece, both && both_at_once(T, H, L.piece));
+            most_dx = std::max(most_dx, std::min<int64_t>((int64_t)dx_blocks(t.bm) * t.bm * t.bn, T * H8 * over(L.piece, 256)));
+        }
+        L.dx = take(most_dx * 4);
     }
     L.total = o;
     return L;
@@ -625,16 +679,17 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         q.ctrl = ctrl;
         q.x = p.x, q.w = p.w, q.ldw = p.ldw, q.d = p.d, q.ldd = p.ldd;
         q.dx = c.at<float>(c.L.dx), q.first = v0 == 0;
-        if (dx && T > 0 && run_dx(q, s) != hipSuccess) return V4MOE_ELAUNCH;
         if (dw) {
             const bool bf16 = dw_type == V4MOE_TYPE_BF16;
             q.dw = MmOut{static_cast<uint8_t*>(dw) + (int64_t)v0 * lddw * (bf16 ? 2 : 4), lddw, n, H, bf16, accumulate != 0};
-            if (run_dw(q, s) != hipSuccess) return V4MOE_ELAUNCH;
         }
+        const bool rows = dx && T > 0;
+        if ((rows && dw ? run_gradients(q, s) : rows ? run_dx(q, s) : dw ? run_dw(q, s) : hipSuccess) != hipSuccess)
+            return V4MOE_ELAUNCH;
     }
     if (dx && T > 0) {
         const dim3 grid((unsigned)std::min<int64_t>(over((int64_t)T * (c.H8 / 4), 256), 8192));
-        const MmVariant& t = dx_tile(T, c.H8, c.L.piece);
+        const MmVariant& t = dx_tile(T, c.H8, c.L.piece, dw && both_at_once(T, H, c.L.piece));
         if (dx_type == V4MOE_TYPE_BF16)
             hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl,
                                c.at<int>(c.L.pos), c.at<float>(c.L.dx), static_cast<uint16_t*>(dx), lddx);
