@@ -79,7 +79,7 @@ constexpr int kListAdapters = 1024;  // counters of sixteen waves fit LDS up to 
 // One block.  Each wave counts its share of the rows, the counts become places (adapter by
 // adapter, wave by wave), and the waves go through their rows again; rows of one adapter
 // among a wave's 64 find each other by a ballot for each bit of the id.
-// 8192 rows 11 us, 512 rows 7.
+// 8192 rows 9 us, 512 rows 7.
 __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t* __restrict__ ids, Listing out, int most)
 {
     extern __shared__ int counts[];               // [16][L + 1], then totals
@@ -878,15 +878,18 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, int block, int a
             for (int q = 0; q < 4; q++) at_row[q] = 32 * s + 8 * q + (lane >> 3) < n ? row(32 * s + 8 * q + (lane >> 3)) : -1;
         };
         auto load = [&](int s, v4u32 (&x)[4], v4u32 (&u)[2 * RC]) {
+            // (opaque: the addresses' parts are made anew, or they take the registers of the loads on their way)
+            int l = lane;
+            asm volatile("" : "+v"(l));
 #pragma unroll
             for (int q = 0; q < 4; q++) {
-                const int c = c0 + 8 * (lane & 7);
+                const int c = c0 + 8 * (l & 7);
                 x[q] = v4u32{0u, 0u, 0u, 0u};
                 if (at_row[q] >= 0 && c < job.N) x[q] = load8(job.x + (int64_t)at_row[q] * job.ldx, c, job.N);
             }
 #pragma unroll
             for (int q = 0; q < 2 * RC; q++) {
-                const int at = q * 64 + lane, i = 32 * s + at / SEGS, sg = at % SEGS;
+                const int at = q * 64 + l, i = 32 * s + at / SEGS, sg = at % SEGS;
                 const int j = j0 + (sg % (SEGS / 2)) * 8;
                 u[q] = v4u32{0u, 0u, 0u, 0u};
                 if (i < n && j < p.rp)
@@ -972,17 +975,22 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, int block, int a
         }
     }
     if (any == 0 && p.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
-    // lane: rank 16 c + r16, columns 16 t + 4 kq .. + 3
+    // The sums of the waves that had steps, in their order, to where neighbouring lanes have neighbouring columns (in
+    // the instruction's result, lane: rank 16 c + r16, columns 16 t + 4 kq .. + 3): 16-byte segments XORed by the row,
+    // or sixteen lanes would write to the same banks.
     float* total = reinterpret_cast<float*>(lds);
     static_assert(sizeof(lds) >= 16 * RC * 64 * 4, "the sums fit");
+    auto total_at = [&](int j, int sg) { return total + j * 64 + (sg ^ (j & 15)) * 4; };
+    const int waves = LISTED ? max(1, min(4, (any + 31) / 32)) : 4;
     for (int w = 0; w < 4; w++) {
+        if (w >= waves) break;
         __syncthreads();
         if (wave == w) {
 #pragma unroll
             for (int c = 0; c < RC; c++)
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    float4* to = reinterpret_cast<float4*>(total + (16 * c + r16) * 64 + 16 * t + 4 * kq);
+                    float4* to = reinterpret_cast<float4*>(total_at(16 * c + r16, 4 * t + kq));
                     float4 v = make_float4(acc[c][t][0], acc[c][t][1], acc[c][t][2], acc[c][t][3]);
                     if (w > 0) {
                         const float4 b = *to;
@@ -993,18 +1001,26 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, int block, int a
         }
     }
     __syncthreads();
-    for (int i = tid; i < 16 * RC * 64; i += 256) {
-        const int j = j0 + i / 64, c = c0 + i % 64;
-        if (j >= p.r || c >= job.N) continue;
-        const int64_t to = ((int64_t)a * p.r + j) * job.N + c;
-        if (job.bf16) {
-            uint16_t* d = static_cast<uint16_t*>(job.d) + to;
-            *d = (uint16_t)bf16x2(p.accumulate ? bf16_to_f32(*d) + total[i] : total[i], 0.0f);
-        } else {
-            float* d = static_cast<float*>(job.d) + to;
-            *d = p.accumulate ? *d + total[i] : total[i];
+    auto store = [&](auto* d) {
+        using T = std::remove_reference_t<decltype(*d)>;
+#pragma unroll 1
+        for (int i = tid; i < 16 * RC * 8; i += 256) {
+            const int jr = i >> 3, sg = i & 7, j = j0 + jr, c = c0 + 8 * sg;
+            if (j >= p.r || c >= job.N) continue;
+            T* row = d + ((int64_t)a * p.r + j) * job.N;
+            const float4 lo = *reinterpret_cast<const float4*>(total_at(jr, 2 * sg)), hi = *reinterpret_cast<const float4*>(total_at(jr, 2 * sg + 1));
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (p.accumulate) {
+                Eight<T> old;
+                old.load(row, c, job.N);
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[e] = old[e] + v[e];
+            }
+            store8f(row, c, job.N, v);
         }
-    }
+    };
+    if (job.bf16) store(static_cast<uint16_t*>(job.d));
+    else store(static_cast<float*>(job.d));
 }
 
 template <int RC, bool LISTED>
@@ -1028,8 +1044,20 @@ __global__ __launch_bounds__(256, RC < 4 ? 3 : 2) void k_lora_gradients(OuterArg
 }
 
 // ---- host ----
-// Whether the rows are listed first: from a few hundred on the tiles' gain outweighs the launch (see k_lora_list).
-bool listed_first(int M, int L) { return M > 256 && L <= kListAdapters; }
+// Whether the rows are listed first.  Unlisted, a tile of 16 rows is gone over once for each adapter among them, up to
+// min(L, 16) times; listed, a tile of 64 has one, but the list takes a launch of 7 to 10 us.  Times in us, K = N = 4096,
+// rank 16, unlisted / listed, rows in any order (in runs):
+//                3 adapters                     16 adapters
+//   rows     forward       backward       forward          backward
+//    512   13/21 (13/21)  22/22 (22/22)   22/21 (14/21)    50/35 (36/34)
+//   1024   18/22 (16/22)  33/27 (30/27)   35/25 (16/24)    72/41 (42/41)
+//   2048   25/27 (19/28)  46/32 (37/32)   53/30 (20/29)   103/46 (52/44)
+//   8192   63/48 (47/49) 122/78 (95/77)  159/50 (49/49)   304/87 (123/84)
+// The order is not known here: the rules lie between.
+bool listed_first(int M, int L, bool backward)
+{
+    return (int64_t)M * std::min(L, 16) > (backward ? 1000 : 8192) && L <= kListAdapters;
+}
 int64_t most_tiles(int64_t M, int64_t L) { return M / kTile + std::min<int64_t>(M, L + 1); }
 
 hipError_t run_list(int M, int L, const int32_t* ids, const Listing& list, hipStream_t s)
@@ -1078,7 +1106,7 @@ hipError_t launch_ring(const ShrinkArgs& p, int jobs, hipStream_t s)
 }
 hipError_t run_shrink(const ShrinkArgs& p, int jobs, hipStream_t s)
 {
-    if (!listed_first(p.M, p.L)) return shrink_by_rank<false>(p, jobs, s);
+    if (!p.list.order) return shrink_by_rank<false>(p, jobs, s);
     for (int j = 0; j < jobs; j++)
         if (!in_place(p.job[j].x, p.job[j].K, p.job[j].ldx) || !aligned_to(p.job[j].f, 16)) return shrink_by_rank<true>(p, jobs, s);
     if (p.r <= 16) return launch_ring<1, 4>(p, jobs, s);
@@ -1089,7 +1117,7 @@ hipError_t run_shrink(const ShrinkArgs& p, int jobs, hipStream_t s)
 template <int RC>
 hipError_t launch_expand(const ExpandArgs& p, int bf16, hipStream_t s)
 {
-    if (listed_first(p.M, p.L)) {
+    if (p.list.order) {
         const int64_t blocks = over(p.N, 256) * most_tiles(p.M, p.L);
         if (blocks > INT32_MAX) return hipErrorInvalidValue;
         auto run = [&](auto one) {
@@ -1132,7 +1160,7 @@ hipError_t outer_by_rank(const OuterArgs& p, hipStream_t s)
 }
 hipError_t run_outer(const OuterArgs& p, hipStream_t s)
 {
-    return listed_first(p.M, p.L) ? outer_by_rank<true>(p, s) : outer_by_rank<false>(p, s);
+    return p.list.order ? outer_by_rank<true>(p, s) : outer_by_rank<false>(p, s);
 }
 
 // Both gradients, in one launch where the rows are listed and all ranks fit a block.
@@ -1147,7 +1175,7 @@ hipError_t launch_gradients(const OuterArgs& o, const ExpandArgs& e, int bf16, h
 }
 hipError_t run_gradients(const OuterArgs& o, const ExpandArgs& e, int bf16, hipStream_t s)
 {
-    if (listed_first(o.M, o.L) && o.r <= 64) {
+    if (o.list.order && o.r <= 64) {
         if (o.r <= 16) return launch_gradients<1>(o, e, bf16, s);
         if (o.r <= 32) return launch_gradients<2>(o, e, bf16, s);
         return launch_gradients<4>(o, e, bf16, s);
@@ -1158,14 +1186,14 @@ hipError_t run_gradients(const OuterArgs& o, const ExpandArgs& e, int bf16, hipS
 
 int ranks(int r) { return (r + 15) / 16 * 16; }
 size_t lora_u(int64_t M, int r) { return up256((size_t)(M * 2 * ranks(r) * 2)); }
-size_t lora_list(int M, int L)
+size_t lora_list(int M, int L, bool backward)
 {
-    if (!listed_first(M, L)) return 0;
+    if (!listed_first(M, L, backward)) return 0;
     return up256((size_t)M * 4) + up256((size_t)(L + 2) * 4) + 256 + up256((size_t)most_tiles(M, L) * sizeof(Tile));
 }
-Listing listing(uint8_t* ws, int M, int L)
+Listing listing(uint8_t* ws, int M, int L, bool backward)
 {
-    if (!listed_first(M, L)) return Listing{};
+    if (!listed_first(M, L, backward)) return Listing{};
     Listing l;
     l.order = reinterpret_cast<int*>(ws);
     l.begin = reinterpret_cast<int*>(ws += up256((size_t)M * 4));
@@ -1199,7 +1227,7 @@ extern "C" {
 __attribute__((visibility("default"))) size_t moe_lora_workspace_bytes(const v4moe_lora* p, int32_t backward)
 {
     if (check_lora(p)) return 0;
-    return lora_list(p->M, p->L) + lora_u(p->M, p->r) * (backward ? 2 : 1);
+    return lora_list(p->M, p->L, backward != 0) + lora_u(p->M, p->r) * (backward ? 2 : 1);
 }
 
 __attribute__((visibility("default"))) int moe_lora_add(const v4moe_lora* p, const void* y, int32_t type, int64_t ldy,
@@ -1221,9 +1249,9 @@ __attribute__((visibility("default"))) int moe_lora_add(const v4moe_lora* p, con
     if (!device_ready()) return V4MOE_EDEVICE;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const Listing list = listing(ws, p->M, p->L);
+    const Listing list = listing(ws, p->M, p->L, false);
     if (list.order && run_list(p->M, p->L, ids, list, s) != hipSuccess) return V4MOE_ELAUNCH;
-    uint16_t* u = reinterpret_cast<uint16_t*>(ws + lora_list(p->M, p->L));
+    uint16_t* u = reinterpret_cast<uint16_t*>(ws + lora_list(p->M, p->L, false));
     const int rp = ranks(p->r);
     const ShrinkArgs sh{p->M, p->L, p->r, rp, ids, scale, {{x, ldx, p->K, a, u}, {}}, list};
     if (run_shrink(sh, 1, s) != hipSuccess) return V4MOE_ELAUNCH;
@@ -1260,9 +1288,9 @@ __attribute__((visibility("default"))) int moe_lora_backward(
     if (!device_ready()) return V4MOE_EDEVICE;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const Listing list = listing(ws, p->M, p->L);
+    const Listing list = listing(ws, p->M, p->L, true);
     if (list.order && run_list(p->M, p->L, ids, list, s) != hipSuccess) return V4MOE_ELAUNCH;
-    ws += lora_list(p->M, p->L);
+    ws += lora_list(p->M, p->L, true);
     uint16_t* du = reinterpret_cast<uint16_t*>(ws);
     uint16_t* u = reinterpret_cast<uint16_t*>(ws + lora_u(p->M, p->r));
     const int rp = ranks(p->r);
