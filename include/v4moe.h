@@ -469,7 +469,8 @@ int moe_clip_grads(int32_t count, const v4moe_tensor* tensors, float max_norm, f
  * Sums are fp32, in an order that depends on the contraction alone: a row's result
  * does not depend on the other rows.  Rows before the first expert's and behind the
  * last one's take no part, and those of outputs are left as they are.  Pointers:
- * aligned to their element. */
+ * aligned to their element.  What a call writes must not overlap what it reads, but
+ * for gradients added to (here and in the two sections below, where more is said). */
 
 /* Workspace bytes of the calls below (host-only, pure; 0 for invalid sizes): operands
  * whose rows do not begin at 16 bytes, or are not a multiple of 8 elements long, are

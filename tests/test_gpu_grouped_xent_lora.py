@@ -331,3 +331,61 @@ def test_adapters_by_the_thousand_and_rows_beyond(M, L):
             most[k] = (f.double()[i[k]].abs() * q[k, None].abs()).sum(2) * s[k, None]
         mag.index_add_(0, i, most[:, :, None] * w.abs()[:, None])
         near(got, want, mag * ((72 + 64) * STEP32 + 2.0 ** -16 + (2 * n + 64) * STEP32))
+
+
+def test_nothing_to_do():
+    """Empty batches: empty results, gradients of weights of zeros, or left alone where added to."""
+    x, w, off = ones(0, 16), ones(3, 8, 16), torch.zeros(4, dtype=torch.int32, device=DEV)
+    assert v4moe.grouped_linear(x, w, off).shape == (0, 8)
+    dx, dw = v4moe.grouped_linear_backward(x, ones(0, 8), w, off)
+    assert dx.shape == (0, 16) and not dw.any()
+    held = ones(3, 8, 16)
+    v4moe.grouped_linear_backward(x, ones(0, 8), w, off, dw=held, accumulate=True)
+    head, t, f = ones(9, 16), torch.zeros(0, dtype=torch.int64, device=DEV), ones(0, t=F32)
+    loss, lse = v4moe.linear_xent(x, head, t)
+    assert loss.shape == lse.shape == (0,)
+    dx, dhead = v4moe.linear_xent_backward(x, head, t, lse, f)
+    assert dx.shape == (0, 16) and not dhead.any()
+    kept = ones(9, 16)
+    v4moe.linear_xent_backward(x, head, t, lse, f, dw=kept, accumulate=True)
+    a, b, ids, scale = ones(2, 3, 16), ones(2, 3, 8), torch.zeros(0, dtype=torch.int32, device=DEV), ones(2, t=F32)
+    assert v4moe.lora_add(ones(0, 8), x, a, b, ids, scale).shape == (0, 8)
+    dx, da, db = v4moe.lora_backward(x, ones(0, 8), a, b, ids, scale)
+    assert dx.shape == (0, 16) and not da.any() and not db.any()
+    da, db = ones(2, 3, 16), ones(2, 3, 8)
+    v4moe.lora_backward(x, ones(0, 8), a, b, ids, scale, da=da, db=db, accumulate=True)
+    torch.cuda.synchronize()
+    assert all(bool((t == 1).all()) for t in (held, kept, da, db))
+
+
+def test_beyond_32_bits():
+    """Operands of more than 2^32 bytes: the last rows equal those of a small call (a row does not depend on others)."""
+    M, K, N = 300007, 8192, 48
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.empty(M, K, dtype=BF16, device=DEV).normal_(generator=g)
+    w = torch.randn(2, N, K, generator=g, device=DEV).to(BF16)
+    off = torch.tensor([0, M - 100, M], dtype=torch.int32, device=DEV)
+    last = slice(M - 100, M)
+    y = v4moe.grouped_linear(x, w, off)
+    few = torch.tensor([0, 0, 100], dtype=torch.int32, device=DEV)
+    assert torch.equal(y[last], v4moe.grouped_linear(x[last].clone(), w, few))
+    dx, dw = v4moe.grouped_linear_backward(x, y, w, off)
+    small = v4moe.grouped_linear_backward(x[last].clone(), y[last].clone(), w, few)
+    assert torch.equal(dx[last], small[0]) and torch.equal(dw[1], small[1][1])
+    a, b, scale = w[:, :8].contiguous(), torch.randn(2, 8, N, generator=g, device=DEV).to(BF16), torch.ones(2, device=DEV)
+    ids = (torch.arange(M, device=DEV) >= M - 100).to(torch.int32)
+    out = v4moe.lora_add(y, x, a, b, ids, scale)
+    assert torch.equal(out[last], v4moe.lora_add(y[last], x[last].clone(), a, b, ids[last], scale))
+    dx2, da, _ = v4moe.lora_backward(x, y, a, b, ids, scale, dx=dx)
+    small = v4moe.lora_backward(x[last].clone(), y[last].clone(), a, b, ids[last], scale)
+    assert torch.equal(dx2[last], small[0])
+    near(da[1].float(), small[1][1].double(), 2.0 ** -7 * small[1][1].double().abs())        # (the rows' order of waves may differ)
+    # the head's rows are the long operand
+    t = torch.tensor([0, M - 1, 77, M - 50], device=DEV)
+    few = torch.randn(4, K, generator=g, device=DEV).mul_(K ** -0.5).to(BF16)
+    loss, lse = v4moe.linear_xent(few, x, t)
+    z = few.float() @ x[t].float().t()
+    assert bool(((lse - z.diagonal()) - loss).abs().max() <= 2.0 ** -23 * ((K + 64) * (few.float().abs() @ x[t].float().abs().t()).max() + 64 * lse.abs().max()))
+    dhead = v4moe.linear_xent_backward(few, x, t, lse, torch.ones(4, device=DEV), dw=dx)[1]
+    alone = v4moe.linear_xent_backward(few, x[t].clone(), torch.arange(4, device=DEV), lse, torch.ones(4, device=DEV))[1]
+    assert torch.equal(dhead[t], alone)
