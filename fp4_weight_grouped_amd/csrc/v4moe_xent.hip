@@ -33,7 +33,7 @@ struct XentCtrl { int n; float largest; };
 
 __device__ __forceinline__ float exp_(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-// (One block: 5 us to 4096 tokens, 10 at 8192, beside products that take milliseconds by then.)
+// (More than kFewTokens of them; one block: 10 us at 8192, beside products that take milliseconds by then.)
 // Numbers the tokens with a target: pos[t] their place among them (-1 for the others),
 // idx the tokens in order.  One block: 4096 tokens a step.
 // loss, lse (or null): zeros for the tokens without one.  g (or null): the incoming gradients.
@@ -98,34 +98,104 @@ __global__ __launch_bounds__(1024) void k_xent_rows(int T, int V, const int64_t*
 
 // The packed rows: x [n][H8] (zeros past H), targets, and in the backward lse and g / largest
 // (a mean's gradients are equal: theirs is exactly 1, and d is not rounded twice).
-__global__ __launch_bounds__(256) void k_xent_pack(int H, int H8, const uint16_t* __restrict__ x, int64_t ldx,
-                                                   const int64_t* __restrict__ targets, const float* __restrict__ lse,
-                                                   const float* __restrict__ g, int64_t gs, const int* __restrict__ idx,
-                                                   const XentCtrl* __restrict__ ctrl, uint16_t* __restrict__ xp,
-                                                   int* __restrict__ yp, float* __restrict__ lsep, float* __restrict__ gp)
+struct PackArgs {
+    int H, H8;
+    const uint16_t* x; int64_t ldx;
+    const int64_t* targets;
+    const float *lse, *g; int64_t gs;           // (or null)
+    uint16_t* xp; int* yp; float *lsep, *gp;
+};
+// row(r): the r-th token with a target
+template <typename F>
+__device__ __forceinline__ void pack_rows(const PackArgs& p, int n, float largest, F&& row)
 {
-    const int segs = H8 / 8;
-    const int64_t all = (int64_t)ctrl->n * segs;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int r = (int)(i / segs), c = (int)(i - (int64_t)r * segs) * 8, t = idx[r];
-        const uint16_t* s = x + t * ldx + c;
+    const int segs = p.H8 / 8;
+    const int64_t all = (int64_t)n * segs;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
+        const int r = (int)(i / segs), c = (int)(i - (int64_t)r * segs) * 8, t = row(r);
+        const uint16_t* s = p.x + t * p.ldx + c;
         v4u32 v;
-        if (c + 8 <= H) {
+        if (c + 8 <= p.H) {
             v = *reinterpret_cast<const v4u32_any*>(s);
         } else {
 #pragma unroll
             for (int u = 0; u < 4; u++)
-                v[u] = (c + 2 * u < H ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < H ? (uint32_t)s[2 * u + 1] << 16 : 0u);
+                v[u] = (c + 2 * u < p.H ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < p.H ? (uint32_t)s[2 * u + 1] << 16 : 0u);
         }
-        *reinterpret_cast<v4u32*>(xp + (int64_t)r * H8 + c) = v;
+        *reinterpret_cast<v4u32*>(p.xp + (int64_t)r * p.H8 + c) = v;
         if (c == 0) {
-            yp[r] = (int)targets[t];
-            if (g) {
-                lsep[r] = lse[t];
-                gp[r] = g[t * gs] / ctrl->largest;
+            p.yp[r] = (int)p.targets[t];
+            if (p.g) {
+                p.lsep[r] = p.lse[t];
+                p.gp[r] = p.g[t * p.gs] / largest;
             }
         }
     }
+}
+__global__ __launch_bounds__(256) void k_xent_pack(PackArgs p, const int* __restrict__ idx, const XentCtrl* __restrict__ ctrl)
+{
+    pack_rows(p, ctrl->n, ctrl->largest, [&](int r) { return idx[r]; });
+}
+
+// Both at once, where one step numbers every token: each block does so for itself, the first one for the later kernels
+// too (1.4 to 2 us less than two launches: 23 tokens, V = 704, H = 64 12.7 -> 11.2 us as a whole, 512 tokens, V = 2048,
+// H = 512 19.9 -> 18.3).
+constexpr int kFewTokens = 4096;
+__global__ __launch_bounds__(1024) void k_xent_rows_pack(int T, int V, PackArgs p, int* __restrict__ pos, int* __restrict__ idx,
+                                                         XentCtrl* __restrict__ ctrl, float* __restrict__ loss,
+                                                         float* __restrict__ lse)
+{
+    __shared__ uint16_t token[kFewTokens];
+    __shared__ int totals[16];
+    __shared__ float largest[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t0 = 4 * tid;
+    const bool first = blockIdx.x == 0;
+    bool has[4];
+    int mine = 0;
+    float big = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        has[u] = false;
+        if (t0 + u < T) {
+            const int64_t y = p.targets[t0 + u];
+            has[u] = y >= 0 && y < V;
+            if (has[u] && p.g) {
+                const float f = fabsf(p.g[(t0 + u) * p.gs]);
+                if (f < INFINITY) big = fmaxf(big, f);
+            }
+            if (first && !has[u] && loss) loss[t0 + u] = lse[t0 + u] = 0.0f;
+        }
+        mine += has[u];
+    }
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(scan, o);
+        if (lane >= o) scan += v;
+        big = fmaxf(big, __shfl_xor(big, o));
+    }
+    if (lane == 63) totals[wave] = scan, largest[wave] = big;
+    __syncthreads();
+    int at = scan - mine, n = 0;
+    big = 0.0f;
+    for (int w = 0; w < 16; w++) {
+        if (w < wave) at += totals[w];
+        n += totals[w];
+        big = fmaxf(big, largest[w]);
+    }
+    big = big > 0.0f ? big : 1.0f;
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+        if (t0 + u < T) {
+            if (first) pos[t0 + u] = has[u] ? at : -1;
+            if (has[u]) {
+                if (first) idx[at] = t0 + u;
+                token[at++] = (uint16_t)(t0 + u);
+            }
+        }
+    if (first && tid == 0) *ctrl = XentCtrl{n, big};
+    __syncthreads();
+    pack_rows(p, n, big, [&](int r) { return (int)token[r]; });
 }
 
 struct LogitsArgs {
@@ -592,13 +662,19 @@ int xent_begin(XentCall& c, int32_t T, int32_t H, int32_t V, const uint16_t* x, 
         c.w = job.dst;
         c.ldw = c.H8;
     }
-    hipLaunchKernelGGL(k_xent_rows, dim3(1), dim3(1024), 0, s, T, V, targets, g, gs, c.at<int>(c.L.pos), c.at<int>(c.L.idx),
-                       c.at<XentCtrl>(c.L.ctrl), loss, lse);
-    const int64_t blocks = over((int64_t)T * (c.H8 / 8), 256);
-    if (blocks > 0)
-        hipLaunchKernelGGL(k_xent_pack, dim3((unsigned)std::min<int64_t>(blocks, 8192)), dim3(256), 0, s, H, c.H8, x, ldx, targets,
-                           lse_in, g, gs, c.at<int>(c.L.idx), c.at<XentCtrl>(c.L.ctrl), c.at<uint16_t>(c.L.x),
-                           c.at<int>(c.L.y), c.at<float>(c.L.lse), c.at<float>(c.L.g));
+    const PackArgs p{H, c.H8, x, ldx, targets, lse_in, g, gs, c.at<uint16_t>(c.L.x), c.at<int>(c.L.y), c.at<float>(c.L.lse),
+                     c.at<float>(c.L.g)};
+    const int64_t segs = (int64_t)T * (c.H8 / 8);
+    if (T <= kFewTokens) {
+        const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(over(segs, 1024), 512));
+        hipLaunchKernelGGL(k_xent_rows_pack, dim3(blocks), dim3(1024), 0, s, T, V, p, c.at<int>(c.L.pos), c.at<int>(c.L.idx),
+                           c.at<XentCtrl>(c.L.ctrl), loss, lse);
+    } else {
+        hipLaunchKernelGGL(k_xent_rows, dim3(1), dim3(1024), 0, s, T, V, targets, g, gs, c.at<int>(c.L.pos), c.at<int>(c.L.idx),
+                           c.at<XentCtrl>(c.L.ctrl), loss, lse);
+        hipLaunchKernelGGL(k_xent_pack, dim3((unsigned)std::min<int64_t>(over(segs, 256), 8192)), dim3(256), 0, s, p,
+                           c.at<int>(c.L.idx), c.at<XentCtrl>(c.L.ctrl));
+    }
     return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }
 

@@ -389,3 +389,31 @@ def test_beyond_32_bits():
     dhead = v4moe.linear_xent_backward(few, x, t, lse, torch.ones(4, device=DEV), dw=dx)[1]
     alone = v4moe.linear_xent_backward(few, x[t].clone(), torch.arange(4, device=DEV), lse, torch.ones(4, device=DEV))[1]
     assert torch.equal(dhead[t], alone)
+
+
+@pytest.mark.parametrize("T", [1, 3, 4095, 4096, 4097, 8193])
+def test_tokens_on_each_side_of_the_ways_to_number_them(T):
+    """Losses of a batch equal those of its halves, bit for bit; all against 64 bits."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x, w = torch.randn(T, 96, generator=g, device=DEV).to(BF16), torch.randn(200, 96, generator=g, device=DEV).mul_(0.1).to(BF16)
+    t = torch.randint(-60, 260, (T,), generator=g, device=DEV)
+    has = (t >= 0) & (t < 200)
+    loss, lse = v4moe.linear_xent(x, w, t)
+    assert not loss[~has].any() and not lse[~has].any()
+    half = (T + 1) // 2
+    for part in (slice(0, half), slice(half, T)):
+        a, b = v4moe.linear_xent(x[part], w, t[part].contiguous())
+        assert torch.equal(a, loss[part]) and torch.equal(b, lse[part])
+    z = x.double() @ w.double().t()
+    want = torch.logsumexp(z, 1) * has
+    near(lse, want, ((96 + 64) * STEP32 * (x.double().abs() @ w.double().abs().t()).amax(1) + (200 + 64) * STEP32 + want.abs() * 4 * STEP32 + 8 * STEP32))
+    dloss = torch.rand(T, generator=g, device=DEV)
+    dx, dw = v4moe.linear_xent_backward(x, w, t, lse, dloss, dx=torch.empty(T, 96, device=DEV), dw=torch.empty(200, 96, device=DEV))
+    p = (z - want[:, None]).exp()
+    hot = torch.zeros_like(p).scatter_(1, t.clamp(0, 199)[:, None], 1.0)
+    d = (p - hot) * (has * dloss.double())[:, None]
+    each = (96 + 64) * STEP32 * (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True) + (200 + 64) * STEP32 + 16 * STEP32
+    db = (p * 3 * each * dloss.double()[:, None] + d.abs() * (2.0 ** -8 + 8 * STEP32)) * has[:, None]
+    wa, xa = w.double().abs(), x.double().abs()
+    near(dx, d @ w.double(), db @ wa + (200 + 64) * STEP32 * ((d.abs() + db) @ wa))
+    near(dw, d.t() @ x.double(), db.t() @ xa + (T + 64) * STEP32 * ((d.abs() + db).t() @ xa))
