@@ -13,7 +13,11 @@
 // Forward: the logits of a tile end in registers, where each row's maximum and sum of
 // exponentials over 64 columns are taken; the parts are joined in a fixed order.
 // Backward: pieces of the vocabulary, of which d is held in bf16 (at most about 256 MiB);
-// the logits are computed again from the same operands, in the same order.
+// the logits are computed again from the same operands, in the same order.  Most of a
+// gradient is its target's term, -g W[y_t] and -g x_t, so that d there is not left at
+// 8 bits: what its rounding left, one number a token, is added to both products (dx: in
+// fp32 where its slices meet; dW: as 16 bits in all, by one more product of the few tokens
+// whose target a tile has).
 #include "v4moe.h"
 #include "v4moe_device.h"
 #include "v4moe_internal.h"
@@ -198,6 +202,13 @@ __global__ __launch_bounds__(1024) void k_xent_rows_pack(int T, int V, PackArgs 
     pack_rows(p, n, big, [&](int r) { return (int)token[r]; });
 }
 
+// What rounding to bf16 leaves of v (0 of what is no number, which stands alone).
+__device__ __forceinline__ float rounding_of(float v)
+{
+    const float hi = bf16_to_f32(bf16x2(v, 0.0f) & 0xFFFFu);
+    return fabsf(hi) < INFINITY ? v - hi : 0.0f;
+}
+
 struct LogitsArgs {
     int T, H, V;                       // V: columns of this piece
     int v0;                            // its first
@@ -210,6 +221,7 @@ struct LogitsArgs {
     // backward
     const float* lse; const float* g;
     uint16_t* d; int64_t ldd;
+    float* rest;                       // what d's rounding left at each token's target
 };
 
 // Logits of a piece, a tile per block, and what becomes of them.  16 tokens, H = 4096, V = 131072: 172 us, W's bytes at
@@ -295,6 +307,13 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
             }
 #pragma unroll
             for (int j = 0; j < L::NI; j++) acc[i][j] *= g;
+            if (target) {
+#pragma unroll
+                for (int j = 0; j < L::NI; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (y == 16 * j + 4 * kq + e) p.rest[m] = rounding_of(acc[i][j][e]);
+            }
             if (end) {
 #pragma unroll
                 for (int j = 0; j < L::NI; j++)
@@ -354,6 +373,7 @@ struct XentGradArgs {
     const XentCtrl* ctrl;
     const uint16_t* x; const uint16_t* w; int64_t ldw;
     const uint16_t* d; int64_t ldd;
+    int v0; const int* y; const float* rest;
     float* dx;                          // [slices][n][H8] of the n packed rows
     int first;                          // the first piece writes dx, the others add to it
     MmOut dw;                           // the piece's rows
@@ -389,6 +409,79 @@ __device__ __forceinline__ void dx_block(const XentGradArgs& p, int block, uint8
     mm_store_tile<L>(acc, smem, o, im * L::BM, in * L::BN);
 }
 
+// Adds what d's rounding left at the targets to a tile of dW: rest[t] x[t] to row y[t].  The block looks through the
+// tokens together, eight a thread at a time; each wave lists those whose target is one of its rows, in order, and
+// multiplies 32 of them at a time.  4096 tokens, tiles of 256x256: 8 us a tile, nearly all of it the latency of three loads
+// in a row (each wave by itself through all tokens 18; steps of 32 tokens that follow each other, as they come, 10).  One
+// target for all 4096, so that one tile has them all: both gradients of 131072 columns 10300 -> 11400 us.
+template <class L>
+__device__ __forceinline__ void add_targets(const XentGradArgs& p, int n, int m0, int n0, uint8_t* smem, v4f (&acc)[L::MI][L::NI])
+{
+    static_assert(!L::RAGGED, "a wave's rows follow each other");
+    constexpr int ROWS = L::MI * 16, NW = L::NW, WORDS = 8 * NW, TOKENS = 64 * WORDS;
+    static_assert(WORDS <= 64 && L::WM * WORDS * 8 + NW * TOKENS * 2 <= L::BYTES, "a word for a lane; a list for a wave");
+    typedef short v8s __attribute__((ext_vector_type(8)));
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), wm = wave / L::WN;
+    const int origin = p.v0 + m0, rows = min(L::BM, p.V - m0), column = n0 + wave % L::WN * L::NI * 16 + r16;
+    uint64_t* words = reinterpret_cast<uint64_t*>(smem);                     // [WM][WORDS]: who has a target in the wave's rows
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + L::WM * WORDS * 8) + wave * TOKENS;
+    for (int base = 0; base < n; base += TOKENS) {
+        if (base > 0) __syncthreads();                                       // (the words before are read)
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            const int t = base + 64 * (8 * wave + u) + lane;
+            const int row = t < n ? p.y[t] - origin : -1;
+#pragma unroll
+            for (int w = 0; w < L::WM; w++) {
+                const uint64_t in = __ballot(row >= w * ROWS && row < min((w + 1) * ROWS, rows));
+                if (lane == 0) words[w * WORDS + 8 * wave + u] = in;
+            }
+        }
+        __syncthreads();
+        uint64_t mine = lane < WORDS ? words[wm * WORDS + lane] : 0;
+        int at = __popcll(mine), all = at;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(all, o);
+            if (lane >= o) all += v;
+        }
+        at = all - at;
+        all = __builtin_amdgcn_readlane(all, 63);
+        for (; mine; mine &= mine - 1) list[at++] = (uint16_t)(64 * lane + __builtin_ctzll(mine));
+        __builtin_amdgcn_wave_barrier();
+        for (int k0 = 0; k0 < all; k0 += 32) {
+            v8s rest, x[L::NI];
+            int row[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int k = k0 + 8 * kq + e, t = base + list[min(k, all - 1)];
+                row[e] = p.y[t] - origin - L::first_row(wm);
+                rest[e] = k < all ? (short)bf16x2(p.rest[t], 0.0f) : (short)0;
+#pragma unroll
+                for (int j = 0; j < L::NI; j++) x[j][e] = (short)p.x[(int64_t)t * p.H8 + min(column + 16 * j, p.H8 - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < L::MI; i++) {
+                v8s a;
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const bool here = row[e] == 16 * i + r16;
+                    any |= here;
+                    a[e] = here ? rest[e] : (short)0;
+                }
+                if (!__ballot(any)) continue;
+#pragma unroll
+                for (int j = 0; j < L::NI; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[j]), __builtin_bit_cast(v8bf, a),
+                                                                        acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+    __syncthreads();                                                         // (the block's LDS is free)
+}
+
 // The piece's rows of dW: the packed tokens are the contraction (the same sizes 798 us).
 template <class L>
 __device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, int block, uint8_t* smem)
@@ -400,6 +493,7 @@ __device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, 
     const MmOperand a{p.d, p.ldd, (p.V + 7) / 8 * 8}, b{p.x, p.H8, p.H8};
     v4f acc[L::MI][L::NI];
     mm_tile<L>(a, b, im * L::BM, in * L::BN, n, smem, acc);
+    add_targets<L>(p, n, im * L::BM, in * L::BN, smem, acc);
     const float s = p.ctrl->largest;
 #pragma unroll
     for (int i = 0; i < L::MI; i++)
@@ -430,12 +524,15 @@ __global__ __launch_bounds__(X::THREADS) void k_xent_gradients(XentGradArgs p, i
     else dw_block<W>(p, tm, tn, (int)blockIdx.x - xblocks, smem);
 }
 
-// dx of every token: the slices' sums in order, times the largest |g|; zeros without a target.
+// dx of every token: the slices' sums in order and what d's rounding left at the target, times the largest |g|; zeros
+// without a target.
 template <typename T_>
 __global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int bm, int bn, int piece,
                                                      const XentCtrl* __restrict__ ctrl,
                                                      const int* __restrict__ pos, const float* __restrict__ acc,
-                                                     T_* __restrict__ dx, int64_t ld)
+                                                     const int* __restrict__ y, const float* __restrict__ rest,
+                                                     const uint16_t* __restrict__ w, int64_t ldw, T_* __restrict__ dx,
+                                                     int64_t ld)
 {
     const int quads = H8 / 4;
     const int64_t all = (int64_t)T * quads;
@@ -444,7 +541,9 @@ __global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int b
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
         const int t = (int)(i / quads), c = (int)(i - (int64_t)t * quads) * 4, m = pos[t];
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (m >= 0)
+        if (m >= 0) {
+            const v2u32 wy = *reinterpret_cast<const v2u32*>(w + y[m] * ldw + c);
+            const float left = rest[m];
             for (int k = 0; k < slices; k += 4) {
                 float4 f[4];
 #pragma unroll
@@ -459,6 +558,11 @@ __global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int b
                     v[3] += f[u].w;
                 }
             }
+            v[0] += left * bf16_to_f32(wy[0] & 0xFFFFu);
+            v[1] += left * bf16_to_f32(wy[0] >> 16);
+            v[2] += left * bf16_to_f32(wy[1] & 0xFFFFu);
+            v[3] += left * bf16_to_f32(wy[1] >> 16);
+        }
         T_* o = dx + t * ld + c;
         if constexpr (sizeof(T_) == 2) {
             const uint32_t lo = bf16x2(v[0] * s, v[1] * s), hi = bf16x2(v[2] * s, v[3] * s);
@@ -580,7 +684,7 @@ hipError_t run_gradients(const XentGradArgs& p, hipStream_t s)
 }
 
 struct XentLayout {
-    size_t ctrl, idx, pos, y, zy, x, parts, lse, g, d, dx, w, total;
+    size_t ctrl, idx, pos, y, zy, x, parts, lse, g, rest, d, dx, w, total;
     bool pad_w;
     int piece;                      // columns of a piece
 };
@@ -611,6 +715,7 @@ XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t l
         L.piece = (int)std::min(most, (V + 255) / 256 * 256);
         L.lse = take(T * 4);
         L.g = take(T * 4);
+        L.rest = take(T * 4);
         L.d = take(T * (int64_t)L.piece * 2);
         // dx of every row, or of fewer rows in slices: dx_blocks tiles then (of either tile, with dW or alone)
         int64_t most_dx = T * H8;
@@ -752,12 +857,14 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         p.y = c.at<int>(c.L.y);
         p.lse = c.at<float>(c.L.lse), p.g = c.at<float>(c.L.g);
         p.d = c.at<uint16_t>(c.L.d), p.ldd = c.L.piece;
+        p.rest = c.at<float>(c.L.rest);
         if (T > 0 && run_logits<true>(p, s) != hipSuccess) return V4MOE_ELAUNCH;
         XentGradArgs q{};
         q.T = T, q.H = H, q.H8 = c.H8, q.V = n;
         q.piece = c.L.piece;
         q.ctrl = ctrl;
         q.x = p.x, q.w = p.w, q.ldw = p.ldw, q.d = p.d, q.ldd = p.ldd;
+        q.v0 = v0, q.y = p.y, q.rest = p.rest;
         q.dx = c.at<float>(c.L.dx), q.first = v0 == 0;
         if (dw) {
             const bool bf16 = dw_type == V4MOE_TYPE_BF16;
@@ -772,10 +879,12 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         const MmVariant& t = dx_tile(T, c.H8, c.L.piece, dw && both_at_once(T, H, c.L.piece));
         if (dx_type == V4MOE_TYPE_BF16)
             hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl,
-                               c.at<int>(c.L.pos), c.at<float>(c.L.dx), static_cast<uint16_t*>(dx), lddx);
+                               c.at<int>(c.L.pos), c.at<float>(c.L.dx), c.at<int>(c.L.y), c.at<float>(c.L.rest), c.w, c.ldw,
+                               static_cast<uint16_t*>(dx), lddx);
         else
             hipLaunchKernelGGL(k_xent_finish<float>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl, c.at<int>(c.L.pos),
-                               c.at<float>(c.L.dx), static_cast<float*>(dx), lddx);
+                               c.at<float>(c.L.dx), c.at<int>(c.L.y), c.at<float>(c.L.rest), c.w, c.ldw, static_cast<float*>(dx),
+                               lddx);
     }
     return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }

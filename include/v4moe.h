@@ -519,8 +519,9 @@ int moe_linear_xent(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t 
  *   d[t][v] = dloss[t] (exp(z[t][v] - lse[t]) - [v = targets[t]])
  *   dx [T][lddx] = d W;  dW [V][lddw] (+)= d^T x (accumulate: added to in fp32, rounded once)
  * dx or dw may be NULL.  dloss fp32, element t at dloss[t * dloss_stride] (0: one for all).
- * d enters the products in bf16 (divided by the largest |dloss| first): fp32 results are
- * good to about 2e-3 of their 2-norm. */
+ * d enters the products in bf16 (divided by the largest |dloss| first), but at the targets
+ * in 16 bits: fp32 results are good to 1e-5 to 1e-3 of their 2-norm, the first where the
+ * probabilities are spread over many columns, the last where a few have them all. */
 int moe_linear_xent_backward(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx,
                              const uint16_t* w, int64_t ldw, const int64_t* targets, const float* lse,
                              const float* dloss, int64_t dloss_stride, void* dx, int32_t dx_type,
