@@ -648,6 +648,18 @@ def _clip_workspace_bytes(count: int) -> int:
     return int(lib().moe_clip_workspace_bytes(count))
 
 
+def _wanted(**gradients) -> None:
+    """Checks name=(asked for, given): one gradient at least is asked for, and none given that is not."""
+    _require(any(need for need, _ in gradients.values()), "no gradient is asked for")
+    for name, (need, given) in gradients.items():
+        _require(need or given is None, f"{name} is given but not asked for")
+
+
+def _out(t: Optional[torch.Tensor], ld: int = 0):
+    """(address, type, leading dimension) of a gradient for the library; of one that is not asked for, nothing."""
+    return (None, TYPE_F32, 0) if t is None else (t.data_ptr(), _type(t), ld)
+
+
 def _grouped(x, w, offsets):
     """(M, E, N, K, GPU, x's leading dimension, addresses of w and of the offsets) of a grouped product, checked."""
     M, (E, N, K) = x.shape[0], w.shape
@@ -675,23 +687,29 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out:
 
 
 def grouped_linear_backward(x: torch.Tensor, dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
-                            dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False):
-    """Gradients of grouped_linear: (dx [M][K], dw [E][N][K]), bf16 unless given; accumulate adds to the given dw."""
+                            dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False,
+                            need_dx: bool = True, need_dw: bool = True):
+    """Gradients of grouped_linear: (dx [M][K], dw [E][N][K]), bf16 unless given; accumulate adds to the given dw.  One that
+    is not needed (frozen weights', say) is not computed: None."""
     M, E, N, K, gpu, ldx, wp, op = _grouped(x, w, offsets)
     lddy = _matrix(dy, M, N, "dy", gpu, torch.bfloat16)
     stream = _raw_stream(gpu)
     dev = x.device
     _require(dw is not None or not accumulate, "accumulate needs dw")
-    if dx is None:
+    if not (need_dx and need_dw):
+        _wanted(dx=(need_dx, dx), dw=(need_dw, dw))
+    if dx is None and need_dx:
         dx = _empty(M, K, torch.bfloat16, dev)
-    if dw is None:
+    if dw is None and need_dw:
         dw = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev)
-    lddx, dwp = _matrix(dx, M, K, "dx", gpu), _dense(dw, (E, N, K), dw.dtype, "dw", gpu)
+    lddx = _matrix(dx, M, K, "dx", gpu) if need_dx else 0
+    if need_dw:
+        _dense(dw, (E, N, K), dw.dtype, "dw", gpu)
     xp, dyp = x.data_ptr(), dy.data_ptr()
     n = lib().moe_grouped_workspace_bytes(M, E, N, K, xp, ldx, dyp, lddy, wp, 1)
     ws = _bytes(n, dev) if n else None
-    _check(lib().moe_grouped_linear_backward(M, E, N, K, xp, ldx, dyp, lddy, wp, op, dx.data_ptr(), _type(dx), lddx, dwp,
-                                             _type(dw), 1 if accumulate else 0, ws.data_ptr() if n else None, n, stream))
+    _check(lib().moe_grouped_linear_backward(M, E, N, K, xp, ldx, dyp, lddy, wp, op, *_out(dx, lddx), *_out(dw)[:2],
+                                             1 if accumulate else 0, ws.data_ptr() if n else None, n, stream))
     return dx, dw
 
 
@@ -719,9 +737,11 @@ def linear_xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
 
 
 def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
-                         dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False):
+                         dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False,
+                         need_dx: bool = True, need_dw: bool = True):
     """Gradients of sum(dloss * loss) for linear_xent's loss: (dx [T][H], dw [V][H]), bf16 unless given; lse from
-    linear_xent; dloss fp32 [T], of any stride (an expanded scalar, say); accumulate adds to the given dw."""
+    linear_xent; dloss fp32 [T], of any stride (an expanded scalar, say); accumulate adds to the given dw.  One that is
+    not needed (a frozen head's dw, say) is not computed: None."""
     T, H, V, gpu, ldx, ldw, tp = _xent(x, w, targets)
     lp = _dense(lse, (T,), torch.float32, "lse", gpu)
     if dloss.get_device() != gpu:
@@ -730,16 +750,19 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     stream = _raw_stream(gpu)
     dev, wp = x.device, w.data_ptr()
     _require(dw is not None or not accumulate, "accumulate needs dw")
-    if dx is None:
+    if not (need_dx and need_dw):
+        _wanted(dx=(need_dx, dx), dw=(need_dw, dw))
+    if dx is None and need_dx:
         dx = _empty(T, H, torch.bfloat16, dev)
-    if dw is None:
+    if dw is None and need_dw:
         dw = _empty(V, H, torch.bfloat16, dev)
-    lddx, lddw = _matrix(dx, T, H, "dx", gpu), _matrix(dw, V, H, "dw", gpu)
+    lddx = _matrix(dx, T, H, "dx", gpu) if need_dx else 0
+    lddw = _matrix(dw, V, H, "dw", gpu) if need_dw else 0
     n = lib().moe_linear_xent_workspace_bytes(T, H, V, wp, ldw, 1)
     ws = _bytes(n, dev)
     _check(lib().moe_linear_xent_backward(T, H, V, x.data_ptr(), ldx, wp, ldw, tp, lp, dloss.data_ptr(), dloss.stride(0),
-                                          dx.data_ptr(), _type(dx), lddx, dw.data_ptr(), _type(dw), lddw,
-                                          1 if accumulate else 0, ws.data_ptr(), n, stream))
+                                          *_out(dx, lddx), *_out(dw, lddw), 1 if accumulate else 0, ws.data_ptr(), n,
+                                          stream))
     return dx, dw
 
 
@@ -773,30 +796,39 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
 
 def lora_backward(x: torch.Tensor, dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
                   scale: torch.Tensor, base: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
-                  da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None, accumulate: bool = False):
+                  da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  need_dx: bool = True, need_da: bool = True, need_db: bool = True):
     """Gradients of lora_add from dy (bf16): (dx [M][K], da [L][r][K], db [L][r][N]), bf16 unless given.  base: the shared
-    projection's dx, added to (of dx's type; dx may be it); accumulate adds to the given da and db."""
+    projection's dx, added to (of dx's type; dx may be it); accumulate adds to the given da and db.  One that is not needed
+    (dx of a first layer, say) is not computed: None."""
     p, gpu, ldx, (ap, bp, ip, sp) = _lora(x, a, b, ids, scale)
     M, N, K, r, L = p.M, p.N, p.K, p.r, p.L
     lddy = _matrix(dy, M, N, "dy", gpu, torch.bfloat16)
     stream = _raw_stream(gpu)
     dev = x.device
-    _require((da is not None and db is not None) or not accumulate, "accumulate needs da and db")
-    if dx is None:
+    if accumulate:
+        _require((need_da or need_db) and (need_da <= (da is not None)) and (need_db <= (db is not None)), "accumulate needs da and db")
+    if not (need_dx and need_da and need_db):
+        _wanted(dx=(need_dx, dx), da=(need_da, da), db=(need_db, db))
+        _require(need_dx or base is None, "base is given but dx is not asked for")
+    if dx is None and need_dx:
         dx = _empty(M, K, torch.bfloat16 if base is None else base.dtype, dev)
-    if da is None:
+    if da is None and need_da:
         da = torch.empty((L, r, K), dtype=torch.bfloat16, device=dev)
-    if db is None:
+    if db is None and need_db:
         db = torch.empty((L, r, N), dtype=torch.bfloat16, device=dev)
-    lddx = _matrix(dx, M, K, "dx", gpu)
+    lddx = _matrix(dx, M, K, "dx", gpu) if need_dx else 0
     ldbase = 0 if base is None else _matrix(base, M, K, "base", gpu, dx.dtype)
-    dap, dbp = _dense(da, (L, r, K), da.dtype, "da", gpu), _dense(db, (L, r, N), db.dtype, "db", gpu)
+    if need_da:
+        _dense(da, (L, r, K), da.dtype, "da", gpu)
+    if need_db:
+        _dense(db, (L, r, N), db.dtype, "db", gpu)
     ref = ctypes.byref(p)
     n = lib().moe_lora_workspace_bytes(ref, 1)
     ws = _bytes(n, dev)
     _check(lib().moe_lora_backward(ref, x.data_ptr(), ldx, dy.data_ptr(), lddy, ap, bp, ip, sp,
-                                   None if base is None else base.data_ptr(), ldbase, dx.data_ptr(), _type(dx), lddx, dap,
-                                   _type(da), dbp, _type(db), 1 if accumulate else 0, ws.data_ptr(), n, stream))
+                                   None if base is None else base.data_ptr(), ldbase, *_out(dx, lddx), *_out(da)[:2],
+                                   *_out(db)[:2], 1 if accumulate else 0, ws.data_ptr(), n, stream))
     return dx, da, db
 
 
