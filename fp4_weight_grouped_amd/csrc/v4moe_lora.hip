@@ -75,118 +75,121 @@ struct Listing {
     int* tiles_n;
     Tile* tiles;
 };
-constexpr int kListAdapters = 1024;  // counters of sixteen waves fit LDS up to here
+constexpr int kListAdapters = 2048;  // of a pass: counters of sixteen waves fit LDS up to here
 // One block.  Each wave counts its share of the rows, the counts become places (adapter by
 // adapter, wave by wave), and the waves go through their rows again; rows of one adapter
-// among a wave's 64 find each other by a ballot for each bit of the id.
+// among a wave's 64 find each other by a ballot for each bit of the id.  More adapters than
+// the counters hold take a pass over the rows for each 2048 of them.
 // 8192 rows 9 us, 512 rows 7.
 __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t* __restrict__ ids, Listing out, int most)
 {
-    extern __shared__ int counts[];               // [16][L + 1], then totals
+    extern __shared__ int counts[];               // [16][n], then [n] first place, [n] first tile
     __shared__ int wave_rows[16], wave_tiles[16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = L + 1;
-    int* begin = counts + 16 * n;                 // [n] first place, [n] first tile
-    int* first_tile = begin + n;
-    for (int i = tid; i < 16 * n; i += 1024) counts[i] = 0;
-    __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int share = (M + 1023) / 1024 * 64, m0 = wave * share, m1 = min(m0 + share, M);
-    int* mine = counts + wave * n;
-    // 512 rows of the wave's share at a time, eight loads on their way together; -1 past the share
-    int id[8];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int q = 0; q < 8; q++) {
-            const int m = base + 64 * q + lane;
-            id[q] = m < m1 ? ids[m] : -1;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; q++) id[q] = base + 64 * q + lane >= m1 ? -1 : id[q] >= 0 && id[q] < L ? id[q] : L;
-    };
-    int bits = 0;
-    while ((n - 1) >> bits) bits++;
-    // id[q]'s place among those of its adapter that the wave has counted, which it then joins
-    auto join = [&](int q) {
-        const int a = max(id[q], 0);
-        const bool in = id[q] >= 0;
-        uint64_t same = __ballot(in);
-        for (int b = 0; b < bits; b++) {
-            const uint64_t ones = __ballot(a >> b & 1);
-            same &= a >> b & 1 ? ones : ~ones;
-        }
-        const int at = in ? mine[a] + __popcll(same & ((1ull << lane) - 1)) : 0;
-        __builtin_amdgcn_wave_barrier();
-        if (in && (same >> lane >> 1) == 0) mine[a] += __popcll(same);       // (the last of them)
-        __builtin_amdgcn_wave_barrier();
-        return at;
-    };
     const bool once = share <= 512;                                 // then the places below the wave's first stay here
-    int at[8];
-    for (int base = m0; base < m1; base += 512) {
-        load(base);
+    int rows_done = 0, tiles_done = 0;
+    for (int a0 = 0; a0 <= L; a0 += kListAdapters) {
+        const int n = min(L + 1 - a0, kListAdapters);               // adapters of this pass, "none" among the last
+        int* begin = counts + 16 * n;
+        int* first_tile = begin + n;
+        for (int i = tid; i < 16 * n; i += 1024) counts[i] = 0;
+        __syncthreads();
+        int* mine = counts + wave * n;
+        // 512 rows of the wave's share at a time, eight loads on their way together; of those past the share and of
+        // other passes' adapters -1
+        int id[8];
+        auto load = [&](int base) {
 #pragma unroll
-        for (int q = 0; q < 8; q++) at[q] = join(q);
-    }
-    __syncthreads();
-    // thread a: adapter a's rows and tiles (n <= 1025: the last by thread 0 too)
-    int rows = 0;
-    if (tid < n)
-        for (int w = 0; w < 16; w++) rows += counts[w * n + tid];
-    int tiles = (rows + kTile - 1) / kTile, r = rows, t = tiles;
+            for (int q = 0; q < 8; q++) {
+                const int m = base + 64 * q + lane;
+                id[q] = m < m1 ? ids[m] : -1;
+            }
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(r, o), v = __shfl_up(t, o);
-        if (lane >= o) r += u, t += v;
-    }
-    if (lane == 63) wave_rows[wave] = r, wave_tiles[wave] = t;
-    __syncthreads();
-    int rows_before = r - rows, tiles_before = t - tiles, all_rows = 0, all_tiles = 0;
-    for (int w = 0; w < 16; w++) {
-        if (w < wave) rows_before += wave_rows[w], tiles_before += wave_tiles[w];
-        all_rows += wave_rows[w], all_tiles += wave_tiles[w];
-    }
-    if (tid < n) {
-        begin[tid] = rows_before;
-        first_tile[tid] = tiles_before;
-        out.begin[tid] = rows_before;
-        int at = rows_before;
-        for (int w = 0; w < 16; w++) {
-            const int c = counts[w * n + tid];
-            counts[w * n + tid] = at;
-            at += c;
+            for (int q = 0; q < 8; q++) {
+                const int a = (id[q] >= 0 && id[q] < L ? id[q] : L) - a0;
+                id[q] = base + 64 * q + lane < m1 && a >= 0 && a < n ? a : -1;
+            }
+        };
+        int bits = 0;
+        while ((n - 1) >> bits) bits++;
+        // id[q]'s place among those of its adapter that the wave has counted, which it then joins
+        auto join = [&](int q) {
+            const int a = max(id[q], 0);
+            const bool in = id[q] >= 0;
+            uint64_t same = __ballot(in);
+            for (int b = 0; b < bits; b++) {
+                const uint64_t ones = __ballot(a >> b & 1);
+                same &= a >> b & 1 ? ones : ~ones;
+            }
+            const int at = in ? mine[a] + __popcll(same & ((1ull << lane) - 1)) : 0;
+            __builtin_amdgcn_wave_barrier();
+            if (in && (same >> lane >> 1) == 0) mine[a] += __popcll(same);       // (the last of them)
+            __builtin_amdgcn_wave_barrier();
+            return at;
+        };
+        int at[8];
+        for (int base = m0; base < m1; base += 512) {
+            load(base);
+#pragma unroll
+            for (int q = 0; q < 8; q++) at[q] = join(q);
         }
-    }
-    if (n > 1024) all_tiles += (M - all_rows + kTile - 1) / kTile;
-    if (n > 1024 && tid == 0) {                    // adapter 1024: none
-        begin[1024] = all_rows;
-        first_tile[1024] = all_tiles - (M - all_rows + kTile - 1) / kTile;
-        out.begin[1024] = all_rows;
-        int at = all_rows;
-        for (int w = 0; w < 16; w++) {
-            const int c = counts[w * n + 1024];
-            counts[w * n + 1024] = at;
-            at += c;
+        __syncthreads();
+        // a thread's adapters: one, or two that follow each other
+        const int each = n > 1024 ? 2 : 1, first = tid * each, last = min(first + each, n);
+        int rows = 0, tiles = 0;
+        for (int a = first; a < last; a++) {
+            int r = 0;
+            for (int w = 0; w < 16; w++) r += counts[w * n + a];
+            rows += r, tiles += (r + kTile - 1) / kTile;
         }
-    }
-    if (tid == 0) {
-        out.begin[n] = M;
-        *out.tiles_n = all_tiles;
-    }
-    __syncthreads();
-    for (int base = m0; base < m1; base += 512) {
-        if (!once) load(base);
+        int r = rows, t = tiles;
 #pragma unroll
-        for (int q = 0; q < 8; q++) {
-            const int a = max(id[q], 0), place = once ? mine[a] + at[q] : join(q), off = place - begin[a];
-            if (id[q] < 0) continue;
-            out.order[place] = base + 64 * q + lane;
-            if (off % kTile == 0) {
-                const int end = a + 1 < n ? begin[a + 1] : M;
-                out.tiles[first_tile[a] + off / kTile] = Tile{a, place, min(kTile, end - place), 0};
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(r, o), v = __shfl_up(t, o);
+            if (lane >= o) r += u, t += v;
+        }
+        if (lane == 63) wave_rows[wave] = r, wave_tiles[wave] = t;
+        __syncthreads();
+        int place = rows_done + r - rows, tile = tiles_done + t - tiles;
+        for (int w = 0; w < 16; w++) {
+            if (w < wave) place += wave_rows[w], tile += wave_tiles[w];
+            rows_done += wave_rows[w], tiles_done += wave_tiles[w];
+        }
+        for (int a = first; a < last; a++) {
+            begin[a] = place;
+            first_tile[a] = tile;
+            out.begin[a0 + a] = place;
+            const int before = place;
+            for (int w = 0; w < 16; w++) {
+                const int c = counts[w * n + a];
+                counts[w * n + a] = place;
+                place += c;
+            }
+            tile += (place - before + kTile - 1) / kTile;
+        }
+        __syncthreads();
+        for (int base = m0; base < m1; base += 512) {
+            if (!once) load(base);
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const int a = max(id[q], 0), p = once ? mine[a] + at[q] : join(q), off = p - begin[a];
+                if (id[q] < 0) continue;
+                out.order[p] = base + 64 * q + lane;
+                if (off % kTile == 0) {
+                    const int end = a + 1 < n ? begin[a + 1] : rows_done;
+                    out.tiles[first_tile[a] + off / kTile] = Tile{a0 + a, p, min(kTile, end - p), 0};
+                }
             }
         }
+        __syncthreads();                                            // (the counts are read)
+    }
+    if (tid == 0) {
+        out.begin[L + 1] = M;
+        *out.tiles_n = tiles_done;
     }
     // no tiles behind the last
-    for (int i = all_tiles + tid; i < most; i += 1024) out.tiles[i] = Tile{-1, 0, 0, 0};
+    for (int i = tiles_done + tid; i < most; i += 1024) out.tiles[i] = Tile{-1, 0, 0, 0};
 }
 
 struct ShrinkJob {
@@ -1058,10 +1061,17 @@ __global__ __launch_bounds__(256, RC < 4 ? 3 : 2) void k_lora_gradients(OuterArg
 //   1024   18/22 (16/22)  33/27 (30/27)   35/25 (16/24)    72/41 (42/41)
 //   2048   25/27 (19/28)  46/32 (37/32)   53/30 (20/29)   103/46 (52/44)
 //   8192   63/48 (47/49) 122/78 (95/77)  159/50 (49/49)   304/87 (123/84)
-// The order is not known here: the rules lie between.
+// The order is not known here: the rules lie between.  Above 1024 adapters, K = N = 1024, rank 16:
+//                      2047 adapters                   4096                            16384
+//   rows     forward        backward        forward         backward         forward          backward
+//   1024   33/43 (15/28)  392/170 (294/90)  33/58 (15/43)  664/255 (553/164)                 2238/733 (2121/625)
+//   2048   46/55 (16/28)  496/220 (346/95)  47/78 (16/45)  847/333 (637/168)                 2732/841 (2401/651)
+//   8192  134/74 (29/39) 1503/304 (1055/121) 141/135 (29/61) 2584/567 (2039/208) 160/296 (31/146) 8572/1372 (7957/710)
+// Backward, an unlisted block of an adapter's sums looks through all rows; forward, a tile never has more than 16.
 bool listed_first(int M, int L, bool backward)
 {
-    return (int64_t)M * std::min(L, 16) > (backward ? 1000 : 8192) && L <= kListAdapters;
+    const int64_t work = (int64_t)M * std::min(L, 16);
+    return backward ? work > 1000 : work > 8192 && L <= 1024;
 }
 int64_t most_tiles(int64_t M, int64_t L) { return M / kTile + std::min<int64_t>(M, L + 1); }
 
@@ -1069,9 +1079,9 @@ hipError_t run_list(int M, int L, const int32_t* ids, const Listing& list, hipSt
 {
     static LdsAllowed allowed;
     const auto kernel = k_lora_list;
-    const int bytes = (16 + 2) * (kListAdapters + 1) * 4;
+    const int bytes = (16 + 2) * kListAdapters * 4;
     if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), bytes, allowed); e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), (16 + 2) * (L + 1) * 4, s, M, L, ids, list, (int)most_tiles(M, L));
+    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), (16 + 2) * std::min(L + 1, kListAdapters) * 4, s, M, L, ids, list, (int)most_tiles(M, L));
     return hipGetLastError();
 }
 
