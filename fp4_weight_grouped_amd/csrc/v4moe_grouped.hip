@@ -265,10 +265,14 @@ hipError_t run_weights(const GroupedArgs& g, hipStream_t s)
 // Both gradients.  Where neither fills the GPU for long they go out in one launch, the end of the one beside the begin of
 // the other, with 128x128 tiles both (3001 rows of 12 experts, 1001 x 499: 30 us with the copies of its odd operands, 36
 // in two launches with the tiles that are best alone, 33 with those in one).
-hipError_t run_both(const GroupedArgs& r, const GroupedArgs& w, hipStream_t s)
+bool one_launch(const GroupedArgs& r, const GroupedArgs& w)
 {
     const int rv = row_variant(r), wv = weight_variant(w);
-    if ((rv == 2 || rv == 3) && wv < 4 && row_tiles(r, 128, 128) <= 1024 && weight_tiles(w, 128, 128) <= 1024)
+    return (rv == 2 || rv == 3) && wv < 4 && row_tiles(r, 128, 128) <= 1024 && weight_tiles(w, 128, 128) <= 1024;
+}
+hipError_t run_both(const GroupedArgs& r, const GroupedArgs& w, hipStream_t s)
+{
+    if (one_launch(r, w))
         return launch_both<RowTile<3, true>::L, Weights128>(r, w, s);
     if (const hipError_t e = run_rows<true>(r, s); e != hipSuccess) return e;
     return run_weights(w, s);
@@ -362,6 +366,20 @@ __attribute__((visibility("default"))) size_t moe_grouped_workspace_bytes(int32_
 {
     if (check_grouped(M, E, N, K)) return 0;
     return grouped_layout(M, E, N, K, x, ldx, dy, lddy, w, backward != 0).total;
+}
+
+__attribute__((visibility("default"))) int32_t moe_grouped_tile(int32_t M, int32_t E, int32_t N, int32_t K, int32_t what,
+                                                                int32_t both)
+{
+    if (check_grouped(M, E, N, K) || what < V4MOE_PRODUCT_FORWARD || what > V4MOE_PRODUCT_DW) return 0;
+    // the sizes as the calls below give them to the launches
+    GroupedArgs y{}, dx{}, dw{};
+    y.M = M, y.N = N, y.K = K, y.E = E;
+    dx.M = M, dx.N = K, dx.K = N, dx.E = E;
+    dw.M = M, dw.N = K, dw.E = E, dw.c.M = N;
+    if (what == V4MOE_PRODUCT_FORWARD) return tile_code(kMmVariants[row_variant(y)]);
+    if (both && one_launch(dx, dw)) return 128 << 16 | 128 | V4MOE_TILE_SHARED;
+    return tile_code(kMmVariants[what == V4MOE_PRODUCT_DX ? row_variant(dx) : weight_variant(dw)]);
 }
 
 __attribute__((visibility("default"))) int moe_grouped_linear(int32_t M, int32_t E, int32_t N, int32_t K,

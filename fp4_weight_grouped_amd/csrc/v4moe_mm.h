@@ -454,6 +454,7 @@ constexpr MmVariant kMmVariants[] = {{16, 64, {4.2f, 4.7f, 5.4f, 5.9f}, {15.1f, 
                                      {64, 64, {4.9f, 5.9f, 6.9f, 9.6f}, {23.6f, 32.0f, 43.9f, 55.2f}},
                                      {128, 128, {7.2f, 8.9f, 13.7f, 16.2f}, {47.5f, 65.6f, 106.7f, 121.9f}},
                                      {256, 256, {15.3f, 32.6f, 41.0f, 59.9f}, {107.7f, 206.0f, 300.5f, 394.1f}}};
+inline int32_t tile_code(const MmVariant& v) { return v.bm << 16 | v.bn; }
 inline float mm_time(const MmVariant& v, int64_t tiles, int64_t K)
 {
     const int64_t rounds = tiles < 1 ? 1 : (tiles + 255) / 256;

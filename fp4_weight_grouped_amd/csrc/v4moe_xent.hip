@@ -589,15 +589,22 @@ hipError_t launch_logits(const LogitsArgs& p, hipStream_t s)
     hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(L::THREADS), L::BYTES, s, p);
     return hipGetLastError();
 }
+// Rows of the logits' tiles: those of the few tokens', 256 columns wide, or of a square one.
+int logits_rows(int64_t T, int64_t H, int64_t V)
+{
+    if (T <= 64) return T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    return kMmVariants[mm_choose(3, H, [&](int64_t bm, int64_t bn) { return over(T, bm) * over(V, bn); })].bm;
+}
 template <bool GRAD>
 hipError_t run_logits(const LogitsArgs& p, hipStream_t s)
 {
-    if (p.T <= 16) return launch_logits<MmTile<1, 4, 1, 4, 4, false, false>, GRAD>(p, s);
-    if (p.T <= 32) return launch_logits<MmTile<1, 4, 2, 4, 3, false, false>, GRAD>(p, s);
-    if (p.T <= 64) return launch_logits<MmTile<1, 4, 4, 4, 2, false, false>, GRAD>(p, s);
-    const int v = mm_choose(3, p.H, [&](int64_t bm, int64_t bn) { return over(p.T, bm) * over(p.V, bn); });
-    if (v == 3) return launch_logits<MmTile<2, 2, 4, 4, 2, false, false>, GRAD>(p, s);
-    return launch_logits<MmTile<2, 4, 8, 4, 2, false, false>, GRAD>(p, s);
+    switch (logits_rows(p.T, p.H, p.V)) {
+    case 16: return launch_logits<MmTile<1, 4, 1, 4, 4, false, false>, GRAD>(p, s);
+    case 32: return launch_logits<MmTile<1, 4, 2, 4, 3, false, false>, GRAD>(p, s);
+    case 64: return launch_logits<MmTile<1, 4, 4, 4, 2, false, false>, GRAD>(p, s);
+    case 128: return launch_logits<MmTile<2, 2, 4, 4, 2, false, false>, GRAD>(p, s);
+    default: return launch_logits<MmTile<2, 4, 8, 4, 2, false, false>, GRAD>(p, s);
+    }
 }
 
 // blocks of dx, whatever n is
@@ -797,6 +804,20 @@ __attribute__((visibility("default"))) size_t moe_linear_xent_workspace_bytes(in
 {
     if (!side_ok(T) || !side_ok(H) || !side_ok(V) || H < 1 || V < 1) return 0;
     return xent_layout(T, H, V, w, ldw, backward != 0).total;
+}
+
+__attribute__((visibility("default"))) int32_t moe_linear_xent_tile(int32_t T, int32_t H, int32_t V, int32_t what, int32_t both)
+{
+    if (!side_ok(T) || !side_ok(H) || !side_ok(V) || T < 1 || H < 1 || V < 1) return 0;
+    if (what < V4MOE_PRODUCT_FORWARD || what > V4MOE_PRODUCT_AGAIN) return 0;
+    const int piece = xent_layout(T, H, V, nullptr, up8(H), true).piece, columns = std::min(piece, V);
+    if (what == V4MOE_PRODUCT_FORWARD || what == V4MOE_PRODUCT_AGAIN) {
+        const int bm = logits_rows(T, H, what == V4MOE_PRODUCT_FORWARD ? V : columns);
+        return bm << 16 | (bm == 128 ? 128 : 256);
+    }
+    const bool shared = both && both_at_once(T, H, piece);
+    const MmVariant& t = what == V4MOE_PRODUCT_DX ? dx_tile(T, up8(H), piece, shared) : kMmVariants[dw_variant(T, H, piece)];
+    return tile_code(t) | (shared ? V4MOE_TILE_SHARED : 0);
 }
 
 __attribute__((visibility("default"))) int moe_linear_xent(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx,

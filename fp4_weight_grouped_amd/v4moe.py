@@ -153,6 +153,9 @@ def lib():
         L.moe_linear_xent.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
         L.moe_linear_xent_backward.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i64,
                                                _vp, _i32, _i64, _i32, _vp, _sz, _vp]
+        L.moe_grouped_tile.argtypes = [_i32] * 6
+        L.moe_linear_xent_tile.argtypes = [_i32] * 5
+        L.moe_grouped_tile.restype = L.moe_linear_xent_tile.restype = _i32
         LP = ctypes.POINTER(LoraC)
         L.moe_lora_workspace_bytes.argtypes = [LP, _i32]
         L.moe_lora_workspace_bytes.restype = _sz

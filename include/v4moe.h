@@ -494,6 +494,17 @@ int moe_grouped_linear_backward(int32_t M, int32_t E, int32_t N, int32_t K, cons
                                 void* dw, int32_t dw_type, int32_t accumulate, void* workspace,
                                 size_t ws_bytes, void* stream);
 
+/* The tile that a product of these calls takes, for a reader of a profile (host-only, pure):
+ * rows << 16 | columns, and V4MOE_TILE_SHARED where both gradients go out in one launch; 0
+ * for invalid arguments.  what: V4MOE_PRODUCT_*; both: both gradients are asked for.  Results
+ * do not depend on it, in any bit. */
+#define V4MOE_PRODUCT_FORWARD 0   /* y; the cross entropy's logits              */
+#define V4MOE_PRODUCT_DX      1
+#define V4MOE_PRODUCT_DW      2
+#define V4MOE_PRODUCT_AGAIN   3   /* the cross entropy's logits in its backward */
+#define V4MOE_TILE_SHARED     (1 << 30)
+int32_t moe_grouped_tile(int32_t M, int32_t E, int32_t N, int32_t K, int32_t what, int32_t both);
+
 /* ---- Softmax cross entropy over a large vocabulary, from the hidden states ----
  *   z = x W^T (x bf16 [T][ldx], W bf16 [V][ldw], H used of both), never in memory as a whole
  *   lse[t] = log sum_v exp(z[t][v]); loss[t] = lse[t] - z[t][targets[t]]
@@ -527,6 +538,11 @@ int moe_linear_xent_backward(int32_t T, int32_t H, int32_t V, const uint16_t* x,
                              const float* dloss, int64_t dloss_stride, void* dx, int32_t dx_type,
                              int64_t lddx, void* dw, int32_t dw_type, int64_t lddw,
                              int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* As moe_grouped_tile, of a cross entropy's products; those of its backward are of the first
+ * piece of the vocabulary.  (dx is cut into slices of the vocabulary for its tile, so that its
+ * last bits do depend on it.) */
+int32_t moe_linear_xent_tile(int32_t T, int32_t H, int32_t V, int32_t what, int32_t both);
 
 /* ---- Low-rank adapters of many requests beside a shared projection ----
  * Row m uses adapter ids[m] (int32 [M] on the device, in any order; outside [0, L): none)
