@@ -180,11 +180,20 @@ struct MmReader {
     }
 };
 
+template <class L>
+__device__ __forceinline__ void mm_zero(v4f (&acc)[L::MI][L::NI])
+{
+#pragma unroll
+    for (int i = 0; i < L::MI; i++)
+#pragma unroll
+        for (int j = 0; j < L::NI; j++) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
 // The sums of a block's tile from (m0, n0): acc[i][j] of a wave (wm, wn) holds, in lane l,
 // row m0 + first_row(wm) + 16 STEP i + l % 16 and columns n0 + 16 (wn NI + j) + 4 (l / 16) .. + 3.
 // B is the instruction's first operand, so that a lane has consecutive columns.  The
-// block's LDS (L::BYTES) is free when it returns.
-template <class L>
+// block's LDS (L::BYTES) is free when it returns.  ADD: to what acc holds, the chain going on.
+template <class L, bool ADD = false>
 __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, int m0, int n0, int K, uint8_t* smem,
                                         v4f (&acc)[L::MI][L::NI])
 {
@@ -220,10 +229,7 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
     MmReader<L::BN, L::BCOL, L::NI> rb;
     ra.begin(L::first_row(wm) / 16, lane);
     rb.begin(wn * L::NI, lane);
-#pragma unroll
-    for (int i = 0; i < L::MI; i++)
-#pragma unroll
-        for (int j = 0; j < L::NI; j++) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (!ADD) mm_zero<L>(acc);
     if (nch > 0) {
 #pragma unroll
         for (int c = 0; c < L::NS; c++)

@@ -17,7 +17,8 @@
 // gradient is its target's term, -g W[y_t] and -g x_t, so that d there is not left at
 // 8 bits: what its rounding left, one number a token, is added to both products (dx: in
 // fp32 where its slices meet; dW: as 16 bits in all, by one more product of the few tokens
-// whose target a tile has).
+// whose target a tile has).  A caller who wants fp32 results as fp32 products give them has
+// all of d as two bf16 numbers, and twice the products for it.
 #include "v4moe.h"
 #include "v4moe_device.h"
 #include "v4moe_internal.h"
@@ -221,6 +222,7 @@ struct LogitsArgs {
     // backward
     const float* lse; const float* g;
     uint16_t* d; int64_t ldd;
+    int64_t plane;                     // to d's second numbers, what the first ones' rounding left; 0: none
     float* rest;                       // what d's rounding left at each token's target
 };
 
@@ -325,6 +327,15 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
         // (columns up to a multiple of 8: the products read whole segments)
         const MmOut o{p.d, p.ldd, n, (p.V + 7) / 8 * 8, 1, 0};
         mm_store_tile<L, false>(acc, smem, o, im * L::BM, in * L::BN);
+        if (p.plane) {
+#pragma unroll
+            for (int i = 0; i < L::MI; i++)
+#pragma unroll
+                for (int j = 0; j < L::NI; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[i][j][e] = rounding_of(acc[i][j][e]);
+            mm_store_tile<L, false>(acc, smem, MmOut{p.d + p.plane, p.ldd, n, o.N, 1, 0}, im * L::BM, in * L::BN);
+        }
     }
 }
 
@@ -373,6 +384,7 @@ struct XentGradArgs {
     const XentCtrl* ctrl;
     const uint16_t* x; const uint16_t* w; int64_t ldw;
     const uint16_t* d; int64_t ldd;
+    int parts; int64_t plane;           // numbers of d, from one to the next
     int v0; const int* y; const float* rest;
     float* dx;                          // [slices][n][H8] of the n packed rows
     int first;                          // the first piece writes dx, the others add to it
@@ -402,9 +414,13 @@ __device__ __forceinline__ void dx_block(const XentGradArgs& p, int block, uint8
     const int slice = turn / (tm * tn), k0 = slice * sl.columns;
     int im, in;
     mm_band(turn % (tm * tn), tm, tn, im, in);
-    const MmOperand a{p.d + k0, p.ldd, n}, b{p.w + k0 * p.ldw, p.ldw, p.H8};
+    const MmOperand b{p.w + k0 * p.ldw, p.ldw, p.H8};
     v4f acc[L::MI][L::NI];
-    mm_tile<L>(a, b, im * L::BM, in * L::BN, max(min(p.V - k0, sl.columns), 0), smem, acc);
+    mm_zero<L>(acc);
+    for (int part = 0; part < p.parts; part++) {
+        const MmOperand a{p.d + part * p.plane + k0, p.ldd, n};
+        mm_tile<L, true>(a, b, im * L::BM, in * L::BN, max(min(p.V - k0, sl.columns), 0), smem, acc);
+    }
     const MmOut o{p.dx + (int64_t)slice * n * p.H8, p.H8, n, p.H8, 0, !p.first};
     mm_store_tile<L>(acc, smem, o, im * L::BM, in * L::BN);
 }
@@ -490,10 +506,14 @@ __device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, 
     if (n == 0 && p.dw.accumulate) return;          // (adding a sum of nothing would turn -0 into 0)
     int im, in;
     mm_band(mm_turn(block, tm * tn), tm, tn, im, in);
-    const MmOperand a{p.d, p.ldd, (p.V + 7) / 8 * 8}, b{p.x, p.H8, p.H8};
+    const MmOperand b{p.x, p.H8, p.H8};
     v4f acc[L::MI][L::NI];
-    mm_tile<L>(a, b, im * L::BM, in * L::BN, n, smem, acc);
-    add_targets<L>(p, n, im * L::BM, in * L::BN, smem, acc);
+    mm_zero<L>(acc);
+    for (int part = 0; part < p.parts; part++) {
+        const MmOperand a{p.d + part * p.plane, p.ldd, (p.V + 7) / 8 * 8};
+        mm_tile<L, true>(a, b, im * L::BM, in * L::BN, n, smem, acc);
+    }
+    if (p.parts == 1) add_targets<L>(p, n, im * L::BM, in * L::BN, smem, acc);
     const float s = p.ctrl->largest;
 #pragma unroll
     for (int i = 0; i < L::MI; i++)
@@ -543,7 +563,7 @@ __global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int b
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (m >= 0) {
             const v2u32 wy = *reinterpret_cast<const v2u32*>(w + y[m] * ldw + c);
-            const float left = rest[m];
+            const float left = rest ? rest[m] : 0.0f;          // (null: d has two numbers)
             for (int k = 0; k < slices; k += 4) {
                 float4 f[4];
 #pragma unroll
@@ -693,7 +713,7 @@ hipError_t run_gradients(const XentGradArgs& p, hipStream_t s)
 struct XentLayout {
     size_t ctrl, idx, pos, y, zy, x, parts, lse, g, rest, d, dx, w, total;
     bool pad_w;
-    int piece;                      // columns of a piece
+    int piece;                      // columns of a piece; half as many where d has two numbers
 };
 XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t ldw, bool backward)
 {
@@ -726,10 +746,11 @@ XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t l
         L.d = take(T * (int64_t)L.piece * 2);
         // dx of every row, or of fewer rows in slices: dx_blocks tiles then (of either tile, with dW or alone)
         int64_t most_dx = T * H8;
-        for (int both = 0; both < 2; both++) {
-            const MmVariant& t = dx_tile(T, H8, L.piece, both && both_at_once(T, H, L.piece));
-            most_dx = std::max(most_dx, std::min<int64_t>((int64_t)dx_blocks(t.bm) * t.bm * t.bn, T * H8 * over(L.piece, 256)));
-        }
+        for (int both = 0; both < 2; both++)
+            for (const int piece : {L.piece, L.piece / 2}) {
+                const MmVariant& t = dx_tile(T, H8, piece, both && both_at_once(T, H, piece));
+                most_dx = std::max(most_dx, std::min<int64_t>((int64_t)dx_blocks(t.bm) * t.bm * t.bn, T * H8 * over(piece, 256)));
+            }
         L.dx = take(most_dx * 4);
     }
     L.total = o;
@@ -861,15 +882,17 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
     if (dloss_stride < 0 || dloss_stride > (1ll << 40)) return V4MOE_EDIMS;
     if (T > 0 && (!lse || !dloss)) return V4MOE_ENULL;
     if (!aligned_to(lse, 4) || !aligned_to(dloss, 4)) return V4MOE_EALIGN;
-    if (T == 0 && (!dw || accumulate)) return V4MOE_OK;
+    if (T == 0 && (!dw || (accumulate & ~V4MOE_GRAD_FULL))) return V4MOE_OK;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     XentCall c;
     if (const int rc = xent_begin(c, T, H, V, x, ldx, w, ldw, targets, lse, dloss, dloss_stride, nullptr, nullptr, workspace,
                                   ws_bytes, true, s))
         return rc;
     const auto* ctrl = c.at<XentCtrl>(c.L.ctrl);
-    for (int v0 = 0; v0 < V; v0 += c.L.piece) {
-        const int n = std::min(c.L.piece, V - v0);
+    const bool full = accumulate & V4MOE_GRAD_FULL, add = accumulate & ~V4MOE_GRAD_FULL;
+    const int piece = full ? c.L.piece / 2 : c.L.piece;
+    for (int v0 = 0; v0 < V; v0 += piece) {
+        const int n = std::min(piece, V - v0);
         LogitsArgs p{};
         p.T = T, p.H = H, p.V = n, p.v0 = v0;
         p.ctrl = ctrl;
@@ -877,19 +900,21 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         p.w = c.w + v0 * c.ldw, p.ldw = c.ldw;
         p.y = c.at<int>(c.L.y);
         p.lse = c.at<float>(c.L.lse), p.g = c.at<float>(c.L.g);
-        p.d = c.at<uint16_t>(c.L.d), p.ldd = c.L.piece;
+        p.d = c.at<uint16_t>(c.L.d), p.ldd = piece;
+        p.plane = full ? (int64_t)T * piece : 0;
         p.rest = c.at<float>(c.L.rest);
         if (T > 0 && run_logits<true>(p, s) != hipSuccess) return V4MOE_ELAUNCH;
         XentGradArgs q{};
         q.T = T, q.H = H, q.H8 = c.H8, q.V = n;
-        q.piece = c.L.piece;
+        q.piece = piece;
+        q.parts = full ? 2 : 1, q.plane = p.plane;
         q.ctrl = ctrl;
         q.x = p.x, q.w = p.w, q.ldw = p.ldw, q.d = p.d, q.ldd = p.ldd;
         q.v0 = v0, q.y = p.y, q.rest = p.rest;
         q.dx = c.at<float>(c.L.dx), q.first = v0 == 0;
         if (dw) {
             const bool bf16 = dw_type == V4MOE_TYPE_BF16;
-            q.dw = MmOut{static_cast<uint8_t*>(dw) + (int64_t)v0 * lddw * (bf16 ? 2 : 4), lddw, n, H, bf16, accumulate != 0};
+            q.dw = MmOut{static_cast<uint8_t*>(dw) + (int64_t)v0 * lddw * (bf16 ? 2 : 4), lddw, n, H, bf16, add};
         }
         const bool rows = dx && T > 0;
         if ((rows && dw ? run_gradients(q, s) : rows ? run_dx(q, s) : dw ? run_dw(q, s) : hipSuccess) != hipSuccess)
@@ -897,15 +922,15 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
     }
     if (dx && T > 0) {
         const dim3 grid((unsigned)std::min<int64_t>(over((int64_t)T * (c.H8 / 4), 256), 8192));
-        const MmVariant& t = dx_tile(T, c.H8, c.L.piece, dw && both_at_once(T, H, c.L.piece));
+        const MmVariant& t = dx_tile(T, c.H8, piece, dw && both_at_once(T, H, piece));
+        const float* rest = full ? nullptr : c.at<float>(c.L.rest);
         if (dx_type == V4MOE_TYPE_BF16)
-            hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl,
-                               c.at<int>(c.L.pos), c.at<float>(c.L.dx), c.at<int>(c.L.y), c.at<float>(c.L.rest), c.w, c.ldw,
+            hipLaunchKernelGGL(k_xent_finish<uint16_t>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, piece, ctrl,
+                               c.at<int>(c.L.pos), c.at<float>(c.L.dx), c.at<int>(c.L.y), rest, c.w, c.ldw,
                                static_cast<uint16_t*>(dx), lddx);
         else
-            hipLaunchKernelGGL(k_xent_finish<float>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, c.L.piece, ctrl, c.at<int>(c.L.pos),
-                               c.at<float>(c.L.dx), c.at<int>(c.L.y), c.at<float>(c.L.rest), c.w, c.ldw, static_cast<float*>(dx),
-                               lddx);
+            hipLaunchKernelGGL(k_xent_finish<float>, grid, dim3(256), 0, s, T, H, c.H8, t.bm, t.bn, piece, ctrl, c.at<int>(c.L.pos),
+                               c.at<float>(c.L.dx), c.at<int>(c.L.y), rest, c.w, c.ldw, static_cast<float*>(dx), lddx);
     }
     return hipGetLastError() == hipSuccess ? V4MOE_OK : V4MOE_ELAUNCH;
 }

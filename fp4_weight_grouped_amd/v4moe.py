@@ -38,6 +38,8 @@ SCORE_SIGMOID = 0
 SCORE_SOFTMAX = 1
 SCORE_SQRTSOFTPLUS = 2
 
+GRAD_FULL = 2
+
 SCALE_BLOCK = 0
 SCALE_ROW = 1
 
@@ -741,10 +743,11 @@ def linear_xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
 
 def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
                          dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, accumulate: bool = False,
-                         need_dx: bool = True, need_dw: bool = True):
+                         need_dx: bool = True, need_dw: bool = True, full: bool = False):
     """Gradients of sum(dloss * loss) for linear_xent's loss: (dx [T][H], dw [V][H]), bf16 unless given; lse from
     linear_xent; dloss fp32 [T], of any stride (an expanded scalar, say); accumulate adds to the given dw.  One that is
-    not needed (a frozen head's dw, say) is not computed: None."""
+    not needed (a frozen head's dw, say) is not computed: None.  full: the logits' gradient in 16 bits of significand in
+    place of bf16's 8, for fp32 results (and sums over many calls) that are good to about 5e-6, in some 5/3 of the time."""
     T, H, V, gpu, ldx, ldw, tp = _xent(x, w, targets)
     lp = _dense(lse, (T,), torch.float32, "lse", gpu)
     if dloss.get_device() != gpu:
@@ -764,8 +767,8 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     n = lib().moe_linear_xent_workspace_bytes(T, H, V, wp, ldw, 1)
     ws = _bytes(n, dev)
     _check(lib().moe_linear_xent_backward(T, H, V, x.data_ptr(), ldx, wp, ldw, tp, lp, dloss.data_ptr(), dloss.stride(0),
-                                          *_out(dx, lddx), *_out(dw, lddw), 1 if accumulate else 0, ws.data_ptr(), n,
-                                          stream))
+                                          *_out(dx, lddx), *_out(dw, lddw), (1 if accumulate else 0) | (GRAD_FULL if full else 0),
+                                          ws.data_ptr(), n, stream))
     return dx, dw
 
 

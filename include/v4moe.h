@@ -532,7 +532,10 @@ int moe_linear_xent(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t 
  * dx or dw may be NULL.  dloss fp32, element t at dloss[t * dloss_stride] (0: one for all).
  * d enters the products in bf16 (divided by the largest |dloss| first), but at the targets
  * in 16 bits: fp32 results are good to 1e-5 to 1e-3 of their 2-norm, the first where the
- * probabilities are spread over many columns, the last where a few have them all. */
+ * probabilities are spread over many columns, the last where a few have them all.
+ * accumulate | V4MOE_GRAD_FULL: all of d in 16 bits, for results that are good to about 5e-6
+ * (what products in fp32 give), at twice the gradients' products. */
+#define V4MOE_GRAD_FULL 2
 int moe_linear_xent_backward(int32_t T, int32_t H, int32_t V, const uint16_t* x, int64_t ldx,
                              const uint16_t* w, int64_t ldw, const int64_t* targets, const float* lse,
                              const float* dloss, int64_t dloss_stride, void* dx, int32_t dx_type,
