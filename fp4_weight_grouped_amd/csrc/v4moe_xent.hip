@@ -224,6 +224,7 @@ struct LogitsArgs {
     uint16_t* d; int64_t ldd;
     int64_t plane;                     // to d's second numbers, what the first ones' rounding left; 0: none
     float* rest;                       // what d's rounding left at each token's target
+    uint16_t* hits; int hits_ld;       // [columns / 64][tokens / 16]: which of 16 tokens have their target in 64 columns
 };
 
 // Logits of a piece, a tile per block, and what becomes of them.  16 tokens, H = 4096, V = 131072: 172 us, W's bytes at
@@ -288,6 +289,8 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
             }
         }
     } else {
+        static_assert(L::NI == 4, "a wave has one group of 64 columns");
+        uint32_t hits = 0;                                             // lane i: of row tile i
 #pragma unroll
         for (int i = 0; i < L::MI; i++) {
             if (mw + 16 * L::STEP * i >= n) break;
@@ -295,7 +298,9 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
             const int y = p.y[m] - p.v0 - nw;
             const float lse = p.lse[m], g = p.g[m];
             // d without the target's 1, which is taken off where a target of the 16 rows lies here
-            const bool end = nw + 16 * L::NI > p.V, target = __ballot((uint32_t)y < 16u * L::NI) != 0;
+            const uint64_t here = __ballot((uint32_t)y < 16u * L::NI && mw + 16 * L::STEP * i + r16 < n);
+            const bool end = nw + 16 * L::NI > p.V, target = here != 0;
+            if (lane == i) hits = (uint32_t)here & 0xFFFFu;
 #pragma unroll
             for (int j = 0; j < L::NI; j++)
 #pragma unroll
@@ -324,6 +329,8 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_logits(LogitsArgs p)
                         if (nw + 16 * j + 4 * kq + e >= p.V) acc[i][j][e] = 0.0f;
             }
         }
+        if (lane < L::MI && mw + 16 * L::STEP * lane < n && nw < p.V)
+            p.hits[(int64_t)(nw >> 6) * p.hits_ld + (mw >> 4) + L::STEP * lane] = (uint16_t)hits;
         // (columns up to a multiple of 8: the products read whole segments)
         const MmOut o{p.d, p.ldd, n, (p.V + 7) / 8 * 8, 1, 0};
         mm_store_tile<L, false>(acc, smem, o, im * L::BM, in * L::BN);
@@ -386,6 +393,7 @@ struct XentGradArgs {
     const uint16_t* d; int64_t ldd;
     int parts; int64_t plane;           // numbers of d, from one to the next
     int v0; const int* y; const float* rest;
+    const uint16_t* hits; int hits_ld;
     float* dx;                          // [slices][n][H8] of the n packed rows
     int first;                          // the first piece writes dx, the others add to it
     MmOut dw;                           // the piece's rows
@@ -425,38 +433,38 @@ __device__ __forceinline__ void dx_block(const XentGradArgs& p, int block, uint8
     mm_store_tile<L>(acc, smem, o, im * L::BM, in * L::BN);
 }
 
-// Adds what d's rounding left at the targets to a tile of dW: rest[t] x[t] to row y[t].  The block looks through the
-// tokens together, eight a thread at a time; each wave lists those whose target is one of its rows, in order, and
-// multiplies 32 of them at a time.  4096 tokens, tiles of 256x256: 8 us a tile, nearly all of it the latency of three loads
-// in a row (each wave by itself through all tokens 18; steps of 32 tokens that follow each other, as they come, 10).  One
-// target for all 4096, so that one tile has them all: both gradients of 131072 columns 10300 -> 11400 us.
+// The tokens, of 4096 from base on, whose target is one of a wave's rows of dW: 64 for each lane.
 template <class L>
-__device__ __forceinline__ void add_targets(const XentGradArgs& p, int n, int m0, int n0, uint8_t* smem, v4f (&acc)[L::MI][L::NI])
+__device__ __forceinline__ uint64_t targets_of(const XentGradArgs& p, int n, int first, int base)
 {
-    static_assert(!L::RAGGED, "a wave's rows follow each other");
-    constexpr int ROWS = L::MI * 16, NW = L::NW, WORDS = 8 * NW, TOKENS = 64 * WORDS;
-    static_assert(WORDS <= 64 && L::WM * WORDS * 8 + NW * TOKENS * 2 <= L::BYTES, "a word for a lane; a list for a wave");
+    const int t = base + 64 * ((int)threadIdx.x & 63);
+    uint64_t in = 0;
+#pragma unroll
+    for (int c = 0; c < L::MI * 16; c += 64)
+        if (t < n && first + c < p.V)
+            in |= *reinterpret_cast<const uint64_t*>(p.hits + (int64_t)((first + c) >> 6) * p.hits_ld + (t >> 4));
+    return n - t < 64 ? in & ((1ull << max(n - t, 0)) - 1) : in;
+}
+
+// Adds what d's rounding left at the targets to a wave's tile of dW: rest[t] x[t] to row y[t], 32 tokens at a time, in
+// order.  `in`: targets_of the first 4096, fetched ahead of the tile.  A wave without any is done; one with a few waits
+// for a list and two loads in a row (1237 tokens, 495 of them with a target, 50021 x 1001: the call 229 -> 238 us, 249 where
+// a block looked through the tokens here; 4096 tokens, V = 131072, H = 4096: 1.2% more, 1.6).  One target for all of 4096 tokens, so that one tile has them
+// all: both gradients of 131072 columns 10300 -> 11400 us.
+template <class L>
+__device__ __forceinline__ void add_targets(const XentGradArgs& p, uint64_t in, int n, int first, int column, uint8_t* smem,
+                                            v4f (&acc)[L::MI][L::NI])
+{
+    static_assert(!L::RAGGED && L::MI % 4 == 0, "a wave's rows follow each other, in groups of 64");
+    static_assert(L::C_BYTES >= 4096 * 2, "the list has the room that the wave's sums have later");
     typedef short v8s __attribute__((ext_vector_type(8)));
     const int lane = threadIdx.x & 63, r16 = lane & 15, kq = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), wm = wave / L::WN;
-    const int origin = p.v0 + m0, rows = min(L::BM, p.V - m0), column = n0 + wave % L::WN * L::NI * 16 + r16;
-    uint64_t* words = reinterpret_cast<uint64_t*>(smem);                     // [WM][WORDS]: who has a target in the wave's rows
-    uint16_t* list = reinterpret_cast<uint16_t*>(smem + L::WM * WORDS * 8) + wave * TOKENS;
-    for (int base = 0; base < n; base += TOKENS) {
-        if (base > 0) __syncthreads();                                       // (the words before are read)
-#pragma unroll
-        for (int u = 0; u < 8; u++) {
-            const int t = base + 64 * (8 * wave + u) + lane;
-            const int row = t < n ? p.y[t] - origin : -1;
-#pragma unroll
-            for (int w = 0; w < L::WM; w++) {
-                const uint64_t in = __ballot(row >= w * ROWS && row < min((w + 1) * ROWS, rows));
-                if (lane == 0) words[w * WORDS + 8 * wave + u] = in;
-            }
-        }
-        __syncthreads();
-        uint64_t mine = lane < WORDS ? words[wm * WORDS + lane] : 0;
-        int at = __popcll(mine), all = at;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + wave * L::C_BYTES);
+    for (int base = 0; base < n; base += 4096) {
+        if (base > 0) in = targets_of<L>(p, n, first, base);
+        if (!__ballot(in != 0)) continue;
+        int at = __popcll(in), all = at;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int v = __shfl_up(all, o);
@@ -464,7 +472,8 @@ __device__ __forceinline__ void add_targets(const XentGradArgs& p, int n, int m0
         }
         at = all - at;
         all = __builtin_amdgcn_readlane(all, 63);
-        for (; mine; mine &= mine - 1) list[at++] = (uint16_t)(64 * lane + __builtin_ctzll(mine));
+        __builtin_amdgcn_wave_barrier();
+        for (; in; in &= in - 1) list[at++] = (uint16_t)(64 * lane + __builtin_ctzll(in));
         __builtin_amdgcn_wave_barrier();
         for (int k0 = 0; k0 < all; k0 += 32) {
             v8s rest, x[L::NI];
@@ -472,7 +481,7 @@ __device__ __forceinline__ void add_targets(const XentGradArgs& p, int n, int m0
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const int k = k0 + 8 * kq + e, t = base + list[min(k, all - 1)];
-                row[e] = p.y[t] - origin - L::first_row(wm);
+                row[e] = p.y[t] - p.v0 - first;
                 rest[e] = k < all ? (short)bf16x2(p.rest[t], 0.0f) : (short)0;
 #pragma unroll
                 for (int j = 0; j < L::NI; j++) x[j][e] = (short)p.x[(int64_t)t * p.H8 + min(column + 16 * j, p.H8 - 1)];
@@ -495,7 +504,7 @@ __device__ __forceinline__ void add_targets(const XentGradArgs& p, int n, int m0
             }
         }
     }
-    __syncthreads();                                                         // (the block's LDS is free)
+    __builtin_amdgcn_wave_barrier();
 }
 
 // The piece's rows of dW: the packed tokens are the contraction (the same sizes 798 us).
@@ -508,12 +517,15 @@ __device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, 
     mm_band(mm_turn(block, tm * tn), tm, tn, im, in);
     const MmOperand b{p.x, p.H8, p.H8};
     v4f acc[L::MI][L::NI];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int first = im * L::BM + L::first_row(wave / L::WN), column = in * L::BN + wave % L::WN * L::NI * 16 + ((int)threadIdx.x & 15);
+    const uint64_t targets = p.parts == 1 ? targets_of<L>(p, n, first, 0) : 0;
     mm_zero<L>(acc);
     for (int part = 0; part < p.parts; part++) {
         const MmOperand a{p.d + part * p.plane, p.ldd, (p.V + 7) / 8 * 8};
         mm_tile<L, true>(a, b, im * L::BM, in * L::BN, n, smem, acc);
     }
-    if (p.parts == 1) add_targets<L>(p, n, im * L::BM, in * L::BN, smem, acc);
+    if (p.parts == 1) add_targets<L>(p, targets, n, first, column, smem, acc);
     const float s = p.ctrl->largest;
 #pragma unroll
     for (int i = 0; i < L::MI; i++)
@@ -710,8 +722,11 @@ hipError_t run_gradients(const XentGradArgs& p, hipStream_t s)
     return hipGetLastError();
 }
 
+// Masks of 16 tokens for a group of columns: whole 64-bit words.
+int64_t hits_ld(int64_t T) { return over(T, 64) * 4; }
+
 struct XentLayout {
-    size_t ctrl, idx, pos, y, zy, x, parts, lse, g, rest, d, dx, w, total;
+    size_t ctrl, idx, pos, y, zy, x, parts, lse, g, rest, hits, d, dx, w, total;
     bool pad_w;
     int piece;                      // columns of a piece; half as many where d has two numbers
 };
@@ -743,6 +758,7 @@ XentLayout xent_layout(int64_t T, int64_t H, int64_t V, const void* w, int64_t l
         L.lse = take(T * 4);
         L.g = take(T * 4);
         L.rest = take(T * 4);
+        L.hits = take(over(L.piece, 64) * hits_ld(T) * 2);
         L.d = take(T * (int64_t)L.piece * 2);
         // dx of every row, or of fewer rows in slices: dx_blocks tiles then (of either tile, with dW or alone)
         int64_t most_dx = T * H8;
@@ -903,6 +919,7 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         p.d = c.at<uint16_t>(c.L.d), p.ldd = piece;
         p.plane = full ? (int64_t)T * piece : 0;
         p.rest = c.at<float>(c.L.rest);
+        p.hits = c.at<uint16_t>(c.L.hits), p.hits_ld = (int)hits_ld(T);
         if (T > 0 && run_logits<true>(p, s) != hipSuccess) return V4MOE_ELAUNCH;
         XentGradArgs q{};
         q.T = T, q.H = H, q.H8 = c.H8, q.V = n;
@@ -911,6 +928,7 @@ __attribute__((visibility("default"))) int moe_linear_xent_backward(
         q.ctrl = ctrl;
         q.x = p.x, q.w = p.w, q.ldw = p.ldw, q.d = p.d, q.ldd = p.ldd;
         q.v0 = v0, q.y = p.y, q.rest = p.rest;
+        q.hits = p.hits, q.hits_ld = p.hits_ld;
         q.dx = c.at<float>(c.L.dx), q.first = v0 == 0;
         if (dw) {
             const bool bf16 = dw_type == V4MOE_TYPE_BF16;
