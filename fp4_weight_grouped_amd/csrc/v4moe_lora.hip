@@ -80,7 +80,9 @@ constexpr int kListAdapters = 2048;  // of a pass: counters of sixteen waves fit
 // adapter, wave by wave), and the waves go through their rows again; rows of one adapter
 // among a wave's 64 find each other by a ballot for each bit of the id.  More adapters than
 // the counters hold take a pass over the rows for each 2048 of them.
-// 8192 rows 9 us, 512 rows 7.
+// 8192 rows 9 us, 512 rows 7 (10 and 8 where one pass of at most 1024 were written as any number of them).
+// MANY: passes of up to 2048 adapters, two a thread; otherwise one pass, an adapter a thread.
+template <bool MANY>
 __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t* __restrict__ ids, Listing out, int most)
 {
     extern __shared__ int counts[];               // [16][n], then [n] first place, [n] first tile
@@ -89,8 +91,8 @@ __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t*
     const int share = (M + 1023) / 1024 * 64, m0 = wave * share, m1 = min(m0 + share, M);
     const bool once = share <= 512;                                 // then the places below the wave's first stay here
     int rows_done = 0, tiles_done = 0;
-    for (int a0 = 0; a0 <= L; a0 += kListAdapters) {
-        const int n = min(L + 1 - a0, kListAdapters);               // adapters of this pass, "none" among the last
+    for (int a0 = 0; MANY ? a0 <= L : a0 == 0; a0 += kListAdapters) {
+        const int n = MANY ? min(L + 1 - a0, kListAdapters) : L + 1;            // adapters of this pass, "none" among the last
         int* begin = counts + 16 * n;
         int* first_tile = begin + n;
         for (int i = tid; i < 16 * n; i += 1024) counts[i] = 0;
@@ -108,7 +110,7 @@ __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t*
 #pragma unroll
             for (int q = 0; q < 8; q++) {
                 const int a = (id[q] >= 0 && id[q] < L ? id[q] : L) - a0;
-                id[q] = base + 64 * q + lane < m1 && a >= 0 && a < n ? a : -1;
+                id[q] = base + 64 * q + lane < m1 && (!MANY || (a >= 0 && a < n)) ? a : -1;
             }
         };
         int bits = 0;
@@ -136,7 +138,8 @@ __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t*
         }
         __syncthreads();
         // a thread's adapters: one, or two that follow each other
-        const int each = n > 1024 ? 2 : 1, first = tid * each, last = min(first + each, n);
+        constexpr int EACH = MANY ? 2 : 1;
+        const int first = tid * EACH, last = min(first + EACH, n);
         int rows = 0, tiles = 0;
         for (int a = first; a < last; a++) {
             int r = 0;
@@ -182,7 +185,7 @@ __global__ __launch_bounds__(1024) void k_lora_list(int M, int L, const int32_t*
                 }
             }
         }
-        __syncthreads();                                            // (the counts are read)
+        if (MANY) __syncthreads();                                  // (the counts are read)
     }
     if (tid == 0) {
         out.begin[L + 1] = M;
@@ -1075,14 +1078,19 @@ bool listed_first(int M, int L, bool backward)
 }
 int64_t most_tiles(int64_t M, int64_t L) { return M / kTile + std::min<int64_t>(M, L + 1); }
 
-hipError_t run_list(int M, int L, const int32_t* ids, const Listing& list, hipStream_t s)
+template <bool MANY>
+hipError_t launch_list(int M, int L, const int32_t* ids, const Listing& list, hipStream_t s)
 {
     static LdsAllowed allowed;
-    const auto kernel = k_lora_list;
-    const int bytes = (16 + 2) * kListAdapters * 4;
-    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), bytes, allowed); e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), (16 + 2) * std::min(L + 1, kListAdapters) * 4, s, M, L, ids, list, (int)most_tiles(M, L));
+    const auto kernel = k_lora_list<MANY>;
+    constexpr int COUNTERS = (16 + 2) * 4, MOST = MANY ? kListAdapters : 1024;
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), COUNTERS * MOST, allowed); e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), COUNTERS * std::min(L + 1, MOST), s, M, L, ids, list, (int)most_tiles(M, L));
     return hipGetLastError();
+}
+hipError_t run_list(int M, int L, const int32_t* ids, const Listing& list, hipStream_t s)
+{
+    return L + 1 > 1024 ? launch_list<true>(M, L, ids, list, s) : launch_list<false>(M, L, ids, list, s);
 }
 
 template <int NJ, bool LISTED>
