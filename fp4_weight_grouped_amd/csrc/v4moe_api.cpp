@@ -48,8 +48,7 @@ DeviceInfo* device_info()
     return di->ok ? di : nullptr;
 }
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 
 bool dims_ok(const v4moe_dims* d)
 {

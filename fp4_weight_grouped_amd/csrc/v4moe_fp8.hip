@@ -924,10 +924,8 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_split(GemmArgs g, const uint16_
     }
 }
 
-inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 inline int64_t chunks(int64_t v) { return (v + 127) / 128; }
-inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 template <typename T>
 hipError_t launch_quant(int mode, int R, int C, const T* x, int64_t ldx, uint8_t* q, int64_t ldq, float* s, uint8_t* qt,

@@ -164,16 +164,7 @@ __global__ __launch_bounds__(256) void k_pad_rows(PadJobs p)
     for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < g.R * segs; i += (int64_t)p.blocks[j] * 256) {
         const int64_t r = i / segs;
         const int c = (int)(i - r * segs) * 8;
-        const uint16_t* s = g.src + r * g.ld + c;
-        v4u32 v;
-        if (c + 8 <= g.C) {
-            v = *reinterpret_cast<const v4u32_any*>(s);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; u++)
-                v[u] = (c + 2 * u < g.C ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < g.C ? (uint32_t)s[2 * u + 1] << 16 : 0u);
-        }
-        *reinterpret_cast<v4u32*>(g.dst + r * C8 + c) = v;
+        *reinterpret_cast<v4u32*>(g.dst + r * C8 + c) = load8(g.src + r * g.ld, c, g.C);
     }
 }
 

@@ -20,6 +20,9 @@ constexpr size_t kScratchBytes = (size_t)16 << 20;
 // split into waves of a few experts each).
 constexpr int kWaveExperts = 8;
 
+inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
 struct MatPtr {
     const uint8_t* fp4;   // packed [E][N/16][K/128][64][16]
     const uint8_t* e8m0;  // packed [E][N/64][K/128][64][4]

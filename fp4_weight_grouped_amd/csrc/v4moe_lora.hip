@@ -33,17 +33,6 @@ namespace {
 // four sums, in order, and these are added in order.
 constexpr int kSlice = 256, kSums = 4;
 
-// Sixteen bytes of a row from element k on; zeros past K.
-__device__ __forceinline__ v4u32 load8(const uint16_t* row, int k, int K)
-{
-    if (k + 8 <= K) return *reinterpret_cast<const v4u32_any*>(row + k);
-    v4u32 v;
-#pragma unroll
-    for (int u = 0; u < 4; u++)
-        v[u] = (k + 2 * u < K ? (uint32_t)row[k + 2 * u] : 0u) | (k + 2 * u + 1 < K ? (uint32_t)row[k + 2 * u + 1] << 16 : 0u);
-    return v;
-}
-
 // The adapters among a tile's rows, one after the other, in the order of their first rows:
 // f(a, mask of a's rows) for every `slots`-th of them from `slot` on.  id: lane l's is row
 // l's, negative for none.

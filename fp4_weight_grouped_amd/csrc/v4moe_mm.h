@@ -32,6 +32,17 @@ typedef v4u32 v4u32_any __attribute__((aligned(2)));
 typedef uint32_t v2u32 __attribute__((ext_vector_type(2)));
 typedef v2u32 v2u32_any __attribute__((aligned(2)));
 
+// Sixteen bytes of a row from element k on; zeros past K.
+__device__ __forceinline__ v4u32 load8(const uint16_t* row, int k, int K)
+{
+    if (k + 8 <= K) return *reinterpret_cast<const v4u32_any*>(row + k);
+    v4u32 v;
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+        v[u] = (k + 2 * u < K ? (uint32_t)row[k + 2 * u] : 0u) | (k + 2 * u + 1 < K ? (uint32_t)row[k + 2 * u + 1] << 16 : 0u);
+    return v;
+}
+
 // What a 16-byte segment past the end of the contraction is copied from.
 static __device__ const uint4 g_mm_zeros[64] = {};
 
@@ -403,8 +414,6 @@ __device__ __forceinline__ void mm_band(int tile, int tm, int tn, int& im, int& 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 inline int64_t over(int64_t n, int64_t b) { return (n + b - 1) / b; }
 

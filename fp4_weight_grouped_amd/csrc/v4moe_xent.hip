@@ -38,9 +38,9 @@ struct XentCtrl { int n; float largest; };
 
 __device__ __forceinline__ float exp_(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-// (More than kFewTokens of them; one block: 10 us at 8192, beside products that take milliseconds by then.)
 // Numbers the tokens with a target: pos[t] their place among them (-1 for the others),
-// idx the tokens in order.  One block: 4096 tokens a step.
+// idx the tokens in order.  More than kFewTokens of them; one block, 4096 tokens a step: 10 us at
+// 8192, beside products that take milliseconds by then.
 // loss, lse (or null): zeros for the tokens without one.  g (or null): the incoming gradients.
 __global__ __launch_bounds__(1024) void k_xent_rows(int T, int V, const int64_t* __restrict__ targets,
                                                     const float* __restrict__ g, int64_t gs, int* __restrict__ pos,
@@ -118,16 +118,7 @@ __device__ __forceinline__ void pack_rows(const PackArgs& p, int n, float larges
     const int64_t all = (int64_t)n * segs;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
         const int r = (int)(i / segs), c = (int)(i - (int64_t)r * segs) * 8, t = row(r);
-        const uint16_t* s = p.x + t * p.ldx + c;
-        v4u32 v;
-        if (c + 8 <= p.H) {
-            v = *reinterpret_cast<const v4u32_any*>(s);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; u++)
-                v[u] = (c + 2 * u < p.H ? (uint32_t)s[2 * u] : 0u) | (c + 2 * u + 1 < p.H ? (uint32_t)s[2 * u + 1] << 16 : 0u);
-        }
-        *reinterpret_cast<v4u32*>(p.xp + (int64_t)r * p.H8 + c) = v;
+        *reinterpret_cast<v4u32*>(p.xp + (int64_t)r * p.H8 + c) = load8(p.x + t * p.ldx, c, p.H);
         if (c == 0) {
             p.yp[r] = (int)p.targets[t];
             if (p.g) {
