@@ -90,8 +90,9 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int tn, int bloc
 
 // Forward and data gradient: row tiles of each expert by column tiles of C.  Few rows: the weights' bytes (1024 rows of
 // 256 experts, 2048 x 4096: 677 us, 6.2 TB/s; 8 rows of 8 experts 25, 5.3).  Many: the matrix units (65536 uneven rows
-// of those experts 1315 us, 0.84 PFLOP/s, with 4.3 GB of weights on the way; 2048 rows each of 32 experts 907, 1.21;
-// data gradient of 32768 rows, 4096 x 2048, 32 experts 536 to 574).
+// of those experts 1305 us, 0.84 PFLOP/s, with 4.3 GB of weights on the way; 2048 rows each of 32 experts 886, 1.24;
+// data gradient of 32768 rows, 4096 x 2048, 32 experts 518; the first launches after a pause, as under a profiler, take up
+// to a tenth longer).
 template <class L>
 __device__ __forceinline__ void rows_tile(const GroupedArgs& g, int tn, int block, int blocks, uint8_t* smem)
 {
@@ -112,8 +113,8 @@ __global__ __launch_bounds__(L::THREADS) void k_grouped_rows(GroupedArgs g, int 
     rows_tile<L>(g, tn, blockIdx.x, gridDim.x, smem);
 }
 
-// Weight gradient: the tiles of each expert's dW, its rows the contraction (32768 rows, 4096 x 2048, 32 experts 645 to
-// 670 us: 16 chunks a tile, so that its begin and its end, with 0.5 GB of dW to store, weigh more).
+// Weight gradient: the tiles of each expert's dW, its rows the contraction (32768 rows, 4096 x 2048, 32 experts 609 us,
+// under a profiler up to 670: 16 chunks a tile, so that its begin and its end, with 0.5 GB of dW to store, weigh more).
 template <class L>
 __device__ __forceinline__ void weights_tile(const GroupedArgs& g, int tm, int tn, int block, uint8_t* smem)
 {

@@ -56,8 +56,8 @@ struct MmOperand {
 
 // WM x WN waves, each MI x NI tiles of 16x16; NS stages of 64 k in LDS.  RAGGED: many tiles end before BM rows (the
 // last one of each group).  The row tiles are then dealt to the wave rows in turn, and those past A's end cost no
-// products, so that such a tile's waves end together and early (65536 rows of 256 experts, 2048 x 4096: 1430 -> 1315 us);
-// whole tiles pay 2.5% for it.
+// products, so that such a tile's waves end together and early (65536 uneven rows of 256 experts, 2048 x 4096: 1408 -> 1305
+// us); whole tiles pay for it (8192x8192x8192 740 -> 779 us, 256 rows for each of those experts 1049 -> 1057).
 template <int WM_, int WN_, int MI_, int NI_, int NS_, bool ACOL_, bool BCOL_, bool RAGGED_ = false>
 struct MmTile {
     static constexpr bool RAGGED = RAGGED_;
@@ -273,7 +273,7 @@ __device__ __forceinline__ void mm_tile(const MmOperand& a, const MmOperand& b, 
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j][s], af[i % D][s], acc[i][j], 0, 0, 0);
     };
     // The copies of a large tile's next stage go out in groups, a row tile's products after each: all at once they
-    // would hold up every wave's products until the memory path has taken them (8192x8192x8192 792 -> 752 us).
+    // would hold up every wave's products until the memory path has taken them (8192x8192x8192, not RAGGED, 792 -> 752 us).
     constexpr int GROUPS = MI >= 4 ? MI / 2 : 1, PER = (L::OPS + GROUPS - 1) / GROUPS;
     // row tiles of this wave with rows in them
     const int live = __builtin_amdgcn_readfirstlane((min(a.n - m0, L::BM) - 16 * wm + 16 * L::WM - 1) / (16 * L::WM));

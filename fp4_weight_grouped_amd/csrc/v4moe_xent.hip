@@ -498,7 +498,7 @@ __device__ __forceinline__ void add_targets(const XentGradArgs& p, uint64_t in, 
     __builtin_amdgcn_wave_barrier();
 }
 
-// The piece's rows of dW: the packed tokens are the contraction (the same sizes 798 us).
+// The piece's rows of dW: the packed tokens are the contraction (the same sizes 830 us, 30 of them the targets').
 template <class L>
 __device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, int block, uint8_t* smem)
 {
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(L::THREADS) void k_xent_dw(XentGradArgs p, int tm, 
     dw_block<L>(p, tm, tn, blockIdx.x, smem);
 }
 // Both, dx's blocks, whose contraction is the longer one, first (1237 tokens, 495 of them with a target, 50021 x 1001:
-// 129 us; one after the other, with the tiles best for each, 148).
+// 138 us, 9 of them the targets'; one after the other, with the tiles best for each, 19 more).
 template <class X, class W>
 __global__ __launch_bounds__(X::THREADS) void k_xent_gradients(XentGradArgs p, int xblocks, int tm, int tn)
 {
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(X::THREADS) void k_xent_gradients(XentGradArgs p, i
 }
 
 // dx of every token: the slices' sums in order and what d's rounding left at the target, times the largest |g|; zeros
-// without a target.
+// without a target.  4096 tokens, H = 4096: 29 us, 7 of them the targets' rows of W.
 template <typename T_>
 __global__ __launch_bounds__(256) void k_xent_finish(int T, int H, int H8, int bm, int bn, int piece,
                                                      const XentCtrl* __restrict__ ctrl,

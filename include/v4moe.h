@@ -474,7 +474,8 @@ int moe_clip_grads(int32_t count, const v4moe_tensor* tensors, float max_norm, f
 
 /* Workspace bytes of the calls below (host-only, pure; 0 for invalid sizes): operands
  * whose rows do not begin at 16 bytes, or are not a multiple of 8 elements long, are
- * copied there first; the pointers are only looked at for that.  16-byte aligned. */
+ * copied there first, by every call and as a whole: of w all experts' rows, whether they
+ * have rows of x or not.  The pointers are only looked at for that.  16-byte aligned. */
 size_t moe_grouped_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K, const uint16_t* x,
                                    int64_t ldx, const uint16_t* dy, int64_t lddy, const uint16_t* w,
                                    int32_t backward);
@@ -553,8 +554,10 @@ int32_t moe_linear_xent_tile(int32_t T, int32_t H, int32_t V, int32_t what, int3
  *   x, dy bf16 rows [M][ldx], [M][lddy]
  * 0 <= M, 1 <= N, K, leading dimensions of bf16 operands, all up to 2^22; 1 <= r <= 512;
  * 1 <= L <= 65535.  Sums are fp32 in a fixed order, the rank-sized intermediates kept to
- * 16 bits of significand; a row's result does not depend on the other rows.  Pointers: aligned
- * to their element. */
+ * 16 bits of significand, as two bf16 numbers (an infinite element of x, dy or a factor may
+ * give NaN where one product would give an infinity); a row's result does not depend on the
+ * other rows.  More than 64 ranks pass in pieces of 64, each over all rows.  Pointers:
+ * aligned to their element. */
 typedef struct {
     int32_t M;      /* rows                       */
     int32_t N;      /* columns of the projection  */
