@@ -439,9 +439,9 @@ __device__ __forceinline__ uint64_t targets_of(const XentGradArgs& p, int n, int
 
 // Adds what d's rounding left at the targets to a wave's tile of dW: rest[t] x[t] to row y[t], 32 tokens at a time, in
 // order.  `in`: targets_of the first 4096, fetched ahead of the tile.  A wave without any is done; one with a few waits
-// for a list and two loads in a row (1237 tokens, 495 of them with a target, 50021 x 1001: the call 229 -> 238 us, 249 where
-// a block looked through the tokens here; 4096 tokens, V = 131072, H = 4096: 1.2% more, 1.6).  One target for all of 4096 tokens, so that one tile has them
-// all: both gradients of 131072 columns 10300 -> 11400 us.
+// for a list and two loads in a row: 1237 tokens, 495 of them with a target, 50021 x 1001, the call 229 -> 238 us (249 where
+// a block looked through the tokens here); 4096 tokens, V = 131072, H = 4096, 1.2% more (1.6).  One target for all of 4096
+// tokens, so that one tile has them all: both gradients of 131072 columns 10000 -> 11400 us.
 template <class L>
 __device__ __forceinline__ void add_targets(const XentGradArgs& p, uint64_t in, int n, int first, int column, uint8_t* smem,
                                             v4f (&acc)[L::MI][L::NI])
@@ -490,8 +490,8 @@ __device__ __forceinline__ void add_targets(const XentGradArgs& p, uint64_t in, 
                 if (!__ballot(any)) continue;
 #pragma unroll
                 for (int j = 0; j < L::NI; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[j]), __builtin_bit_cast(v8bf, a),
-                                                                        acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[j]),
+                                                                        __builtin_bit_cast(v8bf, a), acc[i][j], 0, 0, 0);
             }
         }
     }
@@ -509,7 +509,8 @@ __device__ __forceinline__ void dw_block(const XentGradArgs& p, int tm, int tn, 
     const MmOperand b{p.x, p.H8, p.H8};
     v4f acc[L::MI][L::NI];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int first = im * L::BM + L::first_row(wave / L::WN), column = in * L::BN + wave % L::WN * L::NI * 16 + ((int)threadIdx.x & 15);
+    const int first = im * L::BM + L::first_row(wave / L::WN);
+    const int column = in * L::BN + wave % L::WN * L::NI * 16 + ((int)threadIdx.x & 15);
     const uint64_t targets = p.parts == 1 ? targets_of<L>(p, n, first, 0) : 0;
     mm_zero<L>(acc);
     for (int part = 0; part < p.parts; part++) {
