@@ -13,7 +13,6 @@ import torch
 
 from fp4_weight_grouped_amd import v4moe
 
-pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF16, F32 = torch.bfloat16, torch.float32
 
@@ -79,9 +78,19 @@ def close(got, want, bound, what):
     assert not bool(bad.any()), (what, int(bad.sum()), float((got.double() - want).abs().max()))
 
 
+def test_many_tokens_in_either_tile():
+    """Cases of more than 4096 tokens with a target, which dW's tiles take in turns, are of both tiles."""
+    many = (12000, 40, 3000), (12000, 64, 700), (6000, 2056, 20000)
+    tiles = {H: v4moe.lib().moe_linear_xent_tile(T, H, V, 2, 1) & 0xFFFF for T, H, V in many}
+    assert tiles == {40: 128, 64: 128, 2056: 256}
+
+
 # tokens, width, columns, columns aimed at: few tokens and many; targets of their own and one for all; a partial last
-# tile; a vocabulary in several pieces; products of 128x128 tiles, both in one launch, and of 256x256
+# tile; a vocabulary in several pieces; products of 128x128 tiles, both in one launch, and of 256x256; more than 4096 tokens
+# with a target, all of them in one tile, too
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H,V,aimed", [
+    (12000, 40, 3000, 50), (12000, 64, 700, 1), (6000, 2056, 20000, 300), (6000, 2056, 20000, 1),
     (1, 64, 5000, 1), (3, 40, 5000, 3), (40, 264, 5003, 30), (300, 72, 5000, 100), (300, 104, 5000, 1), (700, 1001, 9001, 200),
     (1500, 136, 9000, 1000), (4100, 32, 66000, 300), (5000, 64, 20011, 1), (700, 2048, 16500, 100), (2000, 1024, 40000, 2),
 ])
@@ -102,6 +111,7 @@ def test_the_targets_keep_their_digits(T, H, V, aimed, pad):
     close(after, before.double() + dw, dw_bound + 2.0 ** -23 * (before.double().abs() + dw.abs() + dw_bound), "dw added to")
 
 
+@pytest.mark.gpu
 def test_rounded_once():
     """The gradients of either type come of the same sums, and repeat themselves."""
     torch.manual_seed(0)
